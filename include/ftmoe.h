@@ -416,6 +416,169 @@ int ftmoe_slice_format(int format, int matrix, int E, int H, int I, int i0, int 
 int ftmoe_quantize_activations(const void* a, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
                                ftmoe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Training operators: what one training step needs around the layer's matrix
+ * products.  The pages serve the layer and have no counterpart.
+ *
+ * They need no handle: the caller owns every buffer, and the calls run on the
+ * current device.  All are asynchronous on `stream`, allocate nothing, read
+ * nothing back to the host and may be captured in a CUDA graph once one of
+ * them has run on the device (the first call looks up a device address and
+ * sets kernel limits).  Sums run in fp32 or wider in a fixed order and are
+ * rounded once; no call uses atomics on values, so results are bit-identical
+ * run to run.  Any H, T, k and E within the limits below is taken; rows whose
+ * bytes are a multiple of 16 move 16 bytes at a time.
+ *
+ * Range checks inside the kernels (an expert, place, id or target out of
+ * range) mark a device word and leave the item out, as each call says;
+ * ftmoe_ops_status reads that word. */
+typedef enum { FTMOE_BF16 = 0, FTMOE_FP32 = 1, FTMOE_FP16 = 2 } ftmoe_dtype;
+
+/* Sort the tokens' rows by expert.  Pair p = t*top_k + j has expert
+ * topk_idx[t][j]; a negative expert drops the pair (a slot that another rank
+ * owns), and so does one >= E, which also marks the status word.
+ *   x:        [T, H] of `dtype`, or NULL (tables only)
+ *   topk_idx: int32 [T, top_k], top_k 1..32, E 1..1024
+ *   offsets:  [E + 1] first place of each expert; offsets[E] = pairs kept
+ *   perm:     [T*top_k] pair at each place, by expert and then by pair id;
+ *             -1 from offsets[E] on
+ *   inv:      [T*top_k] place of each pair, -1 if it is dropped
+ *   xs:       [T*top_k, H]: xs[inv[p]] = x[t]; rows from offsets[E] on stay
+ *             as they were.  NULL iff x is.
+ * offsets, perm and inv have ftmoe_aux's meaning when nothing is dropped.
+ * The gradient of the copy is ftmoe_combine without weights.  T == 0 writes
+ * offsets.  x and xs: 16-byte aligned, not the same. */
+int ftmoe_dispatch(const void* x, int dtype, int T, int H, const int32_t* topk_idx, int top_k, int E,
+                   int32_t* offsets, int32_t* perm, int32_t* inv, void* xs, ftmoe_stream_t stream);
+
+/* out[t] = sum_j w[t][j] * ys[inv[t*top_k + j]] over the kept slots, in slot
+ * order; a token without one gets zeros.  w: fp32 [T, top_k], or NULL for
+ * weights of one.  Rows of dropped slots are not read.  A place outside
+ * [-1, T*top_k) counts as dropped and marks the status word.
+ * ys, out: `dtype`, 16-byte aligned, not the same. */
+int ftmoe_combine(const void* ys, int dtype, int T, int H, int top_k, const int32_t* inv, const float* w, void* out,
+                  ftmoe_stream_t stream);
+
+/* ftmoe_combine's gradient: dys[inv[p]] = w[p] * dout[t] (rows that no kept
+ * pair has stay as they were) and dw[p] = <dout[t], ys[inv[p]]>, 0 for a
+ * dropped pair.  dys may be ys itself (the rows are replaced). */
+int ftmoe_combine_backward(const void* dout, const void* ys, int dtype, int T, int H, int top_k, const int32_t* inv,
+                           const float* w, void* dys, float* dw, ftmoe_stream_t stream);
+
+/* The router's gradient from that of its weights.  With S = sum_j w_j dw_j:
+ *   norm_topk_prob: dlogits[e] = sum over the j with idx_j = e of w_j (dw_j - S)
+ *                   (logits is not read and may be NULL)
+ *   otherwise:      dlogits[e] = p_e (sum over those j of dw_j - S),
+ *                   p = softmax(logits), logits fp32 [T, E] with the bias
+ * topk_idx is the router's own choice, before any slot is dropped; an index
+ * outside [0, E) is left out and marks the status word.  dlogits: fp32
+ * [T, E], written whole. */
+int ftmoe_route_backward(const float* logits, const int32_t* topk_idx, const float* topk_w, const float* dw, int T,
+                         int E, int top_k, int norm_topk_prob, float* dlogits, ftmoe_stream_t stream);
+
+/* out[n] = scale * table[ids[n]].  ids: int32 or int64 (id_bytes 4 or 8); an
+ * id outside [0, V) gives a row of zeros and marks the status word.
+ * table [V, H], out [N, H]: `dtype`, 16-byte aligned, not the same. */
+int ftmoe_embed(const void* table, int dtype, int64_t V, int H, const void* ids, int id_bytes, int64_t N, float scale,
+                void* out, ftmoe_stream_t stream);
+
+/* Bytes of the workspace that ftmoe_embed_backward needs for N tokens of
+ * width H (about 16 N + N H / 4; negative: a status code). */
+int64_t ftmoe_embed_workspace(int64_t N, int H);
+
+/* ftmoe_embed's gradient: dtable[v] = scale * (sum over the n with ids[n] = v
+ * of dout[n], in the order of n, in fp32).  Rows of no token become zeros;
+ * with `accumulate` (fp32 dtable only) the sum is added to dtable and other
+ * rows are not touched.  Tokens whose id is padding_id are left out (-1: none
+ * of the valid ids); other ids outside [0, V) are left out and mark the
+ * status word.  V up to 2^30.
+ *   dout: `dtype` [N, H]; dtable: table_dtype (`dtype` or FTMOE_FP32) [V, H]
+ *   workspace: workspace_bytes >= ftmoe_embed_workspace(N, H); its contents
+ *   matter only during the call */
+int ftmoe_embed_backward(const void* dout, int dtype, const void* ids, int id_bytes, int64_t N, int64_t V, int H,
+                         float scale, int64_t padding_id, void* dtable, int table_dtype, int accumulate,
+                         void* workspace, int64_t workspace_bytes, ftmoe_stream_t stream);
+
+/* Clipped policy loss with a KL term, and its gradient.  For each row n, with
+ * z = logits[n] / temperature and y = targets[n]:
+ *   logp = z_y - log(sum_v exp z_v),  r = exp(logp - old_logp),  A = advantage
+ *   row  = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *          + kl_coef (exp(d) - d - 1),  d = ref_logp - logp
+ *   loss = sum_n weight_n row_n
+ *   dlogits[n] = grad_scale * weight_n * d row / d logits[n]
+ * (the clipped side has no gradient; where both sides are equal the unclipped
+ * one's is taken).  A row of weight 0 is left out: its logits are not read,
+ * row_loss and logp are 0 and its gradient is zeros.  So is a row whose target
+ * is outside [0, V), which also marks the status word.  Logits of -inf have
+ * probability 0; NaN in a counted row reaches its outputs. */
+typedef struct {
+  const void* logits;      /* [N, V] of `dtype`, rows `ld` values apart (ld >= V); any row alignment */
+  int32_t dtype;
+  int32_t id_bytes;        /* 4 or 8: the targets' type */
+  int64_t N, V, ld;
+  const void* targets;     /* int32 or int64 [N] */
+  const float* old_logp;   /* [N] log probability under the policy that sampled */
+  const float* ref_logp;   /* [N] under the reference policy, or NULL (no KL term) */
+  const float* advantage;  /* [N] */
+  const float* weight;     /* [N], e.g. mask / number of counted tokens; NULL: 1/N each */
+  float temperature;       /* > 0 */
+  float clip_low, clip_high; /* >= 0 */
+  float kl_coef;           /* 0: no KL term */
+  float grad_scale;        /* of the gradient only (loss scaling) */
+  float* loss;             /* [1] */
+  float* row_loss;         /* [N], before the weight */
+  float* logp;             /* [N] or NULL */
+  void* dlogits;           /* [N, V] of `dtype`, rows ld_d apart, or NULL (forward only);
+                              may be `logits` itself with ld_d == ld */
+  int64_t ld_d;
+} ftmoe_policy_args;
+
+int ftmoe_policy_loss(const ftmoe_policy_args* args, ftmoe_stream_t stream);
+
+/* One AdamW step over n_tensors tensors.  With g' = grad_scale * g and `step`
+ * counted from 1:
+ *   m <- beta1 m + (1 - beta1) g';  v <- beta2 v + (1 - beta2) g'^2
+ *   p <- p (1 - lr weight_decay)
+ *        - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32.  Tensors may differ in size, types and weight decay; pointers need
+ * only their own type's alignment.  With `master`, p is its rounded copy.
+ * state_bits 8: m and v hold one E4M3 code a value, v's of the root sqrt(v),
+ * with a scale per 256 consecutive values, scale = amax * fl(1/448) and code =
+ * E4M3(value * (448 * fl(1/amax))) in fp32 (blocks whose amax is below 1e-30
+ * are held as zeros); a root above zero keeps at least the smallest code.  Zeros in codes and scales are the state before the first
+ * step.  A gradient that is not finite spoils its value (32 bits) or its
+ * block (8 bits). */
+typedef struct {
+  void* p;               /* [n] of p_dtype, updated */
+  const void* g;         /* [n] of g_dtype */
+  float* master;         /* [n] fp32, updated, or NULL (p itself is the master); 16-bit p only */
+  void* m;               /* [n] fp32, or uint8 codes */
+  void* v;               /* [n] fp32, or uint8 codes of sqrt(v) */
+  float* m_scale;        /* [ceil(n / 256)], 8-bit states only */
+  float* v_scale;
+  int64_t n;
+  float weight_decay;
+  int32_t p_dtype;
+  int32_t g_dtype;       /* p_dtype or FTMOE_FP32 */
+  int32_t state_bits;    /* 8 or 32 */
+} ftmoe_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  const float* grad_scale; /* device [1] or NULL (1); not finite: the whole step is skipped */
+} ftmoe_adamw_params;
+
+/* `tensors` and `params` are host memory, read during the call (the launches
+ * carry the list: no device copy of it is made). */
+int ftmoe_adamw(const ftmoe_adamw_tensor* tensors, int n_tensors, const ftmoe_adamw_params* params,
+                ftmoe_stream_t stream);
+
+/* Synchronise `stream`, read and clear the current device's status word of
+ * the training operators: FTMOE_OK, or FTMOE_ERR_DEVICE_CHECK if a kernel met
+ * an index out of range since the last call.  One word serves all streams. */
+int ftmoe_ops_status(ftmoe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,386 @@
+// Tokens sorted by expert and back: the dispatch (stable sort of the (token,
+// slot) pairs by expert and the copy of each token's row to its sorted
+// places), the weighted combine, and their gradients down to the router's logits.
+//
+// Pair p = t * k + j has expert e_p; a pair whose index is outside [0, E) is
+// dropped.  offsets[e] = #{p : e_p < e}, and a kept pair's place is
+// inv[p] = offsets[e_p] + #{q < p : e_q = e_p}.
+#include "cluster_sort.cuh"
+
+namespace ftmoe {
+
+namespace {
+
+constexpr int kThreads = 256;
+// Pairs up to which every CTA counts its own tokens' places (one launch).
+constexpr int kCountPairs = 4096;
+constexpr int kSlots = 8;  // slots a thread keeps in flight
+
+struct DispatchArgs {
+  const int32_t* idx;
+  int T, k, E, P;
+  int32_t *offsets, *perm, *inv;
+  uint32_t* status;
+};
+
+// offsets from a histogram of the experts; perm's places past the last kept pair become -1.
+__device__ void dispatch_tables(const DispatchArgs& a) {
+  __shared__ int hist[kMaxBins];
+  __shared__ int wsum[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int e = tid; e < kMaxBins; e += kThreads) hist[e] = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int p = tid; p < a.P; p += kThreads) {
+    const int e = a.idx[p];
+    if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
+    bad |= e >= a.E;
+  }
+  if (bad) set_status(a.status, kStatusRange);
+  __syncthreads();
+  constexpr int kPer = kMaxBins / kThreads;
+  int v[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    v[i] = sum;
+    sum += hist[tid * kPer + i];
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += n;
+  }
+  if (lane == 31) wsum[warp] = inc;
+  __syncthreads();
+  int before = 0, kept = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    before += w < warp ? wsum[w] : 0;
+    kept += wsum[w];
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = tid * kPer + i;
+    if (e <= a.E) a.offsets[e] = before + inc - sum + v[i];
+  }
+  if (tid == 0 && a.E == kMaxBins) a.offsets[a.E] = kept;
+  for (int p = kept + tid; p < a.P; p += kThreads) a.perm[p] = -1;
+}
+
+// Few pairs: one launch.  CTA t counts the places of token t's slots itself
+// (a warp per slot reads all P indices; e_q < e_p + [q < p] is the test for
+// "sorts before", and as unsigned values dropped pairs never pass it), then
+// copies the row.  The last CTA writes the tables.
+template <int B>
+__global__ void __launch_bounds__(kThreads) k_dispatch_count(DispatchArgs a, const void* x, int nv, void* xs) {
+  using V = typename Raw<B>::type;
+  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (t == a.T) {
+    dispatch_tables(a);
+    return;
+  }
+  __shared__ int place[32];
+  const V* src = static_cast<const V*>(x) + (int64_t)t * nv;
+  V* dst = static_cast<V*>(xs);
+  V row{};
+  if (x && tid < nv) row = src[tid];
+  for (int j = warp; j < a.k; j += kThreads / 32) {
+    const int p = t * a.k + j, e = a.idx[p];
+    const bool kept = e >= 0 && e < a.E;
+    int n = 0;
+    for (int q = lane; q < a.P; q += 32) n += (unsigned)a.idx[q] < (unsigned)(e + (q < p ? 1 : 0));
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) {
+      place[j] = kept ? n : -1;
+      a.inv[p] = kept ? n : -1;
+      if (kept) a.perm[n] = p;
+    }
+  }
+  if (!x) return;
+  __syncthreads();
+  for (int v = tid; v < nv; v += kThreads) {
+    if (v >= kThreads) row = src[v];
+    for (int j = 0; j < a.k; ++j) {
+      const int at = place[j];
+      if (at >= 0) dst[(int64_t)at * nv + v] = row;
+    }
+  }
+}
+
+// Many pairs: the sort, by one cluster.
+__global__ void __launch_bounds__(kSortCtaThreads) k_dispatch_sort(DispatchArgs a) {
+  extern __shared__ int sort_smem[];
+  bool bad = false;
+  const int placed = cluster_sort(
+      a.P, a.E, sort_smem,
+      [&](int64_t i) {
+        const int e = a.idx[i];
+        bad |= e >= a.E;
+        return e < a.E ? e : -1;
+      },
+      [&](int64_t i, int, int at) {
+        a.inv[i] = at;
+        if (at >= 0) a.perm[at] = (int)i;
+      },
+      [&](int e, int at) { a.offsets[e] = at; });
+  if (bad) set_status(a.status, kStatusRange);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.E] = placed;
+  for (int64_t p = placed + (int64_t)blockIdx.x * kSortCtaThreads + threadIdx.x; p < a.P;
+       p += (int64_t)gridDim.x * kSortCtaThreads)
+    a.perm[p] = -1;
+}
+
+// ... and the copy: each thread reads one piece of a token's row and writes it to the row's k places.
+template <int B>
+__global__ void __launch_bounds__(kThreads) k_dispatch_copy(const void* x, int64_t total, int nv, int k,
+                                                            const int32_t* inv, void* xs) {
+  using V = typename Raw<B>::type;
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= total) return;
+  const int64_t t = i / nv;
+  const int v = (int)(i - t * nv);
+  const V row = static_cast<const V*>(x)[i];
+  V* dst = static_cast<V*>(xs) + v;
+  for (int j = 0; j < k; ++j) {
+    const int at = inv[t * k + j];
+    if (at >= 0) dst[(int64_t)at * nv] = row;
+  }
+}
+
+// A pair's place, -1 if it is dropped or out of range.
+__device__ __forceinline__ int checked_place(int at, int64_t P, uint32_t* status) {
+  if (at < -1 || at >= P) {
+    set_status(status, kStatusRange);
+    return -1;
+  }
+  return at;
+}
+
+// out[t] = sum_j w[t, j] ys[inv[t, j]], slots in order, fp32.
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads) k_combine(const T* ys, int64_t total, int nv, int k, int64_t P,
+                                                      const int32_t* inv, const float* w, T* out, uint32_t* status) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= total) return;
+  const int64_t t = i / nv;
+  const int64_t v = i - t * nv;
+  float acc[N] = {};
+  for (int j0 = 0; j0 < k; j0 += kSlots) {
+    Pack<T, N> y[kSlots];
+    int at[kSlots];
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      at[j] = j0 + j < k ? checked_place(inv[t * k + j0 + j], P, status) : -1;
+      if (at[j] >= 0) y[j] = load_pack<T, N>(ys + ((int64_t)at[j] * nv + v) * N);
+    }
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      if (at[j] < 0) continue;
+      const float wj = w ? w[t * k + j0 + j] : 1.f;
+#pragma unroll
+      for (int c = 0; c < N; ++c) acc[c] = fmaf(wj, y[j].get(c), acc[c]);
+    }
+  }
+  Pack<T, N> o;
+#pragma unroll
+  for (int c = 0; c < N; ++c) o.set(c, acc[c]);
+  store_pack<T, N>(out + (t * nv + v) * N, o);
+}
+
+// dys[inv[p]] = w[p] dout[t], dw[p] = <dout[t], ys[inv[p]]>: W warps take a
+// token's row, kSlots slots at a time.  dys may be ys: a thread reads an
+// element before it writes it, and nobody else reads it.
+template <typename T, int N, int W>
+__global__ void __launch_bounds__(kThreads) k_combine_backward(const T* dout, const T* ys, int T_, int nv, int k,
+                                                               int64_t P, const int32_t* inv, const float* w, T* dys,
+                                                               float* dw, uint32_t* status) {
+  __shared__ float part[kThreads / 32][kSlots];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % W;
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / 32 / W) + warp / W;
+  const bool on = t < T_;
+  if (W == 1 && !on) return;
+  for (int j0 = 0; j0 < k; j0 += kSlots) {
+    int at[kSlots];
+    float wj[kSlots], dot[kSlots];
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      const bool use = on && j0 + j < k;
+      at[j] = use ? checked_place(inv[t * k + j0 + j], P, status) : -1;
+      wj[j] = use ? w[t * k + j0 + j] : 0.f;
+      dot[j] = 0.f;
+    }
+    if (on) {
+      for (int v = sub * 32 + lane; v < nv; v += 32 * W) {
+        const Pack<T, N> d = load_pack<T, N>(dout + (t * nv + v) * N);
+        Pack<T, N> y[kSlots];
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j)
+          if (at[j] >= 0) y[j] = load_pack<T, N>(ys + ((int64_t)at[j] * nv + v) * N);
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+          if (at[j] < 0) continue;
+          Pack<T, N> o;
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            dot[j] = fmaf(d.get(c), y[j].get(c), dot[j]);
+            o.set(c, wj[j] * d.get(c));
+          }
+          store_pack<T, N>(dys + ((int64_t)at[j] * nv + v) * N, o);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) dot[j] = warp_sum_f32(dot[j]);
+    if (W > 1) {
+      if (lane == 0) {
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) part[warp][j] = dot[j];
+      }
+      __syncthreads();
+      if (on && sub == 0 && lane < kSlots && j0 + lane < k) {
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < W; ++q) s += part[warp + q][lane];
+        dw[t * k + j0 + lane] = s;
+      }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+        if (lane == j && j0 + j < k) dw[t * k + j0 + j] = dot[j];
+    }
+  }
+}
+
+// The router's gradient, a warp per token.  With S = sum_j w_j dw_j,
+//   renormalised weights:   dlogits[e] = sum_{j : idx_j = e} w_j (dw_j - S)
+//   full-softmax weights:   dlogits[e] = p_e (sum_{j : idx_j = e} dw_j - S)
+__global__ void __launch_bounds__(kThreads) k_route_backward(const float* logits, const int32_t* idx, const float* w,
+                                                             const float* dw, int T, int E, int k, float* dlogits,
+                                                             uint32_t* status) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (t >= T) return;
+  int ej = -1;
+  float wj = 0.f, dj = 0.f;
+  if (lane < k) {
+    ej = idx[t * k + lane];
+    wj = w[t * k + lane];
+    dj = dw[t * k + lane];
+    if (ej < 0 || ej >= E) {
+      set_status(status, kStatusRange);
+      ej = -1;
+    }
+  }
+  const float S = warp_sum_f32(wj * dj);
+  const float up = logits ? dj : wj * (dj - S);
+  const float* z = logits ? logits + t * E : nullptr;
+  float top = -INFINITY, sum = 0.f;
+  if (z) {
+    for (int e = lane; e < E; e += 32) top = fmaxf(top, z[e]);
+    top = warp_max_f32(top);
+    for (int e = lane; e < E; e += 32) sum += expf(z[e] - top);
+    sum = warp_sum_f32(sum);
+  }
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int e = e0 + lane;
+    float g = 0.f;
+    for (int j = 0; j < k; ++j) {
+      const int other = __shfl_sync(0xffffffffu, ej, j);
+      const float u = __shfl_sync(0xffffffffu, up, j);
+      if (other == e) g += u;
+    }
+    if (e < E) {
+      if (z) g = expf(z[e] - top) / sum * (g - S);
+      dlogits[t * E + e] = g;
+    }
+  }
+}
+
+inline unsigned blocks_of(int64_t n, int per) { return (unsigned)((n + per - 1) / per); }
+
+// The widest access that divides a row: 16 bytes, 4, or 2.
+inline int access_bytes(int row_bytes) { return row_bytes % 16 == 0 ? 16 : row_bytes % 4 == 0 ? 4 : 2; }
+
+constexpr int kSortCtas = 8;
+
+}  // namespace
+
+cudaError_t dispatch_set_limits() {
+  return cudaFuncSetAttribute(k_dispatch_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, cluster_sort_smem(kMaxBins));
+}
+
+cudaError_t launch_dispatch(const TrainDevice& d, const void* x, int row_bytes, int T, const int32_t* topk_idx, int top_k,
+                            int E, int32_t* offsets, int32_t* perm, int32_t* inv, void* xs, cudaStream_t s) {
+  const DispatchArgs a{topk_idx, T, top_k, E, T * top_k, offsets, perm, inv, d.status};
+  const int B = access_bytes(row_bytes), nv = row_bytes / B;
+  if (a.P <= kCountPairs) {
+    if (B == 16) k_dispatch_count<16><<<T + 1, kThreads, 0, s>>>(a, x, nv, xs);
+    else if (B == 4) k_dispatch_count<4><<<T + 1, kThreads, 0, s>>>(a, x, nv, xs);
+    else k_dispatch_count<2><<<T + 1, kThreads, 0, s>>>(a, x, nv, xs);
+    return cudaGetLastError();
+  }
+  cudaError_t e = launch_cluster_sort(k_dispatch_sort, kSortCtas, E, s, a);
+  if (e != cudaSuccess || !x) return e;
+  const int64_t total = (int64_t)T * nv;
+  const unsigned grid = blocks_of(total, kThreads);
+  if (B == 16) k_dispatch_copy<16><<<grid, kThreads, 0, s>>>(x, total, nv, top_k, inv, xs);
+  else if (B == 4) k_dispatch_copy<4><<<grid, kThreads, 0, s>>>(x, total, nv, top_k, inv, xs);
+  else k_dispatch_copy<2><<<grid, kThreads, 0, s>>>(x, total, nv, top_k, inv, xs);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine(const TrainDevice& d, const void* ys, int dtype, int T, int H, int top_k, const int32_t* inv,
+                           const float* w, void* out, cudaStream_t s) {
+  const int64_t P = (int64_t)T * top_k;
+  return with_dtype(dtype, [&](auto type) {
+    using V = decltype(type);
+    constexpr int N = 16 / sizeof(V);
+    const V* y = static_cast<const V*>(ys);
+    V* o = static_cast<V*>(out);
+    if (H % N == 0) {
+      const int64_t total = (int64_t)T * (H / N);
+      k_combine<V, N><<<blocks_of(total, kThreads), kThreads, 0, s>>>(y, total, H / N, top_k, P, inv, w, o, d.status);
+    } else {
+      const int64_t total = (int64_t)T * H;
+      k_combine<V, 1><<<blocks_of(total, kThreads), kThreads, 0, s>>>(y, total, H, top_k, P, inv, w, o, d.status);
+    }
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_combine_backward(const TrainDevice& d, const void* dout, const void* ys, int dtype, int T, int H,
+                                    int top_k, const int32_t* inv, const float* w, void* dys, float* dw,
+                                    cudaStream_t s) {
+  const int64_t P = (int64_t)T * top_k;
+  return with_dtype(dtype, [&](auto type) {
+    using V = decltype(type);
+    const V *g = static_cast<const V*>(dout), *y = static_cast<const V*>(ys);
+    V* o = static_cast<V*>(dys);
+    auto launch = [&](auto n, auto warps) {
+      constexpr int N = decltype(n)::value, W = decltype(warps)::value;
+      k_combine_backward<V, N, W><<<blocks_of(T, kThreads / 32 / W), kThreads, 0, s>>>(g, y, T, H / N, top_k, P, inv,
+                                                                                       w, o, dw, d.status);
+    };
+    auto pick = [&](auto n) {
+      // enough warps to fill the SMs: 1 per token from 16 warps an SM on, else 8
+      if ((int64_t)T >= (int64_t)d.num_sms * 16) launch(n, std::integral_constant<int, 1>());
+      else launch(n, std::integral_constant<int, 8>());
+    };
+    constexpr int N = 16 / sizeof(V);
+    if (H % N == 0) pick(std::integral_constant<int, N>());
+    else pick(std::integral_constant<int, 1>());
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_route_backward(const TrainDevice& d, const float* logits, const int32_t* topk_idx,
+                                  const float* topk_w, const float* dw, int T, int E, int top_k, int norm,
+                                  float* dlogits, cudaStream_t s) {
+  k_route_backward<<<blocks_of(T, kThreads / 32), kThreads, 0, s>>>(norm ? nullptr : logits, topk_idx, topk_w, dw, T, E,
+                                                                    top_k, dlogits, d.status);
+  return cudaGetLastError();
+}
+
+}  // namespace ftmoe

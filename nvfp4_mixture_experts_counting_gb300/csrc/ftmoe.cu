@@ -17,6 +17,15 @@ namespace ftmoe {
 cudaError_t route_set_smem_limits(int H, int E);
 cudaError_t experts_set_smem_limits(int H, int I);
 thread_local Profiler* g_prof = nullptr;
+
+static thread_local std::string g_last_cuda_error;
+
+int cuda_fail(cudaError_t e, const char* what) {
+  char buf[256];
+  snprintf(buf, sizeof buf, "%s: %s", what, cudaGetErrorString(e));
+  g_last_cuda_error = buf;
+  return FTMOE_ERR_CUDA;
+}
 }  // namespace ftmoe
 
 using namespace ftmoe;
@@ -65,15 +74,6 @@ struct ProfScope {
   explicit ProfScope(Profiler* p) : saved(g_prof) { g_prof = p; }
   ~ProfScope() { g_prof = saved; }
 };
-
-thread_local std::string g_last_cuda_error;
-
-int cuda_fail(cudaError_t e, const char* what) {
-  char buf[256];
-  snprintf(buf, sizeof buf, "%s: %s", what, cudaGetErrorString(e));
-  g_last_cuda_error = buf;
-  return FTMOE_ERR_CUDA;
-}
 
 #define CK(call)                                          \
   do {                                                    \

@@ -11,6 +11,9 @@ namespace ftmoe {
 constexpr uint32_t kStatusRange = 1u;    // an in-kernel range check failed
 constexpr uint32_t kStatusTimeout = 2u;  // a bounded wait ran out
 
+// Keeps a CUDA error's text for ftmoe_last_cuda_error; returns FTMOE_ERR_CUDA.
+int cuda_fail(cudaError_t e, const char* what);
+
 // Optional per-launch timing: when set for the calling thread, launchers
 // bracket each kernel with begin/end (CUDA events on the launch stream).
 struct Profiler {

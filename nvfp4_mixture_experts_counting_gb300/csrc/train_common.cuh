@@ -1,0 +1,71 @@
+// Device helpers of the training operators: rows of bf16, fp16 or fp32 values
+// read and written 16 bytes (or one value) at a time, with the arithmetic in fp32.
+#pragma once
+
+#include "common.cuh"
+#include "tma.cuh"
+#include "train.h"
+
+namespace ftmoe {
+
+inline int dtype_bytes(int dtype) { return dtype == FTMOE_FP32 ? 4 : 2; }
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// The unsigned type of an access of B bytes.
+template <int B> struct Raw;
+template <> struct Raw<2> { using type = uint16_t; };
+template <> struct Raw<4> { using type = uint32_t; };
+template <> struct Raw<8> { using type = uint2; };
+template <> struct Raw<16> { using type = uint4; };
+
+// N values of T moved in one access.
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Pack {
+  T v[N];
+  __device__ __forceinline__ float get(int i) const { return to_f32(v[i]); }
+  __device__ __forceinline__ void set(int i, float f) { v[i] = from_f32<T>(f); }
+};
+
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> load_pack(const T* p) {
+  using R = typename Raw<sizeof(T) * N>::type;
+  const R r = *reinterpret_cast<const R*>(p);
+  return *reinterpret_cast<const Pack<T, N>*>(&r);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_pack(T* p, const Pack<T, N>& v) {
+  using R = typename Raw<sizeof(T) * N>::type;
+  *reinterpret_cast<R*>(p) = *reinterpret_cast<const R*>(&v);
+}
+
+__device__ __forceinline__ float warp_sum_f32(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max_f32(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Calls f with a value of the type that a dtype code names.
+template <typename F>
+cudaError_t with_dtype(int dtype, F f) {
+  if (dtype == FTMOE_FP32) return f(float());
+  if (dtype == FTMOE_FP16) return f(__half());
+  return f(__nv_bfloat16());
+}
+
+}  // namespace ftmoe

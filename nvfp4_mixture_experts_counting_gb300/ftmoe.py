@@ -65,6 +65,26 @@ class KernelTime(C.Structure):
     _fields_ = [("name", C.c_char * 48), ("launches", C.c_int64), ("total_ms", C.c_double)]
 
 
+class PolicyArgs(C.Structure):
+    _fields_ = [("logits", C.c_void_p), ("dtype", C.c_int32), ("id_bytes", C.c_int32), ("N", C.c_int64),
+                ("V", C.c_int64), ("ld", C.c_int64), ("targets", C.c_void_p), ("old_logp", C.c_void_p),
+                ("ref_logp", C.c_void_p), ("advantage", C.c_void_p), ("weight", C.c_void_p),
+                ("temperature", C.c_float), ("clip_low", C.c_float), ("clip_high", C.c_float),
+                ("kl_coef", C.c_float), ("grad_scale", C.c_float), ("loss", C.c_void_p), ("row_loss", C.c_void_p),
+                ("logp", C.c_void_p), ("dlogits", C.c_void_p), ("ld_d", C.c_int64)]
+
+
+class AdamwTensor(C.Structure):
+    _fields_ = [("p", C.c_void_p), ("g", C.c_void_p), ("master", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p),
+                ("m_scale", C.c_void_p), ("v_scale", C.c_void_p), ("n", C.c_int64), ("weight_decay", C.c_float),
+                ("p_dtype", C.c_int32), ("g_dtype", C.c_int32), ("state_bits", C.c_int32)]
+
+
+class AdamwParams(C.Structure):
+    _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_double),
+                ("step", C.c_int64), ("grad_scale", C.c_void_p)]
+
+
 _lib = None
 
 #: every symbol the header declares, with its argument and result types
@@ -95,6 +115,22 @@ SIGNATURES = {
                                 C.c_void_p], C.c_int),
     "ftmoe_quantize_activations": ([C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p],
                                    C.c_int),
+    "ftmoe_dispatch": ([C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_void_p,
+                        C.c_void_p, C.c_void_p, C.c_void_p], C.c_int),
+    "ftmoe_combine": ([C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p,
+                       C.c_void_p], C.c_int),
+    "ftmoe_combine_backward": ([C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p,
+                                C.c_void_p, C.c_void_p, C.c_void_p], C.c_int),
+    "ftmoe_route_backward": ([C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int,
+                              C.c_void_p, C.c_void_p], C.c_int),
+    "ftmoe_embed": ([C.c_void_p, C.c_int, C.c_int64, C.c_int, C.c_void_p, C.c_int, C.c_int64, C.c_float, C.c_void_p,
+                     C.c_void_p], C.c_int),
+    "ftmoe_embed_workspace": ([C.c_int64, C.c_int], C.c_int64),
+    "ftmoe_embed_backward": ([C.c_void_p, C.c_int, C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int, C.c_float,
+                              C.c_int64, C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p], C.c_int),
+    "ftmoe_policy_loss": ([C.POINTER(PolicyArgs), C.c_void_p], C.c_int),
+    "ftmoe_adamw": ([C.POINTER(AdamwTensor), C.c_int, C.POINTER(AdamwParams), C.c_void_p], C.c_int),
+    "ftmoe_ops_status": ([C.c_void_p], C.c_int),
 }
 
 
@@ -256,6 +292,129 @@ def ftmoe_quantize_weights(w, rows: int, K: int, codes, scales, globals_, stream
 def ftmoe_quantize_activations(a, rows: int, K: int, codes, scales, stream=None):
     _check(lib().ftmoe_quantize_activations(_ptr(a), rows, K, _ptr(codes), _ptr(scales), _stream(stream)),
            "ftmoe_quantize_activations")
+
+
+# ----------------------------------------------------------------- training operators
+
+BF16, FP32, FP16 = 0, 1, 2
+_DTYPES = {"torch.bfloat16": BF16, "torch.float32": FP32, "torch.float16": FP16}
+
+
+def _dtype(t) -> int:
+    try:
+        return _DTYPES[str(t.dtype)]
+    except KeyError:
+        raise TypeError(f"bf16, fp32 or fp16 expected, got {t.dtype}") from None
+
+
+def _rows(*tensors):
+    """The C calls take contiguous arrays: a strided tensor is refused here."""
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("contiguous tensors expected")
+
+
+def ftmoe_dispatch(x, T: int, H: int, topk_idx, top_k: int, E: int, offsets, perm, inv, xs, stream=None):
+    """Rows of x sorted by expert into xs, and the sort's tables (x and xs None: the tables alone)."""
+    _rows(x, topk_idx, offsets, perm, inv, xs)
+    _check(lib().ftmoe_dispatch(_ptr(x), _dtype(x) if x is not None else BF16, T, H, _ptr(topk_idx), top_k, E,
+                                _ptr(offsets), _ptr(perm), _ptr(inv), _ptr(xs), _stream(stream)), "ftmoe_dispatch")
+
+
+def ftmoe_combine(ys, T: int, H: int, top_k: int, inv, w, out, stream=None):
+    """out[t] = sum_j w[t, j] ys[inv[t, j]]; w None: weights of one (the gradient of ftmoe_dispatch)."""
+    _rows(ys, inv, w, out)
+    _check(lib().ftmoe_combine(_ptr(ys), _dtype(ys), T, H, top_k, _ptr(inv), _ptr(w), _ptr(out), _stream(stream)),
+           "ftmoe_combine")
+
+
+def ftmoe_combine_backward(dout, ys, T: int, H: int, top_k: int, inv, w, dys, dw, stream=None):
+    _rows(dout, ys, inv, w, dys, dw)
+    _check(lib().ftmoe_combine_backward(_ptr(dout), _ptr(ys), _dtype(dout), T, H, top_k, _ptr(inv), _ptr(w),
+                                        _ptr(dys), _ptr(dw), _stream(stream)), "ftmoe_combine_backward")
+
+
+def ftmoe_route_backward(logits, topk_idx, topk_w, dw, T: int, E: int, top_k: int, norm_topk_prob: bool, dlogits,
+                         stream=None):
+    _rows(logits, topk_idx, topk_w, dw, dlogits)
+    _check(lib().ftmoe_route_backward(_ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(dw), T, E, top_k,
+                                      int(norm_topk_prob), _ptr(dlogits), _stream(stream)), "ftmoe_route_backward")
+
+
+def ftmoe_embed(table, V: int, H: int, ids, N: int, scale: float, out, stream=None):
+    _rows(table, ids, out)
+    _check(lib().ftmoe_embed(_ptr(table), _dtype(table), V, H, _ptr(ids), ids.element_size(), N, scale, _ptr(out),
+                             _stream(stream)), "ftmoe_embed")
+
+
+def ftmoe_embed_workspace(N: int, H: int) -> int:
+    """Bytes of workspace for ftmoe_embed_backward."""
+    n = lib().ftmoe_embed_workspace(N, H)
+    _check(min(n, 0), "ftmoe_embed_workspace")
+    return n
+
+
+def ftmoe_embed_backward(dout, ids, N: int, V: int, H: int, scale: float, padding_id: int, dtable, accumulate: bool,
+                         workspace, stream=None):
+    _rows(dout, ids, dtable, workspace)
+    _check(lib().ftmoe_embed_backward(_ptr(dout), _dtype(dout), _ptr(ids), ids.element_size(), N, V, H, scale,
+                                      padding_id, _ptr(dtable), _dtype(dtable), int(accumulate), _ptr(workspace),
+                                      workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                      _stream(stream)), "ftmoe_embed_backward")
+
+
+def policy_args(logits, targets, old_logp, ref_logp, advantage, weight, loss, row_loss, logp=None, dlogits=None,
+                temperature: float = 1.0, clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                grad_scale: float = 1.0) -> PolicyArgs:
+    """Arguments of ftmoe_policy_loss; logits and dlogits [N, V] may have any row stride (last dimension dense)."""
+    _rows(targets, old_logp, ref_logp, advantage, weight, loss, row_loss, logp)
+    N, V = logits.shape
+    for t in (logits, dlogits):
+        if t is not None and V > 1 and t.stride(1) != 1:
+            raise ValueError("logits and dlogits need a dense last dimension")
+    if dlogits is not None and (dlogits.dtype != logits.dtype or dlogits.shape != logits.shape):
+        raise TypeError("dlogits has the shape and type of logits")
+    # a single row's stride says nothing
+    return PolicyArgs(_ptr(logits), _dtype(logits), targets.element_size(), N, V, logits.stride(0) if N > 1 else V,
+                      _ptr(targets), _ptr(old_logp), _ptr(ref_logp), _ptr(advantage), _ptr(weight), temperature,
+                      clip_low, clip_high, kl_coef, grad_scale, _ptr(loss), _ptr(row_loss), _ptr(logp), _ptr(dlogits),
+                      0 if dlogits is None else dlogits.stride(0) if N > 1 else V)
+
+
+def ftmoe_policy_loss(args: PolicyArgs, stream=None):
+    _check(lib().ftmoe_policy_loss(C.byref(args), _stream(stream)), "ftmoe_policy_loss")
+
+
+class AdamwList:
+    """The tensors of ftmoe_adamw: made once, kept with references to them."""
+
+    def __init__(self, tensors):
+        self.tensors = tensors
+        self.array = (AdamwTensor * len(tensors))()
+        for a, t in zip(self.array, tensors):
+            get = t.get
+            _rows(t["p"], t["g"], get("master"), t["m"], t["v"], get("m_scale"), get("v_scale"))
+            a.p, a.g, a.master, a.m, a.v = (_ptr(v) for v in (t["p"], t["g"], get("master"), t["m"], t["v"]))
+            a.m_scale, a.v_scale = _ptr(get("m_scale")), _ptr(get("v_scale"))
+            a.n, a.weight_decay = t["p"].numel(), get("weight_decay", 0.0)
+            a.p_dtype, a.g_dtype = _dtype(t["p"]), _dtype(t["g"])
+            a.state_bits = 8 * t["m"].element_size()
+
+
+def adamw_list(tensors) -> AdamwList:
+    """A list of dicts: p, g, m, v, and where they apply master, m_scale, v_scale, weight_decay."""
+    return AdamwList(list(tensors))
+
+
+def ftmoe_adamw(tensors: AdamwList, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                step: int = 1, grad_scale=None, stream=None):
+    hp = AdamwParams(lr, beta1, beta2, eps, step, _ptr(grad_scale))
+    _check(lib().ftmoe_adamw(tensors.array, len(tensors.array), C.byref(hp), _stream(stream)), "ftmoe_adamw")
+
+
+def ftmoe_ops_status(stream=None) -> int:
+    """Status of the training operators' range checks since the last call (0 or DEVICE_CHECK)."""
+    return lib().ftmoe_ops_status(_stream(stream))
 
 
 # ----------------------------------------------------------------- convenience
