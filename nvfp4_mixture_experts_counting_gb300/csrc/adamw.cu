@@ -22,7 +22,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPer = 8;                  // values a thread updates
 constexpr int kTile = kThreads * kPer;   // a warp's 256 values are one 8-bit block
-constexpr int kMaxTensors = 400;         // in one launch: the descriptors travel as kernel parameters
+// Tensors of one launch: the descriptors travel as kernel parameters, and
+// 29 KB of them cost some 3 us of the launch, so short lists have a kernel of their own.
+constexpr int kFewTensors = 24, kMaxTensors = 400;
 constexpr float kTiny = 1e-30f;          // blocks below it are held as zeros
 
 struct Tensor {
@@ -36,13 +38,16 @@ struct Tensor {
   float decay;     // 1 - lr wd
 };
 
-struct Launch {
+struct Common {
   float b1, ob1, b2, ob2, root_scale, eps, lr;
   const float* grad_scale;
   int count;
-  Tensor t[kMaxTensors];
 };
-static_assert(sizeof(Launch) <= 32764, "kernel parameters");
+template <int CAP>
+struct Launch : Common {
+  Tensor t[CAP];
+};
+static_assert(sizeof(Launch<kMaxTensors>) <= 32764, "kernel parameters");
 
 // kPer consecutive values from `i` on; past n they are zeros.
 template <typename T>
@@ -135,8 +140,8 @@ __device__ __forceinline__ float store_codes(uint8_t* p, int64_t i, int64_t n, c
   return flat ? 0.f : __fmul_rn(top, 1.f / 448.f);
 }
 
-template <typename PT, typename GT, bool MASTER, bool EIGHT>
-__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Launch a) {
+template <typename PT, typename GT, bool MASTER, bool EIGHT, int CAP>
+__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Launch<CAP> a) {
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
   if (!isfinite(gs)) return;  // an overflowed step is skipped
   int lo = 0, hi = a.count - 1;  // the last tensor that starts at or before this tile
@@ -187,13 +192,21 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Laun
 }
 
 template <typename PT, typename GT, bool MASTER>
-void launch_kind(bool eight, uint32_t tiles, const Launch& l, cudaStream_t s) {
-  if (eight) k_adamw<PT, GT, MASTER, true><<<tiles, kThreads, 0, s>>>(l);
-  else k_adamw<PT, GT, MASTER, false><<<tiles, kThreads, 0, s>>>(l);
+void launch_kind(bool eight, uint32_t tiles, const Launch<kMaxTensors>& l, cudaStream_t s) {
+  if (l.count <= kFewTensors) {
+    Launch<kFewTensors> few;
+    static_cast<Common&>(few) = l;
+    for (int i = 0; i < l.count; ++i) few.t[i] = l.t[i];
+    if (eight) k_adamw<PT, GT, MASTER, true, kFewTensors><<<tiles, kThreads, 0, s>>>(few);
+    else k_adamw<PT, GT, MASTER, false, kFewTensors><<<tiles, kThreads, 0, s>>>(few);
+  } else {
+    if (eight) k_adamw<PT, GT, MASTER, true, kMaxTensors><<<tiles, kThreads, 0, s>>>(l);
+    else k_adamw<PT, GT, MASTER, false, kMaxTensors><<<tiles, kThreads, 0, s>>>(l);
+  }
 }
 
 template <typename PT>
-void launch_typed(const ftmoe_adamw_tensor& like, uint32_t tiles, const Launch& l, cudaStream_t s) {
+void launch_typed(const ftmoe_adamw_tensor& like, uint32_t tiles, const Launch<kMaxTensors>& l, cudaStream_t s) {
   const bool eight = like.state_bits == 8, wide = like.g_dtype == FTMOE_FP32, master = like.master != nullptr;
   if constexpr (std::is_same<PT, float>::value) {
     launch_kind<float, float, false>(eight, tiles, l, s);
@@ -214,7 +227,7 @@ inline int kind_of(const ftmoe_adamw_tensor& t) {
 }  // namespace
 
 cudaError_t launch_adamw(const ftmoe_adamw_tensor* list, int n, const ftmoe_adamw_params& hp, cudaStream_t s) {
-  Launch l;
+  Launch<kMaxTensors> l;
   l.b1 = (float)hp.beta1;
   l.ob1 = (float)(1.0 - hp.beta1);
   l.b2 = (float)hp.beta2;
@@ -223,7 +236,10 @@ cudaError_t launch_adamw(const ftmoe_adamw_tensor* list, int n, const ftmoe_adam
   l.eps = (float)hp.eps;
   l.lr = (float)(hp.lr / (1.0 - std::pow(hp.beta1, (double)hp.step)));
   l.grad_scale = hp.grad_scale;
+  uint64_t kinds = 0;
+  for (int i = 0; i < n; ++i) kinds |= list[i].n ? 1ull << kind_of(list[i]) : 0;
   for (int kind = 0; kind < 64; ++kind) {
+    if (!(kinds >> kind & 1)) continue;
     l.count = 0;
     uint32_t tiles = 0;
     const ftmoe_adamw_tensor* like = nullptr;

@@ -161,7 +161,7 @@ int ftmoe_embed_backward(const void* dout, int dtype, const void* ids, int id_by
 
 int ftmoe_policy_loss(const ftmoe_policy_args* a, ftmoe_stream_t stream) {
   if (!a || !known(a->dtype) || (a->id_bytes != 4 && a->id_bytes != 8)) return FTMOE_ERR_INVALID_ARG;
-  if (a->N < 0 || a->N > INT32_MAX || a->V < 1 || a->V > INT32_MAX || a->ld < a->V) return FTMOE_ERR_INVALID_ARG;
+  if (a->N < 0 || a->N > INT32_MAX || a->V < 1 || a->V > (1 << 30) || a->ld < a->V) return FTMOE_ERR_INVALID_ARG;
   if (!(a->temperature > 0.f) || !std::isfinite(a->temperature) || !(a->clip_low >= 0.f) || !(a->clip_high >= 0.f) ||
       !std::isfinite(a->kl_coef) || !std::isfinite(a->grad_scale))
     return FTMOE_ERR_INVALID_ARG;
@@ -215,6 +215,7 @@ int ftmoe_ops_status(ftmoe_stream_t stream) {
   if (e == cudaSuccess) e = cudaMemcpy(&st, d.status, 4, cudaMemcpyDeviceToHost);
   if (e == cudaSuccess) e = cudaMemset(d.status, 0, 4);
   if (e != cudaSuccess) return launched(e, "ftmoe_ops_status");
+  if (st & kStatusTimeout) return FTMOE_ERR_TIMEOUT;
   return st & kStatusRange ? FTMOE_ERR_DEVICE_CHECK : FTMOE_OK;
 }
 

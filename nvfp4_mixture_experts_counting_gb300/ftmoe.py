@@ -168,8 +168,9 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        # the handle alone: a Stream object costs some 3 us a call
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream
     return int(stream)

@@ -491,7 +491,8 @@ def policy_check(i, outs, dtype, temperature=1.0, clip_low=0.2, clip_high=0.2, k
 @pytest.mark.parametrize("N,V,dtype,ld,at", [
     (1, 1, FP32, None, 0), (3, 2, BF16, None, 0), (5, 7, FP16, None, 1), (40, 1000, BF16, None, 0),
     (17, 333, BF16, 340, 3), (9, 4097, FP32, None, 2), (2, 50001, BF16, None, 0), (6, 20011, FP16, 20012, 5),
-    (1, 131072, BF16, None, 0), (700, 65, FP32, None, 0), (2, 200003, FP32, None, 1)])
+    (1, 131072, BF16, None, 0), (700, 65, FP32, None, 0), (2, 200003, FP32, None, 1), (2, 500003, FP32, None, 1),
+    (2100, 2051, BF16, None, 1), (900, 8200, FP32, None, 0), (600, 16001, FP16, 16005, 2)])
 @pytest.mark.parametrize("masked", [0.0, 0.4])
 def test_policy_loss(N, V, dtype, ld, at, masked):
     i = policy_inputs(N + V, N, V, dtype, masked, ld, at)
