@@ -204,7 +204,7 @@ int ftmoe_adamw(const ftmoe_adamw_tensor* tensors, int n, const ftmoe_adamw_para
   if (!any) return FTMOE_OK;
   TrainDevice d;
   if (const int rc = current_device(&d)) return rc;
-  return launched(launch_adamw(tensors, n, *hp, (cudaStream_t)stream), "ftmoe_adamw");
+  return launched(launch_adamw(d, tensors, n, *hp, (cudaStream_t)stream), "ftmoe_adamw");
 }
 
 int ftmoe_ops_status(ftmoe_stream_t stream) {

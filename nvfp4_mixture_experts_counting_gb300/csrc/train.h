@@ -49,6 +49,6 @@ cudaError_t policy_set_limits();
 cudaError_t launch_policy_loss(const TrainDevice& d, const ftmoe_policy_args& a, cudaStream_t s);
 
 // AdamW (adamw.cu).
-cudaError_t launch_adamw(const ftmoe_adamw_tensor* list, int n, const ftmoe_adamw_params& hp, cudaStream_t s);
+cudaError_t launch_adamw(const TrainDevice& d, const ftmoe_adamw_tensor* list, int n, const ftmoe_adamw_params& hp, cudaStream_t s);
 
 }  // namespace ftmoe

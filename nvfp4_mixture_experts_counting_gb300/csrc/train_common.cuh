@@ -60,6 +60,59 @@ __device__ __forceinline__ float warp_max_f32(float v) {
   return v;
 }
 
+// Two fp32 values in one 64-bit register, and the packed arithmetic on them.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Values 2e and 2e + 1 of a piece as fp32, and back.
+template <int N>
+__device__ __forceinline__ uint64_t pair_of(const Pack<float, N>& x, int e) { return pack2(x.v[2 * e], x.v[2 * e + 1]); }
+template <int N>
+__device__ __forceinline__ uint64_t pair_of(const Pack<__nv_bfloat16, N>& x, int e) {
+  const uint32_t b = reinterpret_cast<const uint32_t*>(&x)[e];
+  return pack2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+}
+template <int N>
+__device__ __forceinline__ uint64_t pair_of(const Pack<__half, N>& x, int e) {
+  const float2 f = __half22float2(reinterpret_cast<const __half2*>(&x)[e]);
+  return pack2(f.x, f.y);
+}
+template <int N>
+__device__ __forceinline__ void set_pair(Pack<float, N>& o, int e, uint64_t v) { unpack2(v, o.v[2 * e], o.v[2 * e + 1]); }
+template <int N>
+__device__ __forceinline__ void set_pair(Pack<__nv_bfloat16, N>& o, int e, uint64_t v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  reinterpret_cast<__nv_bfloat162*>(&o)[e] = __floats2bfloat162_rn(lo, hi);
+}
+template <int N>
+__device__ __forceinline__ void set_pair(Pack<__half, N>& o, int e, uint64_t v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  reinterpret_cast<__half2*>(&o)[e] = __floats2half2_rn(lo, hi);
+}
+
 // Calls f with a value of the type that a dtype code names.
 template <typename F>
 cudaError_t with_dtype(int dtype, F f) {
