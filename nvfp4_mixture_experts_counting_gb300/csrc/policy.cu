@@ -29,7 +29,6 @@ constexpr int kMaxChunks = 16; // of a warp's part
 constexpr int kLag = 1;        // chunks between a gradient's departure and the reuse of its buffer
 constexpr int kLongThreads = 512;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -46,9 +45,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
 struct MaxSum {
   float m, s;
 };
-__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float k2) {
-  const float m = fmaxf(a.m, b.m);
-  return {m, a.s * exp2_fast((a.m - m) * k2) + b.s * exp2_fast((b.m - m) * k2)};
+// The joint maximum and sum of a warp's lanes: the maximum first, so that each
+// sum is scaled once (ex2.approx is 5e-8 low on average, and lanes joined pair by pair met it at each step).
+__device__ __forceinline__ MaxSum warp_join(MaxSum run, float k2) {
+  const float m = warp_max_f32(run.m);
+  return {m, warp_sum_f32(run.s * exp2_fast((run.m - m) * k2))};
 }
 
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t v) {
@@ -88,18 +89,6 @@ __device__ __forceinline__ Pack<T, N> zero_pack() {
 #pragma unroll
   for (int e = 0; e < N; ++e) r.set(e, 0.f);
   return r;
-}
-
-// Shared -> global bulk copy (16-byte aligned, a multiple of 16 bytes), and the
-// wait until the sources of all but the last PENDING groups may be overwritten.
-__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int PENDING>
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(PENDING) : "memory");
 }
 
 // One row's 16-byte pieces.  The row starts `skip` values after a 16-byte
@@ -203,16 +192,6 @@ __device__ __forceinline__ void gradient_of_pieces(Pack<T, Row<T>::N>* p, float 
     p[u * 32] = o;
   }
 }
-
-__device__ __forceinline__ MaxSum warp_join(MaxSum run, float k2) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    run = join(run, {__shfl_xor_sync(0xffffffffu, run.m, o), __shfl_xor_sync(0xffffffffu, run.s, o)}, k2);
-  return run;
-}
-
-// This thread's accesses to shared memory before, asynchronous copies' after.
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // 8 bytes to a peer CTA's shared memory, which complete on its barrier.
 __device__ __forceinline__ void send(MaxSum v, MaxSum* slot, uint64_t* bar, int to) {
@@ -392,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_policy(ftmoe_policy_args
       if (lane < ranks) send(run, &exchange[slot][rank * kWarps + warp], meet + slot, lane);
       ok = mbar_wait(meet + slot, turn, status) && ok;
       run = {-FLT_MAX, 0.f};
-      for (int q = lane; q < ranks * kWarps; q += 32) run = join(run, exchange[slot][q], k2);
+      static_assert(kMaxRanks * kWarps <= 32, "a lane a sender");
+      if (lane < ranks * kWarps) run = exchange[slot][lane];
       run = warp_join(run, k2);
       if (!ok) run.s = NAN;
     }
@@ -400,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_policy(ftmoe_policy_args
     m = run.m;
     const float ls = log2f(run.s);
     if (p.w != 0.f) {
-      const float logp = ((zy - m) * k2 - ls) * kLn2;
+      const float logp = (zy - m) / a.temperature - logf(run.s);
       const RowTerms t = row_terms(a, p.n, p.w, logp);
       c = t.c;
       if (speaks) {
@@ -471,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_policy(ftmoe_policy_args
     ok = __all_sync(0xffffffffu, ok);
     p = next;
   }
+  pdl_launch_dependents();
   if (lane == 0) bulk_wait_read<0>();
   if (!ok) {  // a wait ran out: the copies that may still be on their way
     for (int j = 0; j < chunks_of(p); ++j)
@@ -509,27 +490,19 @@ __global__ void __launch_bounds__(kLongThreads) k_policy_long(ftmoe_policy_args 
         for (int e = 0; e < N; ++e) s += exp2_fast((x.get(e) - top) * k2);
         run = {top, s};
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        run = join(run, {__shfl_xor_sync(0xffffffffu, run.m, o), __shfl_xor_sync(0xffffffffu, run.s, o)}, k2);
+      run = warp_join(run, k2);
       if (lane == 0) warp_part[warp] = run;
       __syncthreads();
       if (warp == 0) {
-        run = lane < kLongThreads / 32 ? warp_part[lane] : MaxSum{-FLT_MAX, 0.f};
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-          run = join(run, {__shfl_xor_sync(0xffffffffu, run.m, o), __shfl_xor_sync(0xffffffffu, run.s, o)}, k2);
+        run = warp_join(lane < kLongThreads / 32 ? warp_part[lane] : MaxSum{-FLT_MAX, 0.f}, k2);
         if (lane == 0) exchange[parity] = run;
       }
       cluster.sync();  // two slots suffice, as above
-      run = lane < ranks ? *cluster.map_shared_rank(&exchange[parity], lane) : MaxSum{-FLT_MAX, 0.f};
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        run = join(run, {__shfl_xor_sync(0xffffffffu, run.m, o), __shfl_xor_sync(0xffffffffu, run.s, o)}, k2);
+      run = warp_join(lane < ranks ? *cluster.map_shared_rank(&exchange[parity], lane) : MaxSum{-FLT_MAX, 0.f}, k2);
       parity ^= 1;
       m = run.m;
       ls = log2f(run.s);
-      const float logp = ((zy - m) * k2 - ls) * kLn2;
+      const float logp = (zy - m) / a.temperature - logf(run.s);
       const RowTerms t = row_terms(a, n, w, logp);
       c = t.c;
       if (rank == 0 && tid == 0) {
@@ -563,20 +536,22 @@ __global__ void __launch_bounds__(kLongThreads) k_policy_long(ftmoe_policy_args 
 }
 
 // loss = sum_n w_n row_n in a fixed order, by one CTA.
-__global__ void __launch_bounds__(1024) k_policy_sum(const float* weight, const float* row_loss, int64_t N, float* loss) {
-  __shared__ double part[32];
+constexpr int kSumThreads = 512;
+__global__ void __launch_bounds__(kSumThreads) k_policy_sum(const float* weight, const float* row_loss, int64_t N, float* loss) {
+  __shared__ double part[kSumThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
   double s = 0.0;
-  for (int64_t n = threadIdx.x; n < N; n += 1024) s += (double)(weight ? weight[n] : 1.f / (float)N) * row_loss[n];
+#pragma unroll 4
+  for (int64_t n = threadIdx.x; n < N; n += kSumThreads) s += (double)(weight ? weight[n] : 1.f / (float)N) * row_loss[n];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) part[warp] = s;
   __syncthreads();
-  if (warp == 0) {
-    s = part[lane];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) *loss = (float)s;
+  if (threadIdx.x == 0) {
+    s = 0.0;
+    for (int w = 0; w < kSumThreads / 32; ++w) s += part[w];
+    *loss = (float)s;
   }
 }
 
@@ -634,8 +609,7 @@ cudaError_t launch_policy_loss(const TrainDevice& d, const ftmoe_policy_args& a,
     });
     if (e != cudaSuccess) return e;
   }
-  k_policy_sum<<<1, 1024, 0, s>>>(a.weight, a.row_loss, a.N, a.loss);
-  return cudaGetLastError();
+  return launch_after(k_policy_sum, 1, kSumThreads, s, a.weight, a.row_loss, a.N, a.loss);
 }
 
 }  // namespace ftmoe

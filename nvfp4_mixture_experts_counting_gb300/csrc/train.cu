@@ -39,15 +39,16 @@ int current_device(TrainDevice* out) {
     }
     if (major != 10 || minor != 3) return FTMOE_ERR_DEVICE;
     void* p = nullptr;
+    int sort_ctas = kSortCtas;
     cudaError_t e = cudaGetSymbolAddress(&p, g_ops_status);
-    if (e == cudaSuccess) e = dispatch_set_limits();
-    if (e == cudaSuccess) e = embed_set_limits();
+    if (e == cudaSuccess) e = dispatch_set_limits(&sort_ctas);
+    if (e == cudaSuccess) e = embed_set_limits(&sort_ctas);
     if (e == cudaSuccess) e = policy_set_limits();
     if (e != cudaSuccess) {
       cudaGetLastError();
       return cuda_fail(e, "training operators' set-up");
     }
-    g_devices[dev] = {static_cast<uint32_t*>(p), sms};
+    g_devices[dev] = {static_cast<uint32_t*>(p), sms, sort_ctas};
   }
   *out = g_devices[dev];
   return FTMOE_OK;

@@ -13,12 +13,14 @@ namespace ftmoe {
 struct TrainDevice {
   uint32_t* status;  // device word that the operators' range checks mark
   int num_sms;
+  int sort_ctas;  // CTAs of the cluster that sorts
 };
 
 constexpr int kMaxBins = 1024;  // experts, or values of one radix digit
+constexpr int kSortCtas = 16;   // CTAs of the cluster that sorts, at most (8 is the portable limit)
 
 // Tokens sorted by expert and back (dispatch.cu).
-cudaError_t dispatch_set_limits();
+cudaError_t dispatch_set_limits(int* sort_ctas);
 cudaError_t launch_dispatch(const TrainDevice& d, const void* x, int row_bytes, int T, const int32_t* topk_idx, int top_k,
                             int E, int32_t* offsets, int32_t* perm, int32_t* inv, void* xs, cudaStream_t s);
 cudaError_t launch_combine(const TrainDevice& d, const void* ys, int dtype, int T, int H, int top_k, const int32_t* inv,
@@ -37,7 +39,7 @@ struct EmbedWorkspace {
   int64_t bytes;
 };
 EmbedWorkspace embed_workspace(int64_t N, int H);
-cudaError_t embed_set_limits();
+cudaError_t embed_set_limits(int* sort_ctas);
 cudaError_t launch_embed(const TrainDevice& d, const void* table, int dtype, int64_t V, int H, const void* ids,
                          int id_bytes, int64_t N, float scale, void* out, cudaStream_t s);
 cudaError_t launch_embed_backward(const TrainDevice& d, const void* dout, int dtype, const void* ids, int id_bytes,

@@ -31,7 +31,7 @@ template <> struct Raw<16> { using type = uint4; };
 
 // N values of T moved in one access.
 template <typename T, int N>
-struct alignas(sizeof(T) * N) Pack {
+struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
   T v[N];
   __device__ __forceinline__ float get(int i) const { return to_f32(v[i]); }
   __device__ __forceinline__ void set(int i, float f) { v[i] = from_f32<T>(f); }
@@ -39,14 +39,19 @@ struct alignas(sizeof(T) * N) Pack {
 
 template <typename T, int N>
 __device__ __forceinline__ Pack<T, N> load_pack(const T* p) {
-  using R = typename Raw<sizeof(T) * N>::type;
-  const R r = *reinterpret_cast<const R*>(p);
-  return *reinterpret_cast<const Pack<T, N>*>(&r);
+  constexpr int B = sizeof(T) * N < 16 ? sizeof(T) * N : 16;  // of one access; 32 bytes take two
+  using R = typename Raw<B>::type;
+  Pack<T, N> v;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(v) / B; ++i) reinterpret_cast<R*>(&v)[i] = reinterpret_cast<const R*>(p)[i];
+  return v;
 }
 template <typename T, int N>
 __device__ __forceinline__ void store_pack(T* p, const Pack<T, N>& v) {
-  using R = typename Raw<sizeof(T) * N>::type;
-  *reinterpret_cast<R*>(p) = *reinterpret_cast<const R*>(&v);
+  constexpr int B = sizeof(T) * N < 16 ? sizeof(T) * N : 16;
+  using R = typename Raw<B>::type;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(v) / B; ++i) reinterpret_cast<R*>(p)[i] = reinterpret_cast<const R*>(&v)[i];
 }
 
 __device__ __forceinline__ float warp_sum_f32(float v) {
@@ -111,6 +116,37 @@ __device__ __forceinline__ void set_pair(Pack<__half, N>& o, int e, uint64_t v) 
   float lo, hi;
   unpack2(v, lo, hi);
   reinterpret_cast<__half2*>(&o)[e] = __floats2half2_rn(lo, hi);
+}
+
+// Shared -> global bulk copy (16-byte aligned, a multiple of 16 bytes), and the
+// wait until the sources of all but the last PENDING groups may be overwritten.
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(PENDING) : "memory");
+}
+
+// This thread's accesses to shared memory before, asynchronous copies' after.
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Launches a kernel that calls pdl_wait before it uses what the stream's
+// previous kernel writes: it may start while that one ends.
+template <typename... A, typename... B>
+cudaError_t launch_after(void (*k)(A...), unsigned grid, int threads, cudaStream_t s, B... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, k, static_cast<A>(args)...);
 }
 
 // Calls f with a value of the type that a dtype code names.

@@ -298,12 +298,15 @@ def ftmoe_quantize_activations(a, rows: int, K: int, codes, scales, stream=None)
 # ----------------------------------------------------------------- training operators
 
 BF16, FP32, FP16 = 0, 1, 2
-_DTYPES = {"torch.bfloat16": BF16, "torch.float32": FP32, "torch.float16": FP16}
+_DTYPES = {}  # torch.dtype -> code, once torch is there
 
 
 def _dtype(t) -> int:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16})
     try:
-        return _DTYPES[str(t.dtype)]
+        return _DTYPES[t.dtype]
     except KeyError:
         raise TypeError(f"bf16, fp32 or fp16 expected, got {t.dtype}") from None
 
@@ -391,15 +394,15 @@ class AdamwList:
 
     def __init__(self, tensors):
         self.tensors = tensors
-        self.array = (AdamwTensor * len(tensors))()
-        for a, t in zip(self.array, tensors):
+        entries = []
+        for t in tensors:
             get = t.get
-            _rows(t["p"], t["g"], get("master"), t["m"], t["v"], get("m_scale"), get("v_scale"))
-            a.p, a.g, a.master, a.m, a.v = (_ptr(v) for v in (t["p"], t["g"], get("master"), t["m"], t["v"]))
-            a.m_scale, a.v_scale = _ptr(get("m_scale")), _ptr(get("v_scale"))
-            a.n, a.weight_decay = t["p"].numel(), get("weight_decay", 0.0)
-            a.p_dtype, a.g_dtype = _dtype(t["p"]), _dtype(t["g"])
-            a.state_bits = 8 * t["m"].element_size()
+            p, g, m = t["p"], t["g"], t["m"]
+            arrays = (p, g, get("master"), m, t["v"], get("m_scale"), get("v_scale"))
+            _rows(*arrays)
+            entries.append((*map(_ptr, arrays), p.numel(), get("weight_decay", 0.0), _dtype(p), _dtype(g),
+                            8 * m.element_size()))
+        self.array = (AdamwTensor * len(entries))(*entries)
 
 
 def adamw_list(tensors) -> AdamwList:
