@@ -5,6 +5,9 @@
 // Pair p = t * k + j has expert e_p; a pair whose index is outside [0, E) is
 // dropped.  offsets[e] = #{p : e_p < e}, and a kept pair's place is
 // inv[p] = offsets[e_p] + #{q < p : e_q = e_p}.
+#include <algorithm>
+#include <type_traits>
+
 #include "cluster_sort.cuh"
 
 namespace ftmoe {
@@ -15,7 +18,8 @@ constexpr int kThreads = 256;
 // Pairs up to which every CTA counts its own tokens' places (one launch): at
 // 2048 pairs that takes 4.5 us with the copy, the sort 4.4 us without it; at 4096 7.5 and 4.5 us.
 constexpr int kCountPairs = 2048;
-constexpr int kSlots = 8;  // slots a thread keeps in flight
+constexpr int kSlots = 4;  // slots of the combine that a thread has in flight
+constexpr int kBackSlots = 8;  // and of its gradient
 
 struct DispatchArgs {
   const int32_t* idx;
@@ -123,11 +127,6 @@ __global__ void __launch_bounds__(kThreads) k_dispatch_count(DispatchArgs a, con
   }
 }
 
-// i / n, in 32 bits where that holds it.
-__device__ __forceinline__ int64_t quotient(int64_t i, int n) {
-  return i >> 32 ? i / n : (int64_t)((uint32_t)i / (uint32_t)n);
-}
-
 // Many pairs: the sort, by one cluster.
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) k_dispatch_sort(DispatchArgs a) {
@@ -153,21 +152,28 @@ __global__ void __launch_bounds__(THREADS) k_dispatch_sort(DispatchArgs a) {
     a.perm[p] = -1;
 }
 
-// ... and the copy: each thread reads one piece of a token's row and writes it to the row's k places.
-template <int B>
-__global__ void __launch_bounds__(kThreads) k_dispatch_copy(const void* x, int64_t total, int nv, int k,
+// ... and the copy: each thread reads Q pieces of a token's row, nq apart, and
+// writes them to the row's k places.
+template <int B, int Q>
+__global__ void __launch_bounds__(kThreads) k_dispatch_copy(const void* x, int64_t total, int nv, int nq, int k,
                                                             const int32_t* inv, void* xs) {
   using V = typename Raw<B>::type;
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= total) return;
-  const int64_t t = quotient(i, nv);
-  const int v = (int)(i - t * nv);
-  const V row = static_cast<const V*>(x)[i];
+  const int64_t t = quotient(i, nq);
+  const int v = (int)(i - t * nq);
+  V row[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    if (v + q * nq < nv) row[q] = static_cast<const V*>(x)[t * nv + v + q * nq];
   V* dst = static_cast<V*>(xs) + v;
   pdl_wait();  // inv is the sort's
   for (int j = 0; j < k; ++j) {
     const int at = inv[t * k + j];
-    if (at >= 0) dst[(int64_t)at * nv] = row;
+    if (at < 0) continue;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (v + q * nq < nv) dst[(int64_t)at * nv + q * nq] = row[q];
   }
 }
 
@@ -180,97 +186,125 @@ __device__ __forceinline__ int checked_place(int at, int64_t P, uint32_t* status
   return at;
 }
 
-// out[t] = sum_j w[t, j] ys[inv[t, j]], slots in order, fp32.
-template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) k_combine(const T* ys, int64_t total, int nv, int k, int64_t P,
+// out[t] = sum_j w[t, j] ys[inv[t, j]], slots in order, fp32.  A thread takes Q
+// pieces of the row, nq apart, and kSlots slots at a time, whose loads are
+// issued together: a slot that is dropped or past the last one has its
+// neighbour's row loaded again and not used, as a load under a condition waits
+// for the condition (bf16 T=16384 k=8 took 386 us so, and 111 us would be the copy rate).
+template <typename T, int N, int Q>
+__global__ void __launch_bounds__(kThreads) k_combine(const T* ys, int64_t total, int nv, int nq, int k, int64_t P,
                                                       const int32_t* inv, const float* w, T* out, uint32_t* status) {
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= total) return;
-  const int64_t t = quotient(i, nv);
-  const int64_t v = i - t * nv;
-  float acc[N] = {};
+  const int64_t t = quotient(i, nq);
+  const int v = (int)(i - t * nq);
+  int at_column[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) at_column[q] = min(v + q * nq, nv - 1);
+  float acc[Q][N] = {};
   for (int j0 = 0; j0 < k; j0 += kSlots) {
-    Pack<T, N> y[kSlots];
-    int at[kSlots];
+    Pack<T, N> y[kSlots][Q];
+    int at[kSlots], some = 0;
 #pragma unroll
     for (int j = 0; j < kSlots; ++j) {
       at[j] = j0 + j < k ? checked_place(inv[t * k + j0 + j], P, status) : -1;
-      if (at[j] >= 0) y[j] = load_pack<T, N>(ys + ((int64_t)at[j] * nv + v) * N);
+      some = max(some, at[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      const T* row = ys + (int64_t)(at[j] < 0 ? some : at[j]) * nv * N;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) y[j][q] = load_pack<T, N>(row + (int64_t)at_column[q] * N);
     }
 #pragma unroll
     for (int j = 0; j < kSlots; ++j) {
       if (at[j] < 0) continue;
       const float wj = w ? w[t * k + j0 + j] : 1.f;
 #pragma unroll
-      for (int c = 0; c < N; ++c) acc[c] = fmaf(wj, y[j].get(c), acc[c]);
+      for (int q = 0; q < Q; ++q) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) acc[q][c] = fmaf(wj, y[j][q].get(c), acc[q][c]);
+      }
     }
   }
-  Pack<T, N> o;
 #pragma unroll
-  for (int c = 0; c < N; ++c) o.set(c, acc[c]);
-  store_pack<T, N>(out + (t * nv + v) * N, o);
+  for (int q = 0; q < Q; ++q) {
+    if (v + q * nq >= nv) break;
+    Pack<T, N> o;
+#pragma unroll
+    for (int c = 0; c < N; ++c) o.set(c, acc[q][c]);
+    store_pack<T, N>(out + (t * nv + v + q * nq) * N, o);
+  }
 }
 
 // dys[inv[p]] = w[p] dout[t], dw[p] = <dout[t], ys[inv[p]]>: W warps take a
-// token's row, kSlots slots at a time.  dys may be ys: a thread reads an
-// element before it writes it, and nobody else reads it.
-template <typename T, int N, int W>
-__global__ void __launch_bounds__(kThreads) k_combine_backward(const T* dout, const T* ys, int T_, int nv, int k,
+// token's row, kBackSlots slots at a time, whose loads are issued together (as
+// in k_combine).  dys may be ys: a thread reads an element before it writes it,
+// and no other thread touches it.
+template <typename T, int N, int Q, int W>
+__global__ void __launch_bounds__(kThreads, 3) k_combine_backward(const T* dout, const T* ys, int T_, int nv, int k,
                                                                int64_t P, const int32_t* inv, const float* w, T* dys,
                                                                float* dw, uint32_t* status) {
-  __shared__ float part[kThreads / 32][kSlots];
+  __shared__ float part[kThreads / 32][kBackSlots];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % W;
   const int64_t t = (int64_t)blockIdx.x * (kThreads / 32 / W) + warp / W;
   const bool on = t < T_;
   if (W == 1 && !on) return;
-  for (int j0 = 0; j0 < k; j0 += kSlots) {
-    int at[kSlots];
-    float wj[kSlots], dot[kSlots];
+  for (int j0 = 0; j0 < k; j0 += kBackSlots) {
+    int at[kBackSlots], some = 0;
+    float wj[kBackSlots], dot[kBackSlots];
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
+    for (int j = 0; j < kBackSlots; ++j) {
       const bool use = on && j0 + j < k;
       at[j] = use ? checked_place(inv[t * k + j0 + j], P, status) : -1;
       wj[j] = use ? w[t * k + j0 + j] : 0.f;
       dot[j] = 0.f;
+      some = max(some, at[j]);
     }
-    if (on) {
-      for (int v = sub * 32 + lane; v < nv; v += 32 * W) {
-        const Pack<T, N> d = load_pack<T, N>(dout + (t * nv + v) * N);
-        Pack<T, N> y[kSlots];
+    for (int v = sub * 32 * Q + lane; on && v < nv; v += 32 * Q * W) {
+      Pack<T, N> d[Q], y[kBackSlots][Q];
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j)
-          if (at[j] >= 0) y[j] = load_pack<T, N>(ys + ((int64_t)at[j] * nv + v) * N);
+      for (int q = 0; q < Q; ++q) d[q] = load_pack<T, N>(dout + (t * nv + min(v + q * 32, nv - 1)) * N);
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
-          if (at[j] < 0) continue;
+      for (int j = 0; j < kBackSlots; ++j) {
+        const T* row = ys + (int64_t)(at[j] < 0 ? some : at[j]) * nv * N;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) y[j][q] = load_pack<T, N>(row + (int64_t)min(v + q * 32, nv - 1) * N);
+      }
+#pragma unroll
+      for (int j = 0; j < kBackSlots; ++j) {
+        if (at[j] < 0) continue;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          if (v + q * 32 >= nv) break;
           Pack<T, N> o;
 #pragma unroll
           for (int c = 0; c < N; ++c) {
-            dot[j] = fmaf(d.get(c), y[j].get(c), dot[j]);
-            o.set(c, wj[j] * d.get(c));
+            dot[j] = fmaf(d[q].get(c), y[j][q].get(c), dot[j]);
+            o.set(c, wj[j] * d[q].get(c));
           }
-          store_pack<T, N>(dys + ((int64_t)at[j] * nv + v) * N, o);
+          store_pack<T, N>(dys + ((int64_t)at[j] * nv + v + q * 32) * N, o);
         }
       }
     }
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) dot[j] = warp_sum_f32(dot[j]);
+    for (int j = 0; j < kBackSlots; ++j) dot[j] = warp_sum_f32(dot[j]);
     if (W > 1) {
       if (lane == 0) {
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) part[warp][j] = dot[j];
+        for (int j = 0; j < kBackSlots; ++j) part[warp][j] = dot[j];
       }
       __syncthreads();
-      if (on && sub == 0 && lane < kSlots && j0 + lane < k) {
-        float s = 0.f;
+      if (on && sub == 0 && lane < kBackSlots && j0 + lane < k) {
+        float sum = 0.f;
 #pragma unroll
-        for (int q = 0; q < W; ++q) s += part[warp + q][lane];
-        dw[t * k + j0 + lane] = s;
+        for (int q = 0; q < W; ++q) sum += part[warp + q][lane];
+        dw[t * k + j0 + lane] = sum;
       }
       __syncthreads();
     } else {
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j)
+      for (int j = 0; j < kBackSlots; ++j)
         if (lane == j && j0 + j < k) dw[t * k + j0 + j] = dot[j];
     }
   }
@@ -361,9 +395,10 @@ cudaError_t launch_dispatch(const TrainDevice& d, const void* x, int row_bytes, 
   cudaError_t e = many ? launch_cluster_sort(d, k_dispatch_sort<1024>, 1024, a.P, E, s, a)
                        : launch_cluster_sort(d, k_dispatch_sort<512>, 512, a.P, E, s, a);
   if (e != cudaSuccess || !x) return e;
-  const int64_t total = (int64_t)T * nv;
-  return launch_after(B == 16 ? k_dispatch_copy<16> : B == 4 ? k_dispatch_copy<4> : k_dispatch_copy<2>,
-                      blocks_of(total, kThreads), kThreads, s, x, total, nv, top_k, inv, xs);
+  const int q = B == 16 ? 1 : 4, nq = (nv + q - 1) / q;
+  const int64_t total = (int64_t)T * nq;
+  return launch_after(B == 16 ? k_dispatch_copy<16, 1> : B == 4 ? k_dispatch_copy<4, 4> : k_dispatch_copy<2, 4>,
+                      blocks_of(total, kThreads), kThreads, s, x, total, nv, nq, top_k, inv, xs);
 }
 
 cudaError_t launch_combine(const TrainDevice& d, const void* ys, int dtype, int T, int H, int top_k, const int32_t* inv,
@@ -371,16 +406,17 @@ cudaError_t launch_combine(const TrainDevice& d, const void* ys, int dtype, int 
   const int64_t P = (int64_t)T * top_k;
   return with_dtype(dtype, [&](auto type) {
     using V = decltype(type);
-    constexpr int N = 16 / sizeof(V);
     const V* y = static_cast<const V*>(ys);
     V* o = static_cast<V*>(out);
-    if (H % N == 0) {
-      const int64_t total = (int64_t)T * (H / N);
-      k_combine<V, N><<<blocks_of(total, kThreads), kThreads, 0, s>>>(y, total, H / N, top_k, P, inv, w, o, d.status);
-    } else {
-      const int64_t total = (int64_t)T * H;
-      k_combine<V, 1><<<blocks_of(total, kThreads), kThreads, 0, s>>>(y, total, H, top_k, P, inv, w, o, d.status);
-    }
+    auto launch = [&](auto n, auto columns) {
+      constexpr int N = decltype(n)::value, Q = decltype(columns)::value;
+      const int nv = H / N, nq = (nv + Q - 1) / Q;
+      const int64_t total = (int64_t)T * nq;
+      k_combine<V, N, Q><<<blocks_of(total, kThreads), kThreads, 0, s>>>(y, total, nv, nq, top_k, P, inv, w, o, d.status);
+    };
+    constexpr int N = 16 / sizeof(V);
+    if (H % N == 0) launch(std::integral_constant<int, N>(), std::integral_constant<int, 1>());
+    else launch(std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
     return cudaGetLastError();
   });
 }
@@ -393,19 +429,28 @@ cudaError_t launch_combine_backward(const TrainDevice& d, const void* dout, cons
     using V = decltype(type);
     const V *g = static_cast<const V*>(dout), *y = static_cast<const V*>(ys);
     V* o = static_cast<V*>(dys);
-    auto launch = [&](auto n, auto warps) {
-      constexpr int N = decltype(n)::value, W = decltype(warps)::value;
-      k_combine_backward<V, N, W><<<blocks_of(T, kThreads / 32 / W), kThreads, 0, s>>>(g, y, T, H / N, top_k, P, inv,
-                                                                                       w, o, dw, d.status);
+    auto launch = [&](auto n, auto columns, auto warps) {
+      constexpr int N = decltype(n)::value, Q = decltype(columns)::value, W = decltype(warps)::value;
+      k_combine_backward<V, N, Q, W><<<blocks_of(T, kThreads / 32 / W), kThreads, 0, s>>>(g, y, T, H / N, top_k, P, inv,
+                                                                                          w, o, dw, d.status);
     };
-    auto pick = [&](auto n) {
-      // enough warps to fill the SMs: 1 per token from 16 warps an SM on, else 8
-      if ((int64_t)T >= (int64_t)d.num_sms * 16) launch(n, std::integral_constant<int, 1>());
-      else launch(n, std::integral_constant<int, 8>());
+    auto pick = [&](auto n, auto columns) {
+      // Warps a token, so that few tokens fill the SMs: bf16 H=2560 k=8 with 1, 2, 4 or 8 takes 17.0, 10.3, 8.0,
+      // 7.1 us at T=300, 24.9, 16.6, 14.0, 15.8 us at T=512, 27.2, 21.0, 23.3, 26.2 us at T=1000 and 31.6, 33.1,
+      // 32.3, 34.4 us at T=1500.  Rows moved value by value keep two (172 against 142 us at T=16384 H=1001), and no
+      // warp is without a piece of the row.
+      const int sms = d.num_sms, pieces = H / decltype(n)::value / decltype(columns)::value;
+      int W = T >= 8 * sms ? 1 : T >= 4 * sms ? 2 : T >= 5 * sms / 2 ? 4 : 8;
+      if (decltype(n)::value == 1) W = std::max(W, 2);
+      while (W > 1 && 32 * (W - 1) >= pieces) W /= 2;
+      if (W == 1) launch(n, columns, std::integral_constant<int, 1>());
+      else if (W == 2) launch(n, columns, std::integral_constant<int, 2>());
+      else if (W == 4) launch(n, columns, std::integral_constant<int, 4>());
+      else launch(n, columns, std::integral_constant<int, 8>());
     };
     constexpr int N = 16 / sizeof(V);
-    if (H % N == 0) pick(std::integral_constant<int, N>());
-    else pick(std::integral_constant<int, 1>());
+    if (H % N == 0) pick(std::integral_constant<int, N>(), std::integral_constant<int, 1>());
+    else pick(std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
     return cudaGetLastError();
   });
 }

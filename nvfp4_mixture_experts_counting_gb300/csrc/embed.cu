@@ -27,24 +27,29 @@ constexpr int kLongRun = 16;   // chunks from which a run's sum is shared by a C
 inline int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 inline unsigned blocks_of(int64_t n, int per) { return (unsigned)((n + per - 1) / per); }
 
-template <typename T, int N, typename Id>
-__global__ void __launch_bounds__(kThreads) k_embed(const T* table, int64_t V, int nv, const Id* ids, int64_t total,
+// A thread takes Q pieces of a token's row, nq apart.
+template <typename T, int N, int Q, typename Id>
+__global__ void __launch_bounds__(kThreads) k_embed(const T* table, int64_t V, int nv, int nq, const Id* ids, int64_t total,
                                                     float scale, T* out, uint32_t* status) {
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= total) return;
-  const int64_t n = i / nv, v = i - n * nv;
+  const int64_t n = quotient(i, nq);
+  const int v = (int)(i - n * nq);
   const int64_t id = ids[n];
-  Pack<T, N> o;
-  if (id >= 0 && id < V) {
-    const Pack<T, N> r = load_pack<T, N>(table + (id * nv + v) * N);
+  const bool in = id >= 0 && id < V;
+  if (!in && v == 0) set_status(status, kStatusRange);
+  const T* row = table + (in ? id : 0) * nv * N;
+  Pack<T, N> r[Q];
 #pragma unroll
-    for (int c = 0; c < N; ++c) o.set(c, scale * r.get(c));
-  } else {
-    if (v == 0) set_status(status, kStatusRange);
+  for (int q = 0; q < Q; ++q) r[q] = load_pack<T, N>(row + (int64_t)min(v + q * nq, nv - 1) * N);
 #pragma unroll
-    for (int c = 0; c < N; ++c) o.set(c, 0.f);
+  for (int q = 0; q < Q; ++q) {
+    if (v + q * nq >= nv) break;
+    Pack<T, N> o;
+#pragma unroll
+    for (int c = 0; c < N; ++c) o.set(c, in ? scale * r[q].get(c) : 0.f);
+    store_pack<T, N>(out + (n * nv + v + q * nq) * N, o);
   }
-  store_pack<T, N>(out + i * N, o);
 }
 
 // keys[final] sorted, pos[final] the tokens in that order.  A token whose id
@@ -336,20 +341,22 @@ cudaError_t launch_embed(const TrainDevice& d, const void* table, int dtype, int
                          int id_bytes, int64_t N, float scale, void* out, cudaStream_t s) {
   return with_dtype(dtype, [&](auto type) {
     using E = decltype(type);
-    auto launch = [&](auto n, auto id) {
-      constexpr int W = decltype(n)::value;
+    auto launch = [&](auto n, auto columns, auto id) {
+      constexpr int W = decltype(n)::value, Q = decltype(columns)::value;
       using Id = decltype(id);
-      const int64_t total = N * (H / W);
-      k_embed<E, W, Id><<<blocks_of(total, kThreads), kThreads, 0, s>>>(
-          static_cast<const E*>(table), V, H / W, static_cast<const Id*>(ids), total, scale, static_cast<E*>(out), d.status);
+      const int nv = H / W, nq = (nv + Q - 1) / Q;
+      const int64_t total = N * nq;
+      k_embed<E, W, Q, Id><<<blocks_of(total, kThreads), kThreads, 0, s>>>(static_cast<const E*>(table), V, nv, nq,
+                                                                           static_cast<const Id*>(ids), total, scale,
+                                                                           static_cast<E*>(out), d.status);
     };
-    auto pick = [&](auto n) {
-      if (id_bytes == 8) launch(n, int64_t());
-      else launch(n, int32_t());
+    auto pick = [&](auto n, auto columns) {
+      if (id_bytes == 8) launch(n, columns, int64_t());
+      else launch(n, columns, int32_t());
     };
     constexpr int W = 16 / sizeof(E);
-    if (H % W == 0) pick(std::integral_constant<int, W>());
-    else pick(std::integral_constant<int, 1>());
+    if (H % W == 0) pick(std::integral_constant<int, W>(), std::integral_constant<int, 2>());
+    else pick(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
     return cudaGetLastError();
   });
 }

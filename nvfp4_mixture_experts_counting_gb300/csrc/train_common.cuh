@@ -54,6 +54,11 @@ __device__ __forceinline__ void store_pack(T* p, const Pack<T, N>& v) {
   for (int i = 0; i < (int)sizeof(v) / B; ++i) reinterpret_cast<R*>(p)[i] = reinterpret_cast<const R*>(&v)[i];
 }
 
+// i / n, in 32 bits where that holds it.
+__device__ __forceinline__ int64_t quotient(int64_t i, int n) {
+  return i >> 32 ? i / n : (int64_t)((uint32_t)i / (uint32_t)n);
+}
+
 __device__ __forceinline__ float warp_sum_f32(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
