@@ -26,9 +26,11 @@ constexpr int kMaxRanks = 8;   // CTAs of a cluster
 constexpr int kUnroll = 4;     // 16-byte pieces a lane sums at a time
 constexpr int kChunk = 256;    // 16-byte pieces of one bulk copy
 constexpr int kMaxChunks = 16; // of a warp's part
+constexpr int kShortChunks = 8;  // of a short row
 constexpr int kLag = 1;        // chunks between a gradient's departure and the reuse of its buffer
 constexpr int kLongThreads = 512;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -46,10 +48,11 @@ struct MaxSum {
   float m, s;
 };
 // The joint maximum and sum of a warp's lanes: the maximum first, so that each
-// sum is scaled once (ex2.approx is 5e-8 low on average, and lanes joined pair by pair met it at each step).
+// sum is scaled once, and by expf: ex2.approx is 5e-8 low on average, which a
+// row's every term would meet at each join.
 __device__ __forceinline__ MaxSum warp_join(MaxSum run, float k2) {
   const float m = warp_max_f32(run.m);
-  return {m, warp_sum_f32(run.s * exp2_fast((run.m - m) * k2))};
+  return {m, warp_sum_f32(run.s * expf((run.m - m) * (k2 * kLn2)))};
 }
 
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t v) {
@@ -131,26 +134,85 @@ struct Row {
   }
 };
 
-// What a row's loss takes besides its logits, and what it gives.
-struct RowTerms {
-  float row, c;  // the row's loss; its gradient's coefficient, grad_scale w c / temperature
+// What a row's loss takes besides its logits.
+struct RowInputs {
+  int64_t n, y;
+  float w, old, ref, adv;
 };
-__device__ __forceinline__ RowTerms row_terms(const ftmoe_policy_args& a, int64_t n, float w, float logp) {
-  const float r = expf(logp - a.old_logp[n]), A = a.advantage[n];
-  const float bounded = r < 1.f - a.clip_low ? 1.f - a.clip_low : r > 1.f + a.clip_high ? 1.f + a.clip_high : r;
-  const bool clipped = r * A > bounded * A;  // false for NaN, which then reaches the loss and the gradient
-  float row = -(clipped ? bounded * A : r * A);
-  float c = clipped ? 0.f : -(A * r);
-  if (a.ref_logp && a.kl_coef != 0.f) {
-    const float d = a.ref_logp[n] - logp, ed = expf(d);
-    row += a.kl_coef * (ed - d - 1.f);
-    c += a.kl_coef * (1.f - ed);
-  }
-  return {row, c * (a.grad_scale * w / a.temperature)};
+__device__ __forceinline__ RowInputs row_inputs(const ftmoe_policy_args& a, int64_t n) {
+  return {n, a.id_bytes == 8 ? static_cast<const int64_t*>(a.targets)[n] : static_cast<const int32_t*>(a.targets)[n],
+          a.weight ? a.weight[n] : 1.f / (float)a.N, a.old_logp[n], a.ref_logp ? a.ref_logp[n] : 0.f, a.advantage[n]};
+}
+// A row whose target is out of range is marked (by one thread) and counts nothing.
+__device__ __forceinline__ void check_target(const ftmoe_policy_args& a, RowInputs& r, bool speaks, uint32_t* status) {
+  if (r.y >= 0 && r.y < a.V) return;
+  if (speaks) set_status(status, kStatusRange);
+  r.w = 0.f;
 }
 
-__device__ __forceinline__ int64_t target_of(const ftmoe_policy_args& a, int64_t n) {
-  return a.id_bytes == 8 ? static_cast<const int64_t*>(a.targets)[n] : static_cast<const int32_t*>(a.targets)[n];
+// A log probability as the sum of two fp32 values: rows' losses are of either
+// sign and largely cancel in their sum, so the rounding of a value near 10
+// (5e-7) is kept out of the ratio and the KL term.
+struct LogProb {
+  float hi, lo;
+  __device__ __forceinline__ float value() const { return hi + lo; }
+  // this - v, for a v near it
+  __device__ __forceinline__ float minus(float v) const { return (hi - v) + lo; }
+};
+// a + b as its rounded value and the rounding (0 where that says nothing).
+__device__ __forceinline__ LogProb exact_sum(float a, float b) {
+  const float t = __fadd_rn(a, b), u = __fsub_rn(t, a);
+  const float e = __fadd_rn(__fsub_rn(a, __fsub_rn(t, u)), __fsub_rn(b, u));
+  return {t, isfinite(t) ? e : 0.f};
+}
+// (zy - m) / T - ln s.  One Newton step, ln s = y + (s e^-y - 1), brings the logarithm's error to that of expf.
+__device__ __forceinline__ LogProb log_prob(float zy, float m, float s, float temperature) {
+  const LogProb d = exact_sum(zy, -m);
+  const float q = d.hi / temperature;
+  const float rest = isfinite(q) ? (fmaf(-q, temperature, d.hi) + d.lo) / temperature : 0.f;
+  const float y = logf(s), dy = fmaf(s, expf(-y), -1.f);
+  LogProb r = exact_sum(q, -y);
+  r.lo += rest - dy;
+  return r;
+}
+
+// The clipped ratio's side, and whether the clip holds: false for NaN, which
+// then reaches the loss and the gradient.
+struct Ratio {
+  float r, bounded;
+  bool clipped;
+};
+__device__ __forceinline__ Ratio ratio_of(const ftmoe_policy_args& a, float x, float A) {
+  const float r = expf(x);
+  const float b = r < 1.f - a.clip_low ? 1.f - a.clip_low : r > 1.f + a.clip_high ? 1.f + a.clip_high : r;
+  return {r, b, r * A > b * A};
+}
+// The gradient's coefficient grad_scale w c / temperature.
+__device__ __forceinline__ float gradient_scale(const ftmoe_policy_args& a, const RowInputs& in, float logp) {
+  const Ratio t = ratio_of(a, logp - in.old, in.adv);
+  float c = t.clipped ? 0.f : -(in.adv * t.r);
+  if (a.ref_logp && a.kl_coef != 0.f) c += a.kl_coef * (1.f - expf(in.ref - logp));
+  return c * (a.grad_scale * in.w / a.temperature);
+}
+// The row's loss, by one thread.
+__device__ __forceinline__ void write_row(const ftmoe_policy_args& a, const RowInputs& in, LogProb logp) {
+  const Ratio t = ratio_of(a, logp.minus(in.old), in.adv);
+  float row = -((t.clipped ? t.bounded : t.r) * in.adv);
+  if (a.ref_logp && a.kl_coef != 0.f) {
+    const float d = -logp.minus(in.ref);
+    row += a.kl_coef * (expf(d) - d - 1.f);
+  }
+  a.row_loss[in.n] = row;
+  if (a.logp) a.logp[in.n] = logp.value();
+}
+__device__ __forceinline__ void write_uncounted(const ftmoe_policy_args& a, int64_t n) {
+  a.row_loss[n] = 0.f;
+  if (a.logp) a.logp[n] = 0.f;
+}
+// What every warp takes from a counted row's maximum and sum, and one thread writes.
+__device__ __forceinline__ float finish_row(const ftmoe_policy_args& a, const RowInputs& in, MaxSum run, float zy, bool speaks) {
+  if (speaks) write_row(a, in, log_prob(zy, run.m, run.s, a.temperature));
+  return a.dlogits ? gradient_scale(a, in, (zy - run.m) / a.temperature - logf(run.s)) : 0.f;
 }
 
 // U pieces, 32 apart, join a lane's running maximum and sum.
@@ -224,17 +286,153 @@ __device__ __forceinline__ bool row_given(const void* response, uint32_t& cta) {
   return given != 0;
 }
 
-// One group of warps takes a row: the warps of a cluster of CTAs, or (SOLO,
-// short rows) a single warp.  Each warp copies its part of the row into its
-// own shared memory, sums it, and after the group has exchanged its maxima and
-// sums, turns it into the gradient in place and sends that off: a row is read
-// once and written once, no register holds a load in flight, and the group
-// meets once a row.  The copies go in chunks: a chunk is summed while later ones are
-// on their way, and as soon as its gradient has left its buffer the next row's
-// chunk is asked for.  Clusters take further rows from those not launched yet,
-// so rows of weight 0, which cost half or nothing, leave no SM idle.
-template <typename T, bool SOLO>
-__global__ void __launch_bounds__(kThreads, kMinCtas) k_policy(ftmoe_policy_args a, int part_pieces, uint32_t* status) {
+// A warp's pieces of a row: [lo, hi), and the whole ones [wlo, whi).
+template <typename T>
+struct Part {
+  Row<T> z;
+  RowInputs in;
+  int lo, hi, wlo, whi;
+
+  __device__ __forceinline__ int count() const { return hi - lo; }
+  __device__ __forceinline__ int chunks() const { return (hi - lo + kChunk - 1) / kChunk; }
+  // Chunk j as whole pieces [chunk_lo, chunk_hi); empty if they do not ascend.
+  __device__ __forceinline__ int chunk_lo(int j) const { return max(wlo, lo + j * kChunk); }
+  __device__ __forceinline__ int chunk_hi(int j) const { return min(whi, lo + (j + 1) * kChunk); }
+};
+
+// One warp's work on its part of a row, in its own shared memory.
+template <typename T>
+struct Worker {
+  static constexpr int N = Row<T>::N;
+  const ftmoe_policy_args& a;
+  const int lane;
+  uint32_t* const status;
+  const float k2;
+  Pack<T, N>* buf;      // the part
+  uint64_t* bar;        // a barrier for each chunk
+  uint32_t phases = 0;  // of the barriers
+  bool ok = true;       // no wait has run out
+
+  __device__ Worker(const ftmoe_policy_args& args, int lane_, uint32_t* status_, Pack<T, N>* buf_, uint64_t* bar_)
+      : a(args), lane(lane_), status(status_), k2(kLog2e / args.temperature), buf(buf_), bar(bar_) {}
+  __device__ __forceinline__ T* vals() const { return reinterpret_cast<T*>(buf); }
+
+  // The part of row n that is number `index` of 2^log2_parts * per_cta parts (CTA by CTA).
+  __device__ __forceinline__ Part<T> part_of(int64_t n, int log2_ctas, int cta, int per_cta, int index) const {
+    Part<T> p{Row<T>(static_cast<const T*>(a.logits) + n * a.ld, (int)a.V), row_inputs(a, n), 0, 0, 0, 0};
+    const int pieces = p.z.pieces(), per = (pieces + (1 << log2_ctas) - 1) >> log2_ctas;
+    const int each = (per + per_cta - 1) / per_cta, end = min(pieces, (cta + 1) * per);
+    p.lo = min(end, cta * per + index * each);
+    p.hi = min(end, p.lo + each);
+    p.wlo = max(p.lo, (p.z.skip + N - 1) / N);
+    p.whi = max(p.wlo, min(p.hi, p.z.end / N));
+    return p;
+  }
+  // f(e) for the values e of the pieces that are not whole, among the part's pieces [begin, end).
+  template <typename F>
+  __device__ __forceinline__ void edges(const Part<T>& p, int begin, int end, F f) const {
+    if (lane >= N) return;
+    for (int i = p.lo + begin; i < min(p.wlo, p.lo + end); ++i) f(i * N + lane);
+    for (int i = max(p.whi, p.lo + begin); i < p.lo + end; ++i) f(i * N + lane);
+  }
+  // Asks for a chunk's whole pieces (one lane).
+  __device__ __forceinline__ void fetch(const Part<T>& p, int j) const {
+    const int from = p.chunk_lo(j), to = p.chunk_hi(j);
+    if (p.in.w == 0.f || from >= to) return;
+    mbar_arrive_expect_tx(bar + j, (uint32_t)(to - from) * 16);
+    bulk_g2s(buf + (from - p.lo), p.z.at + (int64_t)from * N, (uint32_t)(to - from) * 16, bar + j);
+  }
+  // The part's maximum and sum, this lane's; `summed(j)` after each chunk.
+  template <typename F>
+  __device__ __forceinline__ MaxSum sum(const Part<T>& p, F summed) {
+    MaxSum r{-FLT_MAX, 0.f};
+    if (p.wlo > p.lo || p.whi < p.hi) {
+      edges(p, 0, p.count(), [&](int e) {
+        vals()[e - p.lo * N] = e >= p.z.skip && e < p.z.end ? p.z.at[e] : from_f32<T>(-INFINITY);
+      });
+      fence_async_smem();
+      __syncwarp();
+    }
+    for (int j = 0; j < p.chunks(); ++j) {
+      if (p.chunk_lo(j) < p.chunk_hi(j)) {
+        ok = ok && mbar_wait(bar + j, phases >> j & 1, status);
+        phases ^= 1u << j;
+      }
+      const int end = min(p.count(), (j + 1) * kChunk);
+      int i = j * kChunk + lane;
+      for (; i + 32 * (kUnroll - 1) < end; i += 32 * kUnroll) add_pieces<T, kUnroll>(buf + i, k2, r.m, r.s);
+      for (; i < end; i += 32) add_pieces<T, 1>(buf + i, k2, r.m, r.s);
+      summed(j);
+    }
+    if (!ok) r.s = NAN;
+    return r;
+  }
+  // The part's gradient c (onehot - softmax), softmax z = 2^((x - m) k2 - ls),
+  // in place and from there to dlogits; `left(j)` (one lane) once the copies up to chunk j are under way.
+  template <typename F>
+  __device__ __forceinline__ void gradient(const Part<T>& p, float m, float ls, float c, float zy, F left) const {
+    const Row<T> g(static_cast<T*>(a.dlogits) + p.in.n * a.ld_d, (int)a.V);
+    const bool same = g.skip == p.z.skip;
+    T* out = g.at + (g.skip - p.z.skip);  // out[e] belongs to the logit z.at[e]
+    const int e0 = max(p.z.skip, p.lo * N), e1 = (int)min((int64_t)p.z.end, (int64_t)p.hi * N);
+    auto mine = [&](int e) { return e >= p.z.skip && e < p.z.end; };
+    if (c == 0.f) {  // nothing of the row's softmax is needed
+      if (same) {
+        for (int i = p.wlo + lane; i < p.whi; i += 32) store_pack<T, N>(out + (int64_t)i * N, zero_pack<T, N>());
+        edges(p, 0, p.count(), [&](int e) {
+          if (mine(e)) out[e] = from_f32<T>(0.f);
+        });
+      } else {
+        for (int e = e0 + lane; e < e1; e += 32) out[e] = from_f32<T>(0.f);
+      }
+      return;
+    }
+    const int target = p.z.skip + (int)p.in.y - p.lo * N;  // among the part's values
+    const float of_target = c * (1.f - exp2_fast((zy - m) * k2 - ls));
+    for (int j = 0; j < p.chunks(); ++j) {
+      const int begin = j * kChunk, end = min(p.count(), begin + kChunk);
+      int i = begin + lane;
+      for (; i + 32 * (kUnroll - 1) < end; i += 32 * kUnroll) gradient_of_pieces<T, kUnroll>(buf + i, k2, m, ls, c);
+      for (; i < end; i += 32) gradient_of_pieces<T, 1>(buf + i, k2, m, ls, c);
+      // the target's own term, by the lane that wrote its piece
+      if (target >= begin * N && target < end * N && target / N % 32 == lane) vals()[target] = from_f32<T>(of_target);
+      fence_async_smem();
+      __syncwarp();
+      if (!same) continue;
+      edges(p, begin, end, [&](int e) {
+        if (mine(e)) out[e] = vals()[e - p.lo * N];
+      });
+      if (lane == 0) {
+        const int from = p.chunk_lo(j), to = p.chunk_hi(j);
+        if (from < to) bulk_s2g(out + (int64_t)from * N, buf + (from - p.lo), (uint32_t)(to - from) * 16);
+        bulk_commit();  // one group a chunk, empty or not
+        left(j);
+      }
+    }
+    if (!same) {  // dlogits' rows are of another alignment: value by value
+      for (int e = e0 + lane; e < e1; e += 32) out[e] = vals()[e - p.lo * N];
+    }
+  }
+  // A wait ran out: waits (as long at most) for the copies that may still be on their way.
+  __device__ __forceinline__ void settle(const Part<T>& p) {
+    for (int j = 0; j < p.chunks(); ++j)
+      if (p.in.w != 0.f && p.chunk_lo(j) < p.chunk_hi(j) && !mbar_wait(bar + j, phases >> j & 1, status)) break;
+  }
+};
+
+// Long rows: the warps of a cluster of CTAs take a row.  Each warp copies its
+// part of the row into its own shared memory, sums it, and after the warps have
+// exchanged their maxima and sums, turns it into the gradient in place and
+// sends that off: a row is read once and written once, no register holds a
+// load in flight, and the warps meet once a row.  The copies go in chunks: a
+// chunk is summed while later ones are on their way, and as soon as its
+// gradient has left its buffer (without a gradient: as soon as it is summed)
+// the next row's chunk is asked for.  Clusters take further rows from those not
+// launched yet, so rows of weight 0, which cost half or nothing, leave no SM
+// idle.  N=4096 V=131072 bf16: 302 us, 94% of the copy rate.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kMinCtas) k_policy(ftmoe_policy_args a, int part_pieces, int further,
+                                                               uint32_t* status) {
   extern __shared__ __align__(128) unsigned char policy_smem[];
   __shared__ uint64_t bars[kWarps][kMaxChunks];
   __shared__ uint64_t meet[2], ask[2];
@@ -242,221 +440,184 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_policy(ftmoe_policy_args
   __shared__ MaxSum exchange[2][kMaxRanks * kWarps];
   constexpr int N = Row<T>::N;
   cg::cluster_group cluster = cg::this_cluster();
-  const int ranks = SOLO ? 1 : (int)cluster.num_blocks(), rank = SOLO ? 0 : (int)cluster.block_rank();
-  const int log2_ranks = 31 - __clz(ranks);
+  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), log2_ranks = 31 - __clz(ranks);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool first_warp = SOLO || warp == 0, speaks = first_warp && rank == 0 && lane == 0;
-  Pack<T, N>* buf = reinterpret_cast<Pack<T, N>*>(policy_smem) + warp * part_pieces;
-  T* vals = reinterpret_cast<T*>(buf);
-  uint64_t* bar = bars[warp];
-  if (lane < kMaxChunks) mbar_init(bar + lane, 1);
-  if (!SOLO && threadIdx.x < 2) {
+  const bool speaks = rank == 0 && threadIdx.x == 0;
+  Worker<T> w(a, lane, status, reinterpret_cast<Pack<T, N>*>(policy_smem) + warp * part_pieces, bars[warp]);
+  if (lane < kMaxChunks) mbar_init(bars[warp] + lane, 1);
+  if (threadIdx.x < 2) {
     mbar_init(meet + threadIdx.x, 1);
     mbar_init(ask + threadIdx.x, 1);
   }
   fence_mbar_init();
   __syncwarp();
-  const float k2 = kLog2e / a.temperature;
-  uint32_t phases = 0;   // of the chunks' barriers
-  uint32_t round = 0;    // rows met so far: slot and phase of what the group shares
-  bool ok = true;        // no wait has run out
+  uint32_t round = 0;  // rows met so far: slot and phase of what the cluster shares
+  auto part_of = [&](int64_t n) { return w.part_of(n, log2_ranks, rank, kWarps, warp); };
 
-  // This warp's pieces of row n: [lo, hi), the whole ones [wlo, whi).
-  struct Part {
-    Row<T> z;
-    int64_t n;
-    int64_t y;
-    float w;
-    int lo, hi, wlo, whi;
+  bool more = true;
+  Part<T> p = part_of(blockIdx.x >> log2_ranks);  // the grid has no more clusters than rows
+  check_target(a, p.in, speaks, status);
+  if (lane == 0)
+    for (int j = 0; j < p.chunks(); ++j) w.fetch(p, j);
+  cluster.sync();  // every CTA's barriers are set before a peer uses them
+  // Thread 0 of each CTA: the number of a further row, into a slot.  With a
+  // gradient the next row is needed late in a row, and asked for at its start
+  // (a cluster that holds rows it cannot start yet is late at the end); without
+  // one it is needed at the start, and asked for a row ahead.
+  auto ask_into = [&](uint32_t slot) {
+    mbar_arrive_expect_tx(ask + slot, 16);
+    if (rank == 0) ask_for_row(response + slot, ask + slot);
   };
-  auto part_of = [&](int64_t n) {
-    Part p{Row<T>(static_cast<const T*>(a.logits) + n * a.ld, (int)a.V), n, target_of(a, n),
-           a.weight ? a.weight[n] : 1.f / (float)a.N, 0, 0, 0, 0};
-    const int pieces = p.z.pieces();
-    if (SOLO) {
-      p.hi = pieces;
-    } else {
-      const int per = (pieces + ranks - 1) >> log2_ranks, each = (per + kWarps - 1) / kWarps;
-      const int end = min(pieces, (rank + 1) * per);
-      p.lo = min(end, rank * per + warp * each);
-      p.hi = min(end, p.lo + each);
-    }
-    p.wlo = max(p.lo, (p.z.skip + N - 1) / N);
-    p.whi = max(p.wlo, min(p.hi, p.z.end / N));
-    return p;
-  };
-  auto check = [&](Part& p) {
-    if (p.y >= 0 && p.y < a.V) return;
-    if (speaks) set_status(status, kStatusRange);
-    p.w = 0.f;
-  };
-  // f(e) for the values e of the pieces that are not whole, among the part's pieces [begin, end).
-  auto edges = [&](const Part& p, int begin, int end, auto f) {
-    if (lane >= N) return;
-    for (int i = p.lo + begin; i < min(p.wlo, p.lo + end); ++i) f(i * N + lane);
-    for (int i = max(p.whi, p.lo + begin); i < p.lo + end; ++i) f(i * N + lane);
-  };
-  // Chunk j of a part, as whole pieces [from, to) (empty: from >= to).
-  auto chunk_lo = [&](const Part& p, int j) { return max(p.wlo, p.lo + j * kChunk); };
-  auto chunk_hi = [&](const Part& p, int j) { return min(p.whi, p.lo + (j + 1) * kChunk); };
-  auto chunks_of = [&](const Part& p) { return (p.hi - p.lo + kChunk - 1) / kChunk; };
-  // Asks for a chunk's whole pieces (lane 0).
-  auto fetch = [&](const Part& p, int j) {
-    const int from = chunk_lo(p, j), to = chunk_hi(p, j);
-    if (p.w == 0.f || from >= to) return;
-    mbar_arrive_expect_tx(bar + j, (uint32_t)(to - from) * 16);
-    bulk_g2s(buf + (from - p.lo), p.z.at + (int64_t)from * N, (uint32_t)(to - from) * 16, bar + j);
-  };
-
-  int64_t n = SOLO ? (int64_t)blockIdx.x * kWarps + warp : blockIdx.x >> log2_ranks;
-  bool more = n < a.N;
-  Part p{Row<T>(nullptr, 0), 0, 0, 0.f, 0, 0, 0, 0};
-  if (more) {
-    p = part_of(n);
-    check(p);
-    if (lane == 0)
-      for (int j = 0; j < chunks_of(p); ++j) fetch(p, j);
-  }
-  if (!SOLO) cluster.sync();  // every CTA's barriers are set before a peer uses them
-  while (more && ok) {
-    const int count = p.hi - p.lo, chunks = chunks_of(p);
+  if (!a.dlogits && further && threadIdx.x == 0) ask_into(0);
+  while (more && w.ok) {
     const uint32_t slot = round & 1, turn = round >> 1 & 1;
-    if (!SOLO && first_warp && lane == 0) {
-      mbar_arrive_expect_tx(ask + slot, 16);
+    if (threadIdx.x == 0) {
       mbar_arrive_expect_tx(meet + slot, (uint32_t)(ranks * kWarps * sizeof(MaxSum)));
-      if (rank == 0) ask_for_row(response + slot, ask + slot);
+      if (a.dlogits && further) ask_into(slot);
     }
-    float c = 0.f, m = -FLT_MAX, s = 0.f, zy = 0.f;
-    if (p.w != 0.f) {
-      zy = to_f32(p.z.at[p.z.skip + p.y]);
-      if (p.wlo > p.lo || p.whi < p.hi) {
-        edges(p, 0, count, [&](int e) {
-          vals[e - p.lo * N] = e >= p.z.skip && e < p.z.end ? p.z.at[e] : from_f32<T>(-INFINITY);
-        });
-        fence_async_smem();
-        __syncwarp();
-      }
-      for (int j = 0; j < chunks; ++j) {
-        if (chunk_lo(p, j) < chunk_hi(p, j)) {
-          ok = ok && mbar_wait(bar + j, phases >> j & 1, status);
-          phases ^= 1u << j;
-        }
-        const int end = min(count, (j + 1) * kChunk);
-        int i = j * kChunk + lane;
-        for (; i + 32 * (kUnroll - 1) < end; i += 32 * kUnroll) add_pieces<T, kUnroll>(buf + i, k2, m, s);
-        for (; i < end; i += 32) add_pieces<T, 1>(buf + i, k2, m, s);
-      }
-      // zy is in hand before the group meets: dlogits may be the logits themselves
-      if (!ok || isnan(zy)) s = NAN;
-    }
-    // The next row: its number, and its target and weight on their way while the group meets.
-    Part next = p;
-    if (SOLO) {
-      n += (int64_t)gridDim.x * kWarps;
-      more = n < a.N;
-    } else {
+    // The next row: its number, and its inputs on their way.
+    Part<T> next = p;
+    int next_chunks = 0, asked = 0;  // the next row's chunks, and those asked for
+    auto find_next = [&]() {
+      more = false;
+      if (!further) return;
       uint32_t cta = 0;
-      ok = ok && mbar_wait(ask + slot, turn, status);
-      more = ok && row_given(response + slot, cta);
+      w.ok = w.ok && mbar_wait(ask + slot, turn, status);
+      more = w.ok && row_given(response + slot, cta);
       fence_async_smem();  // read before the slot is given again
-      n = cta >> log2_ranks;
+      if (more) next = part_of(cta >> log2_ranks);
+    };
+    auto check_next = [&]() {
+      if (!more) return;
+      check_target(a, next.in, speaks, status);
+      next_chunks = next.chunks();
+    };
+    if (!a.dlogits) {
+      find_next();
+      if (more && threadIdx.x == 0) ask_into(slot ^ 1);
+      check_next();
     }
-    if (more) next = part_of(n);
+    MaxSum run{-FLT_MAX, 0.f};
+    float zy = 0.f;
+    if (p.in.w != 0.f) {
+      zy = to_f32(p.z.at[p.z.skip + p.in.y]);
+      run = w.sum(p, [&](int) {
+        if (a.dlogits) return;
+        __syncwarp();
+        if (lane == 0 && asked < next_chunks) w.fetch(next, asked++);
+      });
+      // zy is in hand before the warps meet: dlogits may be the logits themselves
+      if (isnan(zy)) run.s = NAN;
+    }
+    if (a.dlogits) find_next();
 
-    MaxSum run = warp_join({m, s}, k2);
-    if (!SOLO) {
-      // Every warp tells every CTA.  Two sets of slots suffice: a warp sends
-      // into a set again two rows on, when it has heard in the next row from
-      // every warp of the cluster, each after its reads here.
-      if (lane < ranks) send(run, &exchange[slot][rank * kWarps + warp], meet + slot, lane);
-      ok = mbar_wait(meet + slot, turn, status) && ok;
-      run = {-FLT_MAX, 0.f};
-      static_assert(kMaxRanks * kWarps <= 32, "a lane a sender");
-      if (lane < ranks * kWarps) run = exchange[slot][lane];
-      run = warp_join(run, k2);
-      if (!ok) run.s = NAN;
-    }
+    // Every warp tells every CTA.  Two sets of slots suffice: a warp sends
+    // into a set again two rows on, when it has heard in the next row from
+    // every warp of the cluster, each after its reads here.
+    static_assert(kMaxRanks * kWarps <= 32, "a lane a sender");
+    run = warp_join(run, w.k2);
+    if (lane < ranks) send(run, &exchange[slot][rank * kWarps + warp], meet + slot, lane);
+    w.ok = mbar_wait(meet + slot, turn, status) && w.ok;
+    run = warp_join(lane < ranks * kWarps ? exchange[slot][lane] : MaxSum{-FLT_MAX, 0.f}, w.k2);
+    if (!w.ok) run.s = NAN;
     ++round;
-    m = run.m;
-    const float ls = log2f(run.s);
-    if (p.w != 0.f) {
-      const float logp = (zy - m) / a.temperature - logf(run.s);
-      const RowTerms t = row_terms(a, p.n, p.w, logp);
-      c = t.c;
-      if (speaks) {
-        a.row_loss[p.n] = t.row;
-        if (a.logp) a.logp[p.n] = logp;
-      }
-    } else if (speaks) {
-      a.row_loss[p.n] = 0.f;
-      if (a.logp) a.logp[p.n] = 0.f;
-    }
-    if (more) check(next);
-    int asked = 0;  // chunks of the next row asked for
-    const int next_chunks = more && ok ? chunks_of(next) : 0;
+    float c = 0.f;
+    if (p.in.w != 0.f) c = finish_row(a, p.in, run, zy, speaks);
+    else if (speaks) write_uncounted(a, p.in.n);
     if (a.dlogits) {
-      const Row<T> g(static_cast<T*>(a.dlogits) + p.n * a.ld_d, (int)a.V);
-      const bool same = g.skip == p.z.skip;
-      T* out = g.at + (g.skip - p.z.skip);  // out[e] belongs to the logit z.at[e]
-      const int e0 = max(p.z.skip, p.lo * N), e1 = (int)min((int64_t)p.z.end, (int64_t)p.hi * N);
-      if (c == 0.f) {  // nothing of the row's softmax is needed
+      check_next();
+      if (c == 0.f) {  // the buffer is free
         __syncwarp();
         if (lane == 0)
-          for (; asked < next_chunks; ++asked) fetch(next, asked);
-        if (same) {
-          for (int i = p.wlo + lane; i < p.whi; i += 32) store_pack<T, N>(out + (int64_t)i * N, zero_pack<T, N>());
-          edges(p, 0, count, [&](int e) {
-            if (e >= p.z.skip && e < p.z.end) out[e] = from_f32<T>(0.f);
-          });
-        } else {
-          for (int e = e0 + lane; e < e1; e += 32) out[e] = from_f32<T>(0.f);
-        }
+          for (; asked < next_chunks; ++asked) w.fetch(next, asked);
         asked = next_chunks;
-      } else {
-        const int target = p.z.skip + (int)p.y - p.lo * N;  // among the part's values
-        const float of_target = c * (1.f - exp2_fast((zy - m) * k2 - ls));
-        for (int j = 0; j < chunks; ++j) {
-          const int begin = j * kChunk, end = min(count, begin + kChunk);
-          int i = begin + lane;
-          for (; i + 32 * (kUnroll - 1) < end; i += 32 * kUnroll) gradient_of_pieces<T, kUnroll>(buf + i, k2, m, ls, c);
-          for (; i < end; i += 32) gradient_of_pieces<T, 1>(buf + i, k2, m, ls, c);
-          // the target's own term, by the lane that wrote its piece
-          if (target >= begin * N && target < end * N && target / N % 32 == lane) vals[target] = from_f32<T>(of_target);
-          fence_async_smem();
-          __syncwarp();
-          if (!same) continue;
-          edges(p, begin, end, [&](int e) {
-            if (e >= p.z.skip && e < p.z.end) out[e] = vals[e - p.lo * N];
-          });
-          if (lane == 0) {
-            const int from = chunk_lo(p, j), to = chunk_hi(p, j);
-            if (from < to) bulk_s2g(out + (int64_t)from * N, buf + (from - p.lo), (uint32_t)(to - from) * 16);
-            bulk_commit();  // one group a chunk, empty or not
-            if (j >= kLag) {
-              bulk_wait_read<kLag>();  // the gradient of chunk j - kLag has left its buffer
-              if (asked < next_chunks) fetch(next, asked++);
-            }
-          }
-        }
-        if (!same) {
-          for (int e = e0 + lane; e < e1; e += 32) out[e] = vals[e - p.lo * N];
-        }
       }
+      w.gradient(p, run.m, log2f(run.s), c, zy, [&](int j) {
+        if (j < kLag) return;
+        bulk_wait_read<kLag>();  // the gradient of chunk j - kLag has left its buffer
+        if (asked < next_chunks) w.fetch(next, asked++);
+      });
     }
     __syncwarp();
     if (lane == 0) {
       bulk_wait_read<0>();
-      for (; asked < next_chunks; ++asked) fetch(next, asked);
+      for (; asked < next_chunks; ++asked) w.fetch(next, asked);
     }
-    ok = __all_sync(0xffffffffu, ok);
+    w.ok = __all_sync(0xffffffffu, w.ok);
     p = next;
   }
   pdl_launch_dependents();
   if (lane == 0) bulk_wait_read<0>();
-  if (!ok) {  // a wait ran out: the copies that may still be on their way
-    for (int j = 0; j < chunks_of(p); ++j)
-      if (p.w != 0.f && chunk_lo(p, j) < chunk_hi(p, j) && !mbar_wait(bar + j, phases >> j & 1, status)) break;
+  if (!w.ok) w.settle(p);
+}
+
+// Short rows: a warp takes a row, and has the next one on its way in a second
+// buffer while it turns one into its gradient.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kMinCtas) k_policy_short(ftmoe_policy_args a, int pieces, uint32_t* status) {
+  extern __shared__ __align__(128) unsigned char policy_smem[];
+  __shared__ uint64_t bars[2][kWarps][kShortChunks];
+  constexpr int N = Row<T>::N;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Pack<T, N>* first = reinterpret_cast<Pack<T, N>*>(policy_smem) + warp * 2 * pieces;
+  Worker<T> w(a, lane, status, first, bars[0][warp]);
+  if (lane < 2 * kShortChunks) mbar_init(bars[lane / kShortChunks][warp] + lane % kShortChunks, 1);
+  fence_mbar_init();
+  __syncwarp();
+  const int64_t step = (int64_t)gridDim.x * kWarps;
+  int64_t n = (int64_t)blockIdx.x * kWarps + warp;
+  if (n >= a.N) return;
+  // The buffer in use is w's; the other one's barriers have other phases.
+  int side = 0;
+  uint32_t other_phases = 0;
+  auto turn = [&]() {
+    side ^= 1;
+    w.buf = first + side * pieces;
+    w.bar = bars[side][warp];
+    const uint32_t t = w.phases;
+    w.phases = other_phases;
+    other_phases = t;
+  };
+  auto fetch_row = [&](const Part<T>& p) {  // one lane
+    for (int j = 0; j < p.chunks(); ++j) w.fetch(p, j);
+  };
+  Part<T> p = w.part_of(n, 0, 0, 1, 0);
+  check_target(a, p.in, lane == 0, status);
+  if (lane == 0) fetch_row(p);
+  bool more = true;
+  while (more && w.ok) {
+    n += step;
+    more = n < a.N;
+    Part<T> next = p;
+    if (more) next = w.part_of(n, 0, 0, 1, 0);
+    MaxSum run{-FLT_MAX, 0.f};
+    float zy = 0.f, c = 0.f;
+    if (p.in.w != 0.f) {
+      zy = to_f32(p.z.at[p.z.skip + p.in.y]);
+      run = w.sum(p, [](int) {});
+    }
+    if (more) {
+      check_target(a, next.in, lane == 0, status);
+      turn();
+      if (lane == 0) {
+        bulk_wait_read<0>();  // the other buffer's gradient has left
+        fetch_row(next);
+      }
+      turn();
+    }
+    if (p.in.w != 0.f) {
+      run = warp_join(run, w.k2);
+      c = finish_row(a, p.in, run, zy, lane == 0);
+    } else if (lane == 0) {
+      write_uncounted(a, p.in.n);
+    }
+    if (a.dlogits) w.gradient(p, run.m, log2f(run.s), c, zy, [](int) {});
+    w.ok = __all_sync(0xffffffffu, w.ok);
+    p = next;
+    turn();
   }
+  if (lane == 0) bulk_wait_read<0>();
+  if (!w.ok) w.settle(p);
 }
 
 // Rows too long for a cluster's shared memory: the logits are read a second time.
@@ -471,16 +632,13 @@ __global__ void __launch_bounds__(kLongThreads) k_policy_long(ftmoe_policy_args 
   const float k2 = kLog2e / a.temperature;
   int parity = 0;
   for (int64_t n = blockIdx.x / ranks; n < a.N; n += gridDim.x / ranks) {
-    const int64_t y = target_of(a, n);
-    float w = a.weight ? a.weight[n] : 1.f / (float)a.N;
-    const bool valid = y >= 0 && y < a.V;
-    if (!valid && rank == 0 && tid == 0) set_status(status, kStatusRange);
-    if (!valid) w = 0.f;
+    RowInputs in = row_inputs(a, n);
+    check_target(a, in, rank == 0 && tid == 0, status);
     const Row<T> z(static_cast<const T*>(a.logits) + n * a.ld, (int)a.V);
     const int per = (z.pieces() + ranks - 1) / ranks, lo = min(z.pieces(), rank * per), hi = min(z.pieces(), lo + per);
     float c = 0.f, ls = 0.f, m = 0.f;
-    if (w != 0.f) {
-      const float zy = to_f32(z.at[z.skip + y]);
+    if (in.w != 0.f) {
+      const float zy = to_f32(z.at[z.skip + in.y]);
       MaxSum run{-FLT_MAX, 0.f};
       for (int i = lo + tid; i < hi; i += kLongThreads) {
         const Pack<T, N> x = z.load(i);
@@ -502,16 +660,9 @@ __global__ void __launch_bounds__(kLongThreads) k_policy_long(ftmoe_policy_args 
       parity ^= 1;
       m = run.m;
       ls = log2f(run.s);
-      const float logp = (zy - m) / a.temperature - logf(run.s);
-      const RowTerms t = row_terms(a, n, w, logp);
-      c = t.c;
-      if (rank == 0 && tid == 0) {
-        a.row_loss[n] = t.row;
-        if (a.logp) a.logp[n] = logp;
-      }
+      c = finish_row(a, in, run, zy, rank == 0 && tid == 0);
     } else if (rank == 0 && tid == 0) {
-      a.row_loss[n] = 0.f;
-      if (a.logp) a.logp[n] = 0.f;
+      write_uncounted(a, n);
     }
     if (!a.dlogits) continue;
     const Row<T> g(static_cast<T*>(a.dlogits) + n * a.ld_d, (int)a.V);
@@ -520,7 +671,7 @@ __global__ void __launch_bounds__(kLongThreads) k_policy_long(ftmoe_policy_args 
     out.at += g.skip - z.skip;
     out.skip = z.skip;
     out.end = z.end;
-    const int target = z.skip + (int)y;
+    const int target = z.skip + (int)in.y;
     for (int i = lo + tid; i < hi; i += kLongThreads) {
       Pack<T, N> o = zero_pack<T, N>();
       if (c != 0.f) {
@@ -535,29 +686,66 @@ __global__ void __launch_bounds__(kLongThreads) k_policy_long(ftmoe_policy_args 
   cluster.sync();  // no CTA leaves while a peer may still read its exchange slot
 }
 
-// loss = sum_n w_n row_n in a fixed order, by one CTA.
-constexpr int kSumThreads = 512;
+// loss = sum_n w_n row_n in a fixed order, by one CTA: in fp32 with each
+// addition's rounding kept and added at the end (FP64, of which an SM does two
+// a cycle, took 9 us of 16384 rows).
+struct Sum2 {
+  float s, e;
+  __device__ __forceinline__ void add(float v) {
+    const float t = __fadd_rn(s, v), u = __fsub_rn(t, s);
+    e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, u)), __fsub_rn(v, u)));
+    s = t;
+  }
+};
+constexpr int kSumThreads = 1024;
 __global__ void __launch_bounds__(kSumThreads) k_policy_sum(const float* weight, const float* row_loss, int64_t N, float* loss) {
-  __shared__ double part[kSumThreads / 32];
+  __shared__ Sum2 part[kSumThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
-  double s = 0.0;
-#pragma unroll 4
-  for (int64_t n = threadIdx.x; n < N; n += kSumThreads) s += (double)(weight ? weight[n] : 1.f / (float)N) * row_loss[n];
+  Sum2 t{0.f, 0.f};
+  const float each = 1.f / (float)N;
+  for (int64_t n0 = threadIdx.x; n0 < N; n0 += 8 * kSumThreads) {
+    float v[8], w[8];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) part[warp] = s;
+    for (int u = 0; u < 8; ++u) {
+      const int64_t n = min(n0 + u * kSumThreads, N - 1);
+      v[u] = row_loss[n];
+      w[u] = weight ? weight[n] : each;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (n0 + u * kSumThreads >= N) break;
+      const float r = __fmul_rn(v[u], w[u]);
+      t.add(r);
+      t.e = __fadd_rn(t.e, __fmaf_rn(v[u], w[u], -r));
+    }
+  }
+  auto join = [&](int width) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (o >= width) continue;
+      const float s = __shfl_down_sync(0xffffffffu, t.s, o), e = __shfl_down_sync(0xffffffffu, t.e, o);
+      t.add(s);
+      t.e = __fadd_rn(t.e, e);
+    }
+  };
+  join(32);
+  if (lane == 0) part[warp] = t;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    s = 0.0;
-    for (int w = 0; w < kSumThreads / 32; ++w) s += part[w];
-    *loss = (float)s;
+  if (warp == 0) {
+    t = part[lane];
+    join(32);
+    // NaN and infinities are the sum's own: their rounding terms say nothing
+    if (lane == 0) *loss = isfinite(t.s) ? t.s + t.e : t.s;
   }
 }
 
-// A CTA's shared memory for its part of a row: at most, and what lets several CTAs share an SM.
-constexpr int kStageMax = 216 * 1024, kStage = 36 * 1024;
-constexpr int kSoloBytes = 4096;  // rows up to here are a warp's
+// A CTA's shared memory for its part of a row, at most; what an SM has for all of them.
+constexpr int kStageMax = 216 * 1024, kSmemSm = 226 * 1024;
+constexpr int kFixedSmem = 3 * 1024;    // of a CTA besides: barriers, exchange slots, the system's own
+// Rows up to kShortBytes may be a warp's: 16384 bf16 rows of 4 KB take 37 us so and 80 us as a CTA's, of 16 KB
+// 183 and 127 us.  Up to kShortAlways they are even where that leaves warps idle.
+constexpr int kShortBytes = 8 * 1024, kShortAlways = 2 * 1024;
 
 }  // namespace
 
@@ -565,9 +753,9 @@ cudaError_t policy_set_limits() {
   cudaError_t e = cudaSuccess;
   auto set = [&](auto type) {
     using T = decltype(type);
-    const cudaError_t r = cudaFuncSetAttribute(k_policy<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageMax);
+    const cudaError_t r = cudaFuncSetAttribute(k_policy_short<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageMax);
     if (r != cudaSuccess) return r;
-    return cudaFuncSetAttribute(k_policy<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageMax);
+    return cudaFuncSetAttribute(k_policy<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageMax);
   };
   for (int t : {FTMOE_BF16, FTMOE_FP32, FTMOE_FP16})
     if ((e = with_dtype(t, set)) != cudaSuccess) return e;
@@ -580,12 +768,18 @@ cudaError_t launch_policy_loss(const TrainDevice& d, const ftmoe_policy_args& a,
     const int64_t pieces = (a.V * bytes + 15 + 14) / 16;  // of a row at any alignment, at most
     auto part = [&](int ranks) { return ((pieces + ranks - 1) / ranks + kWarps - 1) / kWarps; };  // a warp's pieces
     auto cta_bytes = [&](int ranks) { return part(ranks) * kWarps * 16; };
-    const bool solo = pieces * 16 <= kSoloBytes;
+    auto resident = [&](int64_t smem) { return std::min<int64_t>(kMinCtas, kSmemSm / (smem + kFixedSmem)); };
+    const bool is_short = pieces * 16 <= kShortBytes && (pieces * 16 <= kShortAlways || a.N >= 8 * d.num_sms);
+    // The ranks that have most of an SM's shared memory in use; of (nearly) equals, the most, whose CTAs are more.
     int ranks = 1;
-    while (!solo && ranks < kMaxRanks && cta_bytes(ranks) > kStage) ranks *= 2;
+    for (int r = 2; r <= kMaxRanks; r *= 2)
+      if (cta_bytes(r) * resident(cta_bytes(r)) >= cta_bytes(ranks) * resident(cta_bytes(ranks)) * 98 / 100) ranks = r;
     // few rows: spread each over more CTAs while the SMs are not full and a part has work for its warps
-    while (!solo && ranks < kMaxRanks && a.N * ranks < 2 * d.num_sms && cta_bytes(ranks) >= 2 * kThreads * 16) ranks *= 2;
-    const int64_t smem = solo ? pieces * kWarps * 16 : cta_bytes(ranks);
+    while (ranks < kMaxRanks && a.N * ranks < 2 * d.num_sms && cta_bytes(ranks) >= 2 * kThreads * 16) ranks *= 2;
+    if (cta_bytes(ranks) > kStageMax) ranks = kMaxRanks;
+    const int64_t smem = is_short ? pieces * 2 * kWarps * 16 : cta_bytes(ranks);
+    const bool staged = smem <= kStageMax;
+    if (is_short) ranks = 1;
     cudaLaunchConfig_t c{};
     c.stream = s;
     cudaLaunchAttribute at[1];
@@ -594,18 +788,18 @@ cudaError_t launch_policy_loss(const TrainDevice& d, const ftmoe_policy_args& a,
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     c.attrs = at;
     c.numAttrs = 1;
-    const bool staged = smem <= kStageMax;
     c.blockDim = dim3(staged ? kThreads : kLongThreads);
     c.dynamicSmemBytes = staged ? (size_t)smem : 0;
-    const int64_t want = solo ? (a.N + kWarps - 1) / kWarps : a.N;
-    const int64_t room = solo ? (int64_t)d.num_sms * 6 : staged ? INT32_MAX / ranks : 1 << 24;  // memory ends before
+    const int64_t want = is_short ? (a.N + kWarps - 1) / kWarps : a.N;
+    // short rows: as many warps as fit; long ones: a cluster a row, of which those that run take the rest over
+    const int64_t room = is_short ? d.num_sms * resident(smem) : staged ? INT32_MAX / ranks : 1 << 24;  // memory ends before
     c.gridDim = dim3((unsigned)(std::min(want, room) * ranks));
+    const int further = a.N * ranks > d.num_sms;  // else no cluster waits to be launched
     cudaError_t e = with_dtype(a.dtype, [&](auto type) {
       using T = decltype(type);
       if (!staged) return cudaLaunchKernelEx(&c, k_policy_long<T>, a, d.status);
-      const int each = solo ? (int)pieces : (int)part(ranks);
-      return solo ? cudaLaunchKernelEx(&c, k_policy<T, true>, a, each, d.status)
-                  : cudaLaunchKernelEx(&c, k_policy<T, false>, a, each, d.status);
+      if (is_short) return cudaLaunchKernelEx(&c, k_policy_short<T>, a, (int)pieces, d.status);
+      return cudaLaunchKernelEx(&c, k_policy<T>, a, (int)part(ranks), further, d.status);
     });
     if (e != cudaSuccess) return e;
   }
