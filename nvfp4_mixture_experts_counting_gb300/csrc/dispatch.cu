@@ -190,9 +190,11 @@ __device__ __forceinline__ int checked_place(int at, int64_t P, uint32_t* status
 // pieces of the row, nq apart, and kSlots slots at a time, whose loads are
 // issued together: a slot that is dropped or past the last one has its
 // neighbour's row loaded again and not used, as a load under a condition waits
-// for the condition (bf16 T=16384 k=8 took 386 us so, and 111 us would be the copy rate).
-template <typename T, int N, int Q>
-__global__ void __launch_bounds__(kThreads) k_combine(const T* ys, int64_t total, int nv, int nq, int k, int64_t P,
+// for the condition (bf16 T=16384 k=8 H=2560 took 386 us so).  Rows are read at the
+// copy rate with as many warps an SM as registers allow without spills: 48 with
+// weights (111 us; 64 take 125, 40 take 136), 64 without (111 us; 48 take 122).
+template <typename T, int N, int Q, bool WEIGHTED>
+__global__ void __launch_bounds__(kThreads, N == 1 ? 1 : WEIGHTED ? 6 : 8) k_combine(const T* ys, int64_t total, int nv, int nq, int k, int64_t P,
                                                       const int32_t* inv, const float* w, T* out, uint32_t* status) {
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= total) return;
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) k_combine(const T* ys, int64_t total
 #pragma unroll
     for (int j = 0; j < kSlots; ++j) {
       if (at[j] < 0) continue;
-      const float wj = w ? w[t * k + j0 + j] : 1.f;
+      const float wj = WEIGHTED ? w[t * k + j0 + j] : 1.f;
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
 #pragma unroll
@@ -412,7 +414,8 @@ cudaError_t launch_combine(const TrainDevice& d, const void* ys, int dtype, int 
       constexpr int N = decltype(n)::value, Q = decltype(columns)::value;
       const int nv = H / N, nq = (nv + Q - 1) / Q;
       const int64_t total = (int64_t)T * nq;
-      k_combine<V, N, Q><<<blocks_of(total, kThreads), kThreads, 0, s>>>(y, total, nv, nq, top_k, P, inv, w, o, d.status);
+      const auto kernel = w ? k_combine<V, N, Q, true> : k_combine<V, N, Q, false>;
+      kernel<<<blocks_of(total, kThreads), kThreads, 0, s>>>(y, total, nv, nq, top_k, P, inv, w, o, d.status);
     };
     constexpr int N = 16 / sizeof(V);
     if (H % N == 0) launch(std::integral_constant<int, N>(), std::integral_constant<int, 1>());
