@@ -833,3 +833,85 @@ def test_strided_tensors_are_refused():
     z = torch.zeros(4, 10, device=DEV)
     with pytest.raises(ValueError):
         ftmoe.policy_args(z.t(), o, o, o, o, o, o, o)
+
+
+# ----------------------------------------------------------------- offsets past 32 bits
+
+def test_lookup_and_gradient_in_a_table_past_32_bits():
+    V, H, N = 600_000, 4096, 64  # 2.46e9 values
+    g = gen(80)
+    table = torch.empty(V, H, dtype=BF16, device=DEV)
+    ids = torch.cat([torch.arange(V - 40, V, device=DEV), torch.randint(0, V, (N - 40,), generator=g, device=DEV)])
+    table[ids] = randn(g, N, H, dtype=BF16)
+    out = torch.empty(N, H, dtype=BF16, device=DEV)
+    ftmoe.ftmoe_embed(table, V, H, ids, N, 1.0, out)
+    assert torch.equal(out, table[ids])
+    table.fill_(7.0)
+    ws = torch.empty(ftmoe.ftmoe_embed_workspace(N, H), dtype=torch.uint8, device=DEV)
+    ids[40:] = V - 1  # a run past its chunk
+    ftmoe.ftmoe_embed_backward(out, ids, N, V, H, 1.0, -1, table, False, ws)
+    assert torch.equal(table[V - 40:V - 1], out[:39])
+    last = out[39:].double().sum(0)
+    within(table[V - 1], last, UNIT[BF16] * 1.01 * last.abs() + 2 * 27 * EPS * out[39:].double().abs().sum(0))
+    assert not any(bool(table[a:a + 100_000].any()) for a in range(0, V - 100_000, 100_000))
+
+
+def test_dispatch_and_combine_past_32_bits():
+    T, k, E, H = 70_000, 8, 16, 4096  # 2.29e9 values in sorted order
+    g = gen(81)
+    idx = torch.randint(0, E, (T, k), generator=g, device=DEV, dtype=torch.int32)
+    x = randn(g, T, H, dtype=BF16)
+    i32 = lambda n: torch.empty(n, dtype=torch.int32, device=DEV)
+    off, perm, inv, xs = i32(E + 1), i32(T * k), i32(T * k), torch.empty(T * k, H, dtype=BF16, device=DEV)
+    ftmoe.ftmoe_dispatch(x, T, H, idx, k, E, off, perm, inv, xs)
+    ordered, order = torch.sort(idx.view(-1), stable=True)
+    assert torch.equal(perm, order.int())
+    for a in range(0, T * k, 80_000):
+        assert torch.equal(xs[a:a + 80_000], x[order[a:a + 80_000] // k])
+    out = torch.empty(T, H, dtype=BF16, device=DEV)
+    ftmoe.ftmoe_combine(xs, T, H, k, inv, torch.full((T, k), 0.125, device=DEV), out)
+    assert torch.equal(out, x)  # eight times an eighth of the row, exactly
+    dw = torch.empty(T, k, device=DEV)
+    ftmoe.ftmoe_combine_backward(x, xs, T, H, k, inv, torch.full((T, k), 2.0, device=DEV), xs, dw)
+    for a in range(0, T * k, 80_000):
+        assert torch.equal(xs[a:a + 80_000], 2 * x[order[a:a + 80_000] // k])
+    square = x[-100:].double().square().sum(1, keepdim=True)
+    within(dw[-100:], square.expand(-1, k), 2 * (H + 2) * EPS * square)
+
+
+def test_policy_loss_past_32_bits():
+    N, V = 17_000, 131_072  # 2.23e9 logits
+    g = gen(82)
+    logits = torch.empty(N, V, dtype=BF16, device=DEV)
+    logits.fill_(-3.0)
+    few = policy_inputs(83, 50, V, BF16, masked=0.0)
+    logits[N - 50:] = few["logits"]
+    i = dict(logits=logits, weight=torch.zeros(N, device=DEV), targets=torch.zeros(N, dtype=torch.int64, device=DEV))
+    for n in ("old_logp", "ref_logp", "advantage", "targets", "weight"):
+        i.setdefault(n, torch.zeros(N, device=DEV))
+        i[n][N - 50:] = few[n]
+    want = policy(few, kl_coef=0.1)
+    got = policy(i, in_place=True, kl_coef=0.1)
+    assert torch.equal(got[0], want[0])
+    for a, b in zip(got[1:], want[1:]):
+        assert torch.equal(a[N - 50:], b)
+    assert not got[1][:N - 50].any() and not logits[:N - 50:997].any()
+
+
+def test_adamw_past_32_bits():
+    n, tail = (1 << 31) + 1000, 2048 * 3  # the tail's blocks start on a block's boundary
+    g = gen(84)
+    start = (n - tail) // 256 * 256
+    big = dict(p=torch.zeros(n, dtype=BF16, device=DEV), g=torch.zeros(n, dtype=BF16, device=DEV),
+               m=torch.zeros(n, dtype=torch.uint8, device=DEV), v=torch.zeros(n, dtype=torch.uint8, device=DEV),
+               m_scale=torch.zeros(-(-n // 256), device=DEV), v_scale=torch.zeros(-(-n // 256), device=DEV),
+               weight_decay=0.1)
+    big["p"][start:] = randn(g, n - start, dtype=BF16)
+    big["g"][start:] = randn(g, n - start, dtype=BF16)
+    small = {k: v[start // 256 if "scale" in k else start:].clone() if torch.is_tensor(v) else v for k, v in big.items()}
+    for t in (big, small):
+        ftmoe.ftmoe_adamw(ftmoe.adamw_list([t]), lr=1e-2, step=1)
+    for k, v in small.items():
+        if torch.is_tensor(v):
+            assert torch.equal(big[k][start // 256 if "scale" in k else start:], v), k
+    assert not big["p"][:start:99_991].any() and not big["v"][:start:99_991].any()
