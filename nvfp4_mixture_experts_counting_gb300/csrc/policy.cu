@@ -165,54 +165,45 @@ __device__ __forceinline__ LogProb exact_sum(float a, float b) {
   const float e = __fadd_rn(__fsub_rn(a, __fsub_rn(t, u)), __fsub_rn(b, u));
   return {t, isfinite(t) ? e : 0.f};
 }
-// (zy - m) / T - ln s.  One Newton step, ln s = y + (s e^-y - 1), brings the logarithm's error to that of expf.
-__device__ __forceinline__ LogProb log_prob(float zy, float m, float s, float temperature) {
+// (zy - m) / T - ln s.  One Newton step each, q + (d - q T) / T for the quotient
+// and ln s = y + (s e^-y - 1), brings their errors to those of a product and of expf.
+__device__ __forceinline__ LogProb log_prob(float zy, float m, float s, float temperature, float inv_t) {
   const LogProb d = exact_sum(zy, -m);
-  const float q = d.hi / temperature;
-  const float rest = isfinite(q) ? (fmaf(-q, temperature, d.hi) + d.lo) / temperature : 0.f;
+  const float q = d.hi * inv_t;
+  const float rest = isfinite(q) ? (fmaf(-q, temperature, d.hi) + d.lo) * inv_t : 0.f;
   const float y = logf(s), dy = fmaf(s, expf(-y), -1.f);
   LogProb r = exact_sum(q, -y);
   r.lo += rest - dy;
   return r;
 }
 
-// The clipped ratio's side, and whether the clip holds: false for NaN, which
-// then reaches the loss and the gradient.
-struct Ratio {
-  float r, bounded;
-  bool clipped;
-};
-__device__ __forceinline__ Ratio ratio_of(const ftmoe_policy_args& a, float x, float A) {
-  const float r = expf(x);
-  const float b = r < 1.f - a.clip_low ? 1.f - a.clip_low : r > 1.f + a.clip_high ? 1.f + a.clip_high : r;
-  return {r, b, r * A > b * A};
-}
-// The gradient's coefficient grad_scale w c / temperature.
-__device__ __forceinline__ float gradient_scale(const ftmoe_policy_args& a, const RowInputs& in, float logp) {
-  const Ratio t = ratio_of(a, logp - in.old, in.adv);
-  float c = t.clipped ? 0.f : -(in.adv * t.r);
-  if (a.ref_logp && a.kl_coef != 0.f) c += a.kl_coef * (1.f - expf(in.ref - logp));
-  return c * (a.grad_scale * in.w / a.temperature);
-}
-// The row's loss, by one thread.
-__device__ __forceinline__ void write_row(const ftmoe_policy_args& a, const RowInputs& in, LogProb logp) {
-  const Ratio t = ratio_of(a, logp.minus(in.old), in.adv);
-  float row = -((t.clipped ? t.bounded : t.r) * in.adv);
+// A counted row's gradient coefficient grad_scale w c / temperature, from its
+// maximum, its sum and log2 of that.  A warp that has to write the row's loss
+// (`writes`: by this lane) works with the log probability's rounding; for
+// the coefficient alone, as many times as a row has warps, the rounded value does.
+__device__ __forceinline__ float finish_row(const ftmoe_policy_args& a, const RowInputs& in, MaxSum run, float log2_s,
+                                            float zy, float inv_t, bool warp_writes, bool writes) {
+  LogProb logp{(zy - run.m) * inv_t - log2_s * kLn2, 0.f};
+  if (warp_writes) logp = log_prob(zy, run.m, run.s, a.temperature, inv_t);
+  else if (!a.dlogits) return 0.f;
+  const float r = expf(logp.minus(in.old)), A = in.adv;
+  const float bounded = r < 1.f - a.clip_low ? 1.f - a.clip_low : r > 1.f + a.clip_high ? 1.f + a.clip_high : r;
+  const bool clipped = r * A > bounded * A;  // false for NaN, which then reaches the loss and the gradient
+  float row = -(clipped ? bounded * A : r * A), c = clipped ? 0.f : -(A * r);
   if (a.ref_logp && a.kl_coef != 0.f) {
-    const float d = -logp.minus(in.ref);
-    row += a.kl_coef * (expf(d) - d - 1.f);
+    const float d = -logp.minus(in.ref), ed = expf(d);
+    row += a.kl_coef * (ed - d - 1.f);
+    c += a.kl_coef * (1.f - ed);
   }
-  a.row_loss[in.n] = row;
-  if (a.logp) a.logp[in.n] = logp.value();
+  if (writes) {
+    a.row_loss[in.n] = row;
+    if (a.logp) a.logp[in.n] = logp.value();
+  }
+  return c * (a.grad_scale * in.w * inv_t);
 }
 __device__ __forceinline__ void write_uncounted(const ftmoe_policy_args& a, int64_t n) {
   a.row_loss[n] = 0.f;
   if (a.logp) a.logp[n] = 0.f;
-}
-// What every warp takes from a counted row's maximum and sum, and one thread writes.
-__device__ __forceinline__ float finish_row(const ftmoe_policy_args& a, const RowInputs& in, MaxSum run, float zy, bool speaks) {
-  if (speaks) write_row(a, in, log_prob(zy, run.m, run.s, a.temperature));
-  return a.dlogits ? gradient_scale(a, in, (zy - run.m) / a.temperature - logf(run.s)) : 0.f;
 }
 
 // U pieces, 32 apart, join a lane's running maximum and sum.
@@ -307,14 +298,14 @@ struct Worker {
   const ftmoe_policy_args& a;
   const int lane;
   uint32_t* const status;
-  const float k2;
+  const float inv_t, k2;
   Pack<T, N>* buf;      // the part
   uint64_t* bar;        // a barrier for each chunk
   uint32_t phases = 0;  // of the barriers
   bool ok = true;       // no wait has run out
 
   __device__ Worker(const ftmoe_policy_args& args, int lane_, uint32_t* status_, Pack<T, N>* buf_, uint64_t* bar_)
-      : a(args), lane(lane_), status(status_), k2(kLog2e / args.temperature), buf(buf_), bar(bar_) {}
+      : a(args), lane(lane_), status(status_), inv_t(1.f / args.temperature), k2(kLog2e / args.temperature), buf(buf_), bar(bar_) {}
   __device__ __forceinline__ T* vals() const { return reinterpret_cast<T*>(buf); }
 
   // The part of row n that is number `index` of 2^log2_parts * per_cta parts (CTA by CTA).
@@ -522,7 +513,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_policy(ftmoe_policy_args
     if (!w.ok) run.s = NAN;
     ++round;
     float c = 0.f;
-    if (p.in.w != 0.f) c = finish_row(a, p.in, run, zy, speaks);
+    const float log2_s = log2f(run.s);
+    if (p.in.w != 0.f) c = finish_row(a, p.in, run, log2_s, zy, w.inv_t, rank == 0 && warp == 0, speaks);
     else if (speaks) write_uncounted(a, p.in.n);
     if (a.dlogits) {
       check_next();
@@ -532,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_policy(ftmoe_policy_args
           for (; asked < next_chunks; ++asked) w.fetch(next, asked);
         asked = next_chunks;
       }
-      w.gradient(p, run.m, log2f(run.s), c, zy, [&](int j) {
+      w.gradient(p, run.m, log2_s, c, zy, [&](int j) {
         if (j < kLag) return;
         bulk_wait_read<kLag>();  // the gradient of chunk j - kLag has left its buffer
         if (asked < next_chunks) w.fetch(next, asked++);
@@ -605,13 +597,15 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_policy_short(ftmoe_polic
       }
       turn();
     }
+    float log2_s = 0.f;
     if (p.in.w != 0.f) {
       run = warp_join(run, w.k2);
-      c = finish_row(a, p.in, run, zy, lane == 0);
+      log2_s = log2f(run.s);
+      c = finish_row(a, p.in, run, log2_s, zy, w.inv_t, true, lane == 0);
     } else if (lane == 0) {
       write_uncounted(a, p.in.n);
     }
-    if (a.dlogits) w.gradient(p, run.m, log2f(run.s), c, zy, [](int) {});
+    if (a.dlogits) w.gradient(p, run.m, log2_s, c, zy, [](int) {});
     w.ok = __all_sync(0xffffffffu, w.ok);
     p = next;
     turn();
@@ -660,7 +654,7 @@ __global__ void __launch_bounds__(kLongThreads) k_policy_long(ftmoe_policy_args 
       parity ^= 1;
       m = run.m;
       ls = log2f(run.s);
-      c = finish_row(a, in, run, zy, rank == 0 && tid == 0);
+      c = finish_row(a, in, run, ls, zy, 1.f / a.temperature, rank == 0 && warp == 0, rank == 0 && tid == 0);
     } else if (rank == 0 && tid == 0) {
       write_uncounted(a, n);
     }

@@ -311,43 +311,41 @@ def _dtype(t) -> int:
         raise TypeError(f"bf16, fp32 or fp16 expected, got {t.dtype}") from None
 
 
-def _rows(*tensors):
-    """The C calls take contiguous arrays: a strided tensor is refused here."""
-    for t in tensors:
-        if t is not None and not t.is_contiguous():
-            raise ValueError("contiguous tensors expected")
+def _dense(t):
+    """Address of a contiguous tensor (None stays None): the C calls take no strides."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("contiguous tensors expected")
+    return t.data_ptr()
 
 
 def ftmoe_dispatch(x, T: int, H: int, topk_idx, top_k: int, E: int, offsets, perm, inv, xs, stream=None):
     """Rows of x sorted by expert into xs, and the sort's tables (x and xs None: the tables alone)."""
-    _rows(x, topk_idx, offsets, perm, inv, xs)
-    _check(lib().ftmoe_dispatch(_ptr(x), _dtype(x) if x is not None else BF16, T, H, _ptr(topk_idx), top_k, E,
-                                _ptr(offsets), _ptr(perm), _ptr(inv), _ptr(xs), _stream(stream)), "ftmoe_dispatch")
+    _check(lib().ftmoe_dispatch(_dense(x), BF16 if x is None else _dtype(x), T, H, _dense(topk_idx), top_k, E,
+                                _dense(offsets), _dense(perm), _dense(inv), _dense(xs), _stream(stream)),
+           "ftmoe_dispatch")
 
 
 def ftmoe_combine(ys, T: int, H: int, top_k: int, inv, w, out, stream=None):
     """out[t] = sum_j w[t, j] ys[inv[t, j]]; w None: weights of one (the gradient of ftmoe_dispatch)."""
-    _rows(ys, inv, w, out)
-    _check(lib().ftmoe_combine(_ptr(ys), _dtype(ys), T, H, top_k, _ptr(inv), _ptr(w), _ptr(out), _stream(stream)),
-           "ftmoe_combine")
+    _check(lib().ftmoe_combine(_dense(ys), _dtype(ys), T, H, top_k, _dense(inv), _dense(w), _dense(out),
+                               _stream(stream)), "ftmoe_combine")
 
 
 def ftmoe_combine_backward(dout, ys, T: int, H: int, top_k: int, inv, w, dys, dw, stream=None):
-    _rows(dout, ys, inv, w, dys, dw)
-    _check(lib().ftmoe_combine_backward(_ptr(dout), _ptr(ys), _dtype(dout), T, H, top_k, _ptr(inv), _ptr(w),
-                                        _ptr(dys), _ptr(dw), _stream(stream)), "ftmoe_combine_backward")
+    _check(lib().ftmoe_combine_backward(_dense(dout), _dense(ys), _dtype(dout), T, H, top_k, _dense(inv), _dense(w),
+                                        _dense(dys), _dense(dw), _stream(stream)), "ftmoe_combine_backward")
 
 
 def ftmoe_route_backward(logits, topk_idx, topk_w, dw, T: int, E: int, top_k: int, norm_topk_prob: bool, dlogits,
                          stream=None):
-    _rows(logits, topk_idx, topk_w, dw, dlogits)
-    _check(lib().ftmoe_route_backward(_ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(dw), T, E, top_k,
-                                      int(norm_topk_prob), _ptr(dlogits), _stream(stream)), "ftmoe_route_backward")
+    _check(lib().ftmoe_route_backward(_dense(logits), _dense(topk_idx), _dense(topk_w), _dense(dw), T, E, top_k,
+                                      int(norm_topk_prob), _dense(dlogits), _stream(stream)), "ftmoe_route_backward")
 
 
 def ftmoe_embed(table, V: int, H: int, ids, N: int, scale: float, out, stream=None):
-    _rows(table, ids, out)
-    _check(lib().ftmoe_embed(_ptr(table), _dtype(table), V, H, _ptr(ids), ids.element_size(), N, scale, _ptr(out),
+    _check(lib().ftmoe_embed(_dense(table), _dtype(table), V, H, _dense(ids), ids.element_size(), N, scale, _dense(out),
                              _stream(stream)), "ftmoe_embed")
 
 
@@ -360,10 +358,9 @@ def ftmoe_embed_workspace(N: int, H: int) -> int:
 
 def ftmoe_embed_backward(dout, ids, N: int, V: int, H: int, scale: float, padding_id: int, dtable, accumulate: bool,
                          workspace, stream=None):
-    _rows(dout, ids, dtable, workspace)
-    _check(lib().ftmoe_embed_backward(_ptr(dout), _dtype(dout), _ptr(ids), ids.element_size(), N, V, H, scale,
-                                      padding_id, _ptr(dtable), _dtype(dtable), int(accumulate), _ptr(workspace),
-                                      workspace.numel() * workspace.element_size() if workspace is not None else 0,
+    _check(lib().ftmoe_embed_backward(_dense(dout), _dtype(dout), _dense(ids), ids.element_size(), N, V, H, scale,
+                                      padding_id, _dense(dtable), _dtype(dtable), int(accumulate), _dense(workspace),
+                                      0 if workspace is None else workspace.numel() * workspace.element_size(),
                                       _stream(stream)), "ftmoe_embed_backward")
 
 
@@ -371,18 +368,20 @@ def policy_args(logits, targets, old_logp, ref_logp, advantage, weight, loss, ro
                 temperature: float = 1.0, clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
                 grad_scale: float = 1.0) -> PolicyArgs:
     """Arguments of ftmoe_policy_loss; logits and dlogits [N, V] may have any row stride (last dimension dense)."""
-    _rows(targets, old_logp, ref_logp, advantage, weight, loss, row_loss, logp)
     N, V = logits.shape
-    for t in (logits, dlogits):
-        if t is not None and V > 1 and t.stride(1) != 1:
-            raise ValueError("logits and dlogits need a dense last dimension")
-    if dlogits is not None and (dlogits.dtype != logits.dtype or dlogits.shape != logits.shape):
-        raise TypeError("dlogits has the shape and type of logits")
-    # a single row's stride says nothing
-    return PolicyArgs(_ptr(logits), _dtype(logits), targets.element_size(), N, V, logits.stride(0) if N > 1 else V,
-                      _ptr(targets), _ptr(old_logp), _ptr(ref_logp), _ptr(advantage), _ptr(weight), temperature,
-                      clip_low, clip_high, kl_coef, grad_scale, _ptr(loss), _ptr(row_loss), _ptr(logp), _ptr(dlogits),
-                      0 if dlogits is None else dlogits.stride(0) if N > 1 else V)
+    ld, step = logits.stride()
+    at, ld_d, step_d = None, 0, 1
+    if dlogits is not None:
+        if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
+            raise TypeError("dlogits has the shape and type of logits")
+        at, (ld_d, step_d) = dlogits.data_ptr(), dlogits.stride()
+    if V > 1 and (step != 1 or step_d != 1):
+        raise ValueError("logits and dlogits need a dense last dimension")
+    if N <= 1:  # a single row's stride says nothing
+        ld = ld_d = V
+    return PolicyArgs(logits.data_ptr(), _dtype(logits), targets.element_size(), N, V, ld, _dense(targets),
+                      _dense(old_logp), _dense(ref_logp), _dense(advantage), _dense(weight), temperature, clip_low,
+                      clip_high, kl_coef, grad_scale, _dense(loss), _dense(row_loss), _dense(logp), at, ld_d)
 
 
 def ftmoe_policy_loss(args: PolicyArgs, stream=None):
@@ -398,10 +397,9 @@ class AdamwList:
         for t in tensors:
             get = t.get
             p, g, m = t["p"], t["g"], t["m"]
-            arrays = (p, g, get("master"), m, t["v"], get("m_scale"), get("v_scale"))
-            _rows(*arrays)
-            entries.append((*map(_ptr, arrays), p.numel(), get("weight_decay", 0.0), _dtype(p), _dtype(g),
-                            8 * m.element_size()))
+            entries.append((_dense(p), _dense(g), _dense(get("master")), _dense(m), _dense(t["v"]),
+                            _dense(get("m_scale")), _dense(get("v_scale")), p.numel(), get("weight_decay", 0.0),
+                            _dtype(p), _dtype(g), 8 * m.element_size()))
         self.array = (AdamwTensor * len(entries))(*entries)
 
 
