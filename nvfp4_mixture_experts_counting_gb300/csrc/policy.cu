@@ -19,9 +19,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMinCtas = 6;    // CTAs an SM holds at least, by registers
+constexpr int kMinWarps = 24;  // an SM holds at least, by registers
+constexpr int kWarps = 4;      // of a CTA (k_policy: at most)
 constexpr int kMaxRanks = 8;   // CTAs of a cluster
 constexpr int kUnroll = 4;     // 16-byte pieces a lane sums at a time
 constexpr int kChunk = 256;    // 16-byte pieces of one bulk copy
@@ -421,14 +420,14 @@ struct Worker {
 // the next row's chunk is asked for.  Clusters take further rows from those not
 // launched yet, so rows of weight 0, which cost half or nothing, leave no SM
 // idle.  N=4096 V=131072 bf16: 302 us, 94% of the copy rate.
-template <typename T>
-__global__ void __launch_bounds__(kThreads, kMinCtas) k_policy(ftmoe_policy_args a, int part_pieces, int further,
+template <typename T, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, kMinWarps / WARPS) k_policy(ftmoe_policy_args a, int part_pieces, int further,
                                                                uint32_t* status) {
   extern __shared__ __align__(128) unsigned char policy_smem[];
-  __shared__ uint64_t bars[kWarps][kMaxChunks];
+  __shared__ uint64_t bars[WARPS][kMaxChunks];
   __shared__ uint64_t meet[2], ask[2];
   __shared__ __align__(16) uint4 response[2];
-  __shared__ MaxSum exchange[2][kMaxRanks * kWarps];
+  __shared__ MaxSum exchange[2][kMaxRanks * WARPS];
   constexpr int N = Row<T>::N;
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), log2_ranks = 31 - __clz(ranks);
@@ -443,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_policy(ftmoe_policy_args
   fence_mbar_init();
   __syncwarp();
   uint32_t round = 0;  // rows met so far: slot and phase of what the cluster shares
-  auto part_of = [&](int64_t n) { return w.part_of(n, log2_ranks, rank, kWarps, warp); };
+  auto part_of = [&](int64_t n) { return w.part_of(n, log2_ranks, rank, WARPS, warp); };
 
   bool more = true;
   Part<T> p = part_of(blockIdx.x >> log2_ranks);  // the grid has no more clusters than rows
@@ -463,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_policy(ftmoe_policy_args
   while (more && w.ok) {
     const uint32_t slot = round & 1, turn = round >> 1 & 1;
     if (threadIdx.x == 0) {
-      mbar_arrive_expect_tx(meet + slot, (uint32_t)(ranks * kWarps * sizeof(MaxSum)));
+      mbar_arrive_expect_tx(meet + slot, (uint32_t)(ranks * WARPS * sizeof(MaxSum)));
       if (a.dlogits && further) ask_into(slot);
     }
     // The next row: its number, and its inputs on their way.
@@ -505,11 +504,11 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_policy(ftmoe_policy_args
     // Every warp tells every CTA.  Two sets of slots suffice: a warp sends
     // into a set again two rows on, when it has heard in the next row from
     // every warp of the cluster, each after its reads here.
-    static_assert(kMaxRanks * kWarps <= 32, "a lane a sender");
+    static_assert(kMaxRanks * WARPS <= 32, "a lane a sender");
     run = warp_join(run, w.k2);
-    if (lane < ranks) send(run, &exchange[slot][rank * kWarps + warp], meet + slot, lane);
+    if (lane < ranks) send(run, &exchange[slot][rank * WARPS + warp], meet + slot, lane);
     w.ok = mbar_wait(meet + slot, turn, status) && w.ok;
-    run = warp_join(lane < ranks * kWarps ? exchange[slot][lane] : MaxSum{-FLT_MAX, 0.f}, w.k2);
+    run = warp_join(lane < ranks * WARPS ? exchange[slot][lane] : MaxSum{-FLT_MAX, 0.f}, w.k2);
     if (!w.ok) run.s = NAN;
     ++round;
     float c = 0.f;
@@ -546,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_policy(ftmoe_policy_args
 // Short rows: a warp takes a row, and has the next one on its way in a second
 // buffer while it turns one into its gradient.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, kMinCtas) k_policy_short(ftmoe_policy_args a, int pieces, uint32_t* status) {
+__global__ void __launch_bounds__(kWarps * 32, kMinWarps / kWarps) k_policy_short(ftmoe_policy_args a, int pieces, uint32_t* status) {
   extern __shared__ __align__(128) unsigned char policy_smem[];
   __shared__ uint64_t bars[2][kWarps][kShortChunks];
   constexpr int N = Row<T>::N;
@@ -736,20 +735,28 @@ __global__ void __launch_bounds__(kSumThreads) k_policy_sum(const float* weight,
 
 // A CTA's shared memory for its part of a row, at most; what an SM has for all of them.
 constexpr int kStageMax = 216 * 1024, kSmemSm = 226 * 1024;
-constexpr int kFixedSmem = 3 * 1024;    // of a CTA besides: barriers, exchange slots, the system's own
+constexpr int kFixedSmem = 1280, kWarpSmem = 288;  // of a CTA and of each warp besides: the system's own, barriers, slots
 // Rows up to kShortBytes may be a warp's: 16384 bf16 rows of 4 KB take 37 us so and 80 us as a CTA's, of 16 KB
 // 183 and 127 us.  Up to kShortAlways they are even where that leaves warps idle.
 constexpr int kShortBytes = 8 * 1024, kShortAlways = 2 * 1024;
+// Rows up to here are two warps' instead of four's: 24 KB take 80 and 86 us (8192 rows), 32 KB 109 and 98 us.
+constexpr int kTwoWarpBytes = 24 * 1024;
 
 }  // namespace
+
+static_assert(kShortBytes / 16 + 2 <= kShortChunks * kChunk, "a short row's chunks have barriers");
+static_assert(kStageMax / 16 / kWarps <= kMaxChunks * kChunk && kMaxChunks <= 32, "a part's chunks have barriers and phases");
 
 cudaError_t policy_set_limits() {
   cudaError_t e = cudaSuccess;
   auto set = [&](auto type) {
     using T = decltype(type);
-    const cudaError_t r = cudaFuncSetAttribute(k_policy_short<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageMax);
-    if (r != cudaSuccess) return r;
-    return cudaFuncSetAttribute(k_policy<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageMax);
+    for (const void* k :
+         {(const void*)k_policy_short<T>, (const void*)k_policy<T, 2>, (const void*)k_policy<T, kWarps>}) {
+      const cudaError_t r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageMax);
+      if (r != cudaSuccess) return r;
+    }
+    return cudaSuccess;
   };
   for (int t : {FTMOE_BF16, FTMOE_FP32, FTMOE_FP16})
     if ((e = with_dtype(t, set)) != cudaSuccess) return e;
@@ -758,21 +765,26 @@ cudaError_t policy_set_limits() {
 
 cudaError_t launch_policy_loss(const TrainDevice& d, const ftmoe_policy_args& a, cudaStream_t s) {
   if (a.N > 0) {
-    const int bytes = dtype_bytes(a.dtype);
-    const int64_t pieces = (a.V * bytes + 15 + 14) / 16;  // of a row at any alignment, at most
-    auto part = [&](int ranks) { return ((pieces + ranks - 1) / ranks + kWarps - 1) / kWarps; };  // a warp's pieces
-    auto cta_bytes = [&](int ranks) { return part(ranks) * kWarps * 16; };
-    auto resident = [&](int64_t smem) { return std::min<int64_t>(kMinCtas, kSmemSm / (smem + kFixedSmem)); };
-    const bool is_short = pieces * 16 <= kShortBytes && (pieces * 16 <= kShortAlways || a.N >= 8 * d.num_sms);
+    const int64_t pieces = (a.V * dtype_bytes(a.dtype) + 15 + 14) / 16;  // of a row at any alignment, at most
+    const int64_t bytes = pieces * 16;
+    const bool many = a.N >= 8 * d.num_sms;
+    const bool is_short = bytes <= kShortBytes && (bytes <= kShortAlways || many);
+    const int warps = !is_short && many && bytes <= kTwoWarpBytes ? 2 : kWarps;
+    auto part = [&](int ranks) { return ((pieces + ranks - 1) / ranks + warps - 1) / warps; };  // a warp's pieces
+    auto cta_bytes = [&](int ranks) { return part(ranks) * warps * 16; };
+    auto resident = [&](int64_t smem) {
+      return std::min<int64_t>(kMinWarps / warps, kSmemSm / (smem + kFixedSmem + warps * kWarpSmem));
+    };
     // The ranks that have most of an SM's shared memory in use; of (nearly) equals, the most, whose CTAs are more.
     int ranks = 1;
-    for (int r = 2; r <= kMaxRanks; r *= 2)
+    for (int r = 2; r <= kMaxRanks && warps == kWarps; r *= 2)
       if (cta_bytes(r) * resident(cta_bytes(r)) >= cta_bytes(ranks) * resident(cta_bytes(ranks)) * 98 / 100) ranks = r;
     // few rows: spread each over more CTAs while the SMs are not full and a part has work for its warps
-    while (ranks < kMaxRanks && a.N * ranks < 2 * d.num_sms && cta_bytes(ranks) >= 2 * kThreads * 16) ranks *= 2;
+    while (ranks < kMaxRanks && a.N * ranks < 2 * d.num_sms && cta_bytes(ranks) >= 8192) ranks *= 2;
     if (cta_bytes(ranks) > kStageMax) ranks = kMaxRanks;
     const int64_t smem = is_short ? pieces * 2 * kWarps * 16 : cta_bytes(ranks);
-    const bool staged = smem <= kStageMax;
+    // a part has a barrier for each chunk, so it has kMaxChunks of them at most
+    const bool staged = smem <= kStageMax && (is_short || part(ranks) <= kMaxChunks * kChunk);
     if (is_short) ranks = 1;
     cudaLaunchConfig_t c{};
     c.stream = s;
@@ -782,7 +794,7 @@ cudaError_t launch_policy_loss(const TrainDevice& d, const ftmoe_policy_args& a,
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     c.attrs = at;
     c.numAttrs = 1;
-    c.blockDim = dim3(staged ? kThreads : kLongThreads);
+    c.blockDim = dim3(staged ? warps * 32 : kLongThreads);
     c.dynamicSmemBytes = staged ? (size_t)smem : 0;
     const int64_t want = is_short ? (a.N + kWarps - 1) / kWarps : a.N;
     // short rows: as many warps as fit; long ones: a cluster a row, of which those that run take the rest over
@@ -793,7 +805,8 @@ cudaError_t launch_policy_loss(const TrainDevice& d, const ftmoe_policy_args& a,
       using T = decltype(type);
       if (!staged) return cudaLaunchKernelEx(&c, k_policy_long<T>, a, d.status);
       if (is_short) return cudaLaunchKernelEx(&c, k_policy_short<T>, a, (int)pieces, d.status);
-      return cudaLaunchKernelEx(&c, k_policy<T>, a, (int)part(ranks), further, d.status);
+      const auto k = warps == 2 ? k_policy<T, 2> : k_policy<T, kWarps>;
+      return cudaLaunchKernelEx(&c, k, a, (int)part(ranks), further, d.status);
     });
     if (e != cudaSuccess) return e;
   }

@@ -473,8 +473,10 @@ def policy_check(i, outs, dtype, temperature=1.0, clip_low=0.2, clip_high=0.2, k
         de = e * (dl + 2 * EPS * (4 + t.abs()))
         ref_row, drow = ref_row + b * (e - t - 1), drow + b * (de + dl + 4 * EPS * (e + t.abs() + 1))
         c, dc = c + b * (1 - e), dc + b * (de + 4 * EPS * (e + 1))
-    near = (r - cl).abs() <= 2 * dr  # a ratio at the bound may fall on either side
-    assert int((near & clipped).sum()) == 0
+    # a ratio within its error of a corner may fall on either side: the row is the same there, its slope either's
+    corner = torch.minimum((r - (1 - lo)).abs(), (r - (1 + hi)).abs()) <= 2 * dr
+    assert int(corner.sum()) <= 1 + N // 100
+    dc = dc + torch.where(corner, r * A.abs(), 0.0)
     ref_row, drow = torch.where(use, ref_row, 0.0), torch.where(use, drow, 0.0)
     within(row, ref_row, drow)
     within(loss[0], (w * ref_row).sum(), (w.abs() * drow).sum() + 4 * EPS * (w * ref_row).abs().sum())
@@ -915,3 +917,14 @@ def test_adamw_past_32_bits():
         if torch.is_tensor(v):
             assert torch.equal(big[k][start // 256 if "scale" in k else start:], v), k
     assert not big["p"][:start:99_991].any() and not big["v"][:start:99_991].any()
+
+
+@pytest.mark.parametrize("N,V,dtype", [(1300, 4500, BF16), (1217, 6001, FP32), (1250, 12007, FP16)])
+def test_policy_loss_rows_of_two_warps(N, V, dtype):
+    """Many rows of 8 to 24 KB: two warps a row, several rows a CTA in turn."""
+    i = policy_inputs(90 + V, N, V, dtype, 0.3)
+    kw = dict(temperature=1.1, kl_coef=0.05)
+    policy_check(i, policy(i, **kw), dtype, **kw)
+    a, b = policy(i, grad=False, **kw), policy(i, **kw)
+    for x, y in zip(a[:3], b[:3]):
+        assert torch.equal(x, y)
