@@ -103,7 +103,8 @@ int ftmoe_combine_backward(const void* dout, const void* ys, int dtype, int T, i
   if (!pair_sizes(dtype, T, H, top_k)) return FTMOE_ERR_INVALID_ARG;
   if (T == 0) return FTMOE_OK;
   if (!dout || !ys || !inv || !w || !dys || !dw || dys == dout) return FTMOE_ERR_INVALID_ARG;
-  if (!on(dout, 16) || !on(ys, 16) || !on(dys, 16) || !on(inv, 4) || !on(w, 4) || !on(dw, 4)) return FTMOE_ERR_ALIGNMENT;
+  if (!on(dout, 16) || !on(ys, 16) || !on(dys, 16) || !on(inv, 4) || !on(w, 4) || !on(dw, 4))
+    return FTMOE_ERR_ALIGNMENT;
   TrainDevice d;
   if (const int rc = current_device(&d)) return rc;
   return launched(launch_combine_backward(d, dout, ys, dtype, T, H, top_k, inv, w, dys, dw, (cudaStream_t)stream),
@@ -115,7 +116,8 @@ int ftmoe_route_backward(const float* logits, const int32_t* topk_idx, const flo
   if (T < 0 || E < 1 || E > kMaxBins || top_k < 1 || top_k > 32 || top_k > E) return FTMOE_ERR_INVALID_ARG;
   if (T == 0) return FTMOE_OK;
   if (!topk_idx || !topk_w || !dw || !dlogits || (!norm_topk_prob && !logits)) return FTMOE_ERR_INVALID_ARG;
-  if (!on(logits, 4) || !on(topk_idx, 4) || !on(topk_w, 4) || !on(dw, 4) || !on(dlogits, 4)) return FTMOE_ERR_ALIGNMENT;
+  if (!on(logits, 4) || !on(topk_idx, 4) || !on(topk_w, 4) || !on(dw, 4) || !on(dlogits, 4))
+    return FTMOE_ERR_ALIGNMENT;
   TrainDevice d;
   if (const int rc = current_device(&d)) return rc;
   return launched(launch_route_backward(d, logits, topk_idx, topk_w, dw, T, E, top_k, norm_topk_prob, dlogits,
@@ -136,7 +138,8 @@ int ftmoe_embed(const void* table, int dtype, int64_t V, int H, const void* ids,
   if (!on(table, 16) || !on(out, 16) || !on(ids, id_bytes)) return FTMOE_ERR_ALIGNMENT;
   TrainDevice d;
   if (const int rc = current_device(&d)) return rc;
-  return launched(launch_embed(d, table, dtype, V, H, ids, id_bytes, N, scale, out, (cudaStream_t)stream), "ftmoe_embed");
+  return launched(launch_embed(d, table, dtype, V, H, ids, id_bytes, N, scale, out, (cudaStream_t)stream),
+                  "ftmoe_embed");
 }
 
 int64_t ftmoe_embed_workspace(int64_t N, int H) {
@@ -151,7 +154,8 @@ int ftmoe_embed_backward(const void* dout, int dtype, const void* ids, int id_by
   if (table_dtype != dtype && table_dtype != FTMOE_FP32) return FTMOE_ERR_INVALID_ARG;
   if (accumulate && table_dtype != FTMOE_FP32) return FTMOE_ERR_INVALID_ARG;
   if (!dtable || dtable == dout) return FTMOE_ERR_INVALID_ARG;
-  if (N > 0 && (!dout || !ids || !workspace || workspace_bytes < embed_workspace(N, H).bytes)) return FTMOE_ERR_INVALID_ARG;
+  if (N > 0 && (!dout || !ids || !workspace || workspace_bytes < embed_workspace(N, H).bytes))
+    return FTMOE_ERR_INVALID_ARG;
   if (!on(dout, 16) || !on(dtable, 16) || !on(workspace, 16) || !on(ids, id_bytes)) return FTMOE_ERR_ALIGNMENT;
   TrainDevice d;
   if (const int rc = current_device(&d)) return rc;
@@ -167,7 +171,8 @@ int ftmoe_policy_loss(const ftmoe_policy_args* a, ftmoe_stream_t stream) {
       !std::isfinite(a->kl_coef) || !std::isfinite(a->grad_scale))
     return FTMOE_ERR_INVALID_ARG;
   if (!a->loss) return FTMOE_ERR_INVALID_ARG;
-  if (a->N > 0 && (!a->logits || !a->targets || !a->old_logp || !a->advantage || !a->row_loss)) return FTMOE_ERR_INVALID_ARG;
+  if (a->N > 0 && (!a->logits || !a->targets || !a->old_logp || !a->advantage || !a->row_loss))
+    return FTMOE_ERR_INVALID_ARG;
   if (a->dlogits && a->ld_d < a->V) return FTMOE_ERR_INVALID_ARG;
   if (a->dlogits == a->logits && a->dlogits && a->ld_d != a->ld) return FTMOE_ERR_INVALID_ARG;
   const int b = bytes_of(a->dtype);
@@ -196,7 +201,8 @@ int ftmoe_adamw(const ftmoe_adamw_tensor* tensors, int n, const ftmoe_adamw_para
     if (t.master && t.p_dtype == FTMOE_FP32) return FTMOE_ERR_INVALID_ARG;
     if (t.n == 0) continue;
     any = true;
-    if (!t.p || !t.g || !t.m || !t.v || (t.state_bits == 8 && (!t.m_scale || !t.v_scale))) return FTMOE_ERR_INVALID_ARG;
+    if (!t.p || !t.g || !t.m || !t.v || (t.state_bits == 8 && (!t.m_scale || !t.v_scale)))
+      return FTMOE_ERR_INVALID_ARG;
     const int sb = t.state_bits / 8;
     if (!on(t.p, bytes_of(t.p_dtype)) || !on(t.g, bytes_of(t.g_dtype)) || !on(t.master, 4) || !on(t.m, sb) ||
         !on(t.v, sb) || !on(t.m_scale, 4) || !on(t.v_scale, 4))
@@ -211,10 +217,13 @@ int ftmoe_adamw(const ftmoe_adamw_tensor* tensors, int n, const ftmoe_adamw_para
 int ftmoe_ops_status(ftmoe_stream_t stream) {
   TrainDevice d;
   if (const int rc = current_device(&d)) return rc;
+  const cudaStream_t s = (cudaStream_t)stream;
   uint32_t st = 0;
-  cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
-  if (e == cudaSuccess) e = cudaMemcpy(&st, d.status, 4, cudaMemcpyDeviceToHost);
-  if (e == cudaSuccess) e = cudaMemset(d.status, 0, 4);
+  cudaError_t e = cudaStreamSynchronize(s);
+  // on the stream itself: what it runs next marks a word that has been cleared
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&st, d.status, 4, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(d.status, 0, 4, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return launched(e, "ftmoe_ops_status");
   if (st & kStatusTimeout) return FTMOE_ERR_TIMEOUT;
   return st & kStatusRange ? FTMOE_ERR_DEVICE_CHECK : FTMOE_OK;
