@@ -56,7 +56,8 @@ class Model:
         P = T * k
         i32 = lambda n: new(n, dtype=torch.int32)
         f32 = lambda *s: new(*s, dtype=torch.float32)
-        self.x, self.y, self.xs, self.ys, self.dxs, self.dx = new(T, H), new(T, H), new(P, H), new(P, H), new(P, H), new(T, H)
+        self.x, self.y, self.dx = new(T, H), new(T, H), new(T, H)
+        self.xs, self.ys, self.dxs = new(P, H), new(P, H), new(P, H)
         self.idx, self.w, self.dw, self.droute = new(T, k, dtype=torch.int32), f32(T, k), f32(T, k), f32(T, E)
         self.offsets, self.perm, self.inv = i32(E + 1), i32(P), i32(P)
         self.loss, self.row_loss, self.logp, self.dlogits = f32(1), f32(T), f32(T), new(T, V)

@@ -453,15 +453,16 @@ int ftmoe_dispatch(const void* x, int dtype, int T, int H, const int32_t* topk_i
 
 /* out[t] = sum_j w[t][j] * ys[inv[t*top_k + j]] over the kept slots, in slot
  * order; a token without one gets zeros.  w: fp32 [T, top_k], or NULL for
- * weights of one.  Rows of dropped slots are not read.  A place outside
- * [-1, T*top_k) counts as dropped and marks the status word.
+ * weights of one.  A place outside [-1, T*top_k) counts as dropped and marks
+ * the status word.  ys: [T*top_k, H], whose rows of no pair may hold anything;
  * ys, out: `dtype`, 16-byte aligned, not the same. */
 int ftmoe_combine(const void* ys, int dtype, int T, int H, int top_k, const int32_t* inv, const float* w, void* out,
                   ftmoe_stream_t stream);
 
 /* ftmoe_combine's gradient: dys[inv[p]] = w[p] * dout[t] (rows that no kept
  * pair has stay as they were) and dw[p] = <dout[t], ys[inv[p]]>, 0 for a
- * dropped pair.  dys may be ys itself (the rows are replaced). */
+ * dropped pair.  ys and dys: [T*top_k, H]; dys may be ys itself (the rows are
+ * replaced).  Places out of range as for ftmoe_combine. */
 int ftmoe_combine_backward(const void* dout, const void* ys, int dtype, int T, int H, int top_k, const int32_t* inv,
                            const float* w, void* dys, float* dw, ftmoe_stream_t stream);
 

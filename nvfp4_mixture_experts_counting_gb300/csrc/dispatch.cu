@@ -18,7 +18,7 @@ constexpr int kThreads = 256;
 // Pairs up to which every CTA counts its own tokens' places (one launch): at
 // 2048 pairs that takes 4.5 us with the copy, the sort 4.4 us without it; at 4096 7.5 and 4.5 us.
 constexpr int kCountPairs = 2048;
-constexpr int kSlots = 4;  // slots of the combine that a thread has in flight
+constexpr int kSlots = 4;      // slots of the combine that a thread has in flight
 constexpr int kBackSlots = 8;  // and of its gradient
 
 struct DispatchArgs {
@@ -76,7 +76,8 @@ __device__ void dispatch_tables(const DispatchArgs& a) {
 // Few pairs: one launch.  CTA t counts the places of token t's slots itself
 // (a warp per slot reads all P indices; e_q < e_p + [q < p] is the test for
 // "sorts before", and as unsigned values dropped pairs never pass it), then
-// copies the row.  The first CTA writes the tables.
+// copies the row.  The first CTA writes the tables.  Latency bounds it: 2.6 us at
+// T=16 k=8 H=2560 bf16, of which a launch takes 1.7.
 template <int B>
 __global__ void __launch_bounds__(kThreads) k_dispatch_count(DispatchArgs a, const void* x, int nv, void* xs) {
   using V = typename Raw<B>::type;
@@ -153,7 +154,8 @@ __global__ void __launch_bounds__(THREADS) k_dispatch_sort(DispatchArgs a) {
 }
 
 // ... and the copy: each thread reads Q pieces of a token's row, nq apart, and
-// writes them to the row's k places.
+// writes them to the row's k places.  Bound by the writes: T=16384 k=8 H=2560
+// bf16 110 us, 6.9 TB/s.  The rows are asked for before the sort is done.
 template <int B, int Q>
 __global__ void __launch_bounds__(kThreads) k_dispatch_copy(const void* x, int64_t total, int nv, int nq, int k,
                                                             const int32_t* inv, void* xs) {
@@ -194,8 +196,9 @@ __device__ __forceinline__ int checked_place(int at, int64_t P, uint32_t* status
 // copy rate with as many warps an SM as registers allow without spills: 48 with
 // weights (111 us; 64 take 125, 40 take 136), 64 without (111 us; 48 take 122).
 template <typename T, int N, int Q, bool WEIGHTED>
-__global__ void __launch_bounds__(kThreads, N == 1 ? 1 : WEIGHTED ? 6 : 8) k_combine(const T* ys, int64_t total, int nv, int nq, int k, int64_t P,
-                                                      const int32_t* inv, const float* w, T* out, uint32_t* status) {
+__global__ void __launch_bounds__(kThreads, N == 1 ? 1 : WEIGHTED ? 6 : 8)
+    k_combine(const T* ys, int64_t total, int nv, int nq, int k, int64_t P, const int32_t* inv, const float* w, T* out,
+              uint32_t* status) {
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= total) return;
   const int64_t t = quotient(i, nq);
@@ -242,11 +245,12 @@ __global__ void __launch_bounds__(kThreads, N == 1 ? 1 : WEIGHTED ? 6 : 8) k_com
 // dys[inv[p]] = w[p] dout[t], dw[p] = <dout[t], ys[inv[p]]>: W warps take a
 // token's row, kBackSlots slots at a time, whose loads are issued together (as
 // in k_combine).  dys may be ys: a thread reads an element before it writes it,
-// and no other thread touches it.
+// and no other thread uses it.  Every byte moves once: T=16384 k=8 H=2560 bf16
+// 211 us, 6.8 TB/s, with 24 warps an SM (four slots and 32 warps: 239 us).
 template <typename T, int N, int Q, int W>
-__global__ void __launch_bounds__(kThreads, 3) k_combine_backward(const T* dout, const T* ys, int T_, int nv, int k,
-                                                               int64_t P, const int32_t* inv, const float* w, T* dys,
-                                                               float* dw, uint32_t* status) {
+__global__ void __launch_bounds__(kThreads, 3)
+    k_combine_backward(const T* dout, const T* ys, int T_, int nv, int k, int64_t P, const int32_t* inv, const float* w,
+                       T* dys, float* dw, uint32_t* status) {
   __shared__ float part[kThreads / 32][kBackSlots];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % W;
   const int64_t t = (int64_t)blockIdx.x * (kThreads / 32 / W) + warp / W;
@@ -316,7 +320,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_combine_backward(const T* dout,
 //   renormalised weights:   dlogits[e] = sum_{j : idx_j = e} w_j (dw_j - S)
 //   full-softmax weights:   dlogits[e] = p_e (sum_{j : idx_j = e} dw_j - S)
 // The row is first written as if no expert were chosen (zeros, or -p_e S),
-// then the chosen experts' values over it, each by the lane of its first slot.
+// then the chosen experts' values over it, each by the lane of its first slot
+// (6 us at T=16384 E=256 k=8; every expert compared with every slot took 12).
 template <bool NORM, int N>
 __global__ void __launch_bounds__(kThreads) k_route_backward(const float* logits, const int32_t* idx, const float* w,
                                                              const float* dw, int T, int E, int k, float* dlogits,
@@ -381,8 +386,8 @@ cudaError_t dispatch_set_limits(int* sort_ctas) {
   return e != cudaSuccess ? e : cluster_sort_limits(k_dispatch_sort<1024>, 1024, kMaxBins, sort_ctas);
 }
 
-cudaError_t launch_dispatch(const TrainDevice& d, const void* x, int row_bytes, int T, const int32_t* topk_idx, int top_k,
-                            int E, int32_t* offsets, int32_t* perm, int32_t* inv, void* xs, cudaStream_t s) {
+cudaError_t launch_dispatch(const TrainDevice& d, const void* x, int row_bytes, int T, const int32_t* topk_idx,
+                            int top_k, int E, int32_t* offsets, int32_t* perm, int32_t* inv, void* xs, cudaStream_t s) {
   const DispatchArgs a{topk_idx, T, top_k, E, T * top_k, offsets, perm, inv, d.status};
   const int B = access_bytes(row_bytes), nv = row_bytes / B;
   if (a.P <= kCountPairs) {
@@ -462,7 +467,8 @@ cudaError_t launch_route_backward(const TrainDevice& d, const float* logits, con
                                   const float* topk_w, const float* dw, int T, int E, int top_k, int norm,
                                   float* dlogits, cudaStream_t s) {
   auto launch = [&](auto kernel) {
-    kernel<<<blocks_of(T, kThreads / 32), kThreads, 0, s>>>(logits, topk_idx, topk_w, dw, T, E, top_k, dlogits, d.status);
+    kernel<<<blocks_of(T, kThreads / 32), kThreads, 0, s>>>(logits, topk_idx, topk_w, dw, T, E, top_k, dlogits,
+                                                            d.status);
   };
   const bool wide = E % 4 == 0 && ((uintptr_t)dlogits & 15) == 0;
   if (norm) launch(wide ? k_route_backward<true, 4> : k_route_backward<true, 1>);

@@ -27,10 +27,13 @@ constexpr int kLongRun = 16;   // chunks from which a run's sum is shared by a C
 inline int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 inline unsigned blocks_of(int64_t n, int per) { return (unsigned)((n + per - 1) / per); }
 
-// A thread takes Q pieces of a token's row, nq apart.
+// A thread takes Q pieces of a token's row, nq apart: two 16-byte loads in
+// flight bring N=16384 H=2560 bf16 from 28 to 22 us (the copy rate), and rows of
+// odd widths, which move value by value, take eight.
 template <typename T, int N, int Q, typename Id>
-__global__ void __launch_bounds__(kThreads) k_embed(const T* table, int64_t V, int nv, int nq, const Id* ids, int64_t total,
-                                                    float scale, T* out, uint32_t* status) {
+__global__ void __launch_bounds__(kThreads)
+    k_embed(const T* table, int64_t V, int nv, int nq, const Id* ids, int64_t total, float scale, T* out,
+            uint32_t* status) {
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= total) return;
   const int64_t n = quotient(i, nq);
@@ -55,9 +58,9 @@ __global__ void __launch_bounds__(kThreads) k_embed(const T* table, int64_t V, i
 // keys[final] sorted, pos[final] the tokens in that order.  A token whose id
 // is the padding id or out of range gets key V, so it sorts behind all others.
 template <typename Id>
-__global__ void __launch_bounds__(kSortThreads) k_embed_sort(const Id* ids, int64_t N, int64_t V, int64_t padding_id,
-                                                                int passes, int digit, int32_t* k0, int32_t* k1,
-                                                                int32_t* p0, int32_t* p1, uint32_t* status) {
+__global__ void __launch_bounds__(kSortThreads)
+    k_embed_sort(const Id* ids, int64_t N, int64_t V, int64_t padding_id, int passes, int digit, int32_t* k0,
+                 int32_t* k1, int32_t* p0, int32_t* p1, uint32_t* status) {
   extern __shared__ int sort_smem[];
   pdl_launch_dependents();
   bool bad = false;
@@ -73,7 +76,8 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const Id* ids, int6
       return SortItem{in && id != padding_id ? (int)id : (int)V, (int)i};
     };
     cluster_sort<kSortThreads>(
-        N, 1 << digit, sort_smem, pass == passes - 1, load, [&](int key) { return (key >> shift) & ((1 << digit) - 1); },
+        N, 1 << digit, sort_smem, pass == passes - 1, load,
+        [&](int key) { return (key >> shift) & ((1 << digit) - 1); },
         [&](int64_t, SortItem item, int at) {
           dst_k[at] = item.key;
           dst_p[at] = item.value;
@@ -101,17 +105,14 @@ struct GradArgs {
 };
 
 template <typename TT, int N>
-__device__ __forceinline__ void write_row(TT* dtable, int64_t at, const float (&acc)[N], float scale, int accumulate) {
+__device__ __forceinline__ void write_row(TT* dtable, int64_t at, const float (&acc)[N], float scale,
+                                          int accumulate) {
   Pack<TT, N> o;
   if (accumulate) o = load_pack<TT, N>(dtable + at);
 #pragma unroll
   for (int c = 0; c < N; ++c) o.set(c, accumulate ? fmaf(scale, acc[c], o.get(c)) : scale * acc[c]);
   store_pack<TT, N>(dtable + at, o);
 }
-
-// A lane takes Q pieces of N values of a slice, 32 pieces apart.  Rows whose
-// bytes are no multiple of 16 move value by value (N = 1), and then Q values a
-// lane keep as many bytes in flight as one piece would.
 
 // Zeros to the rows that no token names.  The CTA looks through all ids itself
 // and marks the rows it meets, so it need not wait for the sort: on the SMs that
@@ -167,8 +168,12 @@ __device__ void fill_unnamed(const GradArgs& a, const Id* ids, int cta, TT* dtab
   }
 }
 
-// A warp sums kChunk sorted tokens over a slice of their rows.  A run that
-// lies inside the chunk goes to its row; pieces of longer runs go to `part`.
+// A warp sums kChunk sorted tokens over a slice of their rows, kAhead rows in
+// flight.  A run that lies inside the chunk goes to its row; pieces of longer
+// runs go to `part`.  A lane takes Q pieces of N values of the slice, 32 pieces
+// apart; rows whose bytes are no multiple of 16 move value by value (N = 1), two
+// a lane.  Together with the rows of zeros it is bound by DRAM writes: N=16384
+// V=131072 H=2560 bf16 118 us for 755 MB.
 template <typename T, typename TT, int N, int Q>
 __global__ void __launch_bounds__(kThreads, 4) k_embed_grad(GradArgs a, const T* dout, TT* dtable) {
   const int lane = threadIdx.x & 31;
@@ -216,7 +221,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_embed_grad(GradArgs a, const T*
       }
       if (!end && after == k) continue;
       // the run ends here, or leaves the chunk
-      float* part = head && prev == k ? a.part + 2 * chunk * H : end && next == k ? a.part + (2 * chunk + 1) * H : nullptr;
+      float* part = head && prev == k  ? a.part + 2 * chunk * H
+                    : end && next == k ? a.part + (2 * chunk + 1) * H
+                                       : nullptr;
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const int64_t at = (int64_t)(v + q * 32) * N;
@@ -254,7 +261,7 @@ __device__ __forceinline__ void sum_pieces(const GradArgs& a, int64_t from, int6
 // kWarps chunks, warp w the run that begins in chunk w and goes on: its pieces
 // are added in order.  A run of over kLongRun chunks (text has tokens that make
 // up much of it) is summed by all warps: warp w takes every kWarps-th chunk,
-// then the warps' sums are added in order.
+// then the warps' sums are added in order.  Latency bounds it (some 6 us).
 template <typename TT, int N>
 __global__ void __launch_bounds__(kThreads) k_embed_join(GradArgs a, TT* dtable, int slices) {
   __shared__ float sums[kWarps][32 * N];
@@ -373,11 +380,13 @@ cudaError_t launch_embed_backward(const TrainDevice& d, const void* dout, int dt
   cudaError_t e = cudaSuccess;
   if (N > 0) {
     if (id_bytes == 8)
-      e = launch_cluster_sort(d, k_embed_sort<int64_t>, kSortThreads, N, 1 << digit, s, static_cast<const int64_t*>(ids), N, V,
-                              padding_id, passes, digit, keys[0], keys[1], pos[0], pos[1], d.status);
+      e = launch_cluster_sort(d, k_embed_sort<int64_t>, kSortThreads, N, 1 << digit, s,
+                              static_cast<const int64_t*>(ids), N, V, padding_id, passes, digit, keys[0], keys[1],
+                              pos[0], pos[1], d.status);
     else
-      e = launch_cluster_sort(d, k_embed_sort<int32_t>, kSortThreads, N, 1 << digit, s, static_cast<const int32_t*>(ids), N, V,
-                              padding_id, passes, digit, keys[0], keys[1], pos[0], pos[1], d.status);
+      e = launch_cluster_sort(d, k_embed_sort<int32_t>, kSortThreads, N, 1 << digit, s,
+                              static_cast<const int32_t*>(ids), N, V, padding_id, passes, digit, keys[0], keys[1],
+                              pos[0], pos[1], d.status);
     if (e != cudaSuccess) return e;
   }
   const int last = (passes - 1) & 1;

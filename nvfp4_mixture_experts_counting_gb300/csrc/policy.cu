@@ -19,14 +19,14 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMinWarps = 24;  // an SM holds at least, by registers
-constexpr int kWarps = 4;      // of a CTA (k_policy: at most)
-constexpr int kMaxRanks = 8;   // CTAs of a cluster
-constexpr int kUnroll = 4;     // 16-byte pieces a lane sums at a time
-constexpr int kChunk = 256;    // 16-byte pieces of one bulk copy
-constexpr int kMaxChunks = 16; // of a warp's part
-constexpr int kShortChunks = 8;  // of a short row
-constexpr int kLag = 1;        // chunks between a gradient's departure and the reuse of its buffer
+constexpr int kMinWarps = 24;    // an SM holds at least, by registers
+constexpr int kWarps = 4;        // of a CTA (k_policy: at most)
+constexpr int kMaxRanks = 8;     // CTAs of a cluster
+constexpr int kUnroll = 4;       // 16-byte pieces a lane sums at a time
+constexpr int kChunk = 256;      // 16-byte pieces of one bulk copy
+constexpr int kMaxChunks = 16;   // of a warp's part
+constexpr int kShortChunks = 2;  // of a short row
+constexpr int kLag = 1;          // chunks between a gradient's departure and the reuse of its buffer
 constexpr int kLongThreads = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -250,8 +250,8 @@ __device__ __forceinline__ void send(MaxSum v, MaxSum* slot, uint64_t* bar, int 
   uint32_t at, at_bar;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(slot)), "r"(to));
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at_bar) : "r"(smem_u32(bar)), "r"(to));
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(at), "l"(pack2(v.m, v.s)),
-               "r"(at_bar)
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(at),
+               "l"(pack2(v.m, v.s)), "r"(at_bar)
                : "memory");
 }
 
@@ -259,8 +259,8 @@ __device__ __forceinline__ void send(MaxSum v, MaxSum* slot, uint64_t* bar, int 
 // index, or none, arrives in every CTA of this cluster.
 __device__ __forceinline__ void ask_for_row(void* response, uint64_t* bar) {
   asm volatile(
-      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 [%0], "
-      "[%1];" ::"r"(smem_u32(response)),
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 "
+      "[%0], [%1];" ::"r"(smem_u32(response)),
       "r"(smem_u32(bar))
       : "memory");
 }
@@ -304,7 +304,8 @@ struct Worker {
   bool ok = true;       // no wait has run out
 
   __device__ Worker(const ftmoe_policy_args& args, int lane_, uint32_t* status_, Pack<T, N>* buf_, uint64_t* bar_)
-      : a(args), lane(lane_), status(status_), inv_t(1.f / args.temperature), k2(kLog2e / args.temperature), buf(buf_), bar(bar_) {}
+      : a(args), lane(lane_), status(status_), inv_t(1.f / args.temperature), k2(kLog2e / args.temperature), buf(buf_),
+        bar(bar_) {}
   __device__ __forceinline__ T* vals() const { return reinterpret_cast<T*>(buf); }
 
   // The part of row n that is number `index` of 2^log2_parts * per_cta parts (CTA by CTA).
@@ -358,7 +359,8 @@ struct Worker {
     return r;
   }
   // The part's gradient c (onehot - softmax), softmax z = 2^((x - m) k2 - ls),
-  // in place and from there to dlogits; `left(j)` (one lane) once the copies up to chunk j are under way.
+  // in place and from there to dlogits; `left(j)` (one lane) once the copies up to
+  // chunk j are under way.
   template <typename F>
   __device__ __forceinline__ void gradient(const Part<T>& p, float m, float ls, float c, float zy, F left) const {
     const Row<T> g(static_cast<T*>(a.dlogits) + p.in.n * a.ld_d, (int)a.V);
@@ -419,10 +421,10 @@ struct Worker {
 // gradient has left its buffer (without a gradient: as soon as it is summed)
 // the next row's chunk is asked for.  Clusters take further rows from those not
 // launched yet, so rows of weight 0, which cost half or nothing, leave no SM
-// idle.  N=4096 V=131072 bf16: 302 us, 94% of the copy rate.
+// idle.  Memory bounds it: N=4096 V=131072 bf16 296 us, 96% of the copy rate.
 template <typename T, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, kMinWarps / WARPS) k_policy(ftmoe_policy_args a, int part_pieces, int further,
-                                                               uint32_t* status) {
+__global__ void __launch_bounds__(WARPS * 32, kMinWarps / WARPS)
+    k_policy(ftmoe_policy_args a, int part_pieces, int further, uint32_t* status) {
   extern __shared__ __align__(128) unsigned char policy_smem[];
   __shared__ uint64_t bars[WARPS][kMaxChunks];
   __shared__ uint64_t meet[2], ask[2];
@@ -545,7 +547,8 @@ __global__ void __launch_bounds__(WARPS * 32, kMinWarps / WARPS) k_policy(ftmoe_
 // Short rows: a warp takes a row, and has the next one on its way in a second
 // buffer while it turns one into its gradient.
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32, kMinWarps / kWarps) k_policy_short(ftmoe_policy_args a, int pieces, uint32_t* status) {
+__global__ void __launch_bounds__(kWarps * 32, kMinWarps / kWarps)
+    k_policy_short(ftmoe_policy_args a, int pieces, uint32_t* status) {
   extern __shared__ __align__(128) unsigned char policy_smem[];
   __shared__ uint64_t bars[2][kWarps][kShortChunks];
   constexpr int N = Row<T>::N;
@@ -613,7 +616,9 @@ __global__ void __launch_bounds__(kWarps * 32, kMinWarps / kWarps) k_policy_shor
   if (!w.ok) w.settle(p);
 }
 
-// Rows too long for a cluster's shared memory: the logits are read a second time.
+// Rows too long for a cluster's shared memory (8 parts of 216 KB): the logits are
+// read a second time.  256 rows of 2^20 values: fp32 528 us, 6.1 TB/s of three
+// moves; bf16 353 us, 4.6 TB/s, where a piece holds twice the exponentials.
 template <typename T>
 __global__ void __launch_bounds__(kLongThreads) k_policy_long(ftmoe_policy_args a, uint32_t* status) {
   __shared__ MaxSum warp_part[kLongThreads / 32];
@@ -691,7 +696,8 @@ struct Sum2 {
   }
 };
 constexpr int kSumThreads = 1024;
-__global__ void __launch_bounds__(kSumThreads) k_policy_sum(const float* weight, const float* row_loss, int64_t N, float* loss) {
+__global__ void __launch_bounds__(kSumThreads)
+    k_policy_sum(const float* weight, const float* row_loss, int64_t N, float* loss) {
   __shared__ Sum2 part[kSumThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
@@ -735,17 +741,22 @@ __global__ void __launch_bounds__(kSumThreads) k_policy_sum(const float* weight,
 
 // A CTA's shared memory for its part of a row, at most; what an SM has for all of them.
 constexpr int kStageMax = 216 * 1024, kSmemSm = 226 * 1024;
-constexpr int kFixedSmem = 1280, kWarpSmem = 288;  // of a CTA and of each warp besides: the system's own, barriers, slots
-// Rows up to kShortBytes may be a warp's: 16384 bf16 rows of 4 KB take 37 us so and 80 us as a CTA's, of 16 KB
-// 183 and 127 us.  Up to kShortAlways they are even where that leaves warps idle.
+// Of a CTA and of each warp besides: the system's own, barriers, slots.
+constexpr int kFixedSmem = 1280, kWarpSmem = 288;
+// Rows up to kShortBytes may be a warp's: 16384 bf16 rows of 4 KB take 37 us so and
+// 80 us as a CTA's, of 16 KB 183 and 127 us.  Up to kShortAlways they are even
+// where that leaves warps idle.
 constexpr int kShortBytes = 8 * 1024, kShortAlways = 2 * 1024;
-// Rows up to here are two warps' instead of four's: 24 KB take 80 and 86 us (8192 rows), 32 KB 109 and 98 us.
+// Rows up to here are two warps' instead of four's: 24 KB take 80 and 86 us (8192
+// rows), 32 KB 109 and 98 us.
 constexpr int kTwoWarpBytes = 24 * 1024;
 
 }  // namespace
 
-static_assert(kShortBytes / 16 + 2 <= kShortChunks * kChunk, "a short row's chunks have barriers");
-static_assert(kStageMax / 16 / kWarps <= kMaxChunks * kChunk && kMaxChunks <= 32, "a part's chunks have barriers and phases");
+static_assert(kShortBytes / 16 <= kShortChunks * kChunk && 2 * kShortChunks <= 32,
+              "a short row's chunks have barriers");
+static_assert(kStageMax / 16 / kWarps <= kMaxChunks * kChunk && kMaxChunks <= 32,
+              "a part's chunks have barriers and phases");
 
 cudaError_t policy_set_limits() {
   cudaError_t e = cudaSuccess;
@@ -775,7 +786,8 @@ cudaError_t launch_policy_loss(const TrainDevice& d, const ftmoe_policy_args& a,
     auto resident = [&](int64_t smem) {
       return std::min<int64_t>(kMinWarps / warps, kSmemSm / (smem + kFixedSmem + warps * kWarpSmem));
     };
-    // The ranks that have most of an SM's shared memory in use; of (nearly) equals, the most, whose CTAs are more.
+    // The ranks that have most of an SM's shared memory in use; of (nearly) equals,
+    // the most, whose CTAs are more.
     int ranks = 1;
     for (int r = 2; r <= kMaxRanks && warps == kWarps; r *= 2)
       if (cta_bytes(r) * resident(cta_bytes(r)) >= cta_bytes(ranks) * resident(cta_bytes(ranks)) * 98 / 100) ranks = r;
@@ -797,8 +809,9 @@ cudaError_t launch_policy_loss(const TrainDevice& d, const ftmoe_policy_args& a,
     c.blockDim = dim3(staged ? warps * 32 : kLongThreads);
     c.dynamicSmemBytes = staged ? (size_t)smem : 0;
     const int64_t want = is_short ? (a.N + kWarps - 1) / kWarps : a.N;
-    // short rows: as many warps as fit; long ones: a cluster a row, of which those that run take the rest over
-    const int64_t room = is_short ? d.num_sms * resident(smem) : staged ? INT32_MAX / ranks : 1 << 24;  // memory ends before
+    // short rows: as many warps as fit; long ones: a cluster a row, of which those that
+    // run take the rest over (memory ends before the grid does)
+    const int64_t room = is_short ? d.num_sms * resident(smem) : staged ? INT32_MAX / ranks : 1 << 24;
     c.gridDim = dim3((unsigned)(std::min(want, room) * ranks));
     const int further = a.N * ranks > d.num_sms;  // else no cluster waits to be launched
     cudaError_t e = with_dtype(a.dtype, [&](auto type) {

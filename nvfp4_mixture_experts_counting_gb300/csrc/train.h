@@ -21,8 +21,8 @@ constexpr int kSortCtas = 16;   // CTAs of the cluster that sorts, at most (8 is
 
 // Tokens sorted by expert and back (dispatch.cu).
 cudaError_t dispatch_set_limits(int* sort_ctas);
-cudaError_t launch_dispatch(const TrainDevice& d, const void* x, int row_bytes, int T, const int32_t* topk_idx, int top_k,
-                            int E, int32_t* offsets, int32_t* perm, int32_t* inv, void* xs, cudaStream_t s);
+cudaError_t launch_dispatch(const TrainDevice& d, const void* x, int row_bytes, int T, const int32_t* topk_idx,
+                            int top_k, int E, int32_t* offsets, int32_t* perm, int32_t* inv, void* xs, cudaStream_t s);
 cudaError_t launch_combine(const TrainDevice& d, const void* ys, int dtype, int T, int H, int top_k, const int32_t* inv,
                            const float* w, void* out, cudaStream_t s);
 cudaError_t launch_combine_backward(const TrainDevice& d, const void* dout, const void* ys, int dtype, int T, int H,
@@ -51,6 +51,7 @@ cudaError_t policy_set_limits();
 cudaError_t launch_policy_loss(const TrainDevice& d, const ftmoe_policy_args& a, cudaStream_t s);
 
 // AdamW (adamw.cu).
-cudaError_t launch_adamw(const TrainDevice& d, const ftmoe_adamw_tensor* list, int n, const ftmoe_adamw_params& hp, cudaStream_t s);
+cudaError_t launch_adamw(const TrainDevice& d, const ftmoe_adamw_tensor* list, int n, const ftmoe_adamw_params& hp,
+                         cudaStream_t s);
 
 }  // namespace ftmoe

@@ -97,7 +97,9 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 
 // Values 2e and 2e + 1 of a piece as fp32, and back.
 template <int N>
-__device__ __forceinline__ uint64_t pair_of(const Pack<float, N>& x, int e) { return pack2(x.v[2 * e], x.v[2 * e + 1]); }
+__device__ __forceinline__ uint64_t pair_of(const Pack<float, N>& x, int e) {
+  return pack2(x.v[2 * e], x.v[2 * e + 1]);
+}
 template <int N>
 __device__ __forceinline__ uint64_t pair_of(const Pack<__nv_bfloat16, N>& x, int e) {
   const uint32_t b = reinterpret_cast<const uint32_t*>(&x)[e];
@@ -109,7 +111,9 @@ __device__ __forceinline__ uint64_t pair_of(const Pack<__half, N>& x, int e) {
   return pack2(f.x, f.y);
 }
 template <int N>
-__device__ __forceinline__ void set_pair(Pack<float, N>& o, int e, uint64_t v) { unpack2(v, o.v[2 * e], o.v[2 * e + 1]); }
+__device__ __forceinline__ void set_pair(Pack<float, N>& o, int e, uint64_t v) {
+  unpack2(v, o.v[2 * e], o.v[2 * e + 1]);
+}
 template <int N>
 __device__ __forceinline__ void set_pair(Pack<__nv_bfloat16, N>& o, int e, uint64_t v) {
   float lo, hi;
