@@ -489,8 +489,9 @@ int64_t ftmoe_embed_workspace(int64_t N, int H);
 
 /* ftmoe_embed's gradient: dtable[v] = scale * (sum over the n with ids[n] = v
  * of dout[n], in the order of n, in fp32).  Rows of no token become zeros;
- * with `accumulate` (fp32 dtable only) the sum is added to dtable and other
- * rows are not touched.  Tokens whose id is padding_id are left out (-1: none
+ * with `accumulate` (fp32 dtable only) the sum is added to dtable, where values
+ * below the smallest normal one may count as zero, and other rows are not
+ * touched.  Tokens whose id is padding_id are left out (-1: none
  * of the valid ids); other ids outside [0, V) are left out and mark the
  * status word.  V up to 2^30.
  *   dout: `dtype` [N, H]; dtable: table_dtype (`dtype` or FTMOE_FP32) [V, H]

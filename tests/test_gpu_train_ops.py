@@ -375,6 +375,22 @@ def test_embed_backward_adds_onto_the_table():
     assert torch.equal(got[free], start[free])
 
 
+@pytest.mark.parametrize("H,dtype", [(64, BF16), (36, torch.float32), (33, torch.float16)])
+@pytest.mark.parametrize("N,V,kind", [(1, 5, "all"), (700, 90, "all"), (3000, 40, "few"), (5000, 7000, "all")])
+def test_embed_backward_adds_runs_of_every_length(N, V, kind, H, dtype):
+    """Vector and single additions, rows of one token, of a chunk's and of many chunks'."""
+    g = gen(N + H)
+    dout, ids, start = randn(g, N, H, dtype=dtype), token_ids(g, N, V, kind), randn(g, V, H)
+    got = embed_backward(dout, ids, V, 0.7, start, accumulate=True)
+    scale = float(torch.tensor(0.7))  # as fp32 holds it
+    add = torch.zeros(V, H, dtype=torch.float64, device=DEV).index_add_(0, ids, dout.double()) * scale
+    size = torch.zeros(V, H, dtype=torch.float64, device=DEV).index_add_(0, ids, dout.double().abs()) * scale
+    n = torch.bincount(ids, minlength=V)[:, None].double()
+    within(got, start.double() + add, 2 * (n + 2) * EPS * size + 2 * EPS * (start.double() + add).abs())
+    assert torch.equal(got[n[:, 0] == 0], start[n[:, 0] == 0])
+    assert torch.equal(got, embed_backward(dout, ids, V, 0.7, start, accumulate=True))
+
+
 def test_embed_backward_padding_and_bad_ids():
     g = gen(5)
     N, V, H = 200, 20, 16
