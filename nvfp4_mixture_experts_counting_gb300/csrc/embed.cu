@@ -22,7 +22,12 @@ constexpr int kSortThreads = 512;
 constexpr int kChunk = 32;     // sorted tokens that a warp sums (one per lane)
 constexpr int kAhead = 8;      // rows of them in flight
 constexpr int kZeroBlocks = 1024;  // blocks of table rows whose marks a CTA holds at a time
-constexpr int kDigitBits = 9;  // widest radix digit
+// Widest radix digit.  More bins cost each pass the exchange of more totals, and
+// may save a pass.  With the gradient of H=64, at V=262144 two passes of 10 bits
+// take 3 us more than three of 7 for 8191 tokens, and 58 instead of 61 us for
+// 131072; at V=1000 one of 10 instead of two of 5 takes 37 instead of 44 us there.
+constexpr int kDigitBits = 9, kManyDigitBits = 10;
+constexpr int64_t kManyTokens = 65536;
 constexpr int kLongRun = 16;   // chunks from which a run's sum is shared by a CTA's warps
 
 inline int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -361,8 +366,9 @@ EmbedWorkspace embed_workspace(int64_t N, int H) {
 }
 
 cudaError_t embed_set_limits(int* sort_ctas) {
-  const cudaError_t e = cluster_sort_limits(k_embed_sort<int32_t>, kSortThreads, 1 << kDigitBits, sort_ctas);
-  return e != cudaSuccess ? e : cluster_sort_limits(k_embed_sort<int64_t>, kSortThreads, 1 << kDigitBits, sort_ctas);
+  constexpr int bins = 1 << kManyDigitBits;
+  const cudaError_t e = cluster_sort_limits(k_embed_sort<int32_t>, kSortThreads, bins, sort_ctas);
+  return e != cudaSuccess ? e : cluster_sort_limits(k_embed_sort<int64_t>, kSortThreads, bins, sort_ctas);
 }
 
 cudaError_t launch_embed(const TrainDevice& d, const void* table, int dtype, int64_t V, int H, const void* ids,
@@ -397,7 +403,8 @@ cudaError_t launch_embed_backward(const TrainDevice& d, const void* dout, int dt
   int32_t* pos[2] = {reinterpret_cast<int32_t*>(ws + w.pos[0]), reinterpret_cast<int32_t*>(ws + w.pos[1])};
   int bits = 1;
   while ((V >> bits) != 0) ++bits;  // the largest key is V
-  const int passes = (bits + kDigitBits - 1) / kDigitBits, digit = (bits + passes - 1) / passes;
+  const int widest = N > kManyTokens ? kManyDigitBits : kDigitBits;
+  const int passes = (bits + widest - 1) / widest, digit = (bits + passes - 1) / passes;
   cudaError_t e = cudaSuccess;
   if (N > 0) {
     if (id_bytes == 8)

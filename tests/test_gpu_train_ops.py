@@ -391,6 +391,20 @@ def test_embed_backward_adds_runs_of_every_length(N, V, kind, H, dtype):
     assert torch.equal(got, embed_backward(dout, ids, V, 0.7, start, accumulate=True))
 
 
+@pytest.mark.parametrize("V", [511, 512, 1000, 1023, 1024, 300000, 1 << 20])
+def test_embed_backward_of_many_tokens(V):
+    """Wider digits: one pass up to 1023 rows, two up to 2^20 - 1, three beyond."""
+    N, H = 66001, 8
+    g = gen(V)
+    dout, ids = randn(g, N, H, dtype=BF16), token_ids(g, N, V, "all")
+    got = embed_backward(dout, ids.int(), V, 1.0, torch.full((V, H), 7.0, device=DEV), padding=V - 1)
+    use = ids != V - 1
+    ref = torch.zeros(V, H, dtype=torch.float64, device=DEV).index_add_(0, ids[use], dout[use].double())
+    size = torch.zeros(V, H, dtype=torch.float64, device=DEV).index_add_(0, ids[use], dout[use].double().abs())
+    n = torch.bincount(ids[use], minlength=V)[:, None].double()
+    within(got, ref, 2 * (n + 2) * EPS * size)
+
+
 def test_embed_backward_padding_and_bad_ids():
     g = gen(5)
     N, V, H = 200, 20, 16
