@@ -320,28 +320,44 @@ def _dense(t):
     return t.data_ptr()
 
 
+def _words(t, n: int = 0):
+    """_dense of at least n fp32 or int32 values, as the C calls take them."""
+    if t is not None and (t.element_size() != 4 or t.numel() < n):
+        raise TypeError(f"{n} or more 32-bit values expected, got {t.numel()} of {t.dtype}")
+    return _dense(t)
+
+
+def _floats(t, n: int):
+    """The same for exactly n fp32 values (one look at the bytes: these are many, and made for each step)."""
+    if t is None:
+        return None
+    if t.nbytes != 4 * n or not t.is_contiguous():
+        raise ValueError(f"{n} contiguous fp32 values expected, got {t.numel()} of {t.dtype}")
+    return t.data_ptr()
+
+
 def ftmoe_dispatch(x, T: int, H: int, topk_idx, top_k: int, E: int, offsets, perm, inv, xs, stream=None):
     """Rows of x sorted by expert into xs, and the sort's tables (x and xs None: the tables alone)."""
-    _check(lib().ftmoe_dispatch(_dense(x), BF16 if x is None else _dtype(x), T, H, _dense(topk_idx), top_k, E,
+    _check(lib().ftmoe_dispatch(_dense(x), BF16 if x is None else _dtype(x), T, H, _words(topk_idx), top_k, E,
                                 _dense(offsets), _dense(perm), _dense(inv), _dense(xs), _stream(stream)),
            "ftmoe_dispatch")
 
 
 def ftmoe_combine(ys, T: int, H: int, top_k: int, inv, w, out, stream=None):
     """out[t] = sum_j w[t, j] ys[inv[t, j]]; w None: weights of one (the gradient of ftmoe_dispatch)."""
-    _check(lib().ftmoe_combine(_dense(ys), _dtype(ys), T, H, top_k, _dense(inv), _dense(w), _dense(out),
+    _check(lib().ftmoe_combine(_dense(ys), _dtype(ys), T, H, top_k, _words(inv), _words(w), _dense(out),
                                _stream(stream)), "ftmoe_combine")
 
 
 def ftmoe_combine_backward(dout, ys, T: int, H: int, top_k: int, inv, w, dys, dw, stream=None):
-    _check(lib().ftmoe_combine_backward(_dense(dout), _dense(ys), _dtype(dout), T, H, top_k, _dense(inv), _dense(w),
-                                        _dense(dys), _dense(dw), _stream(stream)), "ftmoe_combine_backward")
+    _check(lib().ftmoe_combine_backward(_dense(dout), _dense(ys), _dtype(dout), T, H, top_k, _words(inv), _words(w),
+                                        _dense(dys), _words(dw), _stream(stream)), "ftmoe_combine_backward")
 
 
 def ftmoe_route_backward(logits, topk_idx, topk_w, dw, T: int, E: int, top_k: int, norm_topk_prob: bool, dlogits,
                          stream=None):
-    _check(lib().ftmoe_route_backward(_dense(logits), _dense(topk_idx), _dense(topk_w), _dense(dw), T, E, top_k,
-                                      int(norm_topk_prob), _dense(dlogits), _stream(stream)), "ftmoe_route_backward")
+    _check(lib().ftmoe_route_backward(_words(logits), _words(topk_idx), _words(topk_w), _words(dw), T, E, top_k,
+                                      int(norm_topk_prob), _words(dlogits), _stream(stream)), "ftmoe_route_backward")
 
 
 def ftmoe_embed(table, V: int, H: int, ids, N: int, scale: float, out, stream=None):
@@ -377,11 +393,14 @@ def policy_args(logits, targets, old_logp, ref_logp, advantage, weight, loss, ro
         at, (ld_d, step_d) = dlogits.data_ptr(), dlogits.stride()
     if V > 1 and (step != 1 or step_d != 1):
         raise ValueError("logits and dlogits need a dense last dimension")
+    if targets.numel() < N:
+        raise ValueError("a target for each row of logits expected")
     if N <= 1:  # a single row's stride says nothing
         ld = ld_d = V
     return PolicyArgs(logits.data_ptr(), _dtype(logits), targets.element_size(), N, V, ld, _dense(targets),
-                      _dense(old_logp), _dense(ref_logp), _dense(advantage), _dense(weight), temperature, clip_low,
-                      clip_high, kl_coef, grad_scale, _dense(loss), _dense(row_loss), _dense(logp), at, ld_d)
+                      _floats(old_logp, N), _floats(ref_logp, N), _floats(advantage, N), _floats(weight, N), temperature,
+                      clip_low, clip_high, kl_coef, grad_scale, _floats(loss, 1), _floats(row_loss, N),
+                      _floats(logp, N), at, ld_d)
 
 
 def ftmoe_policy_loss(args: PolicyArgs, stream=None):
@@ -396,10 +415,14 @@ class AdamwList:
         entries = []
         for t in tensors:
             get = t.get
-            p, g, m = t["p"], t["g"], t["m"]
-            entries.append((_dense(p), _dense(g), _dense(get("master")), _dense(m), _dense(t["v"]),
-                            _dense(get("m_scale")), _dense(get("v_scale")), p.numel(), get("weight_decay", 0.0),
-                            _dtype(p), _dtype(g), 8 * m.element_size()))
+            p, g, m, v = t["p"], t["g"], t["m"], t["v"]
+            n = p.numel()
+            if min(g.numel(), m.numel(), v.numel()) < n or m.element_size() != v.element_size():
+                raise ValueError("g, m and v have p's values, and m and v one type")
+            blocks = (n + 255) // 256
+            entries.append((_dense(p), _dense(g), _words(get("master"), n), _dense(m), _dense(v),
+                            _words(get("m_scale"), blocks), _words(get("v_scale"), blocks), n,
+                            get("weight_decay", 0.0), _dtype(p), _dtype(g), 8 * m.element_size()))
         self.array = (AdamwTensor * len(entries))(*entries)
 
 

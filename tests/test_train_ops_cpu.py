@@ -156,3 +156,47 @@ def test_adamw_lists(lib):
 def test_status_without_a_gpu(lib):
     if no_gpu():
         assert lib.ftmoe_ops_status(None) == DEVICE
+
+
+def test_binding_refuses_wrong_types_and_sizes(lib):
+    """Before any call: on a device the addresses would be read as what they are not."""
+    torch = pytest.importorskip("torch")
+    new = lambda n, dtype=torch.float32: torch.zeros(n, dtype=dtype)
+    half, wide = torch.bfloat16, torch.int64
+    x, idx, w = new((4, 16), half), new((4, 2), torch.int32), new((4, 2))
+    tables = new(9, torch.int32), new(8, torch.int32), new(8, torch.int32)
+    with pytest.raises(TypeError):
+        ftmoe.ftmoe_dispatch(x, 4, 16, idx.long(), 2, 8, *tables, new((8, 16), half), stream=0)
+    for inv, weights in ((tables[1].long(), w), (tables[1], w.to(half))):
+        with pytest.raises(TypeError):
+            ftmoe.ftmoe_combine(new((8, 16), half), 4, 16, 2, inv, weights, x, stream=0)
+    with pytest.raises(TypeError):
+        ftmoe.ftmoe_route_backward(new((4, 8), half), idx, w, w, 4, 8, 2, False, new((4, 8)), stream=0)
+    with pytest.raises(TypeError):
+        ftmoe.ftmoe_embed(x.int(), 4, 16, new(3, wide), 3, 1.0, new((3, 16), half), stream=0)
+
+    def args(**kw):
+        a = dict(logits=new((4, 10), half), targets=new(4, wide), old_logp=new(4), ref_logp=new(4), advantage=new(4),
+                 weight=new(4), loss=new(1), row_loss=new(4), logp=new(4), dlogits=new((4, 10), half))
+        a.update(kw)
+        return ftmoe.policy_args(**a)
+
+    assert args().N == 4 and args(ref_logp=None, weight=None, logp=None, dlogits=None).V == 10
+    for kw in (dict(targets=new(3, wide)), dict(old_logp=new(3)), dict(advantage=new(4, half)), dict(weight=new(2)),
+               dict(loss=new(0)), dict(row_loss=new(3)), dict(logp=new(4, torch.float64)), dict(dlogits=new((4, 10))),
+               dict(dlogits=new((4, 9), half)), dict(logits=new((10, 4), half).t()), dict(ref_logp=new(8)[::2])):
+        with pytest.raises((TypeError, ValueError)):
+            args(**kw)
+
+    def tensors(**kw):
+        a = dict(p=new(300, half), g=new(300, half), m=new(300, torch.uint8), v=new(300, torch.uint8), m_scale=new(2),
+                 v_scale=new(2))
+        a.update(kw)
+        return ftmoe.adamw_list([a])
+
+    assert tensors().array[0].n == 300 and tensors().array[0].state_bits == 8
+    for kw in (dict(g=new(299, half)), dict(m=new(299, torch.uint8)), dict(v=new(300)), dict(v_scale=new(1)),
+               dict(m_scale=new(2, half)), dict(master=new(299)), dict(master=new(300, half)), dict(p=new(300, wide)),
+               dict(p=new(600, half)[::2])):
+        with pytest.raises((TypeError, ValueError)):
+            tensors(**kw)
