@@ -28,6 +28,10 @@ constexpr int kZeroBlocks = 1024;  // blocks of table rows whose marks a CTA hol
 // 131072; at V=1000 one of 10 instead of two of 5 takes 37 instead of 44 us there.
 constexpr int kDigitBits = 9, kManyDigitBits = 10;
 constexpr int64_t kManyTokens = 65536;
+// Bytes of the table for each CTA that fills, at least: it reads all ids, however
+// few rows it has.  N=16384 H=2560 bf16, with and without this limit: V=4096 44
+// and 54 us, V=32000 58 and 67 us; V=131072 125 us with it, 131 with 512 KB.
+constexpr int64_t kFillBytes = 128 * 1024;
 constexpr int kLongRun = 16;   // chunks from which a run's sum is shared by a CTA's warps
 
 inline int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -444,7 +448,10 @@ cudaError_t launch_embed_backward(const TrainDevice& d, const void* dout, int dt
           a.grad_tasks = chunks * a.slices;
           // Many CTAs that fill, as those end at different times (for 1.34 GB: 222 us with 512, 189 with 1024,
           // 182 with 4096), but 2^25 ids read by all of them at most; blocks of up to 32 rows.
-          while (2 << a.cta_bits <= 2048 && 2 << a.cta_bits <= V && (N << (a.cta_bits + 1)) <= 1 << 25) ++a.cta_bits;
+          const int64_t bytes = V * H * (int64_t)sizeof(TT);
+          while (2 << a.cta_bits <= std::min<int64_t>(2048, V) && bytes >> (a.cta_bits + 1) >= kFillBytes &&
+                 (N << (a.cta_bits + 1)) <= 1 << 25)
+            ++a.cta_bits;
           while (a.row_bits < 5 && (V >> (a.row_bits + 1 + a.cta_bits)) > 0) ++a.row_bits;
           const int zero_ctas = accumulate ? 0 : 1 << a.cta_bits;
           a.zero_first = std::min(zero_ctas, 4 * d.num_sms);
