@@ -177,14 +177,14 @@ __device__ __forceinline__ LogProb log_prob(float zy, float m, float s, float te
 }
 
 // A counted row's gradient coefficient grad_scale w c / temperature, from its
-// maximum, its sum and log2 of that.  A warp that has to write the row's loss
-// (`writes`: by this lane) works with the log probability's rounding; for
-// the coefficient alone, as many times as a row has warps, the rounded value does.
-__device__ __forceinline__ float finish_row(const ftmoe_policy_args& a, const RowInputs& in, MaxSum run, float log2_s,
-                                            float zy, float inv_t, bool warp_writes, bool writes) {
-  LogProb logp{(zy - run.m) * inv_t - log2_s * kLn2, 0.f};
-  if (warp_writes) logp = log_prob(zy, run.m, run.s, a.temperature, inv_t);
-  else if (!a.dlogits) return 0.f;
+// maximum and its sum.  Every warp of the row works it out from the same values
+// by the same operations, with the log probability's rounding: warps that took
+// the rounded one could fall on the other side of a clip bound than the warp that
+// writes the row's loss (`warp_writes`, `writes` by this lane), and each wrote its own slope.
+__device__ __forceinline__ float finish_row(const ftmoe_policy_args& a, const RowInputs& in, MaxSum run, float zy,
+                                            float inv_t, bool warp_writes, bool writes) {
+  if (!a.dlogits && !warp_writes) return 0.f;
+  const LogProb logp = log_prob(zy, run.m, run.s, a.temperature, inv_t);
   const float r = expf(logp.minus(in.old)), A = in.adv;
   const float bounded = r < 1.f - a.clip_low ? 1.f - a.clip_low : r > 1.f + a.clip_high ? 1.f + a.clip_high : r;
   const bool clipped = r * A > bounded * A;  // false for NaN, which then reaches the loss and the gradient
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(WARPS * 32, kMinWarps / WARPS)
     ++round;
     float c = 0.f;
     const float log2_s = log2f(run.s);
-    if (p.in.w != 0.f) c = finish_row(a, p.in, run, log2_s, zy, w.inv_t, rank == 0 && warp == 0, speaks);
+    if (p.in.w != 0.f) c = finish_row(a, p.in, run, zy, w.inv_t, rank == 0 && warp == 0, speaks);
     else if (speaks) write_uncounted(a, p.in.n);
     if (a.dlogits) {
       check_next();
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinWarps / kWarps)
     if (p.in.w != 0.f) {
       run = warp_join(run, w.k2);
       log2_s = log2f(run.s);
-      c = finish_row(a, p.in, run, log2_s, zy, w.inv_t, true, lane == 0);
+      c = finish_row(a, p.in, run, zy, w.inv_t, true, lane == 0);
     } else if (lane == 0) {
       write_uncounted(a, p.in.n);
     }
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kLongThreads) k_policy_long(ftmoe_policy_args 
       parity ^= 1;
       m = run.m;
       ls = log2f(run.s);
-      c = finish_row(a, in, run, ls, zy, 1.f / a.temperature, rank == 0 && warp == 0, rank == 0 && tid == 0);
+      c = finish_row(a, in, run, zy, 1.f / a.temperature, rank == 0 && warp == 0, rank == 0 && tid == 0);
     } else if (rank == 0 && tid == 0) {
       write_uncounted(a, n);
     }

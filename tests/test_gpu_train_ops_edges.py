@@ -1,0 +1,69 @@
+"""Edges of the training operators that the sizes and inputs elsewhere do not
+reach.  Bounds are those that test_gpu_train_ops derives, restated where a
+test's quantity differs."""
+
+import numpy as np
+import pytest
+import torch
+
+from nvfp4_mixture_experts_counting_gb300 import ftmoe
+
+from test_gpu_train_ops import BF16, DEV, EPS, FP16, FP32, TINY, UNIT, policy, policy_inputs, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from nvfp4_mixture_experts_counting_gb300 import build
+    build.build()
+    ftmoe.ftmoe_ops_status()
+    yield
+    assert ftmoe.ftmoe_ops_status() == 0  # every test that marks the word reads it
+
+
+# ----------------------------------------------------------------- policy loss: one slope a row
+
+# a warp a row, two warps, four, clusters of CTAs, and rows that are read twice
+ROWS = [(700, 65, FP32), (1300, 2049, BF16), (1300, 4500, BF16), (1217, 6001, FP32), (300, 16001, FP16),
+        (64, 131072, BF16), (200, 50001, FP32), (6, 500003, FP32), (6, 1000003, BF16)]
+
+
+@pytest.mark.parametrize("N,V,dtype", ROWS)
+def test_a_row_at_a_clip_bound_has_one_slope(N, V, dtype):
+    """clip 0 and old_logp the call's own: every ratio is within rounding of both bounds, so either side may
+    be taken, but by all of a row: it is zeros, or -A r (onehot - softmax) w."""
+    i = policy_inputs(N + V, N, V, dtype, masked=0.0)
+    i["ref_logp"] = None
+    i["old_logp"] = policy(i, grad=False)[2]
+    d = policy(i, clip_low=0.0, clip_high=0.0)[3].double()
+    z, y = i["logits"].double(), i["targets"][:, None]
+    p = torch.softmax(z, 1)
+    hot = torch.zeros_like(p).scatter_(1, y, 1.0)
+    logp = (z.gather(1, y)[:, 0] - torch.logsumexp(z, 1))
+    dl = 2 * EPS * (V / 512 + 64 + 6 * z.abs().amax(1))
+    x = logp - i["old_logp"].double()
+    r, k, A = torch.exp(x), i["weight"].double(), i["advantage"].double()
+    dr = r * (dl + 2 * EPS * (4 + x.abs()))
+    ref = (-k * A * r)[:, None] * (hot - p)
+    err = (k * A.abs() * (dr + 10 * EPS * r))[:, None] * (hot + p) + (k * A * r).abs()[:, None] * p * (2 * dl[:, None])
+    slope = ((d - ref).abs() <= UNIT[dtype] * 1.01 * ref.abs() + err + TINY[dtype]).all(1)
+    zeros = (d == 0).all(1)
+    assert bool((slope | zeros).all()), int((~(slope | zeros)).sum())
+
+
+@pytest.mark.parametrize("N,V,dtype", ROWS)
+def test_equal_logits_have_equal_gradients(N, V, dtype):
+    """A row of one value: its gradient is one value off the target, to the last bit."""
+    i = policy_inputs(N + V, N, V, dtype, masked=0.0)
+    i["logits"] = i["logits"][:, :1].expand(N, V).contiguous()
+    lp = -float(np.log(V))
+    i["old_logp"] = lp + 0.1 * torch.sin(torch.arange(N, device=DEV).float())
+    i["ref_logp"] = lp + 0.1 * torch.cos(torch.arange(N, device=DEV).float())
+    d = policy(i, kl_coef=0.3, clip_low=0.5, clip_high=0.5, grad_scale=4096.0)[3]
+    other = (i["targets"] == 0).long()[:, None]
+    value = d.gather(1, other)  # of a column that is not the target's
+    off = torch.ones(N, V, dtype=torch.bool, device=DEV).scatter_(1, i["targets"][:, None], False)
+    assert bool(((d == value) | ~off).all())
