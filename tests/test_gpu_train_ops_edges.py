@@ -8,7 +8,7 @@ import torch
 
 from nvfp4_mixture_experts_counting_gb300 import ftmoe
 
-from test_gpu_train_ops import BF16, DEV, EPS, FP16, FP32, TINY, UNIT, policy, policy_inputs, within
+from test_gpu_train_ops import BF16, DEV, EPS, FP16, FP32, TINY, UNIT, gen, policy, policy_inputs, randn, within
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +67,26 @@ def test_equal_logits_have_equal_gradients(N, V, dtype):
     value = d.gather(1, other)  # of a column that is not the target's
     off = torch.ones(N, V, dtype=torch.bool, device=DEV).scatter_(1, i["targets"][:, None], False)
     assert bool(((d == value) | ~off).all())
+
+
+# ----------------------------------------------------------------- policy loss: next to the reference
+
+@pytest.mark.parametrize("N,V,dtype", [(1000, 3000, FP32), (300, 16001, BF16), (64, 131072, BF16), (4, 500003, FP32)])
+@pytest.mark.parametrize("spread", [1e-1, 1e-3, 1e-4, 1e-5])
+def test_kl_term_of_a_policy_next_to_its_reference(N, V, dtype, spread):
+    """The term alone (no advantage).  With d = ref - logp known to within e, exp(d) - d - 1 is within
+    |exp(d) - 1| e + e^2 of the exact one and its own rounding is relative to its own size; it is never negative."""
+    i = policy_inputs(N + V, N, V, dtype, masked=0.0)
+    z = i["logits"].double()
+    logp = z.gather(1, i["targets"][:, None])[:, 0] - torch.logsumexp(z, 1)
+    i["ref_logp"] = (logp + spread * randn(gen(5), N)).float()
+    i["old_logp"] = logp.float()
+    i["advantage"] = torch.zeros(N, device=DEV)
+    row = policy(i, grad=False, kl_coef=1.0)[1]
+    d = i["ref_logp"].double() - logp
+    exact = torch.expm1(d) - d
+    # e in units of 2^-24: the terms' arguments and ex2.approx (8), their additions along a lane (at most V / 256)
+    # and across lanes and warps with their rescaling (28), the logarithm's own (4)
+    e = EPS * (40 + V / 256)
+    within(row, exact, torch.expm1(d).abs() * e + e * e + 16 * EPS * exact)
+    assert bool((row >= 0).all())
