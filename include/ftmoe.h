@@ -473,7 +473,7 @@ int ftmoe_combine_backward(const void* dout, const void* ys, int dtype, int T, i
  *                   p = softmax(logits), logits fp32 [T, E] with the bias
  * topk_idx is the router's own choice, before any slot is dropped; an index
  * outside [0, E) is left out and marks the status word.  dlogits: fp32
- * [T, E], written whole. */
+ * [T, E], written whole; may be `logits` itself. */
 int ftmoe_route_backward(const float* logits, const int32_t* topk_idx, const float* topk_w, const float* dw, int T,
                          int E, int top_k, int norm_topk_prob, float* dlogits, ftmoe_stream_t stream);
 

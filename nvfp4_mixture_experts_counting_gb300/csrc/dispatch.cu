@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(kThreads) k_route_backward(const float* logits
       ej = -1;
     }
   }
+  const float zj = !NORM && ej >= 0 ? z[ej] : 0.f;  // before the row is written: dlogits may be the logits
   const float S = warp_sum_f32(wj * dj);
   const float up = NORM ? wj * (dj - S) : dj;
   float top = 0.f, sum = 1.f;
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kThreads) k_route_backward(const float* logits
     }
   }
   __syncwarp();  // the row's first values are written
-  if (lane < k && ej >= 0 && first) out[ej] = NORM ? g : expf(z[ej] - top) / sum * (g - S);
+  if (lane < k && ej >= 0 && first) out[ej] = NORM ? g : expf(zj - top) / sum * (g - S);
 }
 
 inline unsigned blocks_of(int64_t n, int per) { return (unsigned)((n + per - 1) / per); }

@@ -90,3 +90,20 @@ def test_kl_term_of_a_policy_next_to_its_reference(N, V, dtype, spread):
     e = EPS * (40 + V / 256)
     within(row, exact, torch.expm1(d).abs() * e + e * e + 16 * EPS * exact)
     assert bool((row >= 0).all())
+
+
+# ----------------------------------------------------------------- in place
+
+@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (5, 3, 7), (33, 8, 256), (9, 32, 1000), (77, 6, 130)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_route_backward_in_place(T, k, E, norm):
+    """dlogits may be the logits: the same bits."""
+    g = gen(T + E)
+    z = randn(g, T, E, std=3.0)
+    top, idx = torch.topk(z, k, dim=1)
+    idx = idx.int().contiguous()
+    w = (torch.softmax(top, 1) if norm else torch.softmax(z, 1).gather(1, idx.long())).contiguous()
+    dw, apart = randn(g, T, k), torch.empty(T, E, device=DEV)
+    ftmoe.ftmoe_route_backward(z, idx, w, dw, T, E, k, norm, apart)
+    ftmoe.ftmoe_route_backward(z, idx, w, dw, T, E, k, norm, z)
+    assert torch.equal(z, apart)
