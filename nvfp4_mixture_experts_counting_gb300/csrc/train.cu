@@ -15,10 +15,15 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr int kMaxH = 1 << 24;
 
-static __device__ uint32_t g_ops_status;
+static __device__ uint32_t g_ops_status[2];  // what the checks mark; what the latest reader took
 
 std::mutex g_mu;
+std::mutex g_status_mu;  // one reader at a time: they share the second word
 TrainDevice g_devices[kMaxDevices] = {};
+
+// The word, cleared as it is read: a copy and a clearing apart would lose a
+// mark that another stream makes between the two.
+__global__ void k_take_status(uint32_t* status, uint32_t* taken) { *taken = atomicExch(status, 0u); }
 
 // Once per device, with that device current: the status word's address and
 // the kernels' shared-memory limits.
@@ -220,10 +225,14 @@ int ftmoe_ops_status(ftmoe_stream_t stream) {
   const cudaStream_t s = (cudaStream_t)stream;
   uint32_t st = 0;
   cudaError_t e = cudaStreamSynchronize(s);
-  // on the stream itself: what it runs next marks a word that has been cleared
-  if (e == cudaSuccess) e = cudaMemcpyAsync(&st, d.status, 4, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(d.status, 0, 4, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess) {
+    std::lock_guard<std::mutex> lk(g_status_mu);
+    // on the stream itself: what it runs next marks a word that has been cleared
+    k_take_status<<<1, 1, 0, s>>>(d.status, d.status + 1);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&st, d.status + 1, 4, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  }
   if (e != cudaSuccess) return launched(e, "ftmoe_ops_status");
   if (st & kStatusTimeout) return FTMOE_ERR_TIMEOUT;
   return st & kStatusRange ? FTMOE_ERR_DEVICE_CHECK : FTMOE_OK;

@@ -2,6 +2,9 @@
 reach.  Bounds are those that test_gpu_train_ops derives, restated where a
 test's quantity differs."""
 
+import threading
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -107,3 +110,38 @@ def test_route_backward_in_place(T, k, E, norm):
     ftmoe.ftmoe_route_backward(z, idx, w, dw, T, E, k, norm, apart)
     ftmoe.ftmoe_route_backward(z, idx, w, dw, T, E, k, norm, z)
     assert torch.equal(z, apart)
+
+
+# ----------------------------------------------------------------- the status word
+
+def test_status_loses_no_mark_of_another_stream():
+    """One thread reads and clears the word on a stream of its own while marks come from another stream: each
+    mark shows in a read that had not returned when it was made."""
+    table, out = torch.zeros(4, 8, device=DEV), torch.zeros(1, 8, device=DEV)
+    bad = torch.full((1,), 9, device=DEV)
+    reader, writer = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    stop, reads = threading.Event(), [0, 0]  # reads that returned, and those that saw a mark
+
+    def read():
+        while not stop.is_set():
+            if ftmoe.ftmoe_ops_status(reader) == -10:
+                reads[1] += 1
+            reads[0] += 1
+
+    thread = threading.Thread(target=read)
+    thread.start()
+    lost = 0
+    try:
+        for _ in range(2000):
+            seen = reads[1]
+            ftmoe.ftmoe_embed(table, 4, 8, bad, 1, 1.0, out, stream=writer)
+            writer.synchronize()  # the mark is made
+            done = reads[0]
+            while reads[0] < done + 2 and thread.is_alive():  # a whole read has begun and returned since
+                time.sleep(0)  # the other thread's turn
+            lost += reads[1] == seen
+    finally:
+        stop.set()
+        thread.join()
+    assert lost == 0
