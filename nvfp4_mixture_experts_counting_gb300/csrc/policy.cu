@@ -176,19 +176,28 @@ __device__ __forceinline__ LogProb log_prob(float zy, float m, float s, float te
   return r;
 }
 
-// exp(d) - 1 - d, e = exp(d) - 1.  Near the reference the difference cancels (of
-// exp(d) - d - 1 nothing is left at |d| = 3e-4), so small d take the series
-// d^2 (1/2 + d/3! + ...) up to d^8, whose rest at 1/4 is 2^-31 of the term; it is never negative.
-__device__ __forceinline__ float kl_term(float d, float e) {
-  if (!(fabsf(d) < 0.25f)) return e - d;
-  float s = 1.f / 40320.f;
+// exp(d) - 1 - d, and e = exp(d) - 1.  Near the reference both differences
+// cancel (of exp(d) - d - 1 nothing is left at |d| = 3e-4), so up to |d| = 1 they
+// come from the series d^2 (1/2! + d/3! + ... + d^9/11!), whose rest is 2^-27 of
+// it; it is never negative.
+__device__ __forceinline__ float kl_term(float d, float& e) {
+  if (!(fabsf(d) < 1.f)) {
+    e = expf(d) - 1.f;
+    return e - d;
+  }
+  float s = 1.f / 39916800.f;
+  s = fmaf(s, d, 1.f / 3628800.f);
+  s = fmaf(s, d, 1.f / 362880.f);
+  s = fmaf(s, d, 1.f / 40320.f);
   s = fmaf(s, d, 1.f / 5040.f);
   s = fmaf(s, d, 1.f / 720.f);
   s = fmaf(s, d, 1.f / 120.f);
   s = fmaf(s, d, 1.f / 24.f);
   s = fmaf(s, d, 1.f / 6.f);
   s = fmaf(s, d, 0.5f);
-  return d * d * s;
+  const float k = d * d * s;
+  e = d + k;
+  return k;
 }
 
 // A counted row's gradient coefficient grad_scale w c / temperature, from its
@@ -205,8 +214,8 @@ __device__ __forceinline__ float finish_row(const ftmoe_policy_args& a, const Ro
   const bool clipped = r * A > bounded * A;  // false for NaN, which then reaches the loss and the gradient
   float row = -(clipped ? bounded * A : r * A), c = clipped ? 0.f : -(A * r);
   if (a.ref_logp && a.kl_coef != 0.f) {
-    const float d = -logp.minus(in.ref), e = expm1f(d);
-    row += a.kl_coef * kl_term(d, e);
+    float e;
+    row += a.kl_coef * kl_term(-logp.minus(in.ref), e);
     c -= a.kl_coef * e;
   }
   if (writes) {
