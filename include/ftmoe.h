@@ -537,6 +537,16 @@ typedef struct {
 
 int ftmoe_policy_loss(const ftmoe_policy_args* args, ftmoe_stream_t stream);
 
+/* Test hook of ftmoe_policy_loss's failure path, off by default and shared by
+ * all threads.  While enabled, one warp of a call's first row never asks for
+ * its first chunk of it, and the call's waits give up after wait_limit_ns (0:
+ * the default limit of one second, which is the most).  The kernel sets the
+ * status word's timeout bit and finishes: that row and those that the same
+ * warp takes part in later come out as NaN, others as usual.  Rows that no
+ * cluster's shared memory holds are not waited for.  No GPU fault or trap is
+ * involved. */
+int ftmoe_test_withhold_policy(int enable, int64_t wait_limit_ns);
+
 /* One AdamW step over n_tensors tensors.  With g' = grad_scale * g and `step`
  * counted from 1:
  *   m <- beta1 m + (1 - beta1) g';  v <- beta2 v + (1 - beta2) g'^2
@@ -577,8 +587,11 @@ int ftmoe_adamw(const ftmoe_adamw_tensor* tensors, int n_tensors, const ftmoe_ad
                 ftmoe_stream_t stream);
 
 /* Synchronise `stream`, read and clear the current device's status word of
- * the training operators: FTMOE_OK, or FTMOE_ERR_DEVICE_CHECK if a kernel met
- * an index out of range since the last call.  One word serves all streams. */
+ * the training operators since the last call: FTMOE_OK,
+ * FTMOE_ERR_DEVICE_CHECK if a kernel met an index out of range, or
+ * FTMOE_ERR_TIMEOUT if a bounded wait of the policy loss ran out: that call's
+ * outputs are not valid (its loss is NaN as a rule), and the next call starts
+ * clean.  One word serves all streams. */
 int ftmoe_ops_status(ftmoe_stream_t stream);
 
 #ifdef __cplusplus

@@ -24,7 +24,7 @@ constexpr int kWarps = 4;        // of a CTA (k_policy: at most)
 constexpr int kMaxRanks = 8;     // CTAs of a cluster
 constexpr int kUnroll = 4;       // 16-byte pieces a lane sums at a time
 constexpr int kChunk = 256;      // 16-byte pieces of one bulk copy
-constexpr int kMaxChunks = 16;   // of a warp's part
+constexpr int kMaxChunks = 14;   // of a warp's part
 constexpr int kShortChunks = 2;  // of a short row
 constexpr int kLag = 1;          // chunks between a gradient's departure and the reuse of its buffer
 constexpr int kLongThreads = 512;
@@ -314,6 +314,33 @@ struct Part {
   __device__ __forceinline__ int chunk_hi(int j) const { return min(whi, lo + (j + 1) * kChunk); }
 };
 
+// Waits that ran out: for a chunk (the warp's rows come out as NaN from then on,
+// and it asks for no further chunk), and for the cluster (the warp leaves).
+constexpr uint32_t kNoChunk = 1u << 30, kNoCluster = 1u << 31, kFailed = kNoChunk | kNoCluster;
+
+// The limits of the waits, and whether a test withholds a chunk, so that one runs out.
+struct Waits {
+  uint64_t limit_ns, meeting_ns;
+  int withhold;
+};
+
+// Gave up: waits (as long at most) for the copies that may still be on their way
+// (the lane that fetches), and for what peers may have sent.  Apart from the
+// kernels, whose loops it would cost registers (2% at N=4096 V=131072).
+__device__ __noinline__ void settle(uint64_t* bar, uint32_t phases, bool fetches, uint64_t limit_ns, uint32_t* status) {
+  if (!fetches) return;
+  for (uint32_t left = phases << 2 >> 18; left; left &= left - 1) {
+    const int j = __ffs(left) - 1;
+    if (!mbar_wait(bar + j, phases >> j & 1, status, limit_ns)) break;
+  }
+}
+__device__ __noinline__ void settle_cluster(uint64_t* meet, uint64_t* ask, uint32_t round, uint64_t limit_ns, uint32_t* status) {
+  for (uint32_t r = round - 1; r <= round; ++r) {
+    mbar_wait(meet + (r & 1), r >> 1 & 1, status, limit_ns);
+    if (ask) mbar_wait(ask + (r & 1), r >> 1 & 1, status, limit_ns);
+  }
+}
+
 // One warp's work on its part of a row, in its own shared memory.
 template <typename T>
 struct Worker {
@@ -324,12 +351,16 @@ struct Worker {
   const float inv_t, k2;
   Pack<T, N>* buf;      // the part
   uint64_t* bar;        // a barrier for each chunk
-  uint32_t phases = 0;  // of the barriers
-  bool ok = true;       // no wait has run out
+  const Waits& waits;
+  uint32_t phases = 0;  // of the barriers; from bit 16 on, chunks on their way (of the lane that fetches)
 
-  __device__ Worker(const ftmoe_policy_args& args, int lane_, uint32_t* status_, Pack<T, N>* buf_, uint64_t* bar_)
+  __device__ Worker(const ftmoe_policy_args& args, int lane_, uint32_t* status_, Pack<T, N>* buf_, uint64_t* bar_,
+                    const Waits& waits_)
       : a(args), lane(lane_), status(status_), inv_t(1.f / args.temperature), k2(kLog2e / args.temperature), buf(buf_),
-        bar(bar_) {}
+        bar(bar_), waits(waits_) {}
+  __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity) const {
+    return mbar_wait(b, parity, status, waits.limit_ns);
+  }
   __device__ __forceinline__ T* vals() const { return reinterpret_cast<T*>(buf); }
 
   // The part of row n that is number `index` of 2^log2_parts * per_cta parts (CTA by CTA).
@@ -350,10 +381,12 @@ struct Worker {
     for (int i = p.lo + begin; i < min(p.wlo, p.lo + end); ++i) f(i * N + lane);
     for (int i = max(p.whi, p.lo + begin); i < p.lo + end; ++i) f(i * N + lane);
   }
-  // Asks for a chunk's whole pieces (one lane).
-  __device__ __forceinline__ void fetch(const Part<T>& p, int j) const {
+  // Asks for a chunk's whole pieces (one lane; none where this warp has given
+  // up, as the barrier may still wait for the row before).
+  __device__ __forceinline__ void fetch(const Part<T>& p, int j) {
     const int from = p.chunk_lo(j), to = p.chunk_hi(j);
-    if (p.in.w == 0.f || from >= to) return;
+    if (p.in.w == 0.f || from >= to || (phases & kFailed)) return;
+    phases |= 0x10000u << j;
     mbar_arrive_expect_tx(bar + j, (uint32_t)(to - from) * 16);
     bulk_g2s(buf + (from - p.lo), p.z.at + (int64_t)from * N, (uint32_t)(to - from) * 16, bar + j);
   }
@@ -370,8 +403,11 @@ struct Worker {
     }
     for (int j = 0; j < p.chunks(); ++j) {
       if (p.chunk_lo(j) < p.chunk_hi(j)) {
-        ok = ok && mbar_wait(bar + j, phases >> j & 1, status);
-        phases ^= 1u << j;
+        if (!(phases & kFailed) && wait(bar + j, phases >> j & 1)) {
+          phases ^= 0x10001u << j;
+        } else {
+          phases |= kNoChunk;
+        }
       }
       const int end = min(p.count(), (j + 1) * kChunk);
       int i = j * kChunk + lane;
@@ -379,7 +415,7 @@ struct Worker {
       for (; i < end; i += 32) add_pieces<T, 1>(buf + i, k2, r.m, r.s);
       summed(j);
     }
-    if (!ok) r.s = NAN;
+    if (phases & kFailed) r.s = NAN;
     return r;
   }
   // The part's gradient c (onehot - softmax), softmax z = 2^((x - m) k2 - ls),
@@ -429,11 +465,6 @@ struct Worker {
       for (int e = e0 + lane; e < e1; e += 32) out[e] = vals()[e - p.lo * N];
     }
   }
-  // A wait ran out: waits (as long at most) for the copies that may still be on their way.
-  __device__ __forceinline__ void settle(const Part<T>& p) {
-    for (int j = 0; j < p.chunks(); ++j)
-      if (p.in.w != 0.f && p.chunk_lo(j) < p.chunk_hi(j) && !mbar_wait(bar + j, phases >> j & 1, status)) break;
-  }
 };
 
 // Long rows: the warps of a cluster of CTAs take a row.  Each warp copies its
@@ -448,7 +479,7 @@ struct Worker {
 // idle.  Memory bounds it: N=4096 V=131072 bf16 296 us, 96% of the copy rate.
 template <typename T, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, kMinWarps / WARPS)
-    k_policy(ftmoe_policy_args a, int part_pieces, int further, uint32_t* status) {
+    k_policy(ftmoe_policy_args a, int part_pieces, int further, Waits waits, uint32_t* status) {
   extern __shared__ __align__(128) unsigned char policy_smem[];
   __shared__ uint64_t bars[WARPS][kMaxChunks];
   __shared__ uint64_t meet[2], ask[2];
@@ -459,7 +490,7 @@ __global__ void __launch_bounds__(WARPS * 32, kMinWarps / WARPS)
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), log2_ranks = 31 - __clz(ranks);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool speaks = rank == 0 && threadIdx.x == 0;
-  Worker<T> w(a, lane, status, reinterpret_cast<Pack<T, N>*>(policy_smem) + warp * part_pieces, bars[warp]);
+  Worker<T> w(a, lane, status, reinterpret_cast<Pack<T, N>*>(policy_smem) + warp * part_pieces, bars[warp], waits);
   if (lane < kMaxChunks) mbar_init(bars[warp] + lane, 1);
   if (threadIdx.x < 2) {
     mbar_init(meet + threadIdx.x, 1);
@@ -473,8 +504,8 @@ __global__ void __launch_bounds__(WARPS * 32, kMinWarps / WARPS)
   bool more = true;
   Part<T> p = part_of(blockIdx.x >> log2_ranks);  // the grid has no more clusters than rows
   check_target(a, p.in, speaks, status);
-  if (lane == 0)
-    for (int j = 0; j < p.chunks(); ++j) w.fetch(p, j);
+  if (lane == 0)  // the test withholds the first chunk of one warp
+    for (int j = waits.withhold && blockIdx.x == 0 && warp == WARPS - 1; j < p.chunks(); ++j) w.fetch(p, j);
   cluster.sync();  // every CTA's barriers are set before a peer uses them
   // Thread 0 of each CTA: the number of a further row, into a slot.  With a
   // gradient the next row is needed late in a row, and asked for at its start
@@ -485,7 +516,7 @@ __global__ void __launch_bounds__(WARPS * 32, kMinWarps / WARPS)
     if (rank == 0) ask_for_row(response + slot, ask + slot);
   };
   if (!a.dlogits && further && threadIdx.x == 0) ask_into(0);
-  while (more && w.ok) {
+  while (more) {
     const uint32_t slot = round & 1, turn = round >> 1 & 1;
     if (threadIdx.x == 0) {
       mbar_arrive_expect_tx(meet + slot, (uint32_t)(ranks * WARPS * sizeof(MaxSum)));
@@ -498,8 +529,8 @@ __global__ void __launch_bounds__(WARPS * 32, kMinWarps / WARPS)
       more = false;
       if (!further) return;
       uint32_t cta = 0;
-      w.ok = w.ok && mbar_wait(ask + slot, turn, status);
-      more = w.ok && row_given(response + slot, cta);
+      if (w.wait(ask + slot, turn)) more = row_given(response + slot, cta);
+      else w.phases |= kNoCluster;
       fence_async_smem();  // read before the slot is given again
       if (more) next = part_of(cta >> log2_ranks);
     };
@@ -530,12 +561,20 @@ __global__ void __launch_bounds__(WARPS * 32, kMinWarps / WARPS)
     // Every warp tells every CTA.  Two sets of slots suffice: a warp sends
     // into a set again two rows on, when it has heard in the next row from
     // every warp of the cluster, each after its reads here.
+    // A wait that ran out makes the row's sum NaN, here and in every CTA that hears
+    // of it; the wait for the others is longer than those before it together.
     static_assert(kMaxRanks * WARPS <= 32, "a lane a sender");
+    if (w.phases & kFailed) run.s = NAN;
     run = warp_join(run, w.k2);
     if (lane < ranks) send(run, &exchange[slot][rank * WARPS + warp], meet + slot, lane);
-    w.ok = mbar_wait(meet + slot, turn, status) && w.ok;
-    run = warp_join(lane < ranks * WARPS ? exchange[slot][lane] : MaxSum{-FLT_MAX, 0.f}, w.k2);
-    if (!w.ok) run.s = NAN;
+    if (!mbar_wait(meet + slot, turn, status, waits.meeting_ns)) w.phases |= kNoCluster;
+    run = lane < ranks * WARPS ? exchange[slot][lane] : MaxSum{-FLT_MAX, 0.f};
+    if (w.phases & kFailed) run.s = NAN;
+    run = warp_join(run, w.k2);
+    if (isnan(run.s)) {
+      w.phases |= __reduce_or_sync(0xffffffffu, w.phases) & kFailed;
+      if (w.phases & kNoCluster) more = false;
+    }
     ++round;
     float c = 0.f;
     const float log2_s = log2f(run.s);
@@ -560,25 +599,32 @@ __global__ void __launch_bounds__(WARPS * 32, kMinWarps / WARPS)
       bulk_wait_read<0>();
       for (; asked < next_chunks; ++asked) w.fetch(next, asked);
     }
-    w.ok = __all_sync(0xffffffffu, w.ok);
     p = next;
   }
   pdl_launch_dependents();
   if (lane == 0) bulk_wait_read<0>();
-  if (!w.ok) w.settle(p);
+  // No CTA leaves before every message and question of the cluster is on its way
+  // (each wait before has its limit), nor, if a wait ran out, before what may still
+  // come to it has come or had the limit's time once more.
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (!(w.phases & kFailed)) return;
+  settle(bars[warp], w.phases, lane == 0, waits.limit_ns, status);
+  if (w.phases & kNoCluster) settle_cluster(meet, further ? ask : nullptr, round, waits.limit_ns, status);
 }
 
 // Short rows: a warp takes a row, and has the next one on its way in a second
 // buffer while it turns one into its gradient.
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32, kMinWarps / kWarps)
-    k_policy_short(ftmoe_policy_args a, int pieces, uint32_t* status) {
+    k_policy_short(ftmoe_policy_args a, int pieces, Waits waits, uint32_t* status) {
   extern __shared__ __align__(128) unsigned char policy_smem[];
   __shared__ uint64_t bars[2][kWarps][kShortChunks];
   constexpr int N = Row<T>::N;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Pack<T, N>* first = reinterpret_cast<Pack<T, N>*>(policy_smem) + warp * 2 * pieces;
-  Worker<T> w(a, lane, status, first, bars[0][warp]);
+  Worker<T> w(a, lane, status, first, bars[0][warp], waits);
   if (lane < 2 * kShortChunks) mbar_init(bars[lane / kShortChunks][warp] + lane % kShortChunks, 1);
   fence_mbar_init();
   __syncwarp();
@@ -596,14 +642,14 @@ __global__ void __launch_bounds__(kWarps * 32, kMinWarps / kWarps)
     w.phases = other_phases;
     other_phases = t;
   };
-  auto fetch_row = [&](const Part<T>& p) {  // one lane
-    for (int j = 0; j < p.chunks(); ++j) w.fetch(p, j);
+  auto fetch_row = [&](const Part<T>& p, int j) {  // one lane
+    for (; j < p.chunks(); ++j) w.fetch(p, j);
   };
   Part<T> p = w.part_of(n, 0, 0, 1, 0);
   check_target(a, p.in, lane == 0, status);
-  if (lane == 0) fetch_row(p);
+  if (lane == 0) fetch_row(p, waits.withhold && blockIdx.x == 0 && warp == 0);  // the test withholds one warp's first chunk
   bool more = true;
-  while (more && w.ok) {
+  while (more) {  // once a wait has run out, the warp's rows come out as NaN, and none is asked for
     n += step;
     more = n < a.N;
     Part<T> next = p;
@@ -619,7 +665,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinWarps / kWarps)
       turn();
       if (lane == 0) {
         bulk_wait_read<0>();  // the other buffer's gradient has left
-        fetch_row(next);
+        fetch_row(next, 0);
       }
       turn();
     }
@@ -632,12 +678,12 @@ __global__ void __launch_bounds__(kWarps * 32, kMinWarps / kWarps)
       write_uncounted(a, p.in.n);
     }
     if (a.dlogits) w.gradient(p, run.m, log2_s, c, zy, [](int) {});
-    w.ok = __all_sync(0xffffffffu, w.ok);
     p = next;
     turn();
   }
   if (lane == 0) bulk_wait_read<0>();
-  if (!w.ok) w.settle(p);
+  if (!(w.phases & kFailed) || lane != 0) return;  // (a lane that fetched and waited in time has nothing on its way)
+  for (int s = 0; s < 2; ++s, turn()) settle(w.bar, w.phases, true, waits.limit_ns, status);
 }
 
 // Rows too long for a cluster's shared memory (8 parts of 216 KB): the logits are
@@ -779,7 +825,7 @@ constexpr int kTwoWarpBytes = 24 * 1024;
 
 static_assert(kShortBytes / 16 <= kShortChunks * kChunk && 2 * kShortChunks <= 32,
               "a short row's chunks have barriers");
-static_assert(kStageMax / 16 / kWarps <= kMaxChunks * kChunk && kMaxChunks <= 32,
+static_assert(kStageMax / 16 / kWarps <= kMaxChunks * kChunk && kMaxChunks <= 14,
               "a part's chunks have barriers and phases");
 
 cudaError_t policy_set_limits() {
@@ -838,12 +884,14 @@ cudaError_t launch_policy_loss(const TrainDevice& d, const ftmoe_policy_args& a,
     const int64_t room = is_short ? d.num_sms * resident(smem) : staged ? INT32_MAX / ranks : 1 << 24;
     c.gridDim = dim3((unsigned)(std::min(want, room) * ranks));
     const int further = a.N * ranks > d.num_sms;  // else no cluster waits to be launched
+    const uint64_t limit_ns = d.test_wait_ns ? d.test_wait_ns : kWaitLimitNs;
+    const Waits waits{limit_ns, 4 * limit_ns, d.test_wait_ns != 0};
     cudaError_t e = with_dtype(a.dtype, [&](auto type) {
       using T = decltype(type);
       if (!staged) return cudaLaunchKernelEx(&c, k_policy_long<T>, a, d.status);
-      if (is_short) return cudaLaunchKernelEx(&c, k_policy_short<T>, a, (int)pieces, d.status);
+      if (is_short) return cudaLaunchKernelEx(&c, k_policy_short<T>, a, (int)pieces, waits, d.status);
       const auto k = warps == 2 ? k_policy<T, 2> : k_policy<T, kWarps>;
-      return cudaLaunchKernelEx(&c, k, a, (int)part(ranks), further, d.status);
+      return cudaLaunchKernelEx(&c, k, a, (int)part(ranks), further, waits, d.status);
     });
     if (e != cudaSuccess) return e;
   }

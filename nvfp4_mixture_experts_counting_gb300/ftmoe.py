@@ -129,6 +129,7 @@ SIGNATURES = {
     "ftmoe_embed_backward": ([C.c_void_p, C.c_int, C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int, C.c_float,
                               C.c_int64, C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p], C.c_int),
     "ftmoe_policy_loss": ([C.POINTER(PolicyArgs), C.c_void_p], C.c_int),
+    "ftmoe_test_withhold_policy": ([C.c_int, C.c_int64], C.c_int),
     "ftmoe_adamw": ([C.POINTER(AdamwTensor), C.c_int, C.POINTER(AdamwParams), C.c_void_p], C.c_int),
     "ftmoe_ops_status": ([C.c_void_p], C.c_int),
 }
@@ -407,6 +408,10 @@ def ftmoe_policy_loss(args: PolicyArgs, stream=None):
     _check(lib().ftmoe_policy_loss(C.byref(args), _stream(stream)), "ftmoe_policy_loss")
 
 
+def ftmoe_test_withhold_policy(enable: bool, wait_limit_ns: int = 0):
+    _check(lib().ftmoe_test_withhold_policy(int(enable), wait_limit_ns), "ftmoe_test_withhold_policy")
+
+
 class AdamwList:
     """The tensors of ftmoe_adamw: made once, kept with references to them."""
 
@@ -438,7 +443,7 @@ def ftmoe_adamw(tensors: AdamwList, lr: float, beta1: float = 0.9, beta2: float 
 
 
 def ftmoe_ops_status(stream=None) -> int:
-    """Status of the training operators' range checks since the last call (0 or DEVICE_CHECK)."""
+    """Status of the training operators' checks and waits since the last call (0, DEVICE_CHECK or TIMEOUT)."""
     return lib().ftmoe_ops_status(_stream(stream))
 
 

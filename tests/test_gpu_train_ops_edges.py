@@ -145,3 +145,34 @@ def test_status_loses_no_mark_of_another_stream():
         stop.set()
         thread.join()
     assert lost == 0
+
+
+# ----------------------------------------------------------------- policy loss: a wait that runs out
+
+@pytest.mark.parametrize("N,V,dtype", [
+    (16384, 65, FP32), (700, 130, BF16),           # a warp a row, several rows or one
+    (1300, 4500, BF16), (300, 16001, FP16),        # two and four warps
+    (300, 131072, BF16), (700, 50001, FP32), (3, 131072, BF16), (1, 20000, BF16)])
+@pytest.mark.parametrize("grad", [True, False])
+def test_policy_loss_wait_that_runs_out(N, V, dtype, grad):
+    """A chunk is never asked for: its wait ends after 2 ms, the call reports it, rows come out as they should or
+    as NaN, and the next call is as good as new."""
+    i = policy_inputs(N + V, N, V, dtype, masked=0.3)
+    i["weight"][0] = 1.0 / N
+    want = policy(i, grad=grad, kl_coef=0.1)
+    assert ftmoe.ftmoe_ops_status() == 0
+    ftmoe.ftmoe_test_withhold_policy(True, 2_000_000)
+    try:
+        got = policy(i, grad=grad, kl_coef=0.1)
+    finally:
+        ftmoe.ftmoe_test_withhold_policy(False)
+    assert ftmoe.ftmoe_ops_status() == -7 and ftmoe.ftmoe_ops_status() == 0
+    assert bool(torch.isnan(got[0]).all())
+    rows = [(g.view(N, -1), w.view(N, -1)) for g, w in zip(got[1:], want[1:]) if w is not None]
+    same = torch.stack([(g == w).all(1) for g, w in rows]).all(0)
+    lost = torch.stack([torch.isnan(g).all(1) for g, _ in rows]).all(0)
+    assert bool((same ^ lost).all())
+    assert bool(lost[0]) and (N < 300 or bool(same.any()))
+    again = policy(i, grad=grad, kl_coef=0.1)
+    assert ftmoe.ftmoe_ops_status() == 0
+    assert all(torch.equal(a, w) for a, w in zip(again, want) if w is not None)
