@@ -384,7 +384,8 @@ def ftmoe_embed_backward(dout, ids, N: int, V: int, H: int, scale: float, paddin
 def policy_args(logits, targets, old_logp, ref_logp, advantage, weight, loss, row_loss, logp=None, dlogits=None,
                 temperature: float = 1.0, clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
                 grad_scale: float = 1.0) -> PolicyArgs:
-    """Arguments of ftmoe_policy_loss; logits and dlogits [N, V] may have any row stride (last dimension dense)."""
+    """Arguments of ftmoe_policy_loss, kept with references to the tensors; logits and dlogits [N, V] may have any
+    row stride (last dimension dense)."""
     N, V = logits.shape
     ld, step = logits.stride()
     at, ld_d, step_d = None, 0, 1
@@ -398,10 +399,12 @@ def policy_args(logits, targets, old_logp, ref_logp, advantage, weight, loss, ro
         raise ValueError("a target for each row of logits expected")
     if N <= 1:  # a single row's stride says nothing
         ld = ld_d = V
-    return PolicyArgs(logits.data_ptr(), _dtype(logits), targets.element_size(), N, V, ld, _dense(targets),
+    args = PolicyArgs(logits.data_ptr(), _dtype(logits), targets.element_size(), N, V, ld, _dense(targets),
                       _floats(old_logp, N), _floats(ref_logp, N), _floats(advantage, N), _floats(weight, N), temperature,
                       clip_low, clip_high, kl_coef, grad_scale, _floats(loss, 1), _floats(row_loss, N),
                       _floats(logp, N), at, ld_d)
+    args.tensors = (logits, targets, old_logp, ref_logp, advantage, weight, loss, row_loss, logp, dlogits)
+    return args
 
 
 def ftmoe_policy_loss(args: PolicyArgs, stream=None):
