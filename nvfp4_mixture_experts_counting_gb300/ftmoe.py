@@ -167,11 +167,18 @@ def _ptr(t) -> Optional[int]:
     return t.ctypes.data
 
 
+_current = None  # torch's functions for the current stream, once torch is there
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        # the handle alone: a Stream object costs some 3 us a call
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        global _current
+        if _current is None:
+            import torch
+            # the handle alone: a Stream object costs some 3 us a call
+            _current = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+        raw, device = _current
+        return raw(device())
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream
     return int(stream)
@@ -299,17 +306,38 @@ def ftmoe_quantize_activations(a, rows: int, K: int, codes, scales, stream=None)
 # ----------------------------------------------------------------- training operators
 
 BF16, FP32, FP16 = 0, 1, 2
-_DTYPES = {}  # torch.dtype -> code, once torch is there
+_INT32, _INT64 = 3, 4
+
+
+class _Codes(dict):
+    """torch.dtype -> code, filled once torch is there; -1 for other types."""
+
+    def __missing__(self, dtype):
+        import torch
+        self.update({torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16, torch.int32: _INT32,
+                     torch.int64: _INT64})
+        return self.setdefault(dtype, -1)
+
+
+_CODES = _Codes()
 
 
 def _dtype(t) -> int:
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16})
-    try:
-        return _DTYPES[t.dtype]
-    except KeyError:
-        raise TypeError(f"bf16, fp32 or fp16 expected, got {t.dtype}") from None
+    code = _CODES[t.dtype]
+    if code not in (BF16, FP32, FP16):
+        raise TypeError(f"bf16, fp32 or fp16 expected, got {t.dtype}")
+    return code
+
+
+def _array(t, code: int, n: int):
+    """Address of a contiguous tensor of n values or more of the type that `code` names (None stays None)."""
+    if t is None:
+        return None
+    if _CODES[t.dtype] != code:
+        raise TypeError(f"{('bf16', 'fp32', 'fp16', 'int32', 'int64')[code]} expected, got {t.dtype}")
+    if t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{n} or more contiguous values expected, got {t.numel()} with strides {t.stride()}")
+    return t.data_ptr()
 
 
 def _dense(t):
@@ -339,26 +367,44 @@ def _floats(t, n: int):
 
 def ftmoe_dispatch(x, T: int, H: int, topk_idx, top_k: int, E: int, offsets, perm, inv, xs, stream=None):
     """Rows of x sorted by expert into xs, and the sort's tables (x and xs None: the tables alone)."""
-    _check(lib().ftmoe_dispatch(_dense(x), BF16 if x is None else _dtype(x), T, H, _words(topk_idx), top_k, E,
-                                _dense(offsets), _dense(perm), _dense(inv), _dense(xs), _stream(stream)),
-           "ftmoe_dispatch")
+    P, dtype = T * top_k, BF16 if x is None else _dtype(x)
+    # A decode step's call takes some 5 us on the host: one look at all tensors (6 calls of _array take 0.3 us
+    # more), and one by one only where something is absent or wrong.
+    if (x is None or xs is None or topk_idx is None or offsets is None or perm is None or inv is None
+            or _CODES[inv.dtype] != _INT32 or not topk_idx.dtype is offsets.dtype is perm.dtype is inv.dtype
+            or xs.dtype is not x.dtype or x.numel() < T * H or xs.numel() < P * H or topk_idx.numel() < P
+            or perm.numel() < P or inv.numel() < P or offsets.numel() <= E
+            or not (x.is_contiguous() and xs.is_contiguous() and topk_idx.is_contiguous() and perm.is_contiguous()
+                    and inv.is_contiguous() and offsets.is_contiguous())):
+        rc = lib().ftmoe_dispatch(_array(x, dtype, T * H), dtype, T, H, _array(topk_idx, _INT32, P), top_k, E,
+                                  _array(offsets, _INT32, E + 1), _array(perm, _INT32, P), _array(inv, _INT32, P),
+                                  _array(xs, dtype, P * H), _stream(stream))
+    else:
+        rc = lib().ftmoe_dispatch(x.data_ptr(), dtype, T, H, topk_idx.data_ptr(), top_k, E, offsets.data_ptr(),
+                                  perm.data_ptr(), inv.data_ptr(), xs.data_ptr(), _stream(stream))
+    _check(rc, "ftmoe_dispatch")
 
 
 def ftmoe_combine(ys, T: int, H: int, top_k: int, inv, w, out, stream=None):
     """out[t] = sum_j w[t, j] ys[inv[t, j]]; w None: weights of one (the gradient of ftmoe_dispatch)."""
-    _check(lib().ftmoe_combine(_dense(ys), _dtype(ys), T, H, top_k, _words(inv), _words(w), _dense(out),
-                               _stream(stream)), "ftmoe_combine")
+    P, dtype = T * top_k, _dtype(ys)
+    _check(lib().ftmoe_combine(_array(ys, dtype, P * H), dtype, T, H, top_k, _array(inv, _INT32, P),
+                               _array(w, FP32, P), _array(out, dtype, T * H), _stream(stream)), "ftmoe_combine")
 
 
 def ftmoe_combine_backward(dout, ys, T: int, H: int, top_k: int, inv, w, dys, dw, stream=None):
-    _check(lib().ftmoe_combine_backward(_dense(dout), _dense(ys), _dtype(dout), T, H, top_k, _words(inv), _words(w),
-                                        _dense(dys), _words(dw), _stream(stream)), "ftmoe_combine_backward")
+    P, dtype = T * top_k, _dtype(dout)
+    _check(lib().ftmoe_combine_backward(_array(dout, dtype, T * H), _array(ys, dtype, P * H), dtype, T, H, top_k,
+                                        _array(inv, _INT32, P), _array(w, FP32, P), _array(dys, dtype, P * H),
+                                        _array(dw, FP32, P), _stream(stream)), "ftmoe_combine_backward")
 
 
 def ftmoe_route_backward(logits, topk_idx, topk_w, dw, T: int, E: int, top_k: int, norm_topk_prob: bool, dlogits,
                          stream=None):
-    _check(lib().ftmoe_route_backward(_words(logits), _words(topk_idx), _words(topk_w), _words(dw), T, E, top_k,
-                                      int(norm_topk_prob), _words(dlogits), _stream(stream)), "ftmoe_route_backward")
+    P = T * top_k
+    _check(lib().ftmoe_route_backward(_array(logits, FP32, T * E), _array(topk_idx, _INT32, P),
+                                      _array(topk_w, FP32, P), _array(dw, FP32, P), T, E, top_k, int(norm_topk_prob),
+                                      _array(dlogits, FP32, T * E), _stream(stream)), "ftmoe_route_backward")
 
 
 def ftmoe_embed(table, V: int, H: int, ids, N: int, scale: float, out, stream=None):

@@ -34,3 +34,75 @@ def test_policy_args_keep_their_tensors():
     assert [n for n, r in alive.items() if r() is None] == []
     del args
     assert [n for n, r in alive.items() if r() is not None] == []
+
+
+# what each call's tensors are: name -> (values, type); the rest of its arguments; the order
+CALLS = {
+    "ftmoe_dispatch": (dict(x=(64, "f16"), topk_idx=(8, "i32"), offsets=(6, "i32"), perm=(8, "i32"), inv=(8, "i32"),
+                            xs=(128, "f16")), dict(T=4, H=16, top_k=2, E=5)),
+    "ftmoe_combine": (dict(ys=(128, "f16"), inv=(8, "i32"), w=(8, "f32"), out=(64, "f16")), dict(T=4, H=16, top_k=2)),
+    "ftmoe_combine_backward": (dict(dout=(64, "f16"), ys=(128, "f16"), inv=(8, "i32"), w=(8, "f32"),
+                                    dys=(128, "f16"), dw=(8, "f32")), dict(T=4, H=16, top_k=2)),
+    "ftmoe_route_backward": (dict(logits=(20, "f32"), topk_idx=(8, "i32"), topk_w=(8, "f32"), dw=(8, "f32"),
+                                  dlogits=(20, "f32")), dict(T=4, E=5, top_k=2, norm_topk_prob=False)),
+}
+
+
+def tensors(name, **changed):
+    """The call's tensors: `changed` gives some a kind of fault."""
+    torch = pytest.importorskip("torch")
+    types = {"f16": torch.float16, "f32": torch.float32, "i32": torch.int32, "ids": torch.int64, "u8": torch.uint8}
+    made = {}
+    for key, (n, kind) in CALLS[name][0].items():
+        fault, dtype = changed.get(key), types[kind]
+        if fault == "short":
+            made[key] = torch.zeros(n - 1, dtype=dtype)
+        elif fault == "strided":
+            made[key] = torch.zeros(2 * n, dtype=dtype)[::2]
+        elif fault is not None:
+            made[key] = torch.zeros(n, dtype=getattr(torch, fault))
+        else:
+            made[key] = torch.zeros(n, dtype=dtype)
+    return made
+
+
+def faults():
+    """Every tensor of every call: too short, strided, and of types of its own width and others."""
+    wrong = {"f16": ["bfloat16", "float32", "int16", "uint8"], "f32": ["int32", "float64", "bfloat16"],
+             "i32": ["float32", "int64", "int16"], "ids": ["float32", "float64", "int16"], "u8": []}
+    for name, (takes, _) in CALLS.items():
+        for key, (_, kind) in takes.items():
+            for fault in ["short", "strided"] + wrong[kind]:
+                yield name, key, fault
+
+
+class Recorder:
+    """Stands for the library: a call that gets there is a call that a GPU would run."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *a: self.calls.append(name) or 0
+
+
+@pytest.fixture()
+def recorder(monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(ftmoe, "lib", lambda: r)
+    return r
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_right_tensors_pass(recorder, name):
+    getattr(ftmoe, name)(**tensors(name), **CALLS[name][1], stream=0)
+    assert recorder.calls == [name]
+
+
+@pytest.mark.parametrize("name,key,fault", list(faults()))
+def test_wrong_tensors_are_refused(recorder, name, key, fault):
+    """On a device the kernel would read or write past the buffer's end, or values of another type."""
+    made = tensors(name, **{key: fault})
+    with pytest.raises((TypeError, ValueError)):
+        getattr(ftmoe, name)(**made, **CALLS[name][1], stream=0)
+    assert recorder.calls == []
