@@ -407,9 +407,20 @@ def ftmoe_route_backward(logits, topk_idx, topk_w, dw, T: int, E: int, top_k: in
                                       _array(dlogits, FP32, T * E), _stream(stream)), "ftmoe_route_backward")
 
 
+def _indices(t, n: int):
+    """Address and bytes of each of a contiguous tensor's n or more int32 or int64 values."""
+    if t is None:
+        return None, 8
+    code = _CODES[t.dtype]
+    if code not in (_INT32, _INT64):
+        raise TypeError(f"int32 or int64 expected, got {t.dtype}")
+    return _array(t, code, n), 4 if code == _INT32 else 8
+
+
 def ftmoe_embed(table, V: int, H: int, ids, N: int, scale: float, out, stream=None):
-    _check(lib().ftmoe_embed(_dense(table), _dtype(table), V, H, _dense(ids), ids.element_size(), N, scale, _dense(out),
-                             _stream(stream)), "ftmoe_embed")
+    dtype, (at, id_bytes) = _dtype(table), _indices(ids, N)
+    _check(lib().ftmoe_embed(_array(table, dtype, V * H), dtype, V, H, at, id_bytes, N, scale,
+                             _array(out, dtype, N * H), _stream(stream)), "ftmoe_embed")
 
 
 def ftmoe_embed_workspace(N: int, H: int) -> int:
@@ -421,8 +432,10 @@ def ftmoe_embed_workspace(N: int, H: int) -> int:
 
 def ftmoe_embed_backward(dout, ids, N: int, V: int, H: int, scale: float, padding_id: int, dtable, accumulate: bool,
                          workspace, stream=None):
-    _check(lib().ftmoe_embed_backward(_dense(dout), _dtype(dout), _dense(ids), ids.element_size(), N, V, H, scale,
-                                      padding_id, _dense(dtable), _dtype(dtable), int(accumulate), _dense(workspace),
+    dtype, table_dtype, (at, id_bytes) = _dtype(dout), _dtype(dtable), _indices(ids, N)
+    _check(lib().ftmoe_embed_backward(_array(dout, dtype, N * H), dtype, at, id_bytes, N, V, H, scale, padding_id,
+                                      _array(dtable, table_dtype, V * H), table_dtype, int(accumulate),
+                                      _dense(workspace),
                                       0 if workspace is None else workspace.numel() * workspace.element_size(),
                                       _stream(stream)), "ftmoe_embed_backward")
 

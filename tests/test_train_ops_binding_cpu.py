@@ -45,13 +45,16 @@ CALLS = {
                                     dys=(128, "f16"), dw=(8, "f32")), dict(T=4, H=16, top_k=2)),
     "ftmoe_route_backward": (dict(logits=(20, "f32"), topk_idx=(8, "i32"), topk_w=(8, "f32"), dw=(8, "f32"),
                                   dlogits=(20, "f32")), dict(T=4, E=5, top_k=2, norm_topk_prob=False)),
+    "ftmoe_embed": (dict(table=(160, "f16"), ids=(7, "ids"), out=(112, "f16")), dict(V=10, H=16, N=7, scale=1.0)),
+    "ftmoe_embed_backward": (dict(dout=(112, "any"), ids=(7, "ids"), dtable=(160, "any")),
+                             dict(V=10, H=16, N=7, scale=1.0, padding_id=-1, accumulate=False, workspace=None)),
 }
 
 
 def tensors(name, **changed):
     """The call's tensors: `changed` gives some a kind of fault."""
     torch = pytest.importorskip("torch")
-    types = {"f16": torch.float16, "f32": torch.float32, "i32": torch.int32, "ids": torch.int64, "u8": torch.uint8}
+    types = {"f16": torch.float16, "f32": torch.float32, "i32": torch.int32, "ids": torch.int64, "any": torch.float32}
     made = {}
     for key, (n, kind) in CALLS[name][0].items():
         fault, dtype = changed.get(key), types[kind]
@@ -69,7 +72,7 @@ def tensors(name, **changed):
 def faults():
     """Every tensor of every call: too short, strided, and of types of its own width and others."""
     wrong = {"f16": ["bfloat16", "float32", "int16", "uint8"], "f32": ["int32", "float64", "bfloat16"],
-             "i32": ["float32", "int64", "int16"], "ids": ["float32", "float64", "int16"], "u8": []}
+             "i32": ["float32", "int64", "int16"], "ids": ["float32", "float64", "int16"], "any": ["float64", "int32", "uint8"]}
     for name, (takes, _) in CALLS.items():
         for key, (_, kind) in takes.items():
             for fault in ["short", "strided"] + wrong[kind]:
