@@ -357,10 +357,10 @@ def _words(t, n: int = 0):
 
 
 def _floats(t, n: int):
-    """The same for exactly n fp32 values (one look at the bytes: these are many, and made for each step)."""
+    """Address of exactly n contiguous fp32 values (None stays None)."""
     if t is None:
         return None
-    if t.nbytes != 4 * n or not t.is_contiguous():
+    if t.nbytes != 4 * n or _CODES[t.dtype] != FP32 or not t.is_contiguous():
         raise ValueError(f"{n} contiguous fp32 values expected, got {t.numel()} of {t.dtype}")
     return t.data_ptr()
 
@@ -445,23 +445,22 @@ def policy_args(logits, targets, old_logp, ref_logp, advantage, weight, loss, ro
                 grad_scale: float = 1.0) -> PolicyArgs:
     """Arguments of ftmoe_policy_loss, kept with references to the tensors; logits and dlogits [N, V] may have any
     row stride (last dimension dense)."""
-    N, V = logits.shape
+    shape, dtype = logits.shape, _dtype(logits)
+    N, V = shape
     ld, step = logits.stride()
     at, ld_d, step_d = None, 0, 1
     if dlogits is not None:
-        if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
+        if dlogits.dtype is not logits.dtype or dlogits.shape != shape:
             raise TypeError("dlogits has the shape and type of logits")
         at, (ld_d, step_d) = dlogits.data_ptr(), dlogits.stride()
     if V > 1 and (step != 1 or step_d != 1):
         raise ValueError("logits and dlogits need a dense last dimension")
-    if targets.numel() < N:
-        raise ValueError("a target for each row of logits expected")
     if N <= 1:  # a single row's stride says nothing
         ld = ld_d = V
-    args = PolicyArgs(logits.data_ptr(), _dtype(logits), targets.element_size(), N, V, ld, _dense(targets),
-                      _floats(old_logp, N), _floats(ref_logp, N), _floats(advantage, N), _floats(weight, N), temperature,
-                      clip_low, clip_high, kl_coef, grad_scale, _floats(loss, 1), _floats(row_loss, N),
-                      _floats(logp, N), at, ld_d)
+    ids, id_bytes = _indices(targets, N)
+    args = PolicyArgs(logits.data_ptr(), dtype, id_bytes, N, V, ld, ids, _floats(old_logp, N), _floats(ref_logp, N),
+                      _floats(advantage, N), _floats(weight, N), temperature, clip_low, clip_high, kl_coef, grad_scale,
+                      _floats(loss, 1), _floats(row_loss, N), _floats(logp, N), at, ld_d)
     args.tensors = (logits, targets, old_logp, ref_logp, advantage, weight, loss, row_loss, logp, dlogits)
     return args
 

@@ -109,3 +109,27 @@ def test_wrong_tensors_are_refused(recorder, name, key, fault):
     with pytest.raises((TypeError, ValueError)):
         getattr(ftmoe, name)(**made, **CALLS[name][1], stream=0)
     assert recorder.calls == []
+
+
+@pytest.mark.parametrize("key", ["old_logp", "ref_logp", "advantage", "weight", "loss", "row_loss", "logp", "targets",
+                                 "dlogits", "logits"])
+def test_policy_args_refuse_other_types(key):
+    """Of the right bytes or the right count, but not the values that the kernel reads."""
+    torch = pytest.importorskip("torch")
+    N, V = 4, 10
+    f = lambda n: torch.zeros(n)
+    made = dict(logits=torch.zeros(N, V), targets=torch.zeros(N, dtype=torch.int32), old_logp=f(N), ref_logp=f(N),
+                advantage=f(N), weight=f(N), loss=f(1), row_loss=f(N), logp=f(N), dlogits=torch.zeros(N, V))
+    assert ftmoe.policy_args(**made).id_bytes == 4
+    n = 1 if key == "loss" else N
+    if key in ("logits", "dlogits"):
+        wrong = [torch.zeros(N, V, dtype=t) for t in (torch.int32, torch.float64, torch.bfloat16)]
+    elif key == "targets":
+        wrong = [torch.zeros(N, dtype=t) for t in (torch.float32, torch.float64, torch.int16)] + [
+            torch.zeros(N - 1, dtype=torch.int64), torch.zeros(2 * N, dtype=torch.int64)[::2]]
+    else:
+        wrong = [torch.zeros(n, dtype=torch.int32), torch.zeros(2 * n, dtype=torch.bfloat16),
+                 torch.zeros(2 * n, dtype=torch.int16), torch.zeros(n, dtype=torch.float64)]
+    for t in wrong:
+        with pytest.raises((TypeError, ValueError)):
+            ftmoe.policy_args(**{**made, key: t})
