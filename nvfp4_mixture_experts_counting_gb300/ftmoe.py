@@ -349,13 +349,6 @@ def _dense(t):
     return t.data_ptr()
 
 
-def _words(t, n: int = 0):
-    """_dense of at least n fp32 or int32 values, as the C calls take them."""
-    if t is not None and (t.element_size() != 4 or t.numel() < n):
-        raise TypeError(f"{n} or more 32-bit values expected, got {t.numel()} of {t.dtype}")
-    return _dense(t)
-
-
 def _floats(t, n: int):
     """Address of exactly n contiguous fp32 values (None stays None)."""
     if t is None:
@@ -483,11 +476,13 @@ class AdamwList:
             get = t.get
             p, g, m, v = t["p"], t["g"], t["m"], t["v"]
             n = p.numel()
-            if min(g.numel(), m.numel(), v.numel()) < n or m.element_size() != v.element_size():
+            if min(g.numel(), m.numel(), v.numel()) < n or m.dtype is not v.dtype:
                 raise ValueError("g, m and v have p's values, and m and v one type")
+            if m.element_size() != 1 and _CODES[m.dtype] != FP32:
+                raise TypeError(f"m and v are fp32 or codes of one byte, got {m.dtype}")
             blocks = (n + 255) // 256
-            entries.append((_dense(p), _dense(g), _words(get("master"), n), _dense(m), _dense(v),
-                            _words(get("m_scale"), blocks), _words(get("v_scale"), blocks), n,
+            entries.append((_dense(p), _dense(g), _array(get("master"), FP32, n), _dense(m), _dense(v),
+                            _array(get("m_scale"), FP32, blocks), _array(get("v_scale"), FP32, blocks), n,
                             get("weight_decay", 0.0), _dtype(p), _dtype(g), 8 * m.element_size()))
         self.array = (AdamwTensor * len(entries))(*entries)
 
@@ -499,7 +494,7 @@ def adamw_list(tensors) -> AdamwList:
 
 def ftmoe_adamw(tensors: AdamwList, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                 step: int = 1, grad_scale=None, stream=None):
-    hp = AdamwParams(lr, beta1, beta2, eps, step, _ptr(grad_scale))
+    hp = AdamwParams(lr, beta1, beta2, eps, step, _array(grad_scale, FP32, 1))
     _check(lib().ftmoe_adamw(tensors.array, len(tensors.array), C.byref(hp), _stream(stream)), "ftmoe_adamw")
 
 

@@ -133,3 +133,34 @@ def test_policy_args_refuse_other_types(key):
     for t in wrong:
         with pytest.raises((TypeError, ValueError)):
             ftmoe.policy_args(**{**made, key: t})
+
+
+def adam_tensors(torch, bits=32, **changed):
+    n, state = 300, torch.float32 if bits == 32 else torch.uint8
+    t = dict(p=torch.zeros(n, dtype=torch.bfloat16), g=torch.zeros(n, dtype=torch.bfloat16),
+             m=torch.zeros(n, dtype=state), v=torch.zeros(n, dtype=state), master=torch.zeros(n),
+             m_scale=torch.zeros(2), v_scale=torch.zeros(2))
+    t.update(changed)
+    return t
+
+
+def test_adamw_refuses_other_types(recorder):
+    torch = pytest.importorskip("torch")
+    for bits in (8, 32):
+        made = ftmoe.adamw_list([adam_tensors(torch, bits)])
+        ftmoe.ftmoe_adamw(made, 1e-3, grad_scale=torch.ones(1), stream=0)
+        for scale in (torch.ones(1, dtype=torch.bfloat16), torch.ones(1, dtype=torch.float64), torch.ones(0),
+                      torch.ones(1, dtype=torch.int32)):
+            with pytest.raises((TypeError, ValueError)):
+                ftmoe.ftmoe_adamw(made, 1e-3, grad_scale=scale, stream=0)
+        for key, dtype, n in (("m_scale", torch.int32, 2), ("v_scale", torch.int32, 2), ("master", torch.int32, 300),
+                              ("m", torch.int32, 300), ("v", torch.int32, 300), ("p", torch.int16, 300),
+                              ("g", torch.int16, 300)):
+            with pytest.raises((TypeError, ValueError)):
+                ftmoe.adamw_list([adam_tensors(torch, bits, **{key: torch.zeros(n, dtype=dtype)})])
+    with pytest.raises((TypeError, ValueError)):  # both of a type that is neither fp32 nor codes
+        ftmoe.adamw_list([adam_tensors(torch, m=torch.zeros(300, dtype=torch.int32),
+                                       v=torch.zeros(300, dtype=torch.int32))])
+    codes = dict(m=torch.zeros(300, dtype=torch.float8_e4m3fn), v=torch.zeros(300, dtype=torch.float8_e4m3fn))
+    assert ftmoe.adamw_list([adam_tensors(torch, **codes)]).array[0].state_bits == 8
+    assert recorder.calls == ["ftmoe_adamw"] * 2
