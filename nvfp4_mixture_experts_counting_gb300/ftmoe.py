@@ -470,9 +470,9 @@ class AdamwList:
     """The tensors of ftmoe_adamw: made once, kept with references to them."""
 
     def __init__(self, tensors):
-        self.tensors = tensors
+        self.tensors = [dict(t) for t in tensors]  # the entries hold addresses, whatever becomes of the caller's dicts
         entries = []
-        for t in tensors:
+        for t in self.tensors:
             get = t.get
             p, g, m, v = t["p"], t["g"], t["m"], t["v"]
             n = p.numel()

@@ -164,3 +164,16 @@ def test_adamw_refuses_other_types(recorder):
     codes = dict(m=torch.zeros(300, dtype=torch.float8_e4m3fn), v=torch.zeros(300, dtype=torch.float8_e4m3fn))
     assert ftmoe.adamw_list([adam_tensors(torch, **codes)]).array[0].state_bits == 8
     assert recorder.calls == ["ftmoe_adamw"] * 2
+
+
+def test_adamw_list_keeps_its_tensors():
+    """Also where the caller puts others into the dicts that the list was made of."""
+    torch = pytest.importorskip("torch")
+    import weakref
+    t = adam_tensors(torch, 8)
+    alive = {n: weakref.ref(v) for n, v in t.items()}
+    made = ftmoe.adamw_list([t])
+    t.clear()
+    assert [n for n, r in alive.items() if r() is None] == []
+    del made
+    assert [n for n, r in alive.items() if r() is not None] == []
