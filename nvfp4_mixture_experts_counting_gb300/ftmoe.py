@@ -167,18 +167,17 @@ def _ptr(t) -> Optional[int]:
     return t.ctypes.data
 
 
-_current = None  # torch's functions for the current stream, once torch is there
+_raw_stream = None  # torch's handle of a device's current stream, once torch is there
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        global _current
-        if _current is None:
+        global _raw_stream
+        if _raw_stream is None:
             import torch
-            # the handle alone: a Stream object costs some 3 us a call
-            _current = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
-        raw, device = _current
-        return raw(device())
+            _raw_stream = torch._C._cuda_getCurrentRawStream
+        # the handle alone (a Stream object costs some 3 us a call), of the current device (-1)
+        return _raw_stream(-1)
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream
     return int(stream)
@@ -314,6 +313,7 @@ class _Codes(dict):
 
     def __missing__(self, dtype):
         import torch
+        self.fp32 = torch.float32
         self.update({torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16, torch.int32: _INT32,
                      torch.int64: _INT64})
         return self.setdefault(dtype, -1)
@@ -349,11 +349,11 @@ def _dense(t):
     return t.data_ptr()
 
 
-def _floats(t, n: int):
-    """Address of exactly n contiguous fp32 values (None stays None)."""
+def _floats(t, n: int, fp32):
+    """Address of exactly n contiguous fp32 values (None stays None); `fp32` is torch's name of the type."""
     if t is None:
         return None
-    if t.nbytes != 4 * n or _CODES[t.dtype] != FP32 or not t.is_contiguous():
+    if t.nbytes != 4 * n or t.dtype is not fp32 or not t.is_contiguous():
         raise ValueError(f"{n} contiguous fp32 values expected, got {t.numel()} of {t.dtype}")
     return t.data_ptr()
 
@@ -405,9 +405,11 @@ def _indices(t, n: int):
     if t is None:
         return None, 8
     code = _CODES[t.dtype]
-    if code not in (_INT32, _INT64):
+    if code != _INT32 and code != _INT64:
         raise TypeError(f"int32 or int64 expected, got {t.dtype}")
-    return _array(t, code, n), 4 if code == _INT32 else 8
+    if t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{n} or more contiguous values expected, got {t.numel()} with strides {t.stride()}")
+    return t.data_ptr(), 4 if code == _INT32 else 8
 
 
 def ftmoe_embed(table, V: int, H: int, ids, N: int, scale: float, out, stream=None):
@@ -450,10 +452,11 @@ def policy_args(logits, targets, old_logp, ref_logp, advantage, weight, loss, ro
         raise ValueError("logits and dlogits need a dense last dimension")
     if N <= 1:  # a single row's stride says nothing
         ld = ld_d = V
-    ids, id_bytes = _indices(targets, N)
-    args = PolicyArgs(logits.data_ptr(), dtype, id_bytes, N, V, ld, ids, _floats(old_logp, N), _floats(ref_logp, N),
-                      _floats(advantage, N), _floats(weight, N), temperature, clip_low, clip_high, kl_coef, grad_scale,
-                      _floats(loss, 1), _floats(row_loss, N), _floats(logp, N), at, ld_d)
+    f32, (ids, id_bytes) = _CODES.fp32, _indices(targets, N)
+    args = PolicyArgs(logits.data_ptr(), dtype, id_bytes, N, V, ld, ids, _floats(old_logp, N, f32),
+                      _floats(ref_logp, N, f32), _floats(advantage, N, f32), _floats(weight, N, f32), temperature,
+                      clip_low, clip_high, kl_coef, grad_scale, _floats(loss, 1, f32), _floats(row_loss, N, f32),
+                      _floats(logp, N, f32), at, ld_d)
     args.tensors = (logits, targets, old_logp, ref_logp, advantage, weight, loss, row_loss, logp, dlogits)
     return args
 

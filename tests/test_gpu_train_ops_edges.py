@@ -176,3 +176,13 @@ def test_policy_loss_wait_that_runs_out(N, V, dtype, grad):
     again = policy(i, grad=grad, kl_coef=0.1)
     assert ftmoe.ftmoe_ops_status() == 0
     assert all(torch.equal(a, w) for a, w in zip(again, want) if w is not None)
+
+
+# ----------------------------------------------------------------- streams
+
+def test_calls_without_a_stream_take_the_current_one():
+    assert ftmoe._stream(None) == torch.cuda.current_stream().cuda_stream
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert ftmoe._stream(None) == side.cuda_stream != 0
+    assert ftmoe._stream(side) == side.cuda_stream
