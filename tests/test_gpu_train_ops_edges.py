@@ -11,7 +11,9 @@ import torch
 
 from nvfp4_mixture_experts_counting_gb300 import ftmoe
 
-from test_gpu_train_ops import BF16, DEV, EPS, FP16, FP32, TINY, UNIT, gen, policy, policy_inputs, randn, within
+import test_gpu_train_ops as base
+from test_gpu_train_ops import (BF16, DEV, EPS, FP16, FP32, TINY, UNIT, gen, policy, policy_check, policy_inputs,
+                                randn, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -145,6 +147,33 @@ def test_status_loses_no_mark_of_another_stream():
         stop.set()
         thread.join()
     assert lost == 0
+
+
+# ----------------------------------------------------------------- variants that other sizes do not reach
+
+@pytest.mark.parametrize("T,k,H,dtype", [
+    (130, 9, 2560, BF16), (400, 3, 2560, BF16), (700, 8, 2560, BF16), (700, 3, 1284, FP32), (1300, 2, 2560, FP16),
+    (130, 3, 1001, BF16), (400, 2, 1001, FP32), (1300, 3, 1001, FP16)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_combine_backward_of_one_to_eight_warps_a_token(T, k, H, dtype, in_place):
+    base.test_combine_backward(T, k, 12, H, dtype, 0.3, in_place)
+
+
+@pytest.mark.parametrize("T,k", [(2047, 1), (1024, 2), (256, 8), (683, 3), (2049, 1), (1025, 2), (257, 8), (32768, 1),
+                                 (4097, 8)])
+def test_dispatch_around_its_limits(T, k):
+    """2048 pairs are the last that one launch counts, 32768 the last of the smaller sort."""
+    base.test_dispatch(T, k, 40, 8, BF16, 0.1)
+
+
+@pytest.mark.parametrize("N,V,dtype", [(5, 900001, BF16), (3, 1048576, FP16), (70, 450000, FP32)])
+def test_policy_loss_of_rows_read_twice(N, V, dtype):
+    i = policy_inputs(N + V, N, V, dtype, masked=0.3)
+    kw = dict(temperature=0.9, kl_coef=0.05, clip_high=0.3)
+    policy_check(i, policy(i, **kw), dtype, **kw)
+    apart = policy(i, ld_d=V + 5, **kw)
+    inp = policy(i, in_place=True, **kw)  # last: it overwrites the logits
+    assert torch.equal(apart[3], inp[3]) and torch.equal(apart[0], inp[0])
 
 
 # ----------------------------------------------------------------- policy loss: a wait that runs out
