@@ -557,9 +557,10 @@ int ftmoe_test_withhold_policy(int enable, int64_t wait_limit_ns);
  * state_bits 8: m and v hold one E4M3 code a value, v's of the root sqrt(v),
  * with a scale per 256 consecutive values, scale = amax * fl(1/448) and code =
  * E4M3(value * (448 * fl(1/amax))) in fp32 (blocks whose amax is below 1e-30
- * are held as zeros); a root above zero keeps at least the smallest code.  Zeros in codes and scales are the state before the first
- * step.  A gradient that is not finite spoils its value (32 bits) or its
- * block (8 bits). */
+ * are held as zeros); a root above zero keeps at least the smallest code.
+ * Zeros in codes and scales are the state before the first step.  A gradient
+ * of NaN spoils its own value.  So does an infinite one, which in 8 bits also
+ * makes the block's scales infinite: the next step spoils the whole block. */
 typedef struct {
   void* p;               /* [n] of p_dtype, updated */
   const void* g;         /* [n] of g_dtype */

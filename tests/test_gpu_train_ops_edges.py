@@ -149,6 +149,46 @@ def test_status_loses_no_mark_of_another_stream():
     assert lost == 0
 
 
+# ----------------------------------------------------------------- AdamW: gradients that are not finite
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_gradient_that_is_not_finite(value, bits):
+    """NaN spoils its own value; an infinity does too, and in 8 bits the states of its block of 256.  Other
+    blocks keep every bit."""
+    n, at = 700, 300
+    g = gen(3)
+
+    def tensors(v):
+        t = dict(p=randn(gen(4), n), g=randn(gen(5), n, std=0.1))
+        if bits == 32:
+            t.update(m=torch.zeros(n, device=DEV), v=torch.zeros(n, device=DEV))
+        else:
+            t.update(m=torch.zeros(n, dtype=torch.uint8, device=DEV), v=torch.zeros(n, dtype=torch.uint8, device=DEV),
+                     m_scale=torch.zeros(3, device=DEV), v_scale=torch.zeros(3, device=DEV))
+        if v is not None:
+            t["g"][at] = v
+        for step in (1, 2):
+            ftmoe.ftmoe_adamw(ftmoe.adamw_list([t]), lr=1e-2, beta2=0.95, step=step)
+            t["g"].copy_(randn(gen(5 + step), n, std=0.1))
+        return t["p"]
+
+    clean, dirty = tensors(None), tensors(value)
+    same = torch.ones(n, dtype=torch.bool, device=DEV)
+    same[at] = False
+    assert not bool(torch.isfinite(dirty[at]))
+    if bits == 8 and value != value or bits == 32:
+        if bits == 8:  # the block's largest is taken of the other values, which may move a code
+            same[256:512] = False
+            rest = torch.arange(n, device=DEV)
+            rest = rest[(rest >= 256) & (rest < 512) & (rest != at)]
+            assert bool(torch.isfinite(dirty[rest]).all())
+    else:
+        same[256:512] = False
+        assert bool(torch.isnan(dirty[256:512]).all())
+    assert torch.equal(dirty[same], clean[same])
+
+
 # ----------------------------------------------------------------- variants that other sizes do not reach
 
 @pytest.mark.parametrize("T,k,H,dtype", [
