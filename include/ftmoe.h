@@ -425,9 +425,10 @@ int ftmoe_quantize_activations(const void* a, int64_t rows, int K, uint8_t* code
  * nothing back to the host and may be captured in a CUDA graph once one of
  * them has run on the device (the first call looks up a device address and
  * sets kernel limits).  Sums run in fp32 or wider in a fixed order and are
- * rounded once; no call uses atomics on values, so results are bit-identical
- * run to run.  Any H, T, k and E within the limits below is taken; rows whose
- * bytes are a multiple of 16 move 16 bytes at a time.
+ * rounded once, so results are bit-identical run to run (onto an existing
+ * table the embedding gradient adds once to each value, as a reduction).  Any
+ * H, T, k and E within the limits below is taken; rows whose bytes are a
+ * multiple of 16 move 16 bytes at a time.
  *
  * Range checks inside the kernels (an expert, place, id or target out of
  * range) mark a device word and leave the item out, as each call says;
@@ -488,7 +489,10 @@ int ftmoe_embed(const void* table, int dtype, int64_t V, int H, const void* ids,
 int64_t ftmoe_embed_workspace(int64_t N, int H);
 
 /* ftmoe_embed's gradient: dtable[v] = scale * (sum over the n with ids[n] = v
- * of dout[n], in the order of n, in fp32).  Rows of no token become zeros;
+ * of dout[n], in fp32).  The order of that sum is fixed: the tokens by id and
+ * n in chunks of 32, each summed in the order of n, then an id's chunks in
+ * order (over 16 of them: every eighth together, then those eight sums).
+ * Rows of no token become zeros;
  * with `accumulate` (fp32 dtable only) the sum is added to dtable, where values
  * below the smallest normal one may count as zero, and other rows are not
  * touched.  Tokens whose id is padding_id are left out (-1: none
@@ -558,6 +562,11 @@ int ftmoe_test_withhold_policy(int enable, int64_t wait_limit_ns);
  * with a scale per 256 consecutive values, scale = amax * fl(1/448) and code =
  * E4M3(value * (448 * fl(1/amax))) in fp32 (blocks whose amax is below 1e-30
  * are held as zeros); a root above zero keeps at least the smallest code.
+ * Codes are rounded to nearest in 3 bits, so a root stays where a step changes
+ * it by less than 3 to 6 %: against the exact one it settles at 1.06 times
+ * (0.92 to 1.24 in nine of ten values) with beta2 = 0.95, 1.36 (1.12 to 1.66)
+ * with 0.99 and 1.10 (0.71 to 1.49) with 0.999, for gradients of one size in a
+ * block.  States of 32 bits have no such offset.
  * Zeros in codes and scales are the state before the first step.  A gradient
  * of NaN spoils its own value.  So does an infinite one, which in 8 bits also
  * makes the block's scales infinite: the next step spoils the whole block. */

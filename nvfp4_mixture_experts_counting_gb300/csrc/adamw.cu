@@ -311,7 +311,8 @@ __device__ __forceinline__ void step_block(const Launch<CAP>& a, const Tensor& t
 // with the next one's values on their way while it updates one.  With 32 such CTAs an
 // SM and 32 blocks each, 267 M values take 408 us (97% of the copy rate); two warps
 // a CTA take 425 us, four 472 us and eight 565 us, as a CTA then holds its place
-// until its last warp is done.
+// until its last warp is done.  A tensor with an array off its alignment moves
+// value by value (64 M values: 215 us instead of 117).
 template <typename PT, typename GT, bool MASTER, int CAP>
 __global__ void __launch_bounds__(32, 32) k_adamw_8bit(const __grid_constant__ Launch<CAP> a) {
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;

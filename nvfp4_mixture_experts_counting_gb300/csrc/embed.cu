@@ -4,9 +4,9 @@
 //   dtable[v] = scale * sum over the n with ids[n] = v of dout[n]   (v = padding_id: 0)
 //
 // The gradient sorts the tokens by id (a stable radix sort by one cluster),
-// sums each run of equal ids in the order of the tokens in fp32, and writes
-// every row of dtable once: no atomics, so the result does not depend on
-// which CTA came first.
+// sums each run of equal ids in fp32 in a fixed order (chunks of 32 sorted
+// tokens, then the chunks), and writes or adds to every row of dtable once, so
+// the result does not depend on which CTA came first.
 #include <algorithm>
 #include <type_traits>
 
@@ -25,7 +25,8 @@ constexpr int kZeroBlocks = 1024;  // blocks of table rows whose marks a CTA hol
 // Widest radix digit.  More bins cost each pass the exchange of more totals, and
 // may save a pass.  With the gradient of H=64, at V=262144 two passes of 10 bits
 // take 3 us more than three of 7 for 8191 tokens, and 58 instead of 61 us for
-// 131072; at V=1000 one of 10 instead of two of 5 takes 37 instead of 44 us there.
+// 131072; at V=1000 one of 10 instead of two of 5 takes 37 instead of 44 us there,
+// and for 8191 tokens as long (15 us).
 constexpr int kDigitBits = 9, kManyDigitBits = 10;
 constexpr int64_t kManyTokens = 65536;
 // Bytes of the table for each CTA that fills, at least: it reads all ids, however
@@ -446,8 +447,9 @@ cudaError_t launch_embed_backward(const TrainDevice& d, const void* dout, int dt
           a.nv = H / W;
           a.slices = (a.nv + 32 * Q - 1) / (32 * Q);
           a.grad_tasks = chunks * a.slices;
-          // Many CTAs that fill, as those end at different times (for 1.34 GB: 222 us with 512, 189 with 1024,
-          // 182 with 4096), but 2^25 ids read by all of them at most; blocks of up to 32 rows.
+          // Many CTAs that fill, as those end at different times (16384 tokens of a table of 1.34 GB: 260 us with 512,
+          // 224 with 1024, 214 with 2048, 208 with 4096), but 2^25 ids read by all of them at most; blocks of up to
+          // 32 rows.
           const int64_t bytes = V * H * (int64_t)sizeof(TT);
           while (2 << a.cta_bits <= std::min<int64_t>(2048, V) && bytes >> (a.cta_bits + 1) >= kFillBytes &&
                  (N << (a.cta_bits + 1)) <= 1 << 25)

@@ -334,7 +334,8 @@ __device__ __noinline__ void settle(uint64_t* bar, uint32_t phases, bool fetches
     if (!mbar_wait(bar + j, phases >> j & 1, status, limit_ns)) break;
   }
 }
-__device__ __noinline__ void settle_cluster(uint64_t* meet, uint64_t* ask, uint32_t round, uint64_t limit_ns, uint32_t* status) {
+__device__ __noinline__ void settle_cluster(uint64_t* meet, uint64_t* ask, uint32_t round, uint64_t limit_ns,
+                                            uint32_t* status) {
   for (uint32_t r = round - 1; r <= round; ++r) {
     mbar_wait(meet + (r & 1), r >> 1 & 1, status, limit_ns);
     if (ask) mbar_wait(ask + (r & 1), r >> 1 & 1, status, limit_ns);
@@ -476,7 +477,8 @@ struct Worker {
 // gradient has left its buffer (without a gradient: as soon as it is summed)
 // the next row's chunk is asked for.  Clusters take further rows from those not
 // launched yet, so rows of weight 0, which cost half or nothing, leave no SM
-// idle.  Memory bounds it: N=4096 V=131072 bf16 296 us, 96% of the copy rate.
+// idle.  Memory bounds it: N=4096 V=131072 bf16, a fifth of the rows left out,
+// 298 us, 95% of the copy rate; all rows 330 us.
 template <typename T, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, kMinWarps / WARPS)
     k_policy(ftmoe_policy_args a, int part_pieces, int further, Waits waits, uint32_t* status) {
@@ -647,7 +649,8 @@ __global__ void __launch_bounds__(kWarps * 32, kMinWarps / kWarps)
   };
   Part<T> p = w.part_of(n, 0, 0, 1, 0);
   check_target(a, p.in, lane == 0, status);
-  if (lane == 0) fetch_row(p, waits.withhold && blockIdx.x == 0 && warp == 0);  // the test withholds one warp's first chunk
+  // the test withholds one warp's first chunk
+  if (lane == 0) fetch_row(p, waits.withhold && blockIdx.x == 0 && warp == 0);
   bool more = true;
   while (more) {  // once a wait has run out, the warp's rows come out as NaN, and none is asked for
     n += step;
@@ -687,8 +690,9 @@ __global__ void __launch_bounds__(kWarps * 32, kMinWarps / kWarps)
 }
 
 // Rows too long for a cluster's shared memory (8 parts of 216 KB): the logits are
-// read a second time.  256 rows of 2^20 values: fp32 528 us, 6.1 TB/s of three
-// moves; bf16 353 us, 4.6 TB/s, where a piece holds twice the exponentials.
+// read a second time.  256 rows of 2^20 values, all with a gradient: fp32 628 us,
+// 5.1 TB/s of three moves; bf16 411 us, 3.9 TB/s, where a piece holds twice the
+// exponentials.
 template <typename T>
 __global__ void __launch_bounds__(kLongThreads) k_policy_long(ftmoe_policy_args a, uint32_t* status) {
   __shared__ MaxSum warp_part[kLongThreads / 32];
@@ -813,12 +817,12 @@ __global__ void __launch_bounds__(kSumThreads)
 constexpr int kStageMax = 216 * 1024, kSmemSm = 226 * 1024;
 // Of a CTA and of each warp besides: the system's own, barriers, slots.
 constexpr int kFixedSmem = 1280, kWarpSmem = 288;
-// Rows up to kShortBytes may be a warp's: 16384 bf16 rows of 4 KB take 37 us so and
-// 80 us as a CTA's, of 16 KB 183 and 127 us.  Up to kShortAlways they are even
+// Rows up to kShortBytes may be a warp's: 16384 bf16 rows of 4 KB take 35 us so and
+// 64 us as two warps', of 16 KB 172 and 111 us.  Up to kShortAlways they are even
 // where that leaves warps idle.
 constexpr int kShortBytes = 8 * 1024, kShortAlways = 2 * 1024;
-// Rows up to here are two warps' instead of four's: 24 KB take 80 and 86 us (8192
-// rows), 32 KB 109 and 98 us.
+// Rows up to here are two warps' instead of four's: 16384 rows of 16 KB take 111 and
+// 117 us, 8192 of 24 KB 79 and 83 us, of 32 KB 106 and 96 us.
 constexpr int kTwoWarpBytes = 24 * 1024;
 
 }  // namespace

@@ -72,7 +72,8 @@ def tensors(name, **changed):
 def faults():
     """Every tensor of every call: too short, strided, and of types of its own width and others."""
     wrong = {"f16": ["bfloat16", "float32", "int16", "uint8"], "f32": ["int32", "float64", "bfloat16"],
-             "i32": ["float32", "int64", "int16"], "ids": ["float32", "float64", "int16"], "any": ["float64", "int32", "uint8"]}
+             "i32": ["float32", "int64", "int16"], "ids": ["float32", "float64", "int16"],
+             "any": ["float64", "int32", "uint8"]}
     for name, (takes, _) in CALLS.items():
         for key, (_, kind) in takes.items():
             for fault in ["short", "strided"] + wrong[kind]:
