@@ -596,6 +596,135 @@ typedef struct {
 int ftmoe_adamw(const ftmoe_adamw_tensor* tensors, int n_tensors, const ftmoe_adamw_params* params,
                 ftmoe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The layer on banks of 8-bit codes: routing from logits, the quantiser, the
+ * experts' products and SwiGLU, with the gradients that pass through them to
+ * the tokens and the router.  The pages serve their banks through formats
+ * that this product reads one of (FTMOE_FMT_FP8_BLOCK) and have no
+ * counterpart to the calls.
+ *
+ * Like the training operators they need no handle, run on the current device,
+ * are asynchronous on `stream`, allocate nothing, may be captured once one of
+ * them has run on the device, give the same bits run to run, and mark the word
+ * that ftmoe_ops_status reads.  One forward pass of a layer:
+ *
+ *   ftmoe_route_topk       logits -> experts and weights of each token
+ *   ftmoe_dispatch         (x NULL) tables of the pairs sorted by expert
+ *   ftmoe_fp8_quantize     tokens -> codes in their experts' rows
+ *   ftmoe_fp8_matmul       gate_up with SwiGLU -> codes of the intermediate
+ *   ftmoe_fp8_matmul       down -> rows
+ *   ftmoe_combine          rows -> tokens
+ *
+ * and to train through it (codes are not trained: the bank stays as it is)
+ * gate_up without `swiglu`, ftmoe_swiglu; then back ftmoe_combine_backward,
+ * ftmoe_fp8_quantize (inv NULL), ftmoe_fp8_matmul with `transpose`,
+ * ftmoe_swiglu_backward, ftmoe_fp8_matmul with `transpose`, ftmoe_combine
+ * without weights, and ftmoe_route_topk_backward.
+ *
+ * Codes are E4M3 (fn) bytes.  Activations have a scale for 128 consecutive
+ * values of a row, stored block by block: scales [ceil(K/128)][rows].  A block
+ * of largest magnitude a has scale = fl(a / 448) and code = E4M3(x fl(448 / a))
+ * in fp32, round to nearest even; blocks with a < 1e-30 are held as zeros; a
+ * NaN or an infinity spoils its block.  Weights are FTMOE_FMT_FP8_BLOCK's
+ * arrays: codes [E][N][K], scales [E][ceil(N/128)][ceil(K/128)]. */
+
+typedef enum { FTMOE_SCORE_SOFTMAX = 0, FTMOE_SCORE_SIGMOID = 1 } ftmoe_score;
+
+/* Experts of each token.  With l = logits[t]:
+ *   s_e = softmax(l)_e or 1 / (1 + exp(-l_e)),  c_e = s_e + bias_e
+ *   the E experts are n_groups equal groups in order; a group is worth the sum
+ *   of its group_best largest c (of one, if only one is available), and only
+ *   the experts of the top_groups best groups stay
+ *   slots 0..top_k-1: the largest c among them, largest first
+ *   w_j = scale s_j / (sum of s over the chosen), or scale s_j without
+ *   norm_topk_prob
+ * Ties go to the lower group and the lower expert; experts are ranked as by
+ * exact arithmetic on the given logits and biases.  An expert whose logit or
+ * bias is -inf is not available, nor is one whose logit is NaN or +inf or whose
+ * bias is not finite, which also marks the status word.  Slots that no expert
+ * is left for get index -1 and weight 0 (ftmoe_dispatch drops them). */
+typedef struct {
+  const void* logits;     /* [T, E] of `dtype`, rows `ld` values apart (ld >= E), any alignment */
+  int32_t dtype;          /* ftmoe_dtype */
+  int32_t T, E;           /* E 1..1024 */
+  int64_t ld;
+  int32_t score;          /* ftmoe_score */
+  int32_t top_k;          /* 1..32, at most top_groups * E / n_groups */
+  int32_t norm_topk_prob;
+  float scale;            /* of the weights; not 0 */
+  const float* bias;      /* [E] or NULL: for the choice only (balance) */
+  int32_t n_groups;       /* 1..32, a divisor of E */
+  int32_t top_groups;     /* 1..n_groups */
+  int32_t group_best;     /* 1 or 2 */
+  int32_t* topk_idx;      /* [T, top_k] */
+  float* topk_w;          /* [T, top_k] */
+} ftmoe_route_args;
+
+int ftmoe_route_topk(const ftmoe_route_args* args, ftmoe_stream_t stream);
+
+/* Its gradient: dlogits [T, E] of `dtype`, rows ld_d apart, from dw [T, top_k],
+ * the gradient of topk_w; topk_idx and topk_w are the forward call's.  The
+ * choice itself and the bias have none.  Written whole; slots of -1 have no
+ * part, an index outside [-1, E) is left out and marks the status word, equal
+ * indices add up.  dlogits may be logits itself (ld_d == ld). */
+int ftmoe_route_topk_backward(const ftmoe_route_args* args, const float* dw, void* dlogits, int64_t ld_d,
+                              ftmoe_stream_t stream);
+
+/* Quantise T rows of x [T, K] of `dtype`, K a multiple of 16.  Without inv
+ * (top_k 1) row t goes to row t of codes [T, K] and scales [ceil(K/128)][T].
+ * With inv [T * top_k] (ftmoe_dispatch's) it goes to the rows inv[t*top_k + j]
+ * of codes [T*top_k, K] and scales [ceil(K/128)][T*top_k]; -1 drops a pair, a
+ * place out of range drops it and marks the status word, and rows of no pair
+ * stay as they were.  `used`: NULL, or the device count of rows of x to handle
+ * (e.g. offsets + E), held to [0, T] with a mark. */
+int ftmoe_fp8_quantize(const void* x, int dtype, int T, int K, const int32_t* inv, int top_k, const int32_t* used,
+                       uint8_t* codes, float* scales, ftmoe_stream_t stream);
+
+/* Quantise E matrices w [E][N][K] of `dtype` to FTMOE_FMT_FP8_BLOCK's arrays,
+ * K a multiple of 16 (a load-time tool). */
+int ftmoe_fp8_quantize_weights(const void* w, int dtype, int E, int N, int K, uint8_t* codes, float* scales,
+                               ftmoe_stream_t stream);
+
+/* Rows of each expert times its matrix.  Rows offsets[e] .. offsets[e+1] - 1
+ * belong to expert e:
+ *   out[r][n] = sum_k x[r][k] w[e][n][k]                      a [M, K], out [M, N]
+ *   transpose:  out[r][k] = sum_n x[r][n] w[e][n][k]          a [M, N], out [M, K]
+ *   swiglu:     h[r][i] = SwiGLU(y[r][i], y[r][N/2 + i]) of the first form's y,
+ *               quantised: out codes [M, N/2], out_scale [N/256][M]
+ * x and w are the values that codes and scales stand for.  Products are exact,
+ * summed on the tensor cores over a block of 128 and in fp32 over the blocks;
+ * y is not rounded before SwiGLU.  Rows of no expert (from offsets[E] on) stay
+ * as they were and may hold anything.  An expert whose rows begin before an
+ * earlier one's first row, fall or leave [0, M] is left out and marks the
+ * status word. */
+typedef struct {
+  const uint8_t* a;        /* codes of the rows */
+  const float* a_scale;    /* [ceil(K/128)][M]; transpose: [ceil(N/128)][M] */
+  const uint8_t* w;        /* [E][N][K] */
+  const float* w_scale;    /* [E][ceil(N/128)][ceil(K/128)] */
+  const int32_t* offsets;  /* device [E + 1], or NULL with E == 1: all M rows */
+  int64_t M;
+  int32_t E, N, K;         /* K a multiple of 16; transpose: N too; swiglu: N a multiple of 256 */
+  int32_t transpose, swiglu;
+  int32_t out_dtype;       /* ftmoe_dtype (not with swiglu) */
+  void* out;               /* not a */
+  float* out_scale;        /* swiglu only */
+} ftmoe_fp8_matmul_args;
+
+int ftmoe_fp8_matmul(const ftmoe_fp8_matmul_args* args, ftmoe_stream_t stream);
+
+/* h = SiLU(gu[:, :I]) * gu[:, I:] in fp32, for gu [rows, 2I] of `dtype`.
+ * scales NULL: out [rows, I] of `dtype`.  Otherwise out is codes [rows, I] and
+ * scales [I/128][rows], I a multiple of 128.  `used`: NULL, or the device count
+ * of rows to handle; the others stay as they were. */
+int ftmoe_swiglu(const void* gu, int dtype, int rows, int I, const int32_t* used, void* out, float* scales,
+                 ftmoe_stream_t stream);
+
+/* Its gradient dgu [rows, 2I] from dh [rows, I]; scales NULL: of `dtype`, and
+ * may be gu itself.  Otherwise codes and scales [2I/128][rows]. */
+int ftmoe_swiglu_backward(const void* dh, const void* gu, int dtype, int rows, int I, const int32_t* used, void* dgu,
+                          float* scales, ftmoe_stream_t stream);
+
 /* Synchronise `stream`, read and clear the current device's status word of
  * the training operators since the last call: FTMOE_OK,
  * FTMOE_ERR_DEVICE_CHECK if a kernel met an index out of range, or

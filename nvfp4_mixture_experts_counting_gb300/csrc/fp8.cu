@@ -1,0 +1,263 @@
+// E4M3 quantisers of activations (a scale for 128 values) and weights (for 128
+// x 128), and SwiGLU between two products with its gradient.
+//
+// All are one pass over their data, bound by DRAM: eight lanes hold a block of
+// 128 values, 16 each, so that a lane reads 32 bytes (64 of fp32) and writes
+// its 16 codes in one store, and a block's largest magnitude takes three
+// shuffles.
+#include "fp8_common.cuh"
+
+namespace ftmoe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kLanes = 8;  // of a block
+constexpr int kPer = kFp8Block / kLanes;
+
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, float (&v)[kPer]) {
+  constexpr int N = 16 / sizeof(T);
+  Pack<T, N> x[kPer / N];
+#pragma unroll
+  for (int i = 0; i < kPer / N; ++i) x[i] = load_pack<T, N>(p + i * N);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) v[i] = x[i / N].get(i % N);
+}
+
+// The scale of the block that this lane's group of eight holds, and this lane's codes.
+__device__ __forceinline__ uint4 quantize16(const float (&v)[kPer], float& scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) top = max(top, magnitude(v[i]));
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const BlockScale b = block_scale(top);
+  scale = b.scale;
+  if (b.mul == 0.f && b.scale == 0.f) return make_uint4(0, 0, 0, 0);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i] = e4m3x4(v[4 * i] * b.mul, v[4 * i + 1] * b.mul, v[4 * i + 2] * b.mul, v[4 * i + 3] * b.mul);
+  return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// A warp takes four neighbouring blocks of a row.  With `inv`, token t's codes
+// go to the rows inv[t * top_k + j].
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_fp8_quantize(const T* x, int T_, int K, const int32_t* inv, int top_k,
+                                                           const int32_t* used, uint8_t* codes, float* scales,
+                                                           uint32_t* status) {
+  pdl_wait();
+  const int rows = used_rows(used, T_, status);
+  const int64_t places = inv ? (int64_t)T_ * top_k : T_;
+  const int blocks = (K + kFp8Block - 1) / kFp8Block, quads = (blocks + 3) / 4;
+  const int lane = threadIdx.x & 31, sub = lane & (kLanes - 1);
+  const int64_t units = (int64_t)rows * quads, step = (int64_t)gridDim.x * (kThreads / 32);
+  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; u < units; u += step) {
+    const int64_t t = quotient(u, quads);
+    const int b = (int)(u - t * quads) * 4 + lane / kLanes, k0 = b * kFp8Block + sub * kPer;
+    const bool on = k0 < K;  // K is a multiple of 16: a lane's values are all there or none is
+    float v[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = 0.f;
+    if (on) load16(x + t * K + k0, v);
+    float scale;
+    const uint4 c = quantize16(v, scale);
+    if (!inv) {
+      if (on) {
+        *reinterpret_cast<uint4*>(codes + t * K + k0) = c;
+        if (sub == 0) scales[(int64_t)b * places + t] = scale;
+      }
+      continue;
+    }
+    int mine = -1;
+    if (lane < top_k) {
+      mine = inv[t * top_k + lane];
+      if (mine < -1 || mine >= places) {
+        set_status(status, kStatusRange);
+        mine = -1;
+      }
+    }
+    for (int j = 0; j < top_k; ++j) {
+      const int at = __shfl_sync(0xffffffffu, mine, j);
+      if (at < 0 || !on) continue;
+      *reinterpret_cast<uint4*>(codes + (int64_t)at * K + k0) = c;
+      if (sub == 0) scales[(int64_t)b * places + at] = scale;
+    }
+  }
+}
+
+// A CTA takes a block of 128 x 128, a row of it per 8 lanes.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_fp8_quantize_weights(const T* w, int N, int K, uint8_t* codes,
+                                                                   float* scales) {
+  __shared__ uint32_t part[kThreads / 32];
+  const int blocks = (K + kFp8Block - 1) / kFp8Block, kb = blockIdx.x % blocks, nb = blockIdx.x / blocks;
+  const int64_t e = blockIdx.y;
+  const int sub = threadIdx.x % kLanes, k0 = kb * kFp8Block + sub * kPer;
+  constexpr int kRows = kThreads / kLanes;
+  uint32_t top = 0;
+  for (int r = threadIdx.x / kLanes; r < kFp8Block; r += kRows) {
+    const int n = nb * kFp8Block + r;
+    if (n >= N || k0 >= K) continue;
+    float v[kPer];
+    load16(w + (e * N + n) * K + k0, v);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) top = max(top, magnitude(v[i]));
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) top = max(top, part[i]);
+  const BlockScale b = block_scale(top);
+  if (threadIdx.x == 0) scales[e * gridDim.x + blockIdx.x] = b.scale;
+  for (int r = threadIdx.x / kLanes; r < kFp8Block; r += kRows) {
+    const int n = nb * kFp8Block + r;
+    if (n >= N || k0 >= K) continue;
+    float v[kPer];
+    load16(w + (e * N + n) * K + k0, v);
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c[i] = b.scale == 0.f ? 0u : e4m3x4(v[4 * i] * b.mul, v[4 * i + 1] * b.mul, v[4 * i + 2] * b.mul, v[4 * i + 3] * b.mul);
+    *reinterpret_cast<uint4*>(codes + (e * N + n) * K + k0) = make_uint4(c[0], c[1], c[2], c[3]);
+  }
+}
+
+// ---------------------------------------------------------------- SwiGLU
+
+// h = g s(g) u, and its gradient from dh: dg = dh u s (1 + g (1 - s)), du = dh g s.
+__device__ __forceinline__ float swiglu(float g, float u) { return g * sigmoid(g) * u; }
+__device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float& dg, float& du) {
+  const float s = sigmoid(g);
+  dg = dh * u * s * (1.f + g * (1.f - s));
+  du = dh * g * s;
+}
+
+// Quantised output: eight lanes take 128 columns of a row.  GRAD writes a row
+// of 2 I codes, gate's first.
+template <typename T, bool GRAD>
+__global__ void __launch_bounds__(kThreads) k_swiglu_fp8(const T* gu, const T* dh, int rows_, int I,
+                                                         const int32_t* used, uint8_t* codes, float* scales,
+                                                         uint32_t* status) {
+  pdl_wait();
+  const int rows = used_rows(used, rows_, status), blocks = I / kFp8Block;
+  const int sub = threadIdx.x % kLanes;
+  const int64_t units = (int64_t)rows * blocks, step = (int64_t)gridDim.x * (kThreads / kLanes);
+  // whole warps leave the loop together: the shuffles need all lanes
+  for (int64_t u0 = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / 32 * 4; u0 < units; u0 += step) {
+    const int64_t u = u0 + (threadIdx.x & 31) / kLanes;
+    const bool on = u < units;
+    const int64_t r = on ? quotient(u, blocks) : 0;
+    const int b = on ? (int)(u - r * blocks) : 0, k0 = b * kFp8Block + sub * kPer;
+    float g[kPer], v[kPer];
+    load16(gu + r * 2 * I + k0, g);
+    load16(gu + r * 2 * I + I + k0, v);
+    float scale;
+    if constexpr (GRAD) {
+      float d[kPer];
+      load16(dh + r * I + k0, d);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) swiglu_grad(d[i], g[i], v[i], g[i], v[i]);
+      const uint4 cg = quantize16(g, scale);
+      if (on) {
+        *reinterpret_cast<uint4*>(codes + r * 2 * I + k0) = cg;
+        if (sub == 0) scales[(int64_t)b * rows_ + r] = scale;
+      }
+      const uint4 cu = quantize16(v, scale);
+      if (on) {
+        *reinterpret_cast<uint4*>(codes + r * 2 * I + I + k0) = cu;
+        if (sub == 0) scales[(int64_t)(blocks + b) * rows_ + r] = scale;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] = swiglu(g[i], v[i]);
+      const uint4 c = quantize16(v, scale);
+      if (on) {
+        *reinterpret_cast<uint4*>(codes + r * I + k0) = c;
+        if (sub == 0) scales[(int64_t)b * rows_ + r] = scale;
+      }
+    }
+  }
+}
+
+// Output in the input's type, V values at a time (1 where rows are not a multiple of 16 bytes).
+template <typename T, int V, bool GRAD>
+__global__ void __launch_bounds__(kThreads) k_swiglu(const T* gu, const T* dh, int rows_, int I, const int32_t* used,
+                                                     T* out, uint32_t* status) {
+  pdl_wait();
+  const int rows = used_rows(used, rows_, status), pieces = I / V;
+  const int64_t units = (int64_t)rows * pieces, step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < units; i += step) {
+    const int64_t r = quotient(i, pieces);
+    const int k = (int)(i - r * pieces) * V;
+    const Pack<T, V> g = load_pack<T, V>(gu + r * 2 * I + k), u = load_pack<T, V>(gu + r * 2 * I + I + k);
+    Pack<T, V> a, b;
+    if constexpr (GRAD) {
+      const Pack<T, V> d = load_pack<T, V>(dh + r * I + k);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float dg, du;
+        swiglu_grad(d.get(j), g.get(j), u.get(j), dg, du);
+        a.set(j, dg);
+        b.set(j, du);
+      }
+      store_pack<T, V>(out + r * 2 * I + k, a);
+      store_pack<T, V>(out + r * 2 * I + I + k, b);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) a.set(j, swiglu(g.get(j), u.get(j)));
+      store_pack<T, V>(out + r * I + k, a);
+    }
+  }
+}
+
+unsigned grid_of(const TrainDevice& d, int64_t work, int per_cta, int ctas_per_sm) {
+  const int64_t need = (work + per_cta - 1) / per_cta, most = (int64_t)d.num_sms * ctas_per_sm;
+  return (unsigned)(need < 1 ? 1 : need < most ? need : most);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_quantize(const TrainDevice& d, const void* x, int dtype, int T, int K, const int32_t* inv,
+                                int top_k, const int32_t* used, uint8_t* codes, float* scales, cudaStream_t s) {
+  return with_dtype(dtype, [&](auto zero) {
+    using V = decltype(zero);
+    const int64_t units = (int64_t)T * ((fp8_blocks(K) + 3) / 4);
+    return launch_after(k_fp8_quantize<V>, grid_of(d, units, kThreads / 32, 16), kThreads, s,
+                        static_cast<const V*>(x), T, K, inv, top_k, used, codes, scales, d.status);
+  });
+}
+
+cudaError_t launch_fp8_quantize_weights(const TrainDevice& d, const void* w, int dtype, int E, int N, int K,
+                                        uint8_t* codes, float* scales, cudaStream_t s) {
+  return with_dtype(dtype, [&](auto zero) {
+    using V = decltype(zero);
+    const dim3 grid((unsigned)fp8_blocks(K) * fp8_blocks(N), E);
+    k_fp8_quantize_weights<V><<<grid, kThreads, 0, s>>>(static_cast<const V*>(w), N, K, codes, scales);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_swiglu(const TrainDevice& d, const void* gu, const void* dh, int dtype, int rows, int I,
+                          const int32_t* used, void* out, float* scales, cudaStream_t s) {
+  return with_dtype(dtype, [&](auto zero) {
+    using V = decltype(zero);
+    const V *g = static_cast<const V*>(gu), *dv = static_cast<const V*>(dh);
+    if (scales) {
+      const unsigned grid = grid_of(d, (int64_t)rows * (I / kFp8Block), kThreads / kLanes, 16);
+      return launch_after(dh ? k_swiglu_fp8<V, true> : k_swiglu_fp8<V, false>, grid, kThreads, s, g, dv, rows, I, used,
+                          static_cast<uint8_t*>(out), scales, d.status);
+    }
+    constexpr int W = 16 / sizeof(V);
+    const bool wide = I % W == 0;
+    const unsigned grid = grid_of(d, (int64_t)rows * (wide ? I / W : I), kThreads, 16);
+    auto* k = wide ? (dh ? k_swiglu<V, W, true> : k_swiglu<V, W, false>)
+                   : (dh ? k_swiglu<V, 1, true> : k_swiglu<V, 1, false>);
+    return launch_after(k, grid, kThreads, s, g, dv, rows, I, used, static_cast<V*>(out), d.status);
+  });
+}
+
+}  // namespace ftmoe

@@ -1,0 +1,44 @@
+// Device helpers of the 8-bit layer: E4M3 conversions and the scale of a block.
+#pragma once
+
+#include "fp8.h"
+#include "train_common.cuh"
+
+namespace ftmoe {
+
+// Four E4M3 codes, the first in the low byte (round to nearest even, saturating; NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return (uint32_t)hi << 16 | lo;
+}
+
+// A block's scale and what its values are multiplied by, from the bits of its
+// largest magnitude (as an integer, so that NaN counts as the largest and
+// spoils the block).  The scale is rounded once; so is the multiplier, whose
+// rounding moves a value by 2^-24 of it before the code's rounding, 2^-4.
+struct BlockScale {
+  float scale, mul;
+};
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
+  const float a = __uint_as_float(amax_bits);
+  if (a < kFp8Tiny) return {0.f, 0.f};
+  return {__fdiv_rn(a, kFp8Max), __fdiv_rn(kFp8Max, a)};
+}
+
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Rows that a call handles: `used` (a count on the device) where it is given.
+// A count out of range marks the status word and is held to the range.
+__device__ __forceinline__ int used_rows(const int32_t* used, int rows, uint32_t* status) {
+  if (!used) return rows;
+  const int n = *used;
+  if (n >= 0 && n <= rows) return n;
+  if (threadIdx.x == 0) set_status(status, kStatusRange);
+  return n < 0 ? 0 : rows;
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+
+}  // namespace ftmoe

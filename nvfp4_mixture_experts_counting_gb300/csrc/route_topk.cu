@@ -1,0 +1,396 @@
+// Routing from logits, and its gradient.
+//
+//   s_e = softmax(l)_e or 1 / (1 + exp(-l_e)),  c_e = s_e + b_e
+//   groups: the sum of a group's one or two largest c; the top_groups best
+//   the top_k largest c in them, ties to the lower index
+//   w_j = scale s_j / sum_i s_i, or scale s_j
+//
+// Experts are ranked as by exact arithmetic.  Where c is a monotone function
+// of the logit (no bias, and groups by their largest value) the logits
+// themselves are ranked, which is exact.  Otherwise c is computed in fp32 with
+// an error bound, and a token where two values that decide are closer than
+// their bounds is ranked again in fp64.  Of N(0, 1) logits with E = 256 that is
+// one token in some hundreds.
+//
+// A warp takes a token; lane i holds the experts i, i + 32, ... as integer keys
+// in the order of the values, so that a round of the selection is one scan of
+// a lane's keys and two warp reductions (the best key, the lowest expert that
+// has it).
+#include <cfloat>
+
+#include "fp8_common.cuh"
+
+namespace ftmoe {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr float kEps = 5.9604645e-8f;  // 2^-24
+
+struct RouteKernelArgs {
+  const void* logits;
+  int64_t ld;
+  int T, E, top_k, sigmoid, norm;
+  float scale;
+  const float* bias;
+  int n_groups, top_groups, group_best, group_size;
+  uint32_t group_magic;  // ceil(2^20 / group_size): e / group_size = e * magic >> 20 for e < 2^10
+  int by_logit;          // c's order is the logits'
+  int32_t* idx;
+  float* w;
+  uint32_t* status;
+};
+
+// An unsigned key in the order of the values; 0 is below every value's.
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);  // -0 becomes 0
+  return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float(key ^ (key >> 31 ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ bool in_groups(const RouteKernelArgs& a, uint32_t groups, int e) {
+  return groups >> ((e * a.group_magic >> 20) & 31) & 1;
+}
+
+__device__ __forceinline__ double warp_max_d(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// The chosen groups as a mask, from the experts' values c[E] (-inf: not
+// available).  L lanes take a group.  `gap`: the least chosen group's value
+// less the best other one's (infinite where there is no such pair).
+template <typename V>
+__device__ __forceinline__ uint32_t choose_groups(const RouteKernelArgs& a, const V* c, int lane, V& gap) {
+  int L = 32;
+  while (L * a.n_groups > 32) L >>= 1;
+  const int g = lane / L;
+  const V none = -(V)INFINITY;
+  V m0 = none, m1 = none;
+  if (g < a.n_groups)
+    for (int i = lane % L; i < a.group_size; i += L) {
+      const V v = c[g * a.group_size + i];
+      m1 = v > m0 ? m0 : v > m1 ? v : m1;
+      m0 = v > m0 ? v : m0;
+    }
+  for (int o = L / 2; o > 0; o >>= 1) {
+    const V p0 = __shfl_xor_sync(0xffffffffu, m0, o), p1 = __shfl_xor_sync(0xffffffffu, m1, o);
+    const V low = p0 < m0 ? p0 : m0, high = p0 < m0 ? m0 : p0;
+    const V next = m1 > p1 ? m1 : p1;
+    m0 = high;
+    m1 = low > next ? low : next;
+  }
+  // one available expert counts alone
+  const V mine = a.group_best == 2 && m1 != none ? m0 + m1 : m0;
+  int before = 0;
+  for (int o = 0; o < a.n_groups; ++o) {
+    const V other = __shfl_sync(0xffffffffu, mine, o * L);
+    before += other > mine || (other == mine && o < g);
+  }
+  const bool head = lane % L == 0 && g < a.n_groups, in = head && before < a.top_groups;
+  uint32_t mask = 0;
+  for (int o = 0; o < a.n_groups; ++o) mask |= (uint32_t)__shfl_sync(0xffffffffu, (int)in, o * L) << o;
+  V least = in ? mine : (V)INFINITY, best = head && !in ? mine : none;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const V x = __shfl_xor_sync(0xffffffffu, least, o), y = __shfl_xor_sync(0xffffffffu, best, o);
+    least = x < least ? x : least;
+    best = y > best ? y : best;
+  }
+  gap = best == none ? (V)INFINITY : least - best;
+  return mask;
+}
+
+template <typename T>
+__device__ __forceinline__ float usable_logit(const T* row, int e) {
+  const float l = to_f32(row[e]);
+  return l < INFINITY ? l : -INFINITY;  // NaN too
+}
+
+// The choice in fp64; returns the expert of slot `lane`, or -1.
+template <typename T>
+__device__ __noinline__ int route_again(const RouteKernelArgs& a, const T* row, double* c, int lane) {
+  double m = 0, total = 1;
+  if (!a.sigmoid) {
+    float top = -INFINITY;
+    for (int e = lane; e < a.E; e += 32) top = fmaxf(top, usable_logit(row, e));
+    m = warp_max_f32(top);
+    double sum = 0;
+    for (int e = lane; e < a.E; e += 32) sum += exp((double)usable_logit(row, e) - m);
+    total = warp_sum_d(sum);
+  }
+  __syncwarp();
+  for (int e = lane; e < a.E; e += 32) {
+    const float l = usable_logit(row, e), b = a.bias ? a.bias[e] : 0.f;
+    const double s = a.sigmoid ? 1 / (1 + exp(-(double)l)) : exp((double)l - m) / total;
+    c[e] = l == -INFINITY || !(fabsf(b) < INFINITY) ? -INFINITY : s + b;
+  }
+  __syncwarp();
+  uint32_t groups = 0xffffffffu;
+  if (a.n_groups > 1) {
+    double gap;
+    groups = choose_groups(a, c, lane, gap);
+  }
+  int mine = -1;
+  for (int j = 0; j < a.top_k; ++j) {
+    double best = -INFINITY;
+    int at = a.E;
+    for (int e = lane; e < a.E; e += 32) {
+      if (a.n_groups > 1 && !in_groups(a, groups, e)) continue;
+      if (c[e] > best) best = c[e], at = e;
+    }
+    const double top = warp_max_d(best);
+    if (top == -INFINITY) break;
+    at = __reduce_min_sync(0xffffffffu, best == top ? at : a.E);
+    if (lane == j) mine = at;
+    if (at % 32 == lane) c[at] = -INFINITY;
+    __syncwarp();
+  }
+  return mine;
+}
+
+// VPL: keys a lane holds.
+template <typename T, int VPL>
+__global__ void __launch_bounds__(kWarps * 32) k_route_topk(const __grid_constant__ RouteKernelArgs a) {
+  extern __shared__ double shared_c[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  double* exact_c = shared_c + warp * a.E;
+  float* c = reinterpret_cast<float*>(exact_c);
+  pdl_wait();
+  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    float l[VPL];
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane + 32 * i;
+      l[i] = e < a.E ? to_f32(row[e]) : -INFINITY;
+      odd |= !(l[i] < INFINITY);
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      l[i] = l[i] < INFINITY ? l[i] : -INFINITY;
+      top = fmaxf(top, l[i]);
+    }
+    float total = 1.f, largest = 1.f;  // the softmax's sum; the largest score
+    if (!a.sigmoid && (!a.by_logit || !a.norm)) {
+      top = warp_max_f32(top);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) sum += l[i] == -INFINITY ? 0.f : expf(l[i] - top);
+      total = warp_sum_f32(sum);
+      largest = 1.f / total;
+    }
+    uint32_t key[VPL];
+    float bound = 0.f;
+    if (a.by_logit) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = l[i] == -INFINITY ? 0u : key_of(l[i]);
+    } else {
+      float far = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int e = lane + 32 * i;
+        key[i] = 0u;
+        if (l[i] == -INFINITY) continue;
+        const float b = a.bias ? __ldg(a.bias + e) : 0.f;
+        if (!(fabsf(b) < INFINITY)) {
+          odd |= b != -INFINITY;
+          continue;
+        }
+        const float v = (a.sigmoid ? sigmoid(l[i]) : expf(l[i] - top) * largest) + b;
+        far = fmaxf(far, fabsf(v));
+        key[i] = key_of(v);
+      }
+      // |error of s| <= 4 eps for the sigmoid (exp 2 eps of it, the sum, the quotient, each s <= 1); for the
+      // softmax (VPL + 18) eps s, from the exponent (|l - top| eps, at most ln E in the mean of the sum), exp
+      // (2 eps), a lane's sum, the joins (5) and the two products.  The bias adds eps |c|.  Two values differ
+      // for sure beyond the sum of their bounds; half is added.
+      bound = 1.5f * kEps * (2.f * (a.sigmoid ? 4.f : (VPL + 18.f) * largest) + 2.f * warp_max_f32(far));
+    }
+    if (odd) set_status(a.status, kStatusRange);
+    bool again = false;
+    if (a.n_groups > 1) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (lane + 32 * i < a.E) c[lane + 32 * i] = key[i] ? value_of(key[i]) : -INFINITY;
+      __syncwarp();
+      float gap;
+      const uint32_t groups = choose_groups(a, c, lane, gap);
+      again = !a.by_logit && gap <= 3.f * bound;  // of sums of two values, which are rounded too
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (!in_groups(a, groups, lane + 32 * i)) key[i] = 0u;
+    }
+    // slot j's expert stays with lane j
+    int mine = -1;
+    uint32_t last = 0u;
+    const int rounds = again ? 0 : a.top_k + !a.by_logit;
+    for (int j = 0; j < rounds; ++j) {
+      uint32_t best = 0u;
+      int at = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (key[i] > best) best = key[i], at = i;
+      const uint32_t high = __reduce_max_sync(0xffffffffu, best);
+      if (!high) break;
+      if (!a.by_logit && last) again |= value_of(last) - value_of(high) <= bound;
+      last = high;
+      const int e = __reduce_min_sync(0xffffffffu, best == high ? lane + 32 * at : 1 << 20);
+      if (lane == j) mine = e;
+      if ((e & 31) == lane) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (i == e / 32) key[i] = 0u;
+      }
+    }
+    if (again) mine = route_again(a, row, exact_c, lane);
+    if (lane >= a.top_k) mine = -1;
+    // weights relative to the largest chosen score, so that scores below fp32's range keep their ratios
+    float s = 0.f;
+    const float z = mine >= 0 ? usable_logit(row, mine) : -INFINITY;
+    if (a.norm) {
+      const float n = a.sigmoid ? fminf(z, 0.f) : z, most = warp_max_f32(n);
+      if (mine >= 0) s = expf(n - most) / (a.sigmoid ? 1.f + expf(-fabsf(z)) : 1.f);
+      const float sum = warp_sum_f32(s);
+      s = sum > 0.f ? s * a.scale / sum : 0.f;
+    } else if (mine >= 0) {
+      s = a.scale * (a.sigmoid ? sigmoid(z) : expf(z - top) * largest);
+    }
+    if (lane < a.top_k) {
+      a.idx[t * a.top_k + lane] = mine;
+      a.w[t * a.top_k + lane] = s;
+    }
+    __syncwarp();
+  }
+}
+
+// ---------------------------------------------------------------- gradient
+
+// With u = dw and D = sum_j w_j u_j, for the expert of slot j
+//   softmax, norm: w_j (u_j - D / scale)   else: p_e (scale u_j - D), and -p_e D for every other expert
+//   sigmoid, norm: w_j (1 - s_j) (u_j - D / scale)   else: w_j (1 - s_j) u_j
+// Slots with the same expert add up.  A warp takes a token: it writes the row
+// of zeros (or of -p_e D) and then the chosen places.
+template <typename T, int V>
+__global__ void __launch_bounds__(kWarps * 32) k_route_topk_backward(const __grid_constant__ RouteKernelArgs a,
+                                                                     const float* dw, T* dlogits, int64_t ld_d) {
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  for (int64_t t = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; t < a.T; t += (int64_t)gridDim.x * kWarps) {
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    T* out = dlogits + t * ld_d;
+    int e = -1;
+    float w = 0.f, u = 0.f, z = 0.f;
+    if (lane < a.top_k) {
+      e = a.idx[t * a.top_k + lane];
+      if (e < -1 || e >= a.E) {
+        set_status(a.status, kStatusRange);
+        e = -1;
+      }
+      if (e >= 0) {
+        w = a.w[t * a.top_k + lane];
+        u = dw[t * a.top_k + lane];
+        if (a.sigmoid || !a.norm) z = usable_logit(row, e);
+      }
+    }
+    const float D = warp_sum_f32(w * u);
+    float g;
+    if (a.sigmoid)
+      g = w * (a.norm ? u - D / a.scale : u) / (1.f + expf(z));
+    else
+      g = a.norm ? w * (u - D / a.scale) : a.scale * u;
+    if (e < 0) g = 0.f;
+    float sum = 0.f;  // over the slots of this expert
+    for (int j = 0; j < a.top_k; ++j) {
+      const int o = __shfl_sync(0xffffffffu, e, j);
+      const float x = __shfl_sync(0xffffffffu, g, j);
+      if (o == e) sum += x;
+    }
+    if (!a.sigmoid && !a.norm) {
+      float top = -INFINITY, part = 0.f;
+      for (int i = lane; i < a.E; i += 32) top = fmaxf(top, usable_logit(row, i));
+      top = warp_max_f32(top);
+      for (int i = lane; i < a.E; i += 32) {
+        const float l = usable_logit(row, i);
+        part += l == -INFINITY ? 0.f : expf(l - top);
+      }
+      const float total = warp_sum_f32(part), inv = total > 0.f ? 1.f / total : 0.f;
+      const float p = z == -INFINITY ? 0.f : expf(z - top) * inv;
+      for (int i = lane; i < a.E; i += 32) {
+        const float l = usable_logit(row, i);
+        out[i] = from_f32<T>(l == -INFINITY ? 0.f : expf(l - top) * inv * -D);
+      }
+      sum = p * (sum - D);
+    } else {
+      Pack<T, V> zero;
+#pragma unroll
+      for (int i = 0; i < V; ++i) zero.set(i, 0.f);
+      __syncwarp();  // logits may be dlogits: the chosen ones are read
+      for (int i = lane * V; i < a.E; i += 32 * V) store_pack<T, V>(out + i, zero);
+    }
+    __syncwarp();
+    if (e >= 0) out[e] = from_f32<T>(sum);
+  }
+}
+
+RouteKernelArgs kernel_args(const TrainDevice& d, const ftmoe_route_args& r) {
+  RouteKernelArgs a{};
+  a.logits = r.logits;
+  a.ld = r.ld;
+  a.T = r.T;
+  a.E = r.E;
+  a.top_k = r.top_k;
+  a.sigmoid = r.score == FTMOE_SCORE_SIGMOID;
+  a.norm = r.norm_topk_prob;
+  a.scale = r.scale;
+  a.bias = r.bias;
+  a.n_groups = r.n_groups;
+  a.top_groups = r.top_groups;
+  a.group_best = r.group_best;
+  a.group_size = r.E / r.n_groups;
+  a.group_magic = (uint32_t)(((1 << 20) + a.group_size - 1) / a.group_size);
+  a.by_logit = !r.bias && (r.n_groups == 1 || r.group_best == 1);
+  a.idx = r.topk_idx;
+  a.w = r.topk_w;
+  a.status = d.status;
+  return a;
+}
+
+unsigned route_grid(const TrainDevice& d, int T) {
+  const int need = (T - 1) / kWarps + 1, most = d.num_sms * 16;
+  return (unsigned)(need < most ? need : most);
+}
+
+}  // namespace
+
+cudaError_t launch_route_topk(const TrainDevice& d, const ftmoe_route_args& r, cudaStream_t s) {
+  const RouteKernelArgs a = kernel_args(d, r);
+  return with_dtype(r.dtype, [&](auto zero) {
+    using T = decltype(zero);
+    const int per = (r.E + 31) / 32;
+    auto* k = per <= 1 ? k_route_topk<T, 1> : per <= 2 ? k_route_topk<T, 2> : per <= 4 ? k_route_topk<T, 4>
+              : per <= 8 ? k_route_topk<T, 8> : per <= 16 ? k_route_topk<T, 16> : k_route_topk<T, 32>;
+    // 32 KB at E = 1024: within what a kernel has without asking
+    return launch_after_smem(k, route_grid(d, r.T), kWarps * 32, kWarps * r.E * sizeof(double), s, a);
+  });
+}
+
+cudaError_t launch_route_topk_backward(const TrainDevice& d, const ftmoe_route_args& r, const float* dw, void* dlogits,
+                                       int64_t ld_d, cudaStream_t s) {
+  const RouteKernelArgs a = kernel_args(d, r);
+  return with_dtype(r.dtype, [&](auto zero) {
+    using T = decltype(zero);
+    constexpr int V = 16 / sizeof(T);
+    const bool wide = r.E % V == 0 && ld_d % V == 0 && ((uintptr_t)dlogits & 15) == 0;
+    return launch_after(wide ? k_route_topk_backward<T, V> : k_route_topk_backward<T, 1>, route_grid(d, r.T),
+                        kWarps * 32, s, a, dw, static_cast<T*>(dlogits), ld_d);
+  });
+}
+
+}  // namespace ftmoe

@@ -145,10 +145,11 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 // Launches a kernel that calls pdl_wait before it uses what the stream's
 // previous kernel writes: it may start while that one ends.
 template <typename... A, typename... B>
-cudaError_t launch_after(void (*k)(A...), unsigned grid, int threads, cudaStream_t s, B... args) {
+cudaError_t launch_after_smem(void (*k)(A...), unsigned grid, int threads, size_t smem, cudaStream_t s, B... args) {
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(grid);
   c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
   c.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -156,6 +157,10 @@ cudaError_t launch_after(void (*k)(A...), unsigned grid, int threads, cudaStream
   c.attrs = at;
   c.numAttrs = 1;
   return cudaLaunchKernelEx(&c, k, static_cast<A>(args)...);
+}
+template <typename... A, typename... B>
+cudaError_t launch_after(void (*k)(A...), unsigned grid, int threads, cudaStream_t s, B... args) {
+  return launch_after_smem(k, grid, threads, 0, s, args...);
 }
 
 // Calls f with a value of the type that a dtype code names.

@@ -85,6 +85,20 @@ class AdamwParams(C.Structure):
                 ("step", C.c_int64), ("grad_scale", C.c_void_p)]
 
 
+class RouteArgs(C.Structure):
+    _fields_ = [("logits", C.c_void_p), ("dtype", C.c_int32), ("T", C.c_int32), ("E", C.c_int32), ("ld", C.c_int64),
+                ("score", C.c_int32), ("top_k", C.c_int32), ("norm_topk_prob", C.c_int32), ("scale", C.c_float),
+                ("bias", C.c_void_p), ("n_groups", C.c_int32), ("top_groups", C.c_int32), ("group_best", C.c_int32),
+                ("topk_idx", C.c_void_p), ("topk_w", C.c_void_p)]
+
+
+class Fp8MatmulArgs(C.Structure):
+    _fields_ = [("a", C.c_void_p), ("a_scale", C.c_void_p), ("w", C.c_void_p), ("w_scale", C.c_void_p),
+                ("offsets", C.c_void_p), ("M", C.c_int64), ("E", C.c_int32), ("N", C.c_int32), ("K", C.c_int32),
+                ("transpose", C.c_int32), ("swiglu", C.c_int32), ("out_dtype", C.c_int32), ("out", C.c_void_p),
+                ("out_scale", C.c_void_p)]
+
+
 _lib = None
 
 #: every symbol the header declares, with its argument and result types
@@ -131,6 +145,16 @@ SIGNATURES = {
     "ftmoe_policy_loss": ([C.POINTER(PolicyArgs), C.c_void_p], C.c_int),
     "ftmoe_test_withhold_policy": ([C.c_int, C.c_int64], C.c_int),
     "ftmoe_adamw": ([C.POINTER(AdamwTensor), C.c_int, C.POINTER(AdamwParams), C.c_void_p], C.c_int),
+    "ftmoe_route_topk": ([C.POINTER(RouteArgs), C.c_void_p], C.c_int),
+    "ftmoe_route_topk_backward": ([C.POINTER(RouteArgs), C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p], C.c_int),
+    "ftmoe_fp8_quantize": ([C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_void_p, C.c_void_p,
+                            C.c_void_p, C.c_void_p], C.c_int),
+    "ftmoe_fp8_quantize_weights": ([C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p,
+                                    C.c_void_p], C.c_int),
+    "ftmoe_fp8_matmul": ([C.POINTER(Fp8MatmulArgs), C.c_void_p], C.c_int),
+    "ftmoe_swiglu": ([C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p], C.c_int),
+    "ftmoe_swiglu_backward": ([C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p,
+                               C.c_void_p], C.c_int),
     "ftmoe_ops_status": ([C.c_void_p], C.c_int),
 }
 
@@ -314,6 +338,7 @@ class _Codes(dict):
     def __missing__(self, dtype):
         import torch
         self.fp32 = torch.float32
+        self.codes = (torch.uint8, torch.float8_e4m3fn)
         self.update({torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16, torch.int32: _INT32,
                      torch.int64: _INT64})
         return self.setdefault(dtype, -1)
@@ -499,6 +524,110 @@ def ftmoe_adamw(tensors: AdamwList, lr: float, beta1: float = 0.9, beta2: float 
                 step: int = 1, grad_scale=None, stream=None):
     hp = AdamwParams(lr, beta1, beta2, eps, step, _array(grad_scale, FP32, 1))
     _check(lib().ftmoe_adamw(tensors.array, len(tensors.array), C.byref(hp), _stream(stream)), "ftmoe_adamw")
+
+
+# ----------------------------------------------------------------- the layer on 8-bit codes
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _codes8(t, n: int):
+    """Address of a contiguous tensor of n E4M3 codes or more (float8_e4m3fn, or their bytes)."""
+    if t is None:
+        return None
+    _CODES[t.dtype]  # fills the table
+    if t.dtype not in _CODES.codes:
+        raise TypeError(f"float8_e4m3fn or uint8 expected, got {t.dtype}")
+    if t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{n} or more contiguous codes expected, got {t.numel()} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _rows(t):
+    """(rows, columns, values between rows) of a matrix whose rows are dense."""
+    if t.dim() != 2:
+        raise ValueError(f"a matrix expected, got {t.dim()} dimensions")
+    n, width = t.shape
+    ld, step = t.stride()
+    if width > 1 and step != 1:
+        raise ValueError("rows need a dense last dimension")
+    return n, width, width if n <= 1 else ld  # a single row's stride says nothing
+
+
+def route_args(logits, topk_idx, topk_w, score: str = "softmax", norm_topk_prob: bool = True, scale: float = 1.0,
+               bias=None, n_groups: int = 1, top_groups: int = 1, group_best: int = 1) -> RouteArgs:
+    """Arguments of ftmoe_route_topk and its gradient, kept with references to the tensors; logits [T, E] may have
+    any row stride, top_k is the width of topk_idx [T, top_k]."""
+    T, E, ld = _rows(logits)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T or topk_w.shape != topk_idx.shape:
+        raise ValueError("topk_idx and topk_w have a row for each of the logits' and one shape")
+    k = topk_idx.shape[1]
+    args = RouteArgs(logits.data_ptr(), _dtype(logits), T, E, ld, SCORES[score], k, int(norm_topk_prob), scale,
+                     _array(bias, FP32, E), n_groups, top_groups, group_best, _array(topk_idx, _INT32, T * k),
+                     _array(topk_w, FP32, T * k))
+    args.tensors = (logits, topk_idx, topk_w, bias)
+    return args
+
+
+def ftmoe_route_topk(args: RouteArgs, stream=None):
+    _check(lib().ftmoe_route_topk(C.byref(args), _stream(stream)), "ftmoe_route_topk")
+
+
+def ftmoe_route_topk_backward(args: RouteArgs, dw, dlogits, stream=None):
+    T, E, ld = _rows(dlogits)
+    if (T, E) != (args.T, args.E) or _dtype(dlogits) != args.dtype:
+        raise TypeError("dlogits has the shape and type of logits")
+    _check(lib().ftmoe_route_topk_backward(C.byref(args), _array(dw, FP32, T * args.top_k), dlogits.data_ptr(), ld,
+                                           _stream(stream)), "ftmoe_route_topk_backward")
+
+
+def ftmoe_fp8_quantize(x, T: int, K: int, inv, top_k: int, codes, scales, used=None, stream=None):
+    """E4M3 codes of x's rows with a scale for 128 values; with inv, in the rows that ftmoe_dispatch's table names."""
+    dtype, rows, blocks = _dtype(x), T * top_k, (K + 127) // 128
+    _check(lib().ftmoe_fp8_quantize(_array(x, dtype, T * K), dtype, T, K, _array(inv, _INT32, rows), top_k,
+                                    _array(used, _INT32, 1), _codes8(codes, rows * K),
+                                    _array(scales, FP32, blocks * rows), _stream(stream)), "ftmoe_fp8_quantize")
+
+
+def ftmoe_fp8_quantize_weights(w, E: int, N: int, K: int, codes, scales, stream=None):
+    dtype, blocks = _dtype(w), (N + 127) // 128 * ((K + 127) // 128)
+    _check(lib().ftmoe_fp8_quantize_weights(_array(w, dtype, E * N * K), dtype, E, N, K, _codes8(codes, E * N * K),
+                                            _array(scales, FP32, E * blocks), _stream(stream)),
+           "ftmoe_fp8_quantize_weights")
+
+
+def ftmoe_fp8_matmul(a, a_scale, w, w_scale, offsets, M: int, E: int, N: int, K: int, out, out_scale=None,
+                     transpose: bool = False, swiglu: bool = False, stream=None):
+    """Each expert's rows of codes times its matrix [N, K] (transpose: times its columns; swiglu: h as codes)."""
+    width, out_width = (N, K) if transpose else (K, N // 2 if swiglu else N)
+    nb, kb = (N + 127) // 128, (K + 127) // 128
+    dtype = 0 if swiglu else _dtype(out)
+    args = Fp8MatmulArgs(_codes8(a, M * width), _array(a_scale, FP32, (nb if transpose else kb) * M),
+                         _codes8(w, E * N * K), _array(w_scale, FP32, E * nb * kb), _array(offsets, _INT32, E + 1), M,
+                         E, N, K, int(transpose), int(swiglu), dtype,
+                         _codes8(out, M * out_width) if swiglu else _array(out, dtype, M * out_width),
+                         _array(out_scale, FP32, out_width // 128 * M) if swiglu else None)
+    _check(lib().ftmoe_fp8_matmul(C.byref(args), _stream(stream)), "ftmoe_fp8_matmul")
+
+
+def _swiglu_out(out, scales, dtype: int, rows: int, width: int):
+    if scales is None:
+        return _array(out, dtype, rows * width), None
+    return _codes8(out, rows * width), _array(scales, FP32, width // 128 * rows)
+
+
+def ftmoe_swiglu(gu, rows: int, I: int, out, scales=None, used=None, stream=None):
+    """out = SiLU(gate) * up, in gu's type or, with scales, as E4M3 codes."""
+    dtype = _dtype(gu)
+    _check(lib().ftmoe_swiglu(_array(gu, dtype, 2 * rows * I), dtype, rows, I, _array(used, _INT32, 1),
+                              *_swiglu_out(out, scales, dtype, rows, I), _stream(stream)), "ftmoe_swiglu")
+
+
+def ftmoe_swiglu_backward(dh, gu, rows: int, I: int, dgu, scales=None, used=None, stream=None):
+    dtype = _dtype(gu)
+    _check(lib().ftmoe_swiglu_backward(_array(dh, dtype, rows * I), _array(gu, dtype, 2 * rows * I), dtype, rows, I,
+                                       _array(used, _INT32, 1), *_swiglu_out(dgu, scales, dtype, rows, 2 * I),
+                                       _stream(stream)), "ftmoe_swiglu_backward")
 
 
 def ftmoe_ops_status(stream=None) -> int:
