@@ -1,112 +1,558 @@
 // Product of E4M3 codes with a scale for each block of 128, grouped by expert:
 //   y[r, n] = sum_b sx[b, r] sw[n / 128, b] sum_{k in block b} qx[r, k] qw[n, k]
-// and with `transpose` the product with the weights' columns (the gradient of
-// the input), or with `swiglu` h = SwiGLU of y's halves as codes and scales.
+// with `transpose` by the weights' columns instead (the gradient of the
+// input), with `swiglu` h = SwiGLU of y's halves as codes and scales.
+//
+// Weights are the MMA's 128-row operand and tokens its columns, as many as a
+// tile has, rounded up to 16: an expert with a few tokens costs its weights'
+// bytes and no empty rows, one with many is cut into equal tiles of at most
+// NMAX.  A block's product of 128 x N lands in tensor memory; eight warps read
+// it, multiply it by the block's scales and add it up in fp32 registers, while
+// the next block's product goes to the other buffer.  (The scales are any
+// fp32, so the tensor cores cannot apply them as they do powers of two.)
+// tcgen05 sums a block of 128 products in fp32, so an output rounds once per
+// block and once at the end.
+//
+// Warps: 0 copies tiles by TMA, 1 issues the MMAs, 2 multiplies sx by sw into
+// shared memory for each block, 4-11 add up.  With SwiGLU a tile is 128 gate
+// and the matching 128 up rows, so that a thread has both halves of a value.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "fp8_common.cuh"
+#include "tc_common.cuh"
 
 namespace ftmoe {
 
 namespace {
 
-// The rows of expert e, none where they begin before an earlier expert's end
-// (`floor`, kept along), fall or leave [0, M]; that marks the status word.
-__device__ __forceinline__ int2 expert_rows(const int32_t* offsets, int e, int M, int& floor, uint32_t* status) {
-  if (!offsets) return make_int2(0, M);
-  const int lo = offsets[e], hi = offsets[e + 1];
-  const bool good = lo >= floor && hi >= lo && hi <= M;
-  floor = max(floor, lo);
-  if (good) return make_int2(lo, hi);
-  set_status(status, kStatusRange);
-  return make_int2(0, 0);
-}
-
-constexpr int kRows = 8;  // of a tile
+constexpr int kThreads = 384;
+constexpr int kEpiWarp0 = 4;      // two warpgroups of epilogue warps
+constexpr int kEpiWarps = 8;
+constexpr int kLaunchRegs = 168, kLowRegs = 72, kEpiRegs = 216;
+static_assert(3 * kLaunchRegs == kLowRegs + 2 * kEpiRegs, "the warpgroups' shares add up to the launch's registers");
+constexpr int kTile = 128 * 128;  // bytes of a weight tile
+constexpr int kSmemMax = 227 * 1024;
 
 struct MatmulArgs {
-  const uint8_t *a, *w;
   const float *a_scale, *w_scale;
   const int32_t* offsets;
-  int M, E, N, K, transpose, swiglu, dtype;
+  int M, E;
+  int C, O;        // lengths of an input's and an output's row (with swiglu O is I)
+  int NB, KB;      // blocks of the weights' rows and columns
+  int JT;          // weight tiles of an expert
+  int dtype;
   void* out;
   float* out_scale;
   uint32_t* status;
 };
 
-__device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float v) {
+// What a kernel form takes of shared and tensor memory.
+template <int NMAX, bool SWIGLU>
+struct Form {
+  static constexpr int kParts = SWIGLU ? 2 : 1;
+  static constexpr int kBox = NMAX < 64 ? 16 : 64;  // tokens of one copy
+  static constexpr int kABytes = kParts * kTile, kBBytes = NMAX * 128;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kCols = kParts * NMAX;  // of an accumulator buffer
+  static constexpr int kBufs = 512 / kCols < 4 ? 512 / kCols : 4;
+  static constexpr int kTmemCols = kBufs * kCols;
+  static constexpr int kWgTokens = NMAX / 2;  // of a warpgroup
+  static constexpr int kOut = SWIGLU ? 2 * kWgTokens * 128 : 0;  // bytes of staged codes
+  static constexpr int kTops = SWIGLU ? 2 * kWgTokens * 4 * 4 : 0;
+  static constexpr int kScales = kBufs * kCols * 4;
+  static constexpr int kFixed = 1024 + kOut + kTops + kScales + 512 + 3 * 4 * (kMaxBins + 1);
+  static constexpr int kStages0 = (kSmemMax - kFixed) / kStageBytes;
+  static constexpr int kStages = kStages0 < 12 ? kStages0 : 12;
+  static constexpr int smem(int E) {
+    return 1024 + kStages * kStageBytes + kOut + kTops + kScales + 512 + 3 * 4 * (E + 1);
+  }
+};
+
+__host__ __device__ constexpr uint32_t idesc_e4m3(int N, bool a_by_columns) {
+  return (1u << 4)                             // D: fp32; A and B E4M3 are 0
+         | ((a_by_columns ? 1u : 0u) << 15)    // A stored by its contracted index
+         | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A tile of work: tokens [row0, row0 + rows) of expert e times weight tile jt.
+struct Unit {
+  int e, jt, row0, rows, N;
+};
+
+struct Tables {
+  const int *start, *count, *first;  // each expert's first row, rows and first unit (first[E]: all)
+  int E;
+};
+
+// Tables of the experts' rows and units, by the whole CTA.  An expert whose
+// rows begin before an earlier one's first row, fall or leave [0, M] has none
+// and marks the status word.
+template <int NMAX>
+__device__ __forceinline__ void make_tables(const MatmulArgs& a, int* start, int* count, int* first) {
+  const int E = a.E, lane = threadIdx.x & 31;
+  if (a.offsets) {
+    for (int e = threadIdx.x; e <= E; e += kThreads) first[e] = a.offsets[e];
+  } else if (threadIdx.x == 0) {
+    first[0] = 0;
+    first[1] = a.M;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int floor = 0, sum = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      const bool on = e < E;
+      const int lo = on ? first[e] : 0, hi = on ? first[e + 1] : 0;
+      int high = lo;  // the largest start up to this expert
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, high, o);
+        if (lane >= o) high = max(high, v);
+      }
+      high = max(high, floor);
+      const bool good = on && lo >= high && hi >= lo && hi <= a.M;
+      if (on && !good) set_status(a.status, kStatusRange);
+      const int n = good ? hi - lo : 0, units = (n + NMAX - 1) / NMAX * a.JT;
+      int upto = units;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      __syncwarp();  // all have read first[]; the next round reads on from first[e0 + 32]
+      if (on) {
+        start[e] = lo;
+        count[e] = n;
+        first[e] = sum + upto - units;
+      }
+      floor = __shfl_sync(0xffffffffu, high, 31);
+      sum += __shfl_sync(0xffffffffu, upto, 31);
+      __syncwarp();
+    }
+    if (lane == 0) first[E] = sum;
+  }
+  __syncthreads();
+}
+
+template <int NMAX>
+__device__ __forceinline__ Unit unit_of(const Tables& t, int u, int JT) {
+  int lo = 0, hi = t.E;  // the last expert whose first unit is not after u
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.first[mid] <= u) lo = mid; else hi = mid;
+  }
+  // experts without units share their successor's first unit: u lies with the last of equals
+  const int n = t.count[lo], tiles = (n + NMAX - 1) / NMAX, r = u - t.first[lo];
+  const int jt = r / tiles, nt = r - jt * tiles;
+  const int per = ((n + tiles - 1) / tiles + 15) & ~15;
+  Unit x;
+  x.e = lo;
+  x.jt = jt;
+  x.row0 = t.start[lo] + nt * per;
+  x.rows = min(per, n - nt * per);
+  x.N = (x.rows + 15) & ~15;
+  return x;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+}
+
+__device__ __forceinline__ void store_value(void* out, int dtype, int64_t i, float v) {
   if (dtype == FTMOE_FP32) static_cast<float*>(out)[i] = v;
   else if (dtype == FTMOE_FP16) static_cast<__half*>(out)[i] = __float2half_rn(v);
   else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
 }
 
-// A thread computes kRows tokens of one output column (with SwiGLU of a gate
-// and an up column).
-__global__ void __launch_bounds__(128) k_fp8_matmul_plain(const __grid_constant__ MatmulArgs a) {
-  __shared__ float xs[kRows][kFp8Block];
-  __shared__ uint32_t tops[kRows][4];
-  const int C = a.transpose ? a.N : a.K, O = a.transpose ? a.K : a.swiglu ? a.N / 2 : a.N;
-  const int CB = (C + 127) / 128, KB = (a.K + 127) / 128, NB = (a.N + 127) / 128;
-  const int o = blockIdx.y * 128 + threadIdx.x;
-  int tile = blockIdx.x, e = 0, floor = 0;
-  uint32_t* status = threadIdx.x == 0 ? a.status : nullptr;
-  int2 r = make_int2(0, 0);
-  for (; e < a.E; ++e) {
-    r = expert_rows(a.offsets, e, a.M, floor, status);
-    const int n = (r.y - r.x + kRows - 1) / kRows;
-    if (tile < n) break;
-    tile -= n;
+template <int NMAX, bool SWIGLU, bool TRANS>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_fp8_matmul(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_w,
+                 const __grid_constant__ CUtensorMap map_x) {
+  using F = Form<NMAX, SWIGLU>;
+  constexpr int kStages = F::kStages, kBufs = F::kBufs;
+  constexpr int kChunks = NMAX / 32;  // of 16 tokens, of each part, for a warpgroup
+  extern __shared__ unsigned char sm_raw[];
+  unsigned char* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
+  unsigned char* staged = sm + kStages * F::kStageBytes;
+  uint32_t* tops = reinterpret_cast<uint32_t*>(staged + F::kOut);
+  float* s_scale = reinterpret_cast<float*>(staged + F::kOut + F::kTops);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staged + F::kOut + F::kTops + F::kScales);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;   // the MMA's commit and the scale warp
+  uint64_t* acc_empty = acc_full + kBufs;
+  uint64_t* drain = acc_empty + kBufs;
+  uint64_t* wg_bar = drain + 1;           // [2], the warps of an epilogue warpgroup
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wg_bar + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* t_start = reinterpret_cast<int*>(staged + F::kOut + F::kTops + F::kScales + 512);
+  int *t_count = t_start + a.E, *t_first = t_count + a.E;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nkb = (a.C + 127) / 128;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < kBufs; ++b) {
+      mbar_init(&acc_full[b], 2);
+      mbar_init(&acc_empty[b], kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    mbar_init(&wg_bar[0], 4);
+    mbar_init(&wg_bar[1], 4);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&map_w);
+    tma_prefetch_desc(&map_x);
   }
-  if (e == a.E) return;
-  const int row0 = r.x + tile * kRows, rows = min(kRows, r.y - row0);
-  const int64_t bank = (int64_t)e * a.N * a.K;
-  float acc[2][kRows] = {};
-  for (int b = 0; b < CB; ++b) {
-    const int c0 = b * 128, len = min(128, C - c0);
-    __syncthreads();
-    for (int i = 0; i < rows; ++i)
-      xs[i][threadIdx.x] =
-          threadIdx.x < len ? e4m3_decode(a.a[(int64_t)(row0 + i) * C + c0 + threadIdx.x]) : 0.f;
-    __syncthreads();
-    if (o >= O) continue;
-    for (int half = 0; half < (a.swiglu ? 2 : 1); ++half) {
-      const int n = o + half * O;
-      float d[kRows] = {};
-      for (int k = 0; k < len; ++k) {
-        const int64_t at = a.transpose ? (int64_t)(c0 + k) * a.K + n : (int64_t)n * a.K + c0 + k;
-        const float w = e4m3_decode(a.w[bank + at]);
-        for (int i = 0; i < kRows; ++i) d[i] += w * xs[i][k];
+  if (warp == 1) tmem_alloc(tmem_slot, F::kTmemCols);
+  pdl_wait();
+  make_tables<NMAX>(a, t_start, t_count, t_first);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Tables tables{t_start, t_count, t_first, a.E};
+  const int n_units = t_first[a.E];
+
+  if (warp < kEpiWarp0) {
+    regs_down<kLowRegs>();
+    if (warp == 0 && lane == 0) {
+      // ---------------- copies
+      int k = 0;
+      for (int u = blockIdx.x; u < n_units && !*abort_flag; u += gridDim.x) {
+        const Unit x = unit_of<NMAX>(tables, u, a.JT);
+        const int boxes = (x.N + F::kBox - 1) / F::kBox;
+        for (int kb = 0; kb < nkb; ++kb, ++k) {
+          const int s = k % kStages;
+          if (k >= kStages && !mbar_wait(&empty[s], (k / kStages - 1) & 1, a.status)) {
+            *abort_flag = 1;
+            break;
+          }
+          unsigned char* sa = sm + s * F::kStageBytes;
+          unsigned char* sb = sa + F::kABytes;
+          mbar_arrive_expect_tx(&full[s], F::kABytes + boxes * F::kBox * 128);
+          if (TRANS) {
+            tma_load_3d(sa, &map_w, x.jt * 128, kb * 128, x.e, &full[s]);
+          } else {
+            tma_load_3d(sa, &map_w, kb * 128, x.jt * 128, x.e, &full[s]);
+            if (SWIGLU) tma_load_3d(sa + kTile, &map_w, kb * 128, a.O + x.jt * 128, x.e, &full[s]);
+          }
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(sb + b * F::kBox * 128, &map_x, kb * 128, x.row0 + b * F::kBox, &full[s]);
+        }
       }
-      const float sw = a.w_scale[((int64_t)e * NB + (a.transpose ? b : n / 128)) * KB + (a.transpose ? n / 128 : b)];
-      for (int i = 0; i < rows; ++i) acc[half][i] += d[i] * (a.a_scale[(int64_t)b * a.M + row0 + i] * sw);
+      // nothing this warp issued may still be landing when the CTA exits
+      for (int q = k > kStages ? k - kStages : 0; q < k; ++q) mbar_wait(&full[q % kStages], (q / kStages) & 1, a.status);
+    } else if (warp == 1 && lane == 0) {
+      // ---------------- products
+      int k = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < n_units && !*abort_flag; u += gridDim.x) {
+        const Unit x = unit_of<NMAX>(tables, u, a.JT);
+        const uint32_t idesc = idesc_e4m3(x.N, TRANS);
+        for (int kb = 0; kb < nkb; ++kb, ++k) {
+          const int s = k % kStages, b = k % kBufs;
+          if ((k >= kBufs && !mbar_wait(&acc_empty[b], (k / kBufs - 1) & 1, a.status)) ||
+              !mbar_wait(&full[s], (k / kStages) & 1, a.status)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(sm + s * F::kStageBytes);
+          const uint64_t adesc = sdesc_k_sw128(sa), bdesc = sdesc_k_sw128(sa + F::kABytes);
+          const int steps = (min(128, a.C - kb * 128) + 31) / 32;
+          const uint32_t d = tmem + b * F::kCols;
+          for (int i = 0; i < steps; ++i) {
+            // 32 contracted values: 32 bytes on within the swizzled rows, or 32 rows on
+            const uint64_t on = TRANS ? i * (32 * 128 >> 4) : i * (32 >> 4);
+            tc_mma_e4m3(d, adesc + on, bdesc + i * (32 >> 4), idesc, i != 0);
+            if (SWIGLU) tc_mma_e4m3(d + NMAX, adesc + on + (kTile >> 4), bdesc + i * (32 >> 4), idesc, i != 0);
+          }
+          tc_commit(&empty[s]);
+          tc_commit(&acc_full[b]);
+        }
+      }
+      tc_commit(drain);
+      mbar_wait(drain, 0, a.status);
+    } else if (warp == 2) {
+      // ---------------- scales: the block's sx sw of each token
+      constexpr int kPer = (NMAX + 31) / 32;
+      int k = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < n_units && !*abort_flag; u += gridDim.x) {
+        const Unit x = unit_of<NMAX>(tables, u, a.JT);
+        const float* sx = a.a_scale + x.row0;
+        // plain: w_scale[e][jt][kb]; by columns: [e][kb][jt]; the up tile lies O rows on
+        const float* sw = a.w_scale + ((int64_t)x.e * a.NB + (TRANS ? 0 : x.jt)) * a.KB + (TRANS ? x.jt : 0);
+        const int64_t sw_step = TRANS ? a.KB : 1, up = (int64_t)(a.O / 128) * a.KB;
+        float v[kPer], w0 = sw[0], w1 = SWIGLU ? sw[up] : 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) v[i] = lane + 32 * i < x.rows ? sx[lane + 32 * i] : 0.f;
+        for (int kb = 0; kb < nkb; ++kb, ++k) {
+          const int b = k % kBufs;
+          if (k >= kBufs && !warp_wait(&acc_empty[b], (k / kBufs - 1) & 1, a.status)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          float* to = s_scale + b * F::kCols;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            if (lane + 32 * i >= NMAX) continue;
+            to[lane + 32 * i] = v[i] * w0;
+            if (SWIGLU) to[NMAX + lane + 32 * i] = v[i] * w1;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_full[b]);
+          if (kb + 1 < nkb) {
+            const float* next = sx + (int64_t)(kb + 1) * a.M;
+            w0 = sw[(kb + 1) * sw_step];
+            if (SWIGLU) w1 = sw[up + kb + 1];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) v[i] = lane + 32 * i < x.rows ? next[lane + 32 * i] : 0.f;
+          }
+        }
+      }
+    }
+  } else {
+    regs_up<kEpiRegs>();
+    // ---------------- sums: warp (wg, q) has TMEM lanes 32q.. and the chunks wg, wg + 2, ... of 16 tokens
+    const int q = warp & 3, wg = (warp - kEpiWarp0) >> 2;
+    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    constexpr int kAll = F::kParts * kChunks;
+    int k = 0;
+    uint32_t wg_phase = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < n_units && !*abort_flag; u += gridDim.x) {
+      const Unit x = unit_of<NMAX>(tables, u, a.JT);
+      const int mine = (x.N / 16 - wg + 1) >> 1;  // chunks of this warpgroup
+      uint64_t acc[kAll][8];
+#pragma unroll
+      for (int i = 0; i < kAll; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = 0ull;
+      for (int kb = 0; kb < nkb; ++kb, ++k) {
+        const int b = k % kBufs;
+        if (!warp_wait(&acc_full[b], (k / kBufs) & 1, a.status)) {
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + lanes + b * F::kCols + 16 * wg;
+        const float* sc = s_scale + b * F::kCols + 16 * wg;
+        uint32_t r[2][16];
+        if (mine > 0) tc_ld16(d, r[0]);
+#pragma unroll
+        for (int i = 0; i < kAll; ++i) {
+          // chunk i: part i / kChunks, tokens 32 (i % kChunks) + 16 wg
+          const int col = i / kChunks * NMAX + i % kChunks * 32;
+          if (i % kChunks < mine) {
+            tc_wait16(r[i & 1]);
+            // the next chunk there is, into the other registers
+            const int n = i + 1, ncol = n / kChunks * NMAX + n % kChunks * 32;
+            if (n < kAll && n % kChunks < mine) tc_ld16(d + ncol, r[n & 1]);
+            const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(sc + col);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const ulonglong2 s = s2[j];
+              acc[i][2 * j] = fma2(pack2(__uint_as_float(r[i & 1][4 * j]), __uint_as_float(r[i & 1][4 * j + 1])), s.x,
+                                   acc[i][2 * j]);
+              acc[i][2 * j + 1] = fma2(pack2(__uint_as_float(r[i & 1][4 * j + 2]), __uint_as_float(r[i & 1][4 * j + 3])),
+                                       s.y, acc[i][2 * j + 1]);
+            }
+          } else if (i + 1 < kAll && (i + 1) % kChunks == 0 && mine > 0) {
+            tc_ld16(d + (i + 1) / kChunks * NMAX, r[(i + 1) & 1]);  // the next part's first
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[b]);
+      }
+      if (!ok) break;
+      if constexpr (!SWIGLU) {
+        const int o = x.jt * 128 + 32 * q + lane;
+        if (o < a.O) {
+#pragma unroll
+          for (int i = 0; i < kAll; ++i) {
+            const int t0 = 32 * i + 16 * wg;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              float lo, hi;
+              unpack2(acc[i][j], lo, hi);
+              const int64_t at = (int64_t)(x.row0 + t0 + 2 * j) * a.O + o;
+              if (t0 + 2 * j < x.rows) store_value(a.out, a.dtype, at, lo);
+              if (t0 + 2 * j + 1 < x.rows) store_value(a.out, a.dtype, at + a.O, hi);
+            }
+          }
+        }
+      } else {
+        // h in the gate's registers; a token's largest magnitude over the 128 columns from the four warps
+        uint32_t* top = tops + wg * F::kWgTokens * 4;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          if (i < mine) {
+            uint32_t best = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              float g0, g1, u0, u1;
+              unpack2(acc[i][j], g0, g1);
+              unpack2(acc[kChunks + i][j], u0, u1);
+              g0 = g0 * sigmoid(g0) * u0;
+              g1 = g1 * sigmoid(g1) * u1;
+              const uint32_t t0 = __reduce_max_sync(0xffffffffu, magnitude(g0));
+              const uint32_t t1 = __reduce_max_sync(0xffffffffu, magnitude(g1));
+              if (lane == 2 * j) best = t0;
+              if (lane == 2 * j + 1) best = t1;
+              acc[i][j] = pack2(g0, g1);
+            }
+            if (lane < 16) top[(16 * i + lane) * 4 + q] = best;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&wg_bar[wg]);
+        ok = warp_wait(&wg_bar[wg], wg_phase, a.status);
+        wg_phase ^= 1;
+        const int t = 32 * q + lane;  // of this warpgroup's tokens
+        float* muls = reinterpret_cast<float*>(top);
+        if (t < F::kWgTokens) {
+          const uint4 v = reinterpret_cast<const uint4*>(top)[t];
+          const BlockScale s = block_scale(max(max(v.x, v.y), max(v.z, v.w)));
+          const int token = t / 16 * 32 + 16 * wg + t % 16;
+          if (token < x.rows) a.out_scale[(int64_t)x.jt * a.M + x.row0 + token] = s.scale;
+          muls[4 * t] = s.scale == 0.f ? 0.f : s.mul;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&wg_bar[wg]);
+        ok = ok && warp_wait(&wg_bar[wg], wg_phase, a.status);
+        wg_phase ^= 1;
+        unsigned char* st = staged + wg * F::kWgTokens * 128;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          if (i < mine) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              float h0, h1;
+              unpack2(acc[i][j], h0, h1);
+              const float m0 = muls[4 * (16 * i + 2 * j)], m1 = muls[4 * (16 * i + 2 * j + 1)];
+              const uint32_t c = e4m3x4(m0 == 0.f ? 0.f : h0 * m0, m1 == 0.f ? 0.f : h1 * m1, 0.f, 0.f);
+              st[(16 * i + 2 * j) * 128 + 32 * q + lane] = (unsigned char)c;
+              st[(16 * i + 2 * j + 1) * 128 + 32 * q + lane] = (unsigned char)(c >> 8);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&wg_bar[wg]);
+        ok = ok && warp_wait(&wg_bar[wg], wg_phase, a.status);
+        wg_phase ^= 1;
+        for (int i = t; i < mine * 16 * 8; i += 128) {
+          const int row = i >> 3, token = row / 16 * 32 + 16 * wg + row % 16;
+          if (token < x.rows)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (int64_t)(x.row0 + token) * a.O + x.jt * 128 +
+                                      (i & 7) * 16) = reinterpret_cast<const uint4*>(st)[i];
+        }
+        if (!ok) *abort_flag = 1;
+      }
     }
   }
-  if (!a.swiglu) {
-    if (o < O)
-      for (int i = 0; i < rows; ++i) store_out(a.out, a.dtype, (int64_t)(row0 + i) * O + o, acc[0][i]);
-    return;
-  }
-  for (int i = 0; i < rows; ++i) {
-    acc[0][i] = acc[0][i] * sigmoid(acc[0][i]) * acc[1][i];
-    const uint32_t top = __reduce_max_sync(0xffffffffu, magnitude(acc[0][i]));
-    if (threadIdx.x % 32 == 0) tops[i][threadIdx.x / 32] = top;
-  }
+  tc_fence_before();
   __syncthreads();
-  for (int i = 0; i < rows; ++i) {
-    const BlockScale s = block_scale(max(max(tops[i][0], tops[i][1]), max(tops[i][2], tops[i][3])));
-    const float v = s.scale == 0.f ? 0.f : acc[0][i] * s.mul;
-    static_cast<uint8_t*>(a.out)[(int64_t)(row0 + i) * O + o] = (uint8_t)e4m3x4(v, 0.f, 0.f, 0.f);
-    if (threadIdx.x == 0) a.out_scale[(int64_t)blockIdx.y * a.M + row0 + i] = s.scale;
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, F::kTmemCols);
   }
+}
+
+// ---------------------------------------------------------------- host
+
+cudaError_t encode_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                       const uint32_t* box) {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  if (!fn) return cudaErrorNotSupported;
+  cuuint64_t d[3], st[2];
+  cuuint32_t b[3], es[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+  }
+  for (int i = 0; i < rank - 1; ++i) st[i] = strides[i];
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), d, st, b, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int NMAX, bool SWIGLU, bool TRANS>
+cudaError_t launch_form(const TrainDevice& d, const ftmoe_fp8_matmul_args& m, const MatmulArgs& a, cudaStream_t s) {
+  using F = Form<NMAX, SWIGLU>;
+  CUtensorMap map_w, map_x;
+  const uint64_t wd[3] = {(uint64_t)m.K, (uint64_t)m.N, (uint64_t)m.E}, ws[2] = {(uint64_t)m.K, (uint64_t)m.N * m.K};
+  const uint32_t wb[3] = {128, 128, 1};
+  cudaError_t e = encode_map(&map_w, m.w, 3, wd, ws, wb);
+  if (e != cudaSuccess) return e;
+  const uint64_t xd[2] = {(uint64_t)a.C, (uint64_t)m.M}, xs[1] = {(uint64_t)a.C};
+  const uint32_t xb[2] = {128, F::kBox};
+  if ((e = encode_map(&map_x, m.a, 2, xd, xs, xb)) != cudaSuccess) return e;
+  auto* k = k_fp8_matmul<NMAX, SWIGLU, TRANS>;
+  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem(kMaxBins))) != cudaSuccess)
+    return e;
+  const int64_t most = (m.M / NMAX + (m.M < m.E ? m.M : m.E)) * a.JT;  // units; held to int by the caller
+  return launch_after_smem(k, (unsigned)(most < d.num_sms ? most : d.num_sms), kThreads, F::smem(m.E), s, a, map_w,
+                           map_x);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_matmul(const TrainDevice& d, const ftmoe_fp8_matmul_args& m, cudaStream_t s) {
-  const MatmulArgs a{m.a, m.w, m.a_scale, m.w_scale, m.offsets, (int)m.M, m.E, m.N, m.K, m.transpose, m.swiglu,
-                     m.out_dtype, m.out, m.out_scale, d.status};
-  const int O = m.transpose ? m.K : m.swiglu ? m.N / 2 : m.N;
-  const dim3 grid((unsigned)(m.M / kRows + m.E), (unsigned)fp8_blocks(O));
-  k_fp8_matmul_plain<<<grid, 128, 0, s>>>(a);
-  return cudaGetLastError();
+  MatmulArgs a{};
+  a.a_scale = m.a_scale;
+  a.w_scale = m.w_scale;
+  a.offsets = m.offsets;
+  a.M = (int)m.M;
+  a.E = m.E;
+  a.C = m.transpose ? m.N : m.K;
+  a.O = m.transpose ? m.K : m.swiglu ? m.N / 2 : m.N;
+  a.NB = fp8_blocks(m.N);
+  a.KB = fp8_blocks(m.K);
+  a.JT = fp8_blocks(a.O);
+  a.dtype = m.out_dtype;
+  a.out = m.out;
+  a.out_scale = m.out_scale;
+  a.status = d.status;
+  // up to 32 tokens an expert in the mean: narrow tiles, whose stages are nearly all weights
+  const bool few = m.M <= (int64_t)32 * m.E;
+  if (m.swiglu) return few ? launch_form<32, true, false>(d, m, a, s) : launch_form<128, true, false>(d, m, a, s);
+  if (m.transpose) return few ? launch_form<32, false, true>(d, m, a, s) : launch_form<256, false, true>(d, m, a, s);
+  return few ? launch_form<32, false, false>(d, m, a, s) : launch_form<256, false, false>(d, m, a, s);
 }
 
 }  // namespace ftmoe
