@@ -58,7 +58,10 @@ struct Form {
   static constexpr int kBufs = 512 / kCols < 4 ? 512 / kCols : 4;
   static constexpr int kTmemCols = kBufs * kCols;
   static constexpr int kWgTokens = NMAX / 2;  // of a warpgroup
-  static constexpr int kOut = SWIGLU ? 2 * kWgTokens * 128 : 0;  // bytes of staged codes
+  // Staging of a warpgroup's outputs: rows of 144 bytes of codes for all its tokens; or 16 tokens' 128 values, rows
+  // of 256 bytes (16 bits, twice) or 528 (fp32).  The paddings keep the warps' stores apart in the banks.
+  static constexpr int kWgOut = SWIGLU ? kWgTokens * 144 : 16 * 528;
+  static constexpr int kOut = 2 * kWgOut;
   static constexpr int kTops = SWIGLU ? 2 * kWgTokens * 4 * 4 : 0;
   static constexpr int kScales = kBufs * kCols * 4;
   static constexpr int kFixed = 1024 + kOut + kTops + kScales + 512 + 3 * 4 * (kMaxBins + 1);
@@ -177,10 +180,34 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
 
-__device__ __forceinline__ void store_value(void* out, int dtype, int64_t i, float v) {
-  if (dtype == FTMOE_FP32) static_cast<float*>(out)[i] = v;
-  else if (dtype == FTMOE_FP16) static_cast<__half*>(out)[i] = __float2half_rn(v);
-  else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+// 16 lanes x 16 columns of tensor memory: lane l of the warp gets the rows
+// l / 4 (r0, r1, r4, r5) and l / 4 + 8 (r2, r3, r6, r7), of each the columns
+// 2 (l % 4) and one more, and the same 8 columns on.
+__device__ __forceinline__ void tc_ld_16x16(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit values, transposed: a lane holds row l / 4 of
+// each, columns 2 (l % 4) and one more; row l % 8 of matrix l / 8 in memory,
+// the registers' column, goes to this lane's address.
+__device__ __forceinline__ void st_matrix_t(void* p, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(p)), "r"(r0),
+               "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t halves(uint64_t v, int dtype) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  if (dtype == FTMOE_FP16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 template <int NMAX, bool SWIGLU, bool TRANS>
@@ -338,21 +365,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     regs_up<kEpiRegs>();
-    // ---------------- sums: warp (wg, q) has TMEM lanes 32q.. and the chunks wg, wg + 2, ... of 16 tokens
+    // ---------------- sums: warp (wg, q) has TMEM lanes 32q.. and the chunks wg, wg + 2, ... of 16 tokens.
+    // acc[i][j][m]: chunk i's tokens 8j + 2 (lane % 4) and one more, output 32q + 8m + lane / 4.  A lane so needs
+    // the scales of a quarter of the tokens: two 8-byte loads for 16 sums (with a lane for each output, its 16
+    // columns took four 16-byte loads, and shared memory was the bound).
     const int q = warp & 3, wg = (warp - kEpiWarp0) >> 2;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     constexpr int kAll = F::kParts * kChunks;
+    unsigned char* st = staged + wg * F::kWgOut;
+    const int t = 32 * q + lane;  // thread of the warpgroup
     int k = 0;
-    uint32_t wg_phase = 0;
+    uint32_t wg_phase = 0, flip = 0;
     bool ok = true;
+    const auto wg_sync = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&wg_bar[wg]);
+      ok = warp_wait(&wg_bar[wg], wg_phase, a.status) && ok;
+      wg_phase ^= 1;
+    };
     for (int u = blockIdx.x; ok && u < n_units && !*abort_flag; u += gridDim.x) {
       const Unit x = unit_of<NMAX>(tables, u, a.JT);
       const int mine = (x.N / 16 - wg + 1) >> 1;  // chunks of this warpgroup
-      uint64_t acc[kAll][8];
+      uint64_t acc[kAll][2][4];
 #pragma unroll
       for (int i = 0; i < kAll; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = 0ull;
+        for (int j = 0; j < 8; ++j) acc[i][j / 4][j % 4] = 0ull;
       for (int kb = 0; kb < nkb; ++kb, ++k) {
         const int b = k % kBufs;
         if (!warp_wait(&acc_full[b], (k / kBufs) & 1, a.status)) {
@@ -362,29 +400,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + lanes + b * F::kCols + 16 * wg;
-        const float* sc = s_scale + b * F::kCols + 16 * wg;
+        const float* sc = s_scale + b * F::kCols + 16 * wg + 2 * (lane & 3);
         uint32_t r[2][16];
-        if (mine > 0) tc_ld16(d, r[0]);
+        if (mine > 0) {
+          tc_ld_16x16(d, r[0]);
+          tc_ld_16x16(d + (16u << 16), r[0] + 8);
+        }
 #pragma unroll
         for (int i = 0; i < kAll; ++i) {
           // chunk i: part i / kChunks, tokens 32 (i % kChunks) + 16 wg
           const int col = i / kChunks * NMAX + i % kChunks * 32;
+          const int n = i + 1, ncol = n / kChunks * NMAX + n % kChunks * 32;
+          if (i % kChunks < mine) tc_wait16(r[i & 1]);
+          // the next chunk there is, into the other registers
+          if (n < kAll && n % kChunks < mine) {
+            tc_ld_16x16(d + ncol, r[n & 1]);
+            tc_ld_16x16(d + ncol + (16u << 16), r[n & 1] + 8);
+          }
           if (i % kChunks < mine) {
-            tc_wait16(r[i & 1]);
-            // the next chunk there is, into the other registers
-            const int n = i + 1, ncol = n / kChunks * NMAX + n % kChunks * 32;
-            if (n < kAll && n % kChunks < mine) tc_ld16(d + ncol, r[n & 1]);
-            const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(sc + col);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const ulonglong2 s = s2[j];
-              acc[i][2 * j] = fma2(pack2(__uint_as_float(r[i & 1][4 * j]), __uint_as_float(r[i & 1][4 * j + 1])), s.x,
-                                   acc[i][2 * j]);
-              acc[i][2 * j + 1] = fma2(pack2(__uint_as_float(r[i & 1][4 * j + 2]), __uint_as_float(r[i & 1][4 * j + 3])),
-                                       s.y, acc[i][2 * j + 1]);
+            for (int j = 0; j < 2; ++j) {
+              const uint64_t s = *reinterpret_cast<const uint64_t*>(sc + col + 8 * j);
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                const uint32_t* v = r[i & 1] + 8 * (m / 2) + 4 * j + 2 * (m % 2);
+                acc[i][j][m] = fma2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), s, acc[i][j][m]);
+              }
             }
-          } else if (i + 1 < kAll && (i + 1) % kChunks == 0 && mine > 0) {
-            tc_ld16(d + (i + 1) / kChunks * NMAX, r[(i + 1) & 1]);  // the next part's first
           }
         }
         tc_fence_before();
@@ -393,19 +435,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if constexpr (!SWIGLU) {
-        const int o = x.jt * 128 + 32 * q + lane;
-        if (o < a.O) {
+        const int o0 = x.jt * 128;
+        const bool wide = a.dtype != FTMOE_FP32 ? a.O % 8 == 0 : a.O % 4 == 0;
 #pragma unroll
-          for (int i = 0; i < kAll; ++i) {
-            const int t0 = 32 * i + 16 * wg;
+        for (int i = 0; i < kChunks; ++i) {
+          if (i >= mine) continue;
+          const int t0 = 32 * i + 16 * wg, rows = min(16, x.rows - t0);
+          const int64_t first = (int64_t)(x.row0 + t0) * a.O + o0;
+          if (a.dtype != FTMOE_FP32) {
+            // [token][128] with the 16-byte pieces of a row turned by the token.  Two buffers in turn: the barrier
+            // between writing and reading one is also behind all reads of the other.
+            unsigned char* to = st + flip;
+            flip ^= 4096;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              float lo, hi;
-              unpack2(acc[i][j], lo, hi);
-              const int64_t at = (int64_t)(x.row0 + t0 + 2 * j) * a.O + o;
-              if (t0 + 2 * j < x.rows) store_value(a.out, a.dtype, at, lo);
-              if (t0 + 2 * j + 1 < x.rows) store_value(a.out, a.dtype, at + a.O, hi);
+            for (int j = 0; j < 2; ++j) {
+              const int token = 8 * j + (lane & 7);
+              st_matrix_t(to + token * 256 + (((4 * q + lane / 8) ^ (token & 7)) << 4), halves(acc[i][j][0], a.dtype),
+                          halves(acc[i][j][1], a.dtype), halves(acc[i][j][2], a.dtype), halves(acc[i][j][3], a.dtype));
             }
+            wg_sync();
+            uint16_t* out = static_cast<uint16_t*>(a.out) + first;
+            if (wide) {
+#pragma unroll
+              for (int n = t; n < 256; n += 128) {
+                const int token = n >> 4, piece = n & 15;
+                if (token < rows && o0 + 8 * piece < a.O)
+                  *reinterpret_cast<uint4*>(out + (int64_t)token * a.O + 8 * piece) =
+                      *reinterpret_cast<const uint4*>(to + token * 256 + ((piece ^ (token & 7)) << 4));
+              }
+            } else if (o0 + t < a.O) {
+              for (int token = 0; token < rows; ++token)
+                out[(int64_t)token * a.O + t] = *reinterpret_cast<const uint16_t*>(
+                    to + token * 256 + (((t >> 3) ^ (token & 7)) << 4) + 2 * (t & 7));
+            }
+          } else {
+            float* to = reinterpret_cast<float*>(st);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                float lo, hi;
+                unpack2(acc[i][j][m], lo, hi);
+                float* at = to + (8 * j + 2 * (lane & 3)) * 132 + 32 * q + 8 * m + lane / 4;
+                at[0] = lo;
+                at[132] = hi;
+              }
+            wg_sync();
+            float* out = static_cast<float*>(a.out) + first;
+            if (wide) {
+#pragma unroll
+              for (int n = t; n < 512; n += 128) {
+                const int token = n >> 5, piece = n & 31;
+                if (token < rows && o0 + 4 * piece < a.O)
+                  *reinterpret_cast<float4*>(out + (int64_t)token * a.O + 4 * piece) =
+                      *reinterpret_cast<const float4*>(to + token * 132 + 4 * piece);
+              }
+            } else if (o0 + t < a.O) {
+              for (int token = 0; token < rows; ++token) out[(int64_t)token * a.O + t] = to[token * 132 + t];
+            }
+            wg_sync();
           }
         }
       } else {
@@ -413,68 +501,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t* top = tops + wg * F::kWgTokens * 4;
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-          if (i < mine) {
-            uint32_t best = 0;
+          if (i >= mine) continue;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 2; ++j) {
+            uint32_t best0 = 0, best1 = 0;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
               float g0, g1, u0, u1;
-              unpack2(acc[i][j], g0, g1);
-              unpack2(acc[kChunks + i][j], u0, u1);
+              unpack2(acc[i][j][m], g0, g1);
+              unpack2(acc[kChunks + i][j][m], u0, u1);
               g0 = g0 * sigmoid(g0) * u0;
               g1 = g1 * sigmoid(g1) * u1;
-              const uint32_t t0 = __reduce_max_sync(0xffffffffu, magnitude(g0));
-              const uint32_t t1 = __reduce_max_sync(0xffffffffu, magnitude(g1));
-              if (lane == 2 * j) best = t0;
-              if (lane == 2 * j + 1) best = t1;
-              acc[i][j] = pack2(g0, g1);
+              best0 = max(best0, magnitude(g0));
+              best1 = max(best1, magnitude(g1));
+              acc[i][j][m] = pack2(g0, g1);
             }
-            if (lane < 16) top[(16 * i + lane) * 4 + q] = best;
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              best0 = max(best0, __shfl_xor_sync(0xffffffffu, best0, o));
+              best1 = max(best1, __shfl_xor_sync(0xffffffffu, best1, o));
+            }
+            if (lane < 4) {
+              top[(16 * i + 8 * j + 2 * lane) * 4 + q] = best0;
+              top[(16 * i + 8 * j + 2 * lane + 1) * 4 + q] = best1;
+            }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&wg_bar[wg]);
-        ok = warp_wait(&wg_bar[wg], wg_phase, a.status);
-        wg_phase ^= 1;
-        const int t = 32 * q + lane;  // of this warpgroup's tokens
+        wg_sync();
         float* muls = reinterpret_cast<float*>(top);
-        if (t < F::kWgTokens) {
+        if (t < 16 * mine) {
           const uint4 v = reinterpret_cast<const uint4*>(top)[t];
           const BlockScale s = block_scale(max(max(v.x, v.y), max(v.z, v.w)));
           const int token = t / 16 * 32 + 16 * wg + t % 16;
           if (token < x.rows) a.out_scale[(int64_t)x.jt * a.M + x.row0 + token] = s.scale;
           muls[4 * t] = s.scale == 0.f ? 0.f : s.mul;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&wg_bar[wg]);
-        ok = ok && warp_wait(&wg_bar[wg], wg_phase, a.status);
-        wg_phase ^= 1;
-        unsigned char* st = staged + wg * F::kWgTokens * 128;
+        wg_sync();
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-          if (i < mine) {
+          if (i >= mine) continue;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 2; ++j) {
+            const int token = 16 * i + 8 * j + 2 * (lane & 3);
+            const float m0 = muls[4 * token], m1 = muls[4 * token + 4];
+            unsigned char* at = st + token * 144 + 32 * q + lane / 4;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
               float h0, h1;
-              unpack2(acc[i][j], h0, h1);
-              const float m0 = muls[4 * (16 * i + 2 * j)], m1 = muls[4 * (16 * i + 2 * j + 1)];
+              unpack2(acc[i][j][m], h0, h1);
               const uint32_t c = e4m3x4(m0 == 0.f ? 0.f : h0 * m0, m1 == 0.f ? 0.f : h1 * m1, 0.f, 0.f);
-              st[(16 * i + 2 * j) * 128 + 32 * q + lane] = (unsigned char)c;
-              st[(16 * i + 2 * j + 1) * 128 + 32 * q + lane] = (unsigned char)(c >> 8);
+              at[8 * m] = (unsigned char)c;
+              at[8 * m + 144] = (unsigned char)(c >> 8);
             }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&wg_bar[wg]);
-        ok = ok && warp_wait(&wg_bar[wg], wg_phase, a.status);
-        wg_phase ^= 1;
-        for (int i = t; i < mine * 16 * 8; i += 128) {
-          const int row = i >> 3, token = row / 16 * 32 + 16 * wg + row % 16;
+        wg_sync();
+        for (int n = t; n < mine * 16 * 8; n += 128) {
+          const int row = n >> 3, token = row / 16 * 32 + 16 * wg + row % 16;
           if (token < x.rows)
             *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (int64_t)(x.row0 + token) * a.O + x.jt * 128 +
-                                      (i & 7) * 16) = reinterpret_cast<const uint4*>(st)[i];
+                                      (n & 7) * 16) = *reinterpret_cast<const uint4*>(st + row * 144 + (n & 7) * 16);
         }
-        if (!ok) *abort_flag = 1;
       }
+      if (!ok) *abort_flag = 1;
     }
   }
   tc_fence_before();
