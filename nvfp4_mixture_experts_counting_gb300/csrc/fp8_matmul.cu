@@ -26,11 +26,11 @@ namespace ftmoe {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kEpiWarp0 = 4;      // two warpgroups of epilogue warps
-constexpr int kEpiWarps = 8;
-constexpr int kLaunchRegs = 168, kLowRegs = 72, kEpiRegs = 216;
-static_assert(3 * kLaunchRegs == kLowRegs + 2 * kEpiRegs, "the warpgroups' shares add up to the launch's registers");
+constexpr int kThreads = 640;
+constexpr int kEpiWarp0 = 4;
+constexpr int kEpiWarps = 16;     // four warpgroups: an FMA pipe fed by two warps stays at three quarters of its rate
+constexpr int kLaunchRegs = 96, kLowRegs = 64, kEpiRegs = 104;
+static_assert(5 * kLaunchRegs == kLowRegs + 4 * kEpiRegs, "the warpgroups' shares add up to the launch's registers");
 constexpr int kTile = 128 * 128;  // bytes of a weight tile
 constexpr int kSmemMax = 227 * 1024;
 
@@ -57,12 +57,13 @@ struct Form {
   static constexpr int kCols = kParts * NMAX;  // of an accumulator buffer
   static constexpr int kBufs = 512 / kCols < 4 ? 512 / kCols : 4;
   static constexpr int kTmemCols = kBufs * kCols;
-  static constexpr int kWgTokens = NMAX / 2;  // of a warpgroup
-  // Staging of a warpgroup's outputs: rows of 144 bytes of codes for all its tokens; or 16 tokens' 128 values, rows
-  // of 256 bytes (16 bits, twice) or 528 (fp32).  The paddings keep the warps' stores apart in the banks.
-  static constexpr int kWgOut = SWIGLU ? kWgTokens * 144 : 16 * 528;
-  static constexpr int kOut = 2 * kWgOut;
-  static constexpr int kTops = SWIGLU ? 2 * kWgTokens * 4 * 4 : 0;
+  // Chunks of 32 tokens, of each part, that an epilogue warpgroup sums.
+  static constexpr int kChunks = (NMAX + 127) / 128;
+  // Staging of a warp's 32 outputs: 16 tokens' in 16 bits, 8 tokens' in fp32 (rows of 36, which keeps the stores'
+  // banks apart), or 32 tokens' codes.
+  static constexpr int kWarpOut = SWIGLU ? 1024 : 1152;
+  static constexpr int kOut = kEpiWarps * kWarpOut;
+  static constexpr int kTops = SWIGLU ? NMAX * 4 * 4 : 0;  // a token's largest magnitude in each warp
   static constexpr int kScales = kBufs * kCols * 4;
   static constexpr int kFixed = 1024 + kOut + kTops + kScales + 512 + 3 * 4 * (kMaxBins + 1);
   static constexpr int kStages0 = (kSmemMax - kFixed) / kStageBytes;
@@ -180,14 +181,25 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
 
-// 16 lanes x 16 columns of tensor memory: lane l of the warp gets the rows
-// l / 4 (r0, r1, r4, r5) and l / 4 + 8 (r2, r3, r6, r7), of each the columns
-// 2 (l % 4) and one more, and the same 8 columns on.
-__device__ __forceinline__ void tc_ld_16x16(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr)
-               : "memory");
+// 16 lanes x 32 columns of tensor memory: lane l of the warp gets, of each 8
+// columns, the values of row l / 4 in the columns 2 (l % 4) and one more, then
+// those of row l / 4 + 8.  Neither this nor the wait orders memory: loads of
+// scales may pass them (what they read is ordered by mbarriers).
+__device__ __forceinline__ void tc_ld_16x32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tc_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+  asm volatile(""
+               : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31]));
 }
 
 // Four 8 x 8 matrices of 16-bit values, transposed: a lane holds row l / 4 of
@@ -216,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap map_x) {
   using F = Form<NMAX, SWIGLU>;
   constexpr int kStages = F::kStages, kBufs = F::kBufs;
-  constexpr int kChunks = NMAX / 32;  // of 16 tokens, of each part, for a warpgroup
+  constexpr int kChunks = F::kChunks;
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
   unsigned char* staged = sm + kStages * F::kStageBytes;
@@ -227,8 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acc_full = empty + kStages;   // the MMA's commit and the scale warp
   uint64_t* acc_empty = acc_full + kBufs;
   uint64_t* drain = acc_empty + kBufs;
-  uint64_t* wg_bar = drain + 1;           // [2], the warps of an epilogue warpgroup
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wg_bar + 2);
+  uint64_t* wg_bar = drain + 1;           // [4], the warps of an epilogue warpgroup
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wg_bar + kEpiWarps / 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* t_start = reinterpret_cast<int*>(staged + F::kOut + F::kTops + F::kScales + 512);
   int *t_count = t_start + a.E, *t_first = t_count + a.E;
@@ -245,8 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&acc_empty[b], kEpiWarps);
     }
     mbar_init(drain, 1);
-    mbar_init(&wg_bar[0], 4);
-    mbar_init(&wg_bar[1], 4);
+    for (int w = 0; w < kEpiWarps / 4; ++w) mbar_init(&wg_bar[w], 4);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&map_w);
@@ -365,32 +376,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     regs_up<kEpiRegs>();
-    // ---------------- sums: warp (wg, q) has TMEM lanes 32q.. and the chunks wg, wg + 2, ... of 16 tokens.
+    // ---------------- sums: warp (wg, q) has TMEM lanes 32q.. and the chunks wg, wg + 4, ... of 32 tokens.
     // acc[i][j][m]: chunk i's tokens 8j + 2 (lane % 4) and one more, output 32q + 8m + lane / 4.  A lane so needs
-    // the scales of a quarter of the tokens: two 8-byte loads for 16 sums (with a lane for each output, its 16
-    // columns took four 16-byte loads, and shared memory was the bound).
+    // the scales of a quarter of the tokens.
     const int q = warp & 3, wg = (warp - kEpiWarp0) >> 2;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     constexpr int kAll = F::kParts * kChunks;
-    unsigned char* st = staged + wg * F::kWgOut;
-    const int t = 32 * q + lane;  // thread of the warpgroup
+    unsigned char* st = staged + (warp - kEpiWarp0) * F::kWarpOut;
     int k = 0;
-    uint32_t wg_phase = 0, flip = 0;
+    uint32_t wg_phase = 0;
     bool ok = true;
-    const auto wg_sync = [&] {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&wg_bar[wg]);
-      ok = warp_wait(&wg_bar[wg], wg_phase, a.status) && ok;
-      wg_phase ^= 1;
-    };
     for (int u = blockIdx.x; ok && u < n_units && !*abort_flag; u += gridDim.x) {
       const Unit x = unit_of<NMAX>(tables, u, a.JT);
-      const int mine = (x.N / 16 - wg + 1) >> 1;  // chunks of this warpgroup
-      uint64_t acc[kAll][2][4];
+      const int mine = ((x.N + 31) / 32 - wg + 3) >> 2;  // chunks of this warpgroup; the last may be half a one
+      uint64_t acc[kAll][4][4];
 #pragma unroll
       for (int i = 0; i < kAll; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j / 4][j % 4] = 0ull;
+        for (int j = 0; j < 16; ++j) acc[i][j / 4][j % 4] = 0ull;
       for (int kb = 0; kb < nkb; ++kb, ++k) {
         const int b = k % kBufs;
         if (!warp_wait(&acc_full[b], (k / kBufs) & 1, a.status)) {
@@ -399,33 +402,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + lanes + b * F::kCols + 16 * wg;
-        const float* sc = s_scale + b * F::kCols + 16 * wg + 2 * (lane & 3);
-        uint32_t r[2][16];
-        if (mine > 0) {
-          tc_ld_16x16(d, r[0]);
-          tc_ld_16x16(d + (16u << 16), r[0] + 8);
-        }
+        const uint32_t d = tmem + lanes + b * F::kCols + 32 * wg;
+        const float* sc = s_scale + b * F::kCols + 32 * wg + 2 * (lane & 3);
 #pragma unroll
         for (int i = 0; i < kAll; ++i) {
-          // chunk i: part i / kChunks, tokens 32 (i % kChunks) + 16 wg
-          const int col = i / kChunks * NMAX + i % kChunks * 32;
-          const int n = i + 1, ncol = n / kChunks * NMAX + n % kChunks * 32;
-          if (i % kChunks < mine) tc_wait16(r[i & 1]);
-          // the next chunk there is, into the other registers
-          if (n < kAll && n % kChunks < mine) {
-            tc_ld_16x16(d + ncol, r[n & 1]);
-            tc_ld_16x16(d + ncol + (16u << 16), r[n & 1] + 8);
-          }
-          if (i % kChunks < mine) {
+          if (i % kChunks >= mine) continue;
+          // chunk i: part i / kChunks, tokens 128 (i % kChunks) + 32 wg
+          const int col = i / kChunks * NMAX + i % kChunks * 128;
+          uint32_t r[32];
+          tc_ld_16x32(d + col, r);
+          tc_ld_16x32(d + col + (16u << 16), r + 16);
+          tc_wait32(r);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint64_t s = *reinterpret_cast<const uint64_t*>(sc + col + 8 * j);
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t s = *reinterpret_cast<const uint64_t*>(sc + col + 8 * j);
 #pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                const uint32_t* v = r[i & 1] + 8 * (m / 2) + 4 * j + 2 * (m % 2);
-                acc[i][j][m] = fma2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), s, acc[i][j][m]);
-              }
+            for (int m = 0; m < 4; ++m) {
+              const uint32_t* v = r + 16 * (m / 2) + 4 * j + 2 * (m % 2);
+              acc[i][j][m] = fma2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), s, acc[i][j][m]);
             }
           }
         }
@@ -435,86 +429,88 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if constexpr (!SWIGLU) {
-        const int o0 = x.jt * 128;
-        const bool wide = a.dtype != FTMOE_FP32 ? a.O % 8 == 0 : a.O % 4 == 0;
+        const int o0 = x.jt * 128 + 32 * q, width = min(32, a.O - o0);  // this warp's outputs
+        if (a.dtype != FTMOE_FP32) {
+          const bool wide = a.O % 8 == 0;
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          if (i >= mine) continue;
-          const int t0 = 32 * i + 16 * wg, rows = min(16, x.rows - t0);
-          const int64_t first = (int64_t)(x.row0 + t0) * a.O + o0;
-          if (a.dtype != FTMOE_FP32) {
-            // [token][128] with the 16-byte pieces of a row turned by the token.  Two buffers in turn: the barrier
-            // between writing and reading one is also behind all reads of the other.
-            unsigned char* to = st + flip;
-            flip ^= 4096;
+          for (int h = 0; h < 2 * kChunks; ++h) {  // by 16 tokens
+            const int i = h / 2, j0 = h % 2 * 2, t0 = 128 * i + 32 * wg + 16 * (h % 2), rows = min(16, x.rows - t0);
+            if (rows <= 0 || width <= 0) continue;
+            // [token][32] with the 16-byte pieces of a row turned by the token
+            __syncwarp();
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int token = 8 * j + (lane & 7);
-              st_matrix_t(to + token * 256 + (((4 * q + lane / 8) ^ (token & 7)) << 4), halves(acc[i][j][0], a.dtype),
-                          halves(acc[i][j][1], a.dtype), halves(acc[i][j][2], a.dtype), halves(acc[i][j][3], a.dtype));
+              st_matrix_t(st + token * 64 + (((lane / 8) ^ (token / 2 & 3)) << 4), halves(acc[i][j0 + j][0], a.dtype),
+                          halves(acc[i][j0 + j][1], a.dtype), halves(acc[i][j0 + j][2], a.dtype),
+                          halves(acc[i][j0 + j][3], a.dtype));
             }
-            wg_sync();
-            uint16_t* out = static_cast<uint16_t*>(a.out) + first;
+            __syncwarp();
+            uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(x.row0 + t0) * a.O + o0;
             if (wide) {
 #pragma unroll
-              for (int n = t; n < 256; n += 128) {
-                const int token = n >> 4, piece = n & 15;
-                if (token < rows && o0 + 8 * piece < a.O)
+              for (int n = lane; n < 64; n += 32) {
+                const int token = n >> 2, piece = n & 3;
+                if (token < rows && 8 * piece < width)
                   *reinterpret_cast<uint4*>(out + (int64_t)token * a.O + 8 * piece) =
-                      *reinterpret_cast<const uint4*>(to + token * 256 + ((piece ^ (token & 7)) << 4));
+                      *reinterpret_cast<const uint4*>(st + token * 64 + ((piece ^ (token / 2 & 3)) << 4));
               }
-            } else if (o0 + t < a.O) {
+            } else if (lane < width) {
               for (int token = 0; token < rows; ++token)
-                out[(int64_t)token * a.O + t] = *reinterpret_cast<const uint16_t*>(
-                    to + token * 256 + (((t >> 3) ^ (token & 7)) << 4) + 2 * (t & 7));
+                out[(int64_t)token * a.O + lane] = *reinterpret_cast<const uint16_t*>(
+                    st + token * 64 + (((lane >> 3) ^ (token / 2 & 3)) << 4) + 2 * (lane & 7));
             }
-          } else {
-            float* to = reinterpret_cast<float*>(st);
+          }
+        } else {
+          const bool wide = a.O % 4 == 0;
+          float* to = reinterpret_cast<float*>(st);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+          for (int h = 0; h < 4 * kChunks; ++h) {  // by 8 tokens
+            const int i = h / 4, t0 = 128 * i + 32 * wg + 8 * (h % 4), rows = min(8, x.rows - t0);
+            if (rows <= 0 || width <= 0) continue;
+            __syncwarp();
 #pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                float lo, hi;
-                unpack2(acc[i][j][m], lo, hi);
-                float* at = to + (8 * j + 2 * (lane & 3)) * 132 + 32 * q + 8 * m + lane / 4;
-                at[0] = lo;
-                at[132] = hi;
-              }
-            wg_sync();
-            float* out = static_cast<float*>(a.out) + first;
+            for (int m = 0; m < 4; ++m) {
+              float lo, hi;
+              unpack2(acc[i][h % 4][m], lo, hi);
+              float* at = to + 2 * (lane & 3) * 36 + 8 * m + lane / 4;
+              at[0] = lo;
+              at[36] = hi;
+            }
+            __syncwarp();
+            float* out = static_cast<float*>(a.out) + (int64_t)(x.row0 + t0) * a.O + o0;
             if (wide) {
 #pragma unroll
-              for (int n = t; n < 512; n += 128) {
-                const int token = n >> 5, piece = n & 31;
-                if (token < rows && o0 + 4 * piece < a.O)
+              for (int n = lane; n < 64; n += 32) {
+                const int token = n >> 3, piece = n & 7;
+                if (token < rows && 4 * piece < width)
                   *reinterpret_cast<float4*>(out + (int64_t)token * a.O + 4 * piece) =
-                      *reinterpret_cast<const float4*>(to + token * 132 + 4 * piece);
+                      *reinterpret_cast<const float4*>(to + token * 36 + 4 * piece);
               }
-            } else if (o0 + t < a.O) {
-              for (int token = 0; token < rows; ++token) out[(int64_t)token * a.O + t] = to[token * 132 + t];
+            } else if (lane < width) {
+              for (int token = 0; token < rows; ++token) out[(int64_t)token * a.O + lane] = to[token * 36 + lane];
             }
-            wg_sync();
           }
         }
       } else {
-        // h in the gate's registers; a token's largest magnitude over the 128 columns from the four warps
-        uint32_t* top = tops + wg * F::kWgTokens * 4;
+        static_assert(!SWIGLU || kChunks == 1, "a warpgroup has one chunk of tokens");
+        const int t0 = 32 * wg;
+        if (mine > 0) {
+          // h in the gate's registers; a token's largest magnitude over the 128 columns from the four warps
+          uint32_t* top = tops + t0 * 4;
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          if (i >= mine) continue;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < 4; ++j) {
             uint32_t best0 = 0, best1 = 0;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
               float g0, g1, u0, u1;
-              unpack2(acc[i][j][m], g0, g1);
-              unpack2(acc[kChunks + i][j][m], u0, u1);
+              unpack2(acc[0][j][m], g0, g1);
+              unpack2(acc[kChunks][j][m], u0, u1);
               g0 = g0 * sigmoid(g0) * u0;
               g1 = g1 * sigmoid(g1) * u1;
               best0 = max(best0, magnitude(g0));
               best1 = max(best1, magnitude(g1));
-              acc[i][j][m] = pack2(g0, g1);
+              acc[0][j][m] = pack2(g0, g1);
             }
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
@@ -522,45 +518,45 @@ __global__ void __launch_bounds__(kThreads, 1)
               best1 = max(best1, __shfl_xor_sync(0xffffffffu, best1, o));
             }
             if (lane < 4) {
-              top[(16 * i + 8 * j + 2 * lane) * 4 + q] = best0;
-              top[(16 * i + 8 * j + 2 * lane + 1) * 4 + q] = best1;
+              top[(8 * j + 2 * lane) * 4 + q] = best0;
+              top[(8 * j + 2 * lane + 1) * 4 + q] = best1;
             }
           }
-        }
-        wg_sync();
-        float* muls = reinterpret_cast<float*>(top);
-        if (t < 16 * mine) {
-          const uint4 v = reinterpret_cast<const uint4*>(top)[t];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&wg_bar[wg]);
+          ok = warp_wait(&wg_bar[wg], wg_phase, a.status);
+          wg_phase ^= 1;
+          // lane t works token t's scale out, in each of the four warps
+          const uint4 v = reinterpret_cast<const uint4*>(top)[lane];
           const BlockScale s = block_scale(max(max(v.x, v.y), max(v.z, v.w)));
-          const int token = t / 16 * 32 + 16 * wg + t % 16;
-          if (token < x.rows) a.out_scale[(int64_t)x.jt * a.M + x.row0 + token] = s.scale;
-          muls[4 * t] = s.scale == 0.f ? 0.f : s.mul;
-        }
-        wg_sync();
+          if (q == 0 && t0 + lane < x.rows) a.out_scale[(int64_t)x.jt * a.M + x.row0 + t0 + lane] = s.scale;
+          const float mul = s.scale == 0.f ? 0.f : s.mul;
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          if (i >= mine) continue;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int token = 16 * i + 8 * j + 2 * (lane & 3);
-            const float m0 = muls[4 * token], m1 = muls[4 * token + 4];
-            unsigned char* at = st + token * 144 + 32 * q + lane / 4;
+          for (int j = 0; j < 4; ++j) {
+            const int token = 8 * j + 2 * (lane & 3);
+            const float m0 = __shfl_sync(0xffffffffu, mul, token), m1 = __shfl_sync(0xffffffffu, mul, token + 1);
+            unsigned char* at = st + token * 32 + lane / 4;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
               float h0, h1;
-              unpack2(acc[i][j][m], h0, h1);
+              unpack2(acc[0][j][m], h0, h1);
               const uint32_t c = e4m3x4(m0 == 0.f ? 0.f : h0 * m0, m1 == 0.f ? 0.f : h1 * m1, 0.f, 0.f);
               at[8 * m] = (unsigned char)c;
-              at[8 * m + 144] = (unsigned char)(c >> 8);
+              at[8 * m + 32] = (unsigned char)(c >> 8);
             }
           }
-        }
-        wg_sync();
-        for (int n = t; n < mine * 16 * 8; n += 128) {
-          const int row = n >> 3, token = row / 16 * 32 + 16 * wg + row % 16;
-          if (token < x.rows)
-            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (int64_t)(x.row0 + token) * a.O + x.jt * 128 +
-                                      (n & 7) * 16) = *reinterpret_cast<const uint4*>(st + row * 144 + (n & 7) * 16);
+          // the warps meet once more, so that none writes the next tile's `top` before all have read this one's
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&wg_bar[wg]);
+          ok = warp_wait(&wg_bar[wg], wg_phase, a.status) && ok;
+          wg_phase ^= 1;
+          if (t0 + lane < x.rows) {
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (int64_t)(x.row0 + t0 + lane) * a.O +
+                                                  x.jt * 128 + 32 * q);
+            const uint4* from = reinterpret_cast<const uint4*>(st + lane * 32);
+            out[0] = from[0];
+            out[1] = from[1];
+          }
         }
       }
       if (!ok) *abort_flag = 1;
