@@ -73,10 +73,10 @@ struct Form {
   }
 };
 
-__host__ __device__ constexpr uint32_t idesc_e4m3(int N, bool a_by_columns) {
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_by_columns, bool b_by_columns) {
   return (1u << 4)                             // D: fp32; A and B E4M3 are 0
-         | ((a_by_columns ? 1u : 0u) << 15)    // A stored by its contracted index
-         | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+         | ((a_by_columns ? 1u : 0u) << 15)    // stored by the contracted index
+         | ((b_by_columns ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 __device__ __forceinline__ void tc_mma_e4m3(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -114,7 +114,7 @@ template <int NMAX>
 __device__ __forceinline__ void make_tables(const MatmulArgs& a, int* start, int* count, int* first) {
   const int E = a.E, lane = threadIdx.x & 31;
   if (a.offsets) {
-    for (int e = threadIdx.x; e <= E; e += kThreads) first[e] = a.offsets[e];
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) first[e] = a.offsets[e];
   } else if (threadIdx.x == 0) {
     first[0] = 0;
     first[1] = a.M;
@@ -157,15 +157,18 @@ __device__ __forceinline__ void make_tables(const MatmulArgs& a, int* start, int
   __syncthreads();
 }
 
-template <int NMAX>
-__device__ __forceinline__ Unit unit_of(const Tables& t, int u, int JT) {
+__device__ __forceinline__ int expert_of(const Tables& t, int u) {
   int lo = 0, hi = t.E;  // the last expert whose first unit is not after u
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (t.first[mid] <= u) lo = mid; else hi = mid;
   }
-  // experts without units share their successor's first unit: u lies with the last of equals
-  const int n = t.count[lo], tiles = (n + NMAX - 1) / NMAX, r = u - t.first[lo];
+  return lo;  // experts without units share their successor's first unit: u lies with the last of equals
+}
+
+template <int NMAX>
+__device__ __forceinline__ Unit unit_of(const Tables& t, int u, int JT) {
+  const int lo = expert_of(t, u), n = t.count[lo], tiles = (n + NMAX - 1) / NMAX, r = u - t.first[lo];
   const int jt = r / tiles, nt = r - jt * tiles;
   const int per = ((n + tiles - 1) / tiles + 15) & ~15;
   Unit x;
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int u = blockIdx.x; ok && u < n_units && !*abort_flag; u += gridDim.x) {
         const Unit x = unit_of<NMAX>(tables, u, a.JT);
-        const uint32_t idesc = idesc_e4m3(x.N, TRANS);
+        const uint32_t idesc = idesc_e4m3(128, x.N, TRANS, false);
         for (int kb = 0; kb < nkb; ++kb, ++k) {
           const int s = k % kStages, b = k % kBufs;
           if ((k >= kBufs && !mbar_wait(&acc_empty[b], (k / kBufs - 1) & 1, a.status)) ||
@@ -570,6 +573,440 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ---------------------------------------------------------------- many tokens
+
+// Tiles of 128 tokens a CTA (the MMA's rows) and 256 weight rows (gate's 128
+// and the matching up's 128 with SwiGLU).  A lane of tensor memory is a token,
+// so a thread's scale of a block is one number for all its columns, and no
+// scales pass through shared memory.
+//
+// CTAS = 2: a pair of CTAs makes one MMA of 256 tokens, each CTA with its own
+// 128 and half of the weight rows, which the tensor cores of both read.  A
+// CTA's shared memory so takes in and gives out 32 KB a block instead of 48
+// for the same products.
+template <int CTAS>
+struct Many {
+  static constexpr int kTokens = 128 * CTAS;
+  static constexpr int kABytes = kTile, kBBytes = 2 * kTile / CTAS;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kBufs = 2, kCols = 256;
+  static constexpr int kTops = 128 * 4 * 4;
+  static constexpr int kStages = CTAS == 2 ? 6 : 4;
+  static constexpr int smem(int E) { return 1024 + kStages * kStageBytes + kTops + 512 + 3 * 4 * (E + 1); }
+  static_assert(1024 + kStages * kStageBytes + kTops + 512 + 3 * 4 * (kMaxBins + 1) <= kSmemMax, "");
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of `p`'s counterpart in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The pair's forms: loads that complete on the first CTA's barrier, MMAs over
+// both CTAs' operands and tensor memories, commits that arrive in both.
+template <int CTAS>
+__device__ __forceinline__ void many_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if (CTAS == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void many_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  if (CTAS == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void many_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  if (CTAS == 1)
+    tc_mma_e4m3(d, adesc, bdesc, idesc, accumulate);
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void many_commit(uint64_t* bar) {
+  if (CTAS == 1)
+    tc_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void many_alloc(uint32_t* dst, uint32_t cols) {
+  if (CTAS == 1) {
+    tmem_alloc(dst, cols);
+    return;
+  }
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void many_dealloc(uint32_t taddr, uint32_t cols) {
+  if (CTAS == 1)
+    tmem_dealloc(taddr, cols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+
+// 32 lanes x 16 columns of tensor memory, a lane's columns in its registers (see tc_ld_16x32 on memory order).
+__device__ __forceinline__ void tc_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// 32 bytes to a 32-byte-aligned address.
+__device__ __forceinline__ void store_32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Columns [c0, c0 + 2 N) of a token's row from N pairs of sums.
+template <int N>
+__device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int c0, const uint64_t (&acc)[N]) {
+  const int64_t at = row * a.O + c0;
+  if (a.dtype != FTMOE_FP32) {
+    uint16_t* out = static_cast<uint16_t*>(a.out) + at;
+    const bool whole = c0 + 2 * N <= a.O;
+    if (whole && a.O % 16 == 0 && ((uintptr_t)out & 31) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; i += 8) {
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = halves(acc[i + j], a.dtype);
+        store_32(out + 2 * i, v);
+      }
+      return;
+    }
+    const bool wide = a.O % 8 == 0;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      uint32_t v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = halves(acc[i + j], a.dtype);
+      if (wide) {
+        if (c0 + 2 * i < a.O) *reinterpret_cast<uint4*>(out + 2 * i) = make_uint4(v[0], v[1], v[2], v[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c0 + 2 * i + j < a.O) out[2 * i + j] = (uint16_t)(v[j / 2] >> (j % 2 * 16));
+      }
+    }
+    return;
+  }
+  float* out = static_cast<float*>(a.out) + at;
+  const bool wide = a.O % 4 == 0;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    float v[4];
+    unpack2(acc[i], v[0], v[1]);
+    unpack2(acc[i + 1], v[2], v[3]);
+    if (wide) {
+      if (c0 + 2 * i < a.O) *reinterpret_cast<float4*>(out + 2 * i) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c0 + 2 * i + j < a.O) out[2 * i + j] = v[j];
+    }
+  }
+}
+
+template <int CTAS, bool SWIGLU, bool TRANS>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_fp8_matmul_many(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_w,
+                      const __grid_constant__ CUtensorMap map_x) {
+  using F = Many<CTAS>;
+  constexpr int kStages = F::kStages, kBufs = F::kBufs;
+  extern __shared__ unsigned char sm_raw[];
+  unsigned char* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
+  uint32_t* tops = reinterpret_cast<uint32_t*>(sm + kStages * F::kStageBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kStages * F::kStageBytes + F::kTops);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;
+  uint64_t* acc_empty = acc_full + kBufs;
+  uint64_t* drain = acc_empty + kBufs;
+  uint64_t* row_bar = drain + 1;  // [4], the warps that hold the same tokens
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(row_bar + 4);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* t_start = reinterpret_cast<int*>(sm + kStages * F::kStageBytes + F::kTops + 512);
+  int *t_count = t_start + a.E, *t_first = t_count + a.E;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nkb = (a.C + 127) / 128;
+  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
+  const int worker = blockIdx.x / CTAS, workers = gridDim.x / CTAS;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < kBufs; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], CTAS * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    for (int w = 0; w < 4; ++w) mbar_init(&row_bar[w], 4);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&map_w);
+    tma_prefetch_desc(&map_x);
+  }
+  if (warp == 1) many_alloc<CTAS>(tmem_slot, kBufs * F::kCols);
+  pdl_wait();
+  make_tables<F::kTokens>(a, t_start, t_count, t_first);
+  tc_fence_before();
+  if (CTAS == 2) cluster_sync(); else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Tables tables{t_start, t_count, t_first, a.E};
+  const int n_units = t_first[a.E];
+  const auto unit = [&](int u) {
+    const int e = expert_of(tables, u), n = t_count[e], tiles = (n + F::kTokens - 1) / F::kTokens, r = u - t_first[e];
+    Unit x;
+    x.e = e;
+    x.jt = r / tiles;
+    const int at = (r - x.jt * tiles) * F::kTokens + (int)rank * 128;  // this CTA's tokens
+    x.row0 = t_start[e] + at;
+    x.rows = min(128, n - at);  // none (or fewer than none) in a pair's second CTA, maybe
+    x.N = 256;
+    return x;
+  };
+
+  if (warp < kEpiWarp0) {
+    regs_down<kLowRegs>();
+    if (warp == 0 && lane == 0) {
+      // ---------------- copies
+      int k = 0;
+      for (int u = worker; u < n_units && !*abort_flag; u += workers) {
+        const Unit x = unit(u);
+        for (int kb = 0; kb < nkb; ++kb, ++k) {
+          const int s = k % kStages;
+          if (k >= kStages && !mbar_wait(&empty[s], (k / kStages - 1) & 1, a.status)) {
+            *abort_flag = 1;
+            break;
+          }
+          unsigned char* sa = sm + s * F::kStageBytes;
+          unsigned char* sb = sa + F::kABytes;
+          const uint32_t bar = CTAS == 2 ? at_rank(&full[s], 0) : smem_u32(&full[s]);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], CTAS * F::kStageBytes);
+          many_load_2d<CTAS>(sa, &map_x, kb * 128, x.row0, bar);
+#pragma unroll
+          for (int h = 0; h < 2 / CTAS; ++h) {
+            const int half = CTAS == 2 ? (int)rank : h;  // of the weight rows
+            const int n0 = SWIGLU ? half * a.O + x.jt * 128 : x.jt * 256 + half * 128;
+            if (TRANS)
+              many_load_3d<CTAS>(sb + h * kTile, &map_w, n0, kb * 128, x.e, bar);
+            else
+              many_load_3d<CTAS>(sb + h * kTile, &map_w, kb * 128, n0, x.e, bar);
+          }
+        }
+      }
+      // nothing this warp issued may still be landing when the CTA exits (the pair's second CTA waits for the first)
+      if (rank == 0)
+        for (int q = k > kStages ? k - kStages : 0; q < k; ++q) mbar_wait(&full[q % kStages], (q / kStages) & 1, a.status);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ---------------- products
+      constexpr uint32_t idesc = idesc_e4m3(F::kTokens, TRANS && CTAS == 1 ? 128 : 256, false, TRANS);
+      int k = 0;
+      bool ok = true;
+      for (int u = worker; ok && u < n_units && !*abort_flag; u += workers) {
+        for (int kb = 0; kb < nkb; ++kb, ++k) {
+          const int s = k % kStages, b = k % kBufs;
+          if ((k >= kBufs && !mbar_wait(&acc_empty[b], (k / kBufs - 1) & 1, a.status)) ||
+              !mbar_wait(&full[s], (k / kStages) & 1, a.status)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(sm + s * F::kStageBytes);
+          const uint64_t adesc = sdesc_k_sw128(sa), bdesc = sdesc_k_sw128(sa + F::kABytes);
+          const int steps = (min(128, a.C - kb * 128) + 31) / 32;
+          const uint32_t d = tmem + b * F::kCols;
+          for (int i = 0; i < steps; ++i) {
+            // 32 contracted values: 32 bytes on within the swizzled rows, or 32 rows on
+            const uint64_t on = TRANS ? i * (32 * 128 >> 4) : i * (32 >> 4);
+            many_mma<CTAS>(d, adesc + i * (32 >> 4), bdesc + on, idesc, i != 0);
+            if (TRANS && CTAS == 1) many_mma<CTAS>(d + 128, adesc + i * (32 >> 4), bdesc + on + (kTile >> 4), idesc, i != 0);
+          }
+          many_commit<CTAS>(&empty[s]);
+          many_commit<CTAS>(&acc_full[b]);
+        }
+      }
+      if (CTAS == 1)
+        tc_commit(drain);
+      else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
+                     : "memory");
+      mbar_wait(drain, 0, a.status);
+    }
+  } else {
+    regs_up<kEpiRegs>();
+    // ---------------- sums: warp (wg, q) has tokens 32q.. and the columns [64 wg, 64 wg + 64), with SwiGLU
+    // [32 wg, 32 wg + 32) of gate and up
+    const int q = warp & 3, wg = (warp - kEpiWarp0) >> 2;
+    const uint32_t from = tmem + ((uint32_t)(32 * q) << 16);
+    const int col[2] = {SWIGLU ? 32 * wg : 64 * wg, SWIGLU ? 128 + 32 * wg : 64 * wg + 32};
+    int k = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = worker; ok && u < n_units && !*abort_flag; u += workers) {
+      const Unit x = unit(u);
+      const int token = 32 * q + lane;
+      const bool on = token < x.rows;
+      const float* sx = a.a_scale + x.row0 + token;
+      // weights' scales: [e][block of rows][block of columns]; TRANS contracts the rows
+      const int nb = SWIGLU ? x.jt : 2 * x.jt + wg / 2;
+      const bool there = nb * 128 < a.O;  // a last tile may have only its first half
+      const float* sw = a.w_scale + ((int64_t)x.e * a.NB + (TRANS ? 0 : nb)) * a.KB + (TRANS ? nb : 0);
+      const int64_t sw_step = TRANS ? a.KB : 1, up = (int64_t)(a.O / 128) * a.KB;
+      uint64_t acc[2][16];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) acc[i / 16][i % 16] = 0ull;
+      float v = on ? *sx : 0.f, w0 = there ? *sw : 0.f, w1 = SWIGLU ? sw[up] : 0.f;
+      for (int kb = 0; kb < nkb; ++kb, ++k) {
+        const int b = k % kBufs;
+        const float s0 = v * w0, s1 = SWIGLU ? v * w1 : s0;
+        if (kb + 1 < nkb) {
+          sx += a.M;
+          sw += sw_step;
+          v = on ? *sx : 0.f;
+          w0 = there ? *sw : 0.f;
+          if (SWIGLU) w1 = sw[up];
+        }
+        if (!warp_wait(&acc_full[b], (k / kBufs) & 1, a.status)) {
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t r[16];
+          tc_ld_32x16(from + b * F::kCols + col[h / 2] + 16 * (h % 2), r);
+          if (h == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (CTAS == 2) mbar_arrive_at(at_rank(&acc_empty[b], 0)); else mbar_arrive(&acc_empty[b]);
+            }
+          }
+          const uint64_t s2 = h < 2 ? pack2(s0, s0) : pack2(s1, s1);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint64_t& sum = acc[h / 2][8 * (h % 2) + i];
+            sum = fma2(pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), s2, sum);
+          }
+        }
+      }
+      if (!ok) break;
+      if constexpr (!SWIGLU) {
+        if (on) {
+          const int c0 = x.jt * 256 + 64 * wg;
+          if (c0 < a.O) store_row<16>(a, x.row0 + token, c0, acc[0]);
+          if (c0 + 32 < a.O) store_row<16>(a, x.row0 + token, c0 + 32, acc[1]);
+        }
+      } else {
+        // a token's 128 values of h lie in the four warps of its rows
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float g0, g1, u0, u1;
+          unpack2(acc[0][i], g0, g1);
+          unpack2(acc[1][i], u0, u1);
+          g0 = g0 * sigmoid(g0) * u0;
+          g1 = g1 * sigmoid(g1) * u1;
+          best = max(best, max(magnitude(g0), magnitude(g1)));
+          acc[0][i] = pack2(g0, g1);
+        }
+        tops[token * 4 + wg] = best;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&row_bar[q]);
+        ok = warp_wait(&row_bar[q], phase, a.status);
+        phase ^= 1;
+        const uint4 t = reinterpret_cast<const uint4*>(tops)[token];
+        const BlockScale s = block_scale(max(max(t.x, t.y), max(t.z, t.w)));
+        // met once more, so that none writes the next tile's `tops` before all have read this one's
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&row_bar[q]);
+        ok = warp_wait(&row_bar[q], phase, a.status) && ok;
+        phase ^= 1;
+        if (on) {
+          uint32_t c[8];
+          const float mul = s.mul;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float h0, h1, h2, h3;
+            unpack2(acc[0][2 * i], h0, h1);
+            unpack2(acc[0][2 * i + 1], h2, h3);
+            c[i] = s.scale == 0.f ? 0u : e4m3x4(h0 * mul, h1 * mul, h2 * mul, h3 * mul);
+          }
+          uint8_t* out = static_cast<uint8_t*>(a.out) + (int64_t)(x.row0 + token) * a.O + x.jt * 128 + 32 * wg;
+          if (((uintptr_t)out & 31) == 0) {
+            store_32(out, c);
+          } else {
+            reinterpret_cast<uint4*>(out)[0] = make_uint4(c[0], c[1], c[2], c[3]);
+            reinterpret_cast<uint4*>(out)[1] = make_uint4(c[4], c[5], c[6], c[7]);
+          }
+          if (wg == 0) a.out_scale[(int64_t)x.jt * a.M + x.row0 + token] = s.scale;
+        }
+      }
+      if (!ok) *abort_flag = 1;
+    }
+  }
+  tc_fence_before();
+  // the pair leaves together: neither may signal into a CTA that is gone
+  __syncthreads();
+  if (CTAS == 2) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    many_dealloc<CTAS>(tmem, kBufs * F::kCols);
+  }
+}
+
 // ---------------------------------------------------------------- host
 
 cudaError_t encode_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
@@ -596,23 +1033,59 @@ cudaError_t encode_map(CUtensorMap* m, const void* base, int rank, const uint64_
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int NMAX, bool SWIGLU, bool TRANS>
-cudaError_t launch_form(const TrainDevice& d, const ftmoe_fp8_matmul_args& m, const MatmulArgs& a, cudaStream_t s) {
-  using F = Form<NMAX, SWIGLU>;
-  CUtensorMap map_w, map_x;
+// Tensor maps of the weights (boxes of 128 x 128 bytes) and of the rows (`box` of them).
+cudaError_t make_maps(const ftmoe_fp8_matmul_args& m, int C, int box, CUtensorMap* map_w, CUtensorMap* map_x) {
   const uint64_t wd[3] = {(uint64_t)m.K, (uint64_t)m.N, (uint64_t)m.E}, ws[2] = {(uint64_t)m.K, (uint64_t)m.N * m.K};
   const uint32_t wb[3] = {128, 128, 1};
-  cudaError_t e = encode_map(&map_w, m.w, 3, wd, ws, wb);
+  const cudaError_t e = encode_map(map_w, m.w, 3, wd, ws, wb);
   if (e != cudaSuccess) return e;
-  const uint64_t xd[2] = {(uint64_t)a.C, (uint64_t)m.M}, xs[1] = {(uint64_t)a.C};
-  const uint32_t xb[2] = {128, F::kBox};
-  if ((e = encode_map(&map_x, m.a, 2, xd, xs, xb)) != cudaSuccess) return e;
-  auto* k = k_fp8_matmul<NMAX, SWIGLU, TRANS>;
-  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem(kMaxBins))) != cudaSuccess)
-    return e;
-  const int64_t most = (m.M / NMAX + (m.M < m.E ? m.M : m.E)) * a.JT;  // units; held to int by the caller
-  return launch_after_smem(k, (unsigned)(most < d.num_sms ? most : d.num_sms), kThreads, F::smem(m.E), s, a, map_w,
-                           map_x);
+  const uint64_t xd[2] = {(uint64_t)C, (uint64_t)m.M}, xs[1] = {(uint64_t)C};
+  const uint32_t xb[2] = {128, (uint32_t)box};
+  return encode_map(map_x, m.a, 2, xd, xs, xb);
+}
+
+// `most`: units there may be; a cluster of `ctas` works on one at a time.
+template <typename K>
+cudaError_t launch_units(K* k, const TrainDevice& d, int64_t most, int ctas, int smem, int smem_max, const MatmulArgs& a,
+                         const CUtensorMap& map_w, const CUtensorMap& map_x, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max);
+  if (e != cudaSuccess) return e;
+  const int64_t workers = d.num_sms / ctas;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)((most < workers ? most : workers) * ctas));
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim = {(unsigned)ctas, 1, 1};
+  c.attrs = at;
+  c.numAttrs = 2;
+  return cudaLaunchKernelEx(&c, k, a, map_w, map_x);
+}
+
+template <int NMAX, bool SWIGLU, bool TRANS>
+cudaError_t launch_few(const TrainDevice& d, const ftmoe_fp8_matmul_args& m, MatmulArgs a, cudaStream_t s) {
+  using F = Form<NMAX, SWIGLU>;
+  CUtensorMap map_w, map_x;
+  const cudaError_t e = make_maps(m, a.C, F::kBox, &map_w, &map_x);
+  if (e != cudaSuccess) return e;
+  a.JT = fp8_blocks(a.O);
+  return launch_units(k_fp8_matmul<NMAX, SWIGLU, TRANS>, d, (m.M / NMAX + (m.M < m.E ? m.M : m.E)) * a.JT, 1,
+                      F::smem(m.E), F::smem(kMaxBins), a, map_w, map_x, s);
+}
+
+template <int CTAS, bool SWIGLU, bool TRANS>
+cudaError_t launch_many(const TrainDevice& d, const ftmoe_fp8_matmul_args& m, MatmulArgs a, cudaStream_t s) {
+  using F = Many<CTAS>;
+  CUtensorMap map_w, map_x;
+  const cudaError_t e = make_maps(m, a.C, 128, &map_w, &map_x);
+  if (e != cudaSuccess) return e;
+  a.JT = SWIGLU ? a.O / 128 : (a.O + 255) / 256;
+  return launch_units(k_fp8_matmul_many<CTAS, SWIGLU, TRANS>, d, (m.M / F::kTokens + (m.M < m.E ? m.M : m.E)) * a.JT,
+                      CTAS, F::smem(m.E), F::smem(kMaxBins), a, map_w, map_x, s);
 }
 
 }  // namespace
@@ -628,16 +1101,18 @@ cudaError_t launch_fp8_matmul(const TrainDevice& d, const ftmoe_fp8_matmul_args&
   a.O = m.transpose ? m.K : m.swiglu ? m.N / 2 : m.N;
   a.NB = fp8_blocks(m.N);
   a.KB = fp8_blocks(m.K);
-  a.JT = fp8_blocks(a.O);
   a.dtype = m.out_dtype;
   a.out = m.out;
   a.out_scale = m.out_scale;
   a.status = d.status;
   // up to 32 tokens an expert in the mean: narrow tiles, whose stages are nearly all weights
-  const bool few = m.M <= (int64_t)32 * m.E;
-  if (m.swiglu) return few ? launch_form<32, true, false>(d, m, a, s) : launch_form<128, true, false>(d, m, a, s);
-  if (m.transpose) return few ? launch_form<32, false, true>(d, m, a, s) : launch_form<256, false, true>(d, m, a, s);
-  return few ? launch_form<32, false, false>(d, m, a, s) : launch_form<256, false, false>(d, m, a, s);
+  if (m.M <= (int64_t)32 * m.E) {
+    if (m.swiglu) return launch_few<32, true, false>(d, m, a, s);
+    return m.transpose ? launch_few<32, false, true>(d, m, a, s) : launch_few<32, false, false>(d, m, a, s);
+  }
+  constexpr int kCtas = 1;
+  if (m.swiglu) return launch_many<kCtas, true, false>(d, m, a, s);
+  return m.transpose ? launch_many<kCtas, false, true>(d, m, a, s) : launch_many<kCtas, false, false>(d, m, a, s);
 }
 
 }  // namespace ftmoe
