@@ -26,11 +26,13 @@ namespace ftmoe {
 
 namespace {
 
-constexpr int kThreads = 640;
-constexpr int kEpiWarp0 = 4;
-constexpr int kEpiWarps = 16;     // four warpgroups: an FMA pipe fed by two warps stays at three quarters of its rate
-constexpr int kLaunchRegs = 96, kLowRegs = 64, kEpiRegs = 104;
-static_assert(5 * kLaunchRegs == kLowRegs + 4 * kEpiRegs, "the warpgroups' shares add up to the launch's registers");
+constexpr int kFewThreads = 256;
+constexpr int kManyThreads = 384;
+constexpr int kEpiWarp0 = 4;       // the first of the warps that sum
+constexpr int kFewWarps = 4, kManyWarps = 8;
+// Registers a thread: at launch, of warps 0-3, of the others.
+constexpr int kLaunchRegs = 168, kLowRegs = 72, kEpiRegs = 216;
+static_assert(3 * kLaunchRegs == kLowRegs + 2 * kEpiRegs, "the warpgroups' shares add up to the launch's registers");
 constexpr int kTile = 128 * 128;  // bytes of a weight tile
 constexpr int kSmemMax = 227 * 1024;
 
@@ -57,12 +59,11 @@ struct Form {
   static constexpr int kCols = kParts * NMAX;  // of an accumulator buffer
   static constexpr int kBufs = 512 / kCols < 4 ? 512 / kCols : 4;
   static constexpr int kTmemCols = kBufs * kCols;
-  // Chunks of 32 tokens, of each part, that an epilogue warpgroup sums.
-  static constexpr int kChunks = (NMAX + 127) / 128;
+  static constexpr int kChunks = NMAX / 32;  // of 32 tokens
   // Staging of a warp's 32 outputs: 16 tokens' in 16 bits, 8 tokens' in fp32 (rows of 36, which keeps the stores'
   // banks apart), or 32 tokens' codes.
   static constexpr int kWarpOut = SWIGLU ? 1024 : 1152;
-  static constexpr int kOut = kEpiWarps * kWarpOut;
+  static constexpr int kOut = kFewWarps * kWarpOut;
   static constexpr int kTops = SWIGLU ? NMAX * 4 * 4 : 0;  // a token's largest magnitude in each warp
   static constexpr int kScales = kBufs * kCols * 4;
   static constexpr int kFixed = 1024 + kOut + kTops + kScales + 512 + 3 * 4 * (kMaxBins + 1);
@@ -180,8 +181,19 @@ __device__ __forceinline__ Unit unit_of(const Tables& t, int u, int JT) {
   return x;
 }
 
+// mbar_wait for waits that are mostly over when they begin.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
+    if ((i & 255) == 0 && globaltimer() - t0 > kWaitLimitNs) {
+      set_status(status, kStatusTimeout);
+      return false;
+    }
+  return true;
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+  return __all_sync(0xffffffffu, wait(bar, parity, status));
 }
 
 // 16 lanes x 32 columns of tensor memory: lane l of the warp gets, of each 8
@@ -214,9 +226,13 @@ __device__ __forceinline__ void st_matrix_t(void* p, uint32_t r0, uint32_t r1, u
                : "memory");
 }
 
+__device__ __forceinline__ uint32_t halves(float lo, float hi, int dtype);
 __device__ __forceinline__ uint32_t halves(uint64_t v, int dtype) {
   float lo, hi;
   unpack2(v, lo, hi);
+  return halves(lo, hi, dtype);
+}
+__device__ __forceinline__ uint32_t halves(float lo, float hi, int dtype) {
   if (dtype == FTMOE_FP16) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -226,8 +242,8 @@ __device__ __forceinline__ uint32_t halves(uint64_t v, int dtype) {
 }
 
 template <int NMAX, bool SWIGLU, bool TRANS>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_fp8_matmul(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_w,
+__global__ void __launch_bounds__(kFewThreads, 1)
+    k_fp8_matmul_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_w,
                  const __grid_constant__ CUtensorMap map_x) {
   using F = Form<NMAX, SWIGLU>;
   constexpr int kStages = F::kStages, kBufs = F::kBufs;
@@ -242,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acc_full = empty + kStages;   // the MMA's commit and the scale warp
   uint64_t* acc_empty = acc_full + kBufs;
   uint64_t* drain = acc_empty + kBufs;
-  uint64_t* wg_bar = drain + 1;           // [4], the warps of an epilogue warpgroup
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wg_bar + kEpiWarps / 4);
+  uint64_t* wg_bar = drain + 1;           // the warps that sum
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wg_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* t_start = reinterpret_cast<int*>(staged + F::kOut + F::kTops + F::kScales + 512);
   int *t_count = t_start + a.E, *t_first = t_count + a.E;
@@ -257,10 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < kBufs; ++b) {
       mbar_init(&acc_full[b], 2);
-      mbar_init(&acc_empty[b], kEpiWarps);
+      mbar_init(&acc_empty[b], kFewWarps);
     }
     mbar_init(drain, 1);
-    for (int w = 0; w < kEpiWarps / 4; ++w) mbar_init(&wg_bar[w], 4);
+    mbar_init(wg_bar, kFewWarps);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&map_w);
@@ -277,7 +293,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_units = t_first[a.E];
 
   if (warp < kEpiWarp0) {
-    regs_down<kLowRegs>();
     if (warp == 0 && lane == 0) {
       // ---------------- copies
       int k = 0;
@@ -286,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int boxes = (x.N + F::kBox - 1) / F::kBox;
         for (int kb = 0; kb < nkb; ++kb, ++k) {
           const int s = k % kStages;
-          if (k >= kStages && !mbar_wait(&empty[s], (k / kStages - 1) & 1, a.status)) {
+          if (k >= kStages && !wait(&empty[s], (k / kStages - 1) & 1, a.status)) {
             *abort_flag = 1;
             break;
           }
@@ -314,8 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idesc = idesc_e4m3(128, x.N, TRANS, false);
         for (int kb = 0; kb < nkb; ++kb, ++k) {
           const int s = k % kStages, b = k % kBufs;
-          if ((k >= kBufs && !mbar_wait(&acc_empty[b], (k / kBufs - 1) & 1, a.status)) ||
-              !mbar_wait(&full[s], (k / kStages) & 1, a.status)) {
+          if ((k >= kBufs && !wait(&acc_empty[b], (k / kBufs - 1) & 1, a.status)) ||
+              !wait(&full[s], (k / kStages) & 1, a.status)) {
             *abort_flag = 1;
             ok = false;
             break;
@@ -378,20 +393,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    regs_up<kEpiRegs>();
-    // ---------------- sums: warp (wg, q) has TMEM lanes 32q.. and the chunks wg, wg + 4, ... of 32 tokens.
+    // ---------------- sums: warp q has TMEM lanes 32q..
     // acc[i][j][m]: chunk i's tokens 8j + 2 (lane % 4) and one more, output 32q + 8m + lane / 4.  A lane so needs
     // the scales of a quarter of the tokens.
-    const int q = warp & 3, wg = (warp - kEpiWarp0) >> 2;
+    const int q = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     constexpr int kAll = F::kParts * kChunks;
-    unsigned char* st = staged + (warp - kEpiWarp0) * F::kWarpOut;
+    unsigned char* st = staged + q * F::kWarpOut;
     int k = 0;
     uint32_t wg_phase = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < n_units && !*abort_flag; u += gridDim.x) {
       const Unit x = unit_of<NMAX>(tables, u, a.JT);
-      const int mine = ((x.N + 31) / 32 - wg + 3) >> 2;  // chunks of this warpgroup; the last may be half a one
+      const int mine = (x.N + 31) / 32;  // chunks there are; the last may be half a one
       uint64_t acc[kAll][4][4];
 #pragma unroll
       for (int i = 0; i < kAll; ++i)
@@ -405,13 +419,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + lanes + b * F::kCols + 32 * wg;
-        const float* sc = s_scale + b * F::kCols + 32 * wg + 2 * (lane & 3);
+        const uint32_t d = tmem + lanes + b * F::kCols;
+        const float* sc = s_scale + b * F::kCols + 2 * (lane & 3);
 #pragma unroll
         for (int i = 0; i < kAll; ++i) {
           if (i % kChunks >= mine) continue;
-          // chunk i: part i / kChunks, tokens 128 (i % kChunks) + 32 wg
-          const int col = i / kChunks * NMAX + i % kChunks * 128;
+          // chunk i: part i / kChunks, tokens 32 (i % kChunks)
+          const int col = i / kChunks * NMAX + i % kChunks * 32;
           uint32_t r[32];
           tc_ld_16x32(d + col, r);
           tc_ld_16x32(d + col + (16u << 16), r + 16);
@@ -437,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool wide = a.O % 8 == 0;
 #pragma unroll
           for (int h = 0; h < 2 * kChunks; ++h) {  // by 16 tokens
-            const int i = h / 2, j0 = h % 2 * 2, t0 = 128 * i + 32 * wg + 16 * (h % 2), rows = min(16, x.rows - t0);
+            const int i = h / 2, j0 = h % 2 * 2, t0 = 32 * i + 16 * (h % 2), rows = min(16, x.rows - t0);
             if (rows <= 0 || width <= 0) continue;
             // [token][32] with the 16-byte pieces of a row turned by the token
             __syncwarp();
@@ -469,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float* to = reinterpret_cast<float*>(st);
 #pragma unroll
           for (int h = 0; h < 4 * kChunks; ++h) {  // by 8 tokens
-            const int i = h / 4, t0 = 128 * i + 32 * wg + 8 * (h % 4), rows = min(8, x.rows - t0);
+            const int i = h / 4, t0 = 32 * i + 8 * (h % 4), rows = min(8, x.rows - t0);
             if (rows <= 0 || width <= 0) continue;
             __syncwarp();
 #pragma unroll
@@ -496,11 +510,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        static_assert(!SWIGLU || kChunks == 1, "a warpgroup has one chunk of tokens");
-        const int t0 = 32 * wg;
-        if (mine > 0) {
+        static_assert(!SWIGLU || kChunks == 1, "one chunk of tokens");
+        {
           // h in the gate's registers; a token's largest magnitude over the 128 columns from the four warps
-          uint32_t* top = tops + t0 * 4;
+          uint32_t* top = tops;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t best0 = 0, best1 = 0;
@@ -526,13 +539,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&wg_bar[wg]);
-          ok = warp_wait(&wg_bar[wg], wg_phase, a.status);
+          if (lane == 0) mbar_arrive(wg_bar);
+          ok = warp_wait(wg_bar, wg_phase, a.status);
           wg_phase ^= 1;
           // lane t works token t's scale out, in each of the four warps
           const uint4 v = reinterpret_cast<const uint4*>(top)[lane];
           const BlockScale s = block_scale(max(max(v.x, v.y), max(v.z, v.w)));
-          if (q == 0 && t0 + lane < x.rows) a.out_scale[(int64_t)x.jt * a.M + x.row0 + t0 + lane] = s.scale;
+          if (q == 0 && lane < x.rows) a.out_scale[(int64_t)x.jt * a.M + x.row0 + lane] = s.scale;
           const float mul = s.scale == 0.f ? 0.f : s.mul;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -550,11 +563,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // the warps meet once more, so that none writes the next tile's `top` before all have read this one's
           __syncwarp();
-          if (lane == 0) mbar_arrive(&wg_bar[wg]);
-          ok = warp_wait(&wg_bar[wg], wg_phase, a.status) && ok;
+          if (lane == 0) mbar_arrive(wg_bar);
+          ok = warp_wait(wg_bar, wg_phase, a.status) && ok;
           wg_phase ^= 1;
-          if (t0 + lane < x.rows) {
-            uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (int64_t)(x.row0 + t0 + lane) * a.O +
+          if (lane < x.rows) {
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (int64_t)(x.row0 + lane) * a.O +
                                                   x.jt * 128 + 32 * q);
             const uint4* from = reinterpret_cast<const uint4*>(st + lane * 32);
             out[0] = from[0];
@@ -590,7 +603,7 @@ struct Many {
   static constexpr int kABytes = kTile, kBBytes = 2 * kTile / CTAS;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kBufs = 2, kCols = 256;
-  static constexpr int kTops = 128 * 4 * 4;
+  static constexpr int kTops = 128 * 2 * 4;  // a token's largest magnitude in each warpgroup
   static constexpr int kStages = CTAS == 2 ? 6 : 4;
   static constexpr int smem(int E) { return 1024 + kStages * kStageBytes + kTops + 512 + 3 * 4 * (E + 1); }
   static_assert(1024 + kStages * kStageBytes + kTops + 512 + 3 * 4 * (kMaxBins + 1) <= kSmemMax, "");
@@ -704,35 +717,34 @@ __device__ __forceinline__ void store_32(void* p, const uint32_t (&v)[8]) {
                : "memory");
 }
 
-// Columns [c0, c0 + 2 N) of a token's row from N pairs of sums.
+// Columns [c0, c0 + N) of a token's row.
 template <int N>
-__device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int c0, const uint64_t (&acc)[N]) {
+__device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int c0, const float* v) {
   const int64_t at = row * a.O + c0;
   if (a.dtype != FTMOE_FP32) {
     uint16_t* out = static_cast<uint16_t*>(a.out) + at;
-    const bool whole = c0 + 2 * N <= a.O;
-    if (whole && a.O % 16 == 0 && ((uintptr_t)out & 31) == 0) {
+    if (c0 + N <= a.O && a.O % 16 == 0 && ((uintptr_t)out & 31) == 0) {
 #pragma unroll
-      for (int i = 0; i < N; i += 8) {
-        uint32_t v[8];
+      for (int i = 0; i < N; i += 16) {
+        uint32_t p[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = halves(acc[i + j], a.dtype);
-        store_32(out + 2 * i, v);
+        for (int j = 0; j < 8; ++j) p[j] = halves(v[i + 2 * j], v[i + 2 * j + 1], a.dtype);
+        store_32(out + i, p);
       }
       return;
     }
     const bool wide = a.O % 8 == 0;
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      uint32_t v[4];
+    for (int i = 0; i < N; i += 8) {
+      uint32_t p[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = halves(acc[i + j], a.dtype);
+      for (int j = 0; j < 4; ++j) p[j] = halves(v[i + 2 * j], v[i + 2 * j + 1], a.dtype);
       if (wide) {
-        if (c0 + 2 * i < a.O) *reinterpret_cast<uint4*>(out + 2 * i) = make_uint4(v[0], v[1], v[2], v[3]);
+        if (c0 + i < a.O) *reinterpret_cast<uint4*>(out + i) = make_uint4(p[0], p[1], p[2], p[3]);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (c0 + 2 * i + j < a.O) out[2 * i + j] = (uint16_t)(v[j / 2] >> (j % 2 * 16));
+          if (c0 + i + j < a.O) out[i + j] = (uint16_t)(p[j / 2] >> (j % 2 * 16));
       }
     }
     return;
@@ -740,22 +752,19 @@ __device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int 
   float* out = static_cast<float*>(a.out) + at;
   const bool wide = a.O % 4 == 0;
 #pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    float v[4];
-    unpack2(acc[i], v[0], v[1]);
-    unpack2(acc[i + 1], v[2], v[3]);
+  for (int i = 0; i < N; i += 4) {
     if (wide) {
-      if (c0 + 2 * i < a.O) *reinterpret_cast<float4*>(out + 2 * i) = make_float4(v[0], v[1], v[2], v[3]);
+      if (c0 + i < a.O) *reinterpret_cast<float4*>(out + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (c0 + 2 * i + j < a.O) out[2 * i + j] = v[j];
+        if (c0 + i + j < a.O) out[i + j] = v[i + j];
     }
   }
 }
 
 template <int CTAS, bool SWIGLU, bool TRANS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kManyThreads, 1)
     k_fp8_matmul_many(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_w,
                       const __grid_constant__ CUtensorMap map_x) {
   using F = Many<CTAS>;
@@ -785,10 +794,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < kBufs; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], CTAS * kEpiWarps);
+      mbar_init(&acc_empty[b], CTAS * kManyWarps);
     }
     mbar_init(drain, 1);
-    for (int w = 0; w < 4; ++w) mbar_init(&row_bar[w], 4);
+    for (int w = 0; w < 4; ++w) mbar_init(&row_bar[w], kManyWarps / 4);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&map_w);
@@ -824,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Unit x = unit(u);
         for (int kb = 0; kb < nkb; ++kb, ++k) {
           const int s = k % kStages;
-          if (k >= kStages && !mbar_wait(&empty[s], (k / kStages - 1) & 1, a.status)) {
+          if (k >= kStages && !wait(&empty[s], (k / kStages - 1) & 1, a.status)) {
             *abort_flag = 1;
             break;
           }
@@ -855,8 +864,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = worker; ok && u < n_units && !*abort_flag; u += workers) {
         for (int kb = 0; kb < nkb; ++kb, ++k) {
           const int s = k % kStages, b = k % kBufs;
-          if ((k >= kBufs && !mbar_wait(&acc_empty[b], (k / kBufs - 1) & 1, a.status)) ||
-              !mbar_wait(&full[s], (k / kStages) & 1, a.status)) {
+          if ((k >= kBufs && !wait(&acc_empty[b], (k / kBufs - 1) & 1, a.status)) ||
+              !wait(&full[s], (k / kStages) & 1, a.status)) {
             *abort_flag = 1;
             ok = false;
             break;
@@ -885,11 +894,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     regs_up<kEpiRegs>();
-    // ---------------- sums: warp (wg, q) has tokens 32q.. and the columns [64 wg, 64 wg + 64), with SwiGLU
-    // [32 wg, 32 wg + 32) of gate and up
+    // ---------------- sums: warp (wg, q) has tokens 32q.. and the columns [128 wg, 128 wg + 128), with SwiGLU
+    // [64 wg, 64 wg + 64) of gate and up.  Plain FMAs: packed ones are no faster here, and the pairs' alignment
+    // costs registers.
     const int q = warp & 3, wg = (warp - kEpiWarp0) >> 2;
-    const uint32_t from = tmem + ((uint32_t)(32 * q) << 16);
-    const int col[2] = {SWIGLU ? 32 * wg : 64 * wg, SWIGLU ? 128 + 32 * wg : 64 * wg + 32};
+    const uint32_t from = tmem + ((uint32_t)(32 * q) << 16) + (SWIGLU ? 64 : 128) * wg;
     int k = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -899,13 +908,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool on = token < x.rows;
       const float* sx = a.a_scale + x.row0 + token;
       // weights' scales: [e][block of rows][block of columns]; TRANS contracts the rows
-      const int nb = SWIGLU ? x.jt : 2 * x.jt + wg / 2;
+      const int nb = SWIGLU ? x.jt : 2 * x.jt + wg;
       const bool there = nb * 128 < a.O;  // a last tile may have only its first half
       const float* sw = a.w_scale + ((int64_t)x.e * a.NB + (TRANS ? 0 : nb)) * a.KB + (TRANS ? nb : 0);
       const int64_t sw_step = TRANS ? a.KB : 1, up = (int64_t)(a.O / 128) * a.KB;
-      uint64_t acc[2][16];
+      float acc[128];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) acc[i / 16][i % 16] = 0ull;
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
       float v = on ? *sx : 0.f, w0 = there ? *sw : 0.f, w1 = SWIGLU ? sw[up] : 0.f;
       for (int kb = 0; kb < nkb; ++kb, ++k) {
         const int b = k % kBufs;
@@ -924,72 +933,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int h = 0; h < 8; ++h) {
           uint32_t r[16];
-          tc_ld_32x16(from + b * F::kCols + col[h / 2] + 16 * (h % 2), r);
-          if (h == 3) {
+          tc_ld_32x16(from + b * F::kCols + (SWIGLU && h >= 4 ? 128 - 64 : 0) + 16 * h, r);
+          if (h == 7) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
               if (CTAS == 2) mbar_arrive_at(at_rank(&acc_empty[b], 0)); else mbar_arrive(&acc_empty[b]);
             }
           }
-          const uint64_t s2 = h < 2 ? pack2(s0, s0) : pack2(s1, s1);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint64_t& sum = acc[h / 2][8 * (h % 2) + i];
-            sum = fma2(pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), s2, sum);
-          }
+          for (int i = 0; i < 16; ++i) acc[16 * h + i] = fmaf(__uint_as_float(r[i]), h < 4 ? s0 : s1, acc[16 * h + i]);
         }
       }
       if (!ok) break;
       if constexpr (!SWIGLU) {
-        if (on) {
-          const int c0 = x.jt * 256 + 64 * wg;
-          if (c0 < a.O) store_row<16>(a, x.row0 + token, c0, acc[0]);
-          if (c0 + 32 < a.O) store_row<16>(a, x.row0 + token, c0 + 32, acc[1]);
-        }
+        const int c0 = x.jt * 256 + 128 * wg;
+        if (on && c0 < a.O) store_row<128>(a, x.row0 + token, c0, acc);
       } else {
-        // a token's 128 values of h lie in the four warps of its rows
+        // a token's 128 values of h lie in the two warps of its rows
         uint32_t best = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float g0, g1, u0, u1;
-          unpack2(acc[0][i], g0, g1);
-          unpack2(acc[1][i], u0, u1);
-          g0 = g0 * sigmoid(g0) * u0;
-          g1 = g1 * sigmoid(g1) * u1;
-          best = max(best, max(magnitude(g0), magnitude(g1)));
-          acc[0][i] = pack2(g0, g1);
+        for (int i = 0; i < 64; ++i) {
+          acc[i] = acc[i] * sigmoid(acc[i]) * acc[64 + i];
+          best = max(best, magnitude(acc[i]));
         }
-        tops[token * 4 + wg] = best;
+        tops[token * 2 + wg] = best;
         __syncwarp();
         if (lane == 0) mbar_arrive(&row_bar[q]);
         ok = warp_wait(&row_bar[q], phase, a.status);
         phase ^= 1;
-        const uint4 t = reinterpret_cast<const uint4*>(tops)[token];
-        const BlockScale s = block_scale(max(max(t.x, t.y), max(t.z, t.w)));
+        const BlockScale s = block_scale(max(best, tops[token * 2 + (wg ^ 1)]));
         // met once more, so that none writes the next tile's `tops` before all have read this one's
         __syncwarp();
         if (lane == 0) mbar_arrive(&row_bar[q]);
         ok = warp_wait(&row_bar[q], phase, a.status) && ok;
         phase ^= 1;
         if (on) {
-          uint32_t c[8];
           const float mul = s.mul;
+          uint8_t* out = static_cast<uint8_t*>(a.out) + (int64_t)(x.row0 + token) * a.O + x.jt * 128 + 64 * wg;
+          const bool wide = ((uintptr_t)out & 31) == 0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float h0, h1, h2, h3;
-            unpack2(acc[0][2 * i], h0, h1);
-            unpack2(acc[0][2 * i + 1], h2, h3);
-            c[i] = s.scale == 0.f ? 0u : e4m3x4(h0 * mul, h1 * mul, h2 * mul, h3 * mul);
-          }
-          uint8_t* out = static_cast<uint8_t*>(a.out) + (int64_t)(x.row0 + token) * a.O + x.jt * 128 + 32 * wg;
-          if (((uintptr_t)out & 31) == 0) {
-            store_32(out, c);
-          } else {
-            reinterpret_cast<uint4*>(out)[0] = make_uint4(c[0], c[1], c[2], c[3]);
-            reinterpret_cast<uint4*>(out)[1] = make_uint4(c[4], c[5], c[6], c[7]);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float* f = acc + 32 * h + 4 * i;
+              c[i] = s.scale == 0.f ? 0u : e4m3x4(f[0] * mul, f[1] * mul, f[2] * mul, f[3] * mul);
+            }
+            if (wide) {
+              store_32(out + 32 * h, c);
+            } else {
+              reinterpret_cast<uint4*>(out + 32 * h)[0] = make_uint4(c[0], c[1], c[2], c[3]);
+              reinterpret_cast<uint4*>(out + 32 * h)[1] = make_uint4(c[4], c[5], c[6], c[7]);
+            }
           }
           if (wg == 0) a.out_scale[(int64_t)x.jt * a.M + x.row0 + token] = s.scale;
         }
@@ -1046,14 +1044,14 @@ cudaError_t make_maps(const ftmoe_fp8_matmul_args& m, int C, int box, CUtensorMa
 
 // `most`: units there may be; a cluster of `ctas` works on one at a time.
 template <typename K>
-cudaError_t launch_units(K* k, const TrainDevice& d, int64_t most, int ctas, int smem, int smem_max, const MatmulArgs& a,
-                         const CUtensorMap& map_w, const CUtensorMap& map_x, cudaStream_t s) {
+cudaError_t launch_units(K* k, int threads, const TrainDevice& d, int64_t most, int ctas, int smem, int smem_max,
+                         const MatmulArgs& a, const CUtensorMap& map_w, const CUtensorMap& map_x, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max);
   if (e != cudaSuccess) return e;
   const int64_t workers = d.num_sms / ctas;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((unsigned)((most < workers ? most : workers) * ctas));
-  c.blockDim = dim3(kThreads);
+  c.blockDim = dim3(threads);
   c.dynamicSmemBytes = smem;
   c.stream = s;
   cudaLaunchAttribute at[2];
@@ -1073,8 +1071,8 @@ cudaError_t launch_few(const TrainDevice& d, const ftmoe_fp8_matmul_args& m, Mat
   const cudaError_t e = make_maps(m, a.C, F::kBox, &map_w, &map_x);
   if (e != cudaSuccess) return e;
   a.JT = fp8_blocks(a.O);
-  return launch_units(k_fp8_matmul<NMAX, SWIGLU, TRANS>, d, (m.M / NMAX + (m.M < m.E ? m.M : m.E)) * a.JT, 1,
-                      F::smem(m.E), F::smem(kMaxBins), a, map_w, map_x, s);
+  return launch_units(k_fp8_matmul_few<NMAX, SWIGLU, TRANS>, kFewThreads, d,
+                      (m.M / NMAX + (m.M < m.E ? m.M : m.E)) * a.JT, 1, F::smem(m.E), F::smem(kMaxBins), a, map_w, map_x, s);
 }
 
 template <int CTAS, bool SWIGLU, bool TRANS>
@@ -1084,8 +1082,8 @@ cudaError_t launch_many(const TrainDevice& d, const ftmoe_fp8_matmul_args& m, Ma
   const cudaError_t e = make_maps(m, a.C, 128, &map_w, &map_x);
   if (e != cudaSuccess) return e;
   a.JT = SWIGLU ? a.O / 128 : (a.O + 255) / 256;
-  return launch_units(k_fp8_matmul_many<CTAS, SWIGLU, TRANS>, d, (m.M / F::kTokens + (m.M < m.E ? m.M : m.E)) * a.JT,
-                      CTAS, F::smem(m.E), F::smem(kMaxBins), a, map_w, map_x, s);
+  return launch_units(k_fp8_matmul_many<CTAS, SWIGLU, TRANS>, kManyThreads, d,
+                      (m.M / F::kTokens + (m.M < m.E ? m.M : m.E)) * a.JT, CTAS, F::smem(m.E), F::smem(kMaxBins), a, map_w, map_x, s);
 }
 
 }  // namespace
