@@ -602,7 +602,7 @@ struct Many {
   static constexpr int kTokens = 128 * CTAS;
   static constexpr int kABytes = kTile, kBBytes = 2 * kTile / CTAS;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kBufs = 2, kCols = 256;
+  static constexpr int kBufs = 2, kCols = 256;  // a warp that issues MMAs has a buffer
   static constexpr int kTops = 128 * 2 * 4;  // a token's largest magnitude in each warpgroup
   static constexpr int kStages = CTAS == 2 ? 6 : 4;
   static constexpr int smem(int E) { return 1024 + kStages * kStageBytes + kTops + 512 + 3 * 4 * (E + 1); }
@@ -615,7 +615,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
 // The address of `p`'s counterpart in the cluster's CTA `rank`.
 __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
@@ -624,7 +624,9 @@ __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
   return r;
 }
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  // the default scope: at .cluster the arrival took some 1000 cycles, and only reads of tensor memory, which are
+  // over, go before it
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // The pair's forms: loads that complete on the first CTA's barrier, MMAs over
@@ -698,6 +700,15 @@ __device__ __forceinline__ void many_dealloc(uint32_t taddr, uint32_t cols) {
     tmem_dealloc(taddr, cols);
   else
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+
+// g / (1 + exp(-g)) by the approximate power of two and reciprocal: within (|g| + 8) 2^-24 of it, while the code that h
+// gets is rounded by up to 2^-4.  (The precise forms made a tile's end 9700 cycles long instead of some 3000.)
+__device__ __forceinline__ float silu_quick(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return g * r;
 }
 
 // 32 lanes x 16 columns of tensor memory, a lane's columns in its registers (see tc_ld_16x32 on memory order).
@@ -796,7 +807,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], CTAS * kManyWarps);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     for (int w = 0; w < 4; ++w) mbar_init(&row_bar[w], kManyWarps / 4);
     *abort_flag = 0;
     fence_mbar_init();
@@ -856,14 +867,18 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       // nothing this warp issued may still be landing when the CTA exits (the pair's second CTA waits for the first)
       if (rank == 0)
         for (int q = k > kStages ? k - kStages : 0; q < k; ++q) mbar_wait(&full[q % kStages], (q / kStages) & 1, a.status);
-    } else if (warp == 1 && lane == 0 && rank == 0) {
-      // ---------------- products
+    } else if ((warp == 1 || warp == 3) && lane == 0 && rank == 0) {
+      // ---------------- products: warp 1 has the even blocks, warp 3 the odd ones.  Issuing waits while the tensor
+      // cores are behind, and what comes between two blocks (the commits, the waits for the next one's buffers) is
+      // longer than what they then still have to do; so one warp issues while the other one waits.
       constexpr uint32_t idesc = idesc_e4m3(F::kTokens, TRANS && CTAS == 1 ? 128 : 256, false, TRANS);
+      const int b = warp >> 1;
       int k = 0;
       bool ok = true;
       for (int u = worker; ok && u < n_units && !*abort_flag; u += workers) {
         for (int kb = 0; kb < nkb; ++kb, ++k) {
-          const int s = k % kStages, b = k % kBufs;
+          if ((k & 1) != b) continue;
+          const int s = k % kStages;
           if ((k >= kBufs && !wait(&acc_empty[b], (k / kBufs - 1) & 1, a.status)) ||
               !wait(&full[s], (k / kStages) & 1, a.status)) {
             *abort_flag = 1;
@@ -881,8 +896,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             many_mma<CTAS>(d, adesc + i * (32 >> 4), bdesc + on, idesc, i != 0);
             if (TRANS && CTAS == 1) many_mma<CTAS>(d + 128, adesc + i * (32 >> 4), bdesc + on + (kTile >> 4), idesc, i != 0);
           }
-          many_commit<CTAS>(&empty[s]);
           many_commit<CTAS>(&acc_full[b]);
+          many_commit<CTAS>(&empty[s]);
         }
       }
       if (CTAS == 1)
@@ -915,17 +930,27 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      float v = on ? *sx : 0.f, w0 = there ? *sw : 0.f, w1 = SWIGLU ? sw[up] : 0.f;
+      // the scales of three blocks on their way: each comes from another line, maybe from DRAM
+      constexpr int kAhead = 3;
+      float v[kAhead], w0[kAhead], w1[kAhead];
+      const auto fetch = [&](int kb, int to) {
+        if (kb >= nkb) return;
+        v[to] = on ? sx[(int64_t)kb * a.M] : 0.f;
+        w0[to] = there ? sw[kb * sw_step] : 0.f;
+        if (SWIGLU) w1[to] = sw[up + kb];
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) fetch(i, i);
       for (int kb = 0; kb < nkb; ++kb, ++k) {
         const int b = k % kBufs;
-        const float s0 = v * w0, s1 = SWIGLU ? v * w1 : s0;
-        if (kb + 1 < nkb) {
-          sx += a.M;
-          sw += sw_step;
-          v = on ? *sx : 0.f;
-          w0 = there ? *sw : 0.f;
-          if (SWIGLU) w1 = sw[up];
+        const float s0 = v[0] * w0[0], s1 = SWIGLU ? v[0] * w1[0] : s0;
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) {
+          v[i] = v[i + 1];
+          w0[i] = w0[i + 1];
+          if (SWIGLU) w1[i] = w1[i + 1];
         }
+        fetch(kb + kAhead, kAhead - 1);
         if (!warp_wait(&acc_full[b], (k / kBufs) & 1, a.status)) {
           *abort_flag = 1;
           ok = false;
@@ -956,7 +981,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         uint32_t best = 0;
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
-          acc[i] = acc[i] * sigmoid(acc[i]) * acc[64 + i];
+          acc[i] = silu_quick(acc[i]) * acc[64 + i];
           best = max(best, magnitude(acc[i]));
         }
         tops[token * 2 + wg] = best;
@@ -1108,7 +1133,7 @@ cudaError_t launch_fp8_matmul(const TrainDevice& d, const ftmoe_fp8_matmul_args&
     if (m.swiglu) return launch_few<32, true, false>(d, m, a, s);
     return m.transpose ? launch_few<32, false, true>(d, m, a, s) : launch_few<32, false, false>(d, m, a, s);
   }
-  constexpr int kCtas = 1;
+  constexpr int kCtas = 2;
   if (m.swiglu) return launch_many<kCtas, true, false>(d, m, a, s);
   return m.transpose ? launch_many<kCtas, false, true>(d, m, a, s) : launch_many<kCtas, false, false>(d, m, a, s);
 }
