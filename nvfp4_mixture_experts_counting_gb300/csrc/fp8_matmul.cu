@@ -185,12 +185,17 @@ __device__ __forceinline__ Unit unit_of(const Tables& t, int u, int JT) {
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
-  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
-    if ((i & 255) == 0 && globaltimer() - t0 > kWaitLimitNs) {
+  for (uint32_t i = 1;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done) : "r"(smem_u32(bar)), "r"(parity), "r"(20000u) : "memory");
+    if (done) return true;
+    if (globaltimer() - t0 > kWaitLimitNs) {
       set_status(status, kStatusTimeout);
       return false;
     }
-  return true;
+  }
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
   return __all_sync(0xffffffffu, wait(bar, parity, status));
@@ -839,12 +844,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     regs_down<kLowRegs>();
     if (warp == 0 && lane == 0) {
       // ---------------- copies
-      int k = 0;
+      int s = 0, k = 0;
+      uint32_t phase = 1;
       for (int u = worker; u < n_units && !*abort_flag; u += workers) {
         const Unit x = unit(u);
         for (int kb = 0; kb < nkb; ++kb, ++k) {
-          const int s = k % kStages;
-          if (k >= kStages && !wait(&empty[s], (k / kStages - 1) & 1, a.status)) {
+          if (!wait(&empty[s], phase, a.status)) {
             *abort_flag = 1;
             break;
           }
@@ -862,6 +867,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             else
               many_load_3d<CTAS>(sb + h * kTile, &map_w, kb * 128, n0, x.e, bar);
           }
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
       }
       // nothing this warp issued may still be landing when the CTA exits (the pair's second CTA waits for the first)
@@ -871,34 +880,45 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       // ---------------- products: warp 1 has the even blocks, warp 3 the odd ones.  Issuing waits while the tensor
       // cores are behind, and what comes between two blocks (the commits, the waits for the next one's buffers) is
       // longer than what they then still have to do; so one warp issues while the other one waits.
+      // Few instructions matter here: the summing warps leave few issue slots.
       constexpr uint32_t idesc = idesc_e4m3(F::kTokens, TRANS && CTAS == 1 ? 128 : 256, false, TRANS);
-      const int b = warp >> 1;
-      int k = 0;
+      static_assert(kStages % 2 == 0, "a warp has every other stage");
+      // 32 contracted values: 32 bytes on within the swizzled rows, or 32 rows on
+      constexpr uint64_t kStepA = 32 >> 4, kStepB = TRANS ? 32 * 128 >> 4 : 32 >> 4;
+      const int b = warp >> 1, last_steps = (a.C - (nkb - 1) * 128 + 31) / 32;
+      const uint64_t adesc0 = sdesc_k_sw128(smem_u32(sm)), bdesc0 = sdesc_k_sw128(smem_u32(sm) + F::kABytes);
+      const uint32_t d = tmem + b * F::kCols;
+      int s = b, first = b;  // the stage; this warp's first block of the unit
+      uint32_t full_phase = 0, acc_phase = 1;  // a new barrier's phase 1 counts as over
       bool ok = true;
       for (int u = worker; ok && u < n_units && !*abort_flag; u += workers) {
-        for (int kb = 0; kb < nkb; ++kb, ++k) {
-          if ((k & 1) != b) continue;
-          const int s = k % kStages;
-          if ((k >= kBufs && !wait(&acc_empty[b], (k / kBufs - 1) & 1, a.status)) ||
-              !wait(&full[s], (k / kStages) & 1, a.status)) {
+        int kb = first;
+        for (; kb < nkb; kb += 2) {
+          if (!wait(&acc_empty[b], acc_phase, a.status) || !wait(&full[s], full_phase, a.status)) {
             *abort_flag = 1;
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(sm + s * F::kStageBytes);
-          const uint64_t adesc = sdesc_k_sw128(sa), bdesc = sdesc_k_sw128(sa + F::kABytes);
-          const int steps = (min(128, a.C - kb * 128) + 31) / 32;
-          const uint32_t d = tmem + b * F::kCols;
-          for (int i = 0; i < steps; ++i) {
-            // 32 contracted values: 32 bytes on within the swizzled rows, or 32 rows on
-            const uint64_t on = TRANS ? i * (32 * 128 >> 4) : i * (32 >> 4);
-            many_mma<CTAS>(d, adesc + i * (32 >> 4), bdesc + on, idesc, i != 0);
-            if (TRANS && CTAS == 1) many_mma<CTAS>(d + 128, adesc + i * (32 >> 4), bdesc + on + (kTile >> 4), idesc, i != 0);
+          const uint64_t adesc = adesc0 + s * (F::kStageBytes >> 4), bdesc = bdesc0 + s * (F::kStageBytes >> 4);
+          const int steps = kb == nkb - 1 ? last_steps : 4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i >= steps) break;
+            many_mma<CTAS>(d, adesc + i * kStepA, bdesc + i * kStepB, idesc, i != 0);
+            if (TRANS && CTAS == 1)
+              many_mma<CTAS>(d + 128, adesc + i * kStepA, bdesc + i * kStepB + (kTile >> 4), idesc, i != 0);
           }
           many_commit<CTAS>(&acc_full[b]);
           many_commit<CTAS>(&empty[s]);
+          acc_phase ^= 1;
+          s += 2;
+          if (s >= kStages) {
+            s -= kStages;
+            full_phase ^= 1;
+          }
         }
+        first = kb - nkb;  // 0 or 1: the blocks of all units are counted on
       }
       if (CTAS == 1)
         tc_commit(drain);
@@ -910,8 +930,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   } else {
     regs_up<kEpiRegs>();
     // ---------------- sums: warp (wg, q) has tokens 32q.. and the columns [128 wg, 128 wg + 128), with SwiGLU
-    // [64 wg, 64 wg + 64) of gate and up.  Plain FMAs: packed ones are no faster here, and the pairs' alignment
-    // costs registers.
+    // [64 wg, 64 wg + 64) of gate and up.  Packed FMAs: no faster than plain ones here, but half the instructions.
     const int q = warp & 3, wg = (warp - kEpiWarp0) >> 2;
     const uint32_t from = tmem + ((uint32_t)(32 * q) << 16) + (SWIGLU ? 64 : 128) * wg;
     int k = 0;
@@ -927,10 +946,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const bool there = nb * 128 < a.O;  // a last tile may have only its first half
       const float* sw = a.w_scale + ((int64_t)x.e * a.NB + (TRANS ? 0 : nb)) * a.KB + (TRANS ? nb : 0);
       const int64_t sw_step = TRANS ? a.KB : 1, up = (int64_t)(a.O / 128) * a.KB;
-      float acc[128];
+      uint64_t acc2[64];
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      // the scales of three blocks on their way: each comes from another line, maybe from DRAM
+      for (int i = 0; i < 64; ++i) acc2[i] = 0ull;
       constexpr int kAhead = 3;
       float v[kAhead], w0[kAhead], w1[kAhead];
       const auto fetch = [&](int kb, int to) {
@@ -942,8 +960,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) fetch(i, i);
       for (int kb = 0; kb < nkb; ++kb, ++k) {
-        const int b = k % kBufs;
+        const int b = k & 1;
         const float s0 = v[0] * w0[0], s1 = SWIGLU ? v[0] * w1[0] : s0;
+        const uint64_t s2[2] = {pack2(s0, s0), pack2(s1, s1)};
 #pragma unroll
         for (int i = 0; i + 1 < kAhead; ++i) {
           v[i] = v[i + 1];
@@ -951,7 +970,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           if (SWIGLU) w1[i] = w1[i + 1];
         }
         fetch(kb + kAhead, kAhead - 1);
-        if (!warp_wait(&acc_full[b], (k / kBufs) & 1, a.status)) {
+        if (!warp_wait(&acc_full[b], (k >> 1) & 1, a.status)) {
           *abort_flag = 1;
           ok = false;
           break;
@@ -969,10 +988,15 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             }
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[16 * h + i] = fmaf(__uint_as_float(r[i]), h < 4 ? s0 : s1, acc[16 * h + i]);
+          for (int i = 0; i < 8; ++i)
+            acc2[8 * h + i] =
+                fma2(pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), s2[h / 4], acc2[8 * h + i]);
         }
       }
       if (!ok) break;
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) unpack2(acc2[i], acc[2 * i], acc[2 * i + 1]);
       if constexpr (!SWIGLU) {
         const int c0 = x.jt * 256 + 128 * wg;
         if (on && c0 < a.O) store_row<128>(a, x.row0 + token, c0, acc);
@@ -1133,7 +1157,7 @@ cudaError_t launch_fp8_matmul(const TrainDevice& d, const ftmoe_fp8_matmul_args&
     if (m.swiglu) return launch_few<32, true, false>(d, m, a, s);
     return m.transpose ? launch_few<32, false, true>(d, m, a, s) : launch_few<32, false, false>(d, m, a, s);
   }
-  constexpr int kCtas = 2;
+  constexpr int kCtas = 1;
   if (m.swiglu) return launch_many<kCtas, true, false>(d, m, a, s);
   return m.transpose ? launch_many<kCtas, false, true>(d, m, a, s) : launch_many<kCtas, false, false>(d, m, a, s);
 }
