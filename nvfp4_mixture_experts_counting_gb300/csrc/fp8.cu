@@ -129,9 +129,9 @@ __global__ void __launch_bounds__(kThreads) k_fp8_quantize_weights(const T* w, i
 // ---------------------------------------------------------------- SwiGLU
 
 // h = g s(g) u, and its gradient from dh: dg = dh u s (1 + g (1 - s)), du = dh g s.
-__device__ __forceinline__ float swiglu(float g, float u) { return g * sigmoid(g) * u; }
+__device__ __forceinline__ float swiglu(float g, float u) { return g * sigmoid_rcp(g) * u; }
 __device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float& dg, float& du) {
-  const float s = sigmoid(g);
+  const float s = sigmoid_rcp(g);
   dg = dh * u * s * (1.f + g * (1.f - s));
   du = dh * g * s;
 }
@@ -183,33 +183,50 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_fp8(const T* gu, const T* d
   }
 }
 
-// Output in the input's type, V values at a time (1 where rows are not a multiple of 16 bytes).
+// Output in the input's type.  A warp takes 128 V columns of a row: four
+// pieces a lane, 32 pieces apart, of V = 16 bytes' values, or of one value
+// where rows are not a multiple of 16 bytes (whose loads are so issued
+// together and stay whole lines).
+constexpr int kPieces = 4;
 template <typename T, int V, bool GRAD>
 __global__ void __launch_bounds__(kThreads) k_swiglu(const T* gu, const T* dh, int rows_, int I, const int32_t* used,
                                                      T* out, uint32_t* status) {
   pdl_wait();
-  const int rows = used_rows(used, rows_, status), pieces = I / V;
-  const int64_t units = (int64_t)rows * pieces, step = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < units; i += step) {
-    const int64_t r = quotient(i, pieces);
-    const int k = (int)(i - r * pieces) * V;
-    const Pack<T, V> g = load_pack<T, V>(gu + r * 2 * I + k), u = load_pack<T, V>(gu + r * 2 * I + I + k);
-    Pack<T, V> a, b;
-    if constexpr (GRAD) {
-      const Pack<T, V> d = load_pack<T, V>(dh + r * I + k);
+  constexpr int kWide = 32 * V * kPieces;
+  const int rows = used_rows(used, rows_, status), chunks = (I + kWide - 1) / kWide;
+  const int64_t units = (int64_t)rows * chunks, step = (int64_t)gridDim.x * (kThreads / 32);
+  for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; i < units; i += step) {
+    const int64_t r = quotient(i, chunks);
+    const int k0 = (int)(i - r * chunks) * kWide + (threadIdx.x & 31) * V;
+    const T *g = gu + r * 2 * I, *u = g + I, *d = GRAD ? dh + r * I : nullptr;
+    T* o = out + r * (GRAD ? 2 : 1) * I;
+    Pack<T, V> pg[kPieces], pu[kPieces], pd[kPieces];
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      const int k = k0 + 32 * V * p;
+      if (k >= I) continue;
+      pg[p] = load_pack<T, V>(g + k);
+      pu[p] = load_pack<T, V>(u + k);
+      if (GRAD) pd[p] = load_pack<T, V>(d + k);
+    }
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      const int k = k0 + 32 * V * p;
+      if (k >= I) continue;
+      Pack<T, V> a, b;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        float dg, du;
-        swiglu_grad(d.get(j), g.get(j), u.get(j), dg, du);
-        a.set(j, dg);
-        b.set(j, du);
+        if constexpr (GRAD) {
+          float dg, du;
+          swiglu_grad(pd[p].get(j), pg[p].get(j), pu[p].get(j), dg, du);
+          a.set(j, dg);
+          b.set(j, du);
+        } else {
+          a.set(j, swiglu(pg[p].get(j), pu[p].get(j)));
+        }
       }
-      store_pack<T, V>(out + r * 2 * I + k, a);
-      store_pack<T, V>(out + r * 2 * I + I + k, b);
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) a.set(j, swiglu(g.get(j), u.get(j)));
-      store_pack<T, V>(out + r * I + k, a);
+      store_pack<T, V>(o + k, a);
+      if (GRAD) store_pack<T, V>(o + I + k, b);
     }
   }
 }
@@ -253,7 +270,8 @@ cudaError_t launch_swiglu(const TrainDevice& d, const void* gu, const void* dh, 
     }
     constexpr int W = 16 / sizeof(V);
     const bool wide = I % W == 0;
-    const unsigned grid = grid_of(d, (int64_t)rows * (wide ? I / W : I), kThreads, 16);
+    const int per_warp = 32 * kPieces * (wide ? W : 1);
+    const unsigned grid = grid_of(d, (int64_t)rows * ((I + per_warp - 1) / per_warp), kThreads / 32, 16);
     auto* k = wide ? (dh ? k_swiglu<V, W, true> : k_swiglu<V, W, false>)
                    : (dh ? k_swiglu<V, 1, true> : k_swiglu<V, 1, false>);
     return launch_after(k, grid, kThreads, s, g, dv, rows, I, used, static_cast<V*>(out), d.status);

@@ -41,4 +41,12 @@ __device__ __forceinline__ int used_rows(const int32_t* used, int rows, uint32_t
 
 __device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
 
+// The same with the approximate reciprocal: within 5 2^-24 (expf 2, the sum 1, the reciprocal 2) at a third of the
+// instructions.
+__device__ __forceinline__ float sigmoid_rcp(float z) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + expf(-z)));
+  return r;
+}
+
 }  // namespace ftmoe

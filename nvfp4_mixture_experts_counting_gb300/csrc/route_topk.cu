@@ -12,10 +12,11 @@
 // their bounds is ranked again in fp64.  Of N(0, 1) logits with E = 256 that is
 // one token in some hundreds.
 //
-// A warp takes a token; lane i holds the experts i, i + 32, ... as integer keys
-// in the order of the values, so that a round of the selection is one scan of
-// a lane's keys and two warp reductions (the best key, the lowest expert that
-// has it).
+// A warp takes a token; lane i holds the experts i, i + 32, ...  With the
+// lanes' largest values sorted, the (k+1)-th of them is below or at the (k+1)-th
+// of all values, so the few values from it on hold the choice: they are
+// gathered, a lane each, and each counts those before it.  (k rounds of finding
+// the largest value by two reductions took twice the instructions.)
 #include <cfloat>
 
 #include "fp8_common.cuh"
@@ -35,23 +36,16 @@ struct RouteKernelArgs {
   const float* bias;
   int n_groups, top_groups, group_best, group_size;
   uint32_t group_magic;  // ceil(2^20 / group_size): e / group_size = e * magic >> 20 for e < 2^10
+  int group_lanes;       // lanes that look at a group
   int by_logit;          // c's order is the logits'
   int32_t* idx;
   float* w;
   uint32_t* status;
 };
 
-// An unsigned key in the order of the values; 0 is below every value's.
-__device__ __forceinline__ uint32_t key_of(float v) {
-  const uint32_t b = __float_as_uint(v + 0.f);  // -0 becomes 0
-  return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
-}
-__device__ __forceinline__ float value_of(uint32_t key) {
-  return __uint_as_float(key ^ (key >> 31 ? 0x80000000u : 0xffffffffu));
-}
-
 __device__ __forceinline__ bool in_groups(const RouteKernelArgs& a, uint32_t groups, int e) {
-  return groups >> ((e * a.group_magic >> 20) & 31) & 1;
+  const int g = e * a.group_magic >> 20;
+  return g < a.n_groups && groups >> g * a.group_lanes & 1;
 }
 
 __device__ __forceinline__ double warp_max_d(double v) {
@@ -60,14 +54,12 @@ __device__ __forceinline__ double warp_max_d(double v) {
   return v;
 }
 
-// The chosen groups as a mask, from the experts' values c[E] (-inf: not
-// available).  L lanes take a group.  `gap`: the least chosen group's value
-// less the best other one's (infinite where there is no such pair).
+// The chosen groups as a mask (group g at bit g L), from the experts' values
+// c[E] (-inf: not available).  L lanes take a group.  `gap`: the least chosen
+// group's value less the best other one's (infinite where there is no such pair).
 template <typename V>
 __device__ __forceinline__ uint32_t choose_groups(const RouteKernelArgs& a, const V* c, int lane, V& gap) {
-  int L = 32;
-  while (L * a.n_groups > 32) L >>= 1;
-  const int g = lane / L;
+  const int L = a.group_lanes, g = lane / L;
   const V none = -(V)INFINITY;
   V m0 = none, m1 = none;
   if (g < a.n_groups)
@@ -91,8 +83,7 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteKernelArgs& a, cons
     before += other > mine || (other == mine && o < g);
   }
   const bool head = lane % L == 0 && g < a.n_groups, in = head && before < a.top_groups;
-  uint32_t mask = 0;
-  for (int o = 0; o < a.n_groups; ++o) mask |= (uint32_t)__shfl_sync(0xffffffffu, (int)in, o * L) << o;
+  const uint32_t mask = __ballot_sync(0xffffffffu, in);
   V least = in ? mine : (V)INFINITY, best = head && !in ? mine : none;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -152,65 +143,98 @@ __device__ __noinline__ int route_again(const RouteKernelArgs& a, const T* row, 
   return mine;
 }
 
-// VPL: keys a lane holds.
+// 1 / (1 + exp(-l)) by the approximate power of two (4 eps) and reciprocal (2 eps).
+__device__ __forceinline__ float sigmoid_quick(float l) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
+
+__device__ __forceinline__ float warp_max_redux(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+
+// The warp's values, largest in lane 0 (a bitonic sort).
+__device__ __forceinline__ float sort_lanes(float v, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int step = size / 2; step > 0; step >>= 1) {
+      const float o = __shfl_xor_sync(0xffffffffu, v, step);
+      v = ((lane & step) == 0) == ((lane & size) == 0) ? fmaxf(v, o) : fminf(v, o);
+    }
+  return v;
+}
+
+// The candidates and slots of a token.
+struct Chosen {
+  float value[32], slot_value[33];
+  int expert[32], slot_expert[33];
+};
+
+// VPL: experts a lane holds.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(kWarps * 32) k_route_topk(const __grid_constant__ RouteKernelArgs a) {
   extern __shared__ double shared_c[];
+  __shared__ Chosen shared_chosen[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   double* exact_c = shared_c + warp * a.E;
-  float* c = reinterpret_cast<float*>(exact_c);
+  float* shared_f = reinterpret_cast<float*>(exact_c);
+  Chosen& ch = shared_chosen[warp];
   pdl_wait();
+  float bias[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 32 * i;
+    bias[i] = a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
+  }
   for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    float l[VPL];
+    float c[VPL];  // the logits, then what is ranked; -inf: not available
     bool odd = false;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = lane + 32 * i;
-      l[i] = e < a.E ? to_f32(row[e]) : -INFINITY;
-      odd |= !(l[i] < INFINITY);
+      c[i] = e < a.E ? to_f32(row[e]) : -INFINITY;
     }
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      l[i] = l[i] < INFINITY ? l[i] : -INFINITY;
-      top = fmaxf(top, l[i]);
+      const bool usable = c[i] < INFINITY;
+      odd |= !usable;
+      c[i] = usable ? c[i] : -INFINITY;
+      top = fmaxf(top, c[i]);
     }
     float total = 1.f, largest = 1.f;  // the softmax's sum; the largest score
     if (!a.sigmoid && (!a.by_logit || !a.norm)) {
-      top = warp_max_f32(top);
+      top = warp_max_redux(top);
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) sum += l[i] == -INFINITY ? 0.f : expf(l[i] - top);
+      for (int i = 0; i < VPL; ++i) sum += c[i] == -INFINITY ? 0.f : expf(c[i] - top);
       total = warp_sum_f32(sum);
       largest = 1.f / total;
     }
-    uint32_t key[VPL];
     float bound = 0.f;
-    if (a.by_logit) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = l[i] == -INFINITY ? 0u : key_of(l[i]);
-    } else {
+    if (!a.by_logit) {
       float far = 0.f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 32 * i;
-        key[i] = 0u;
-        if (l[i] == -INFINITY) continue;
-        const float b = a.bias ? __ldg(a.bias + e) : 0.f;
-        if (!(fabsf(b) < INFINITY)) {
-          odd |= b != -INFINITY;
-          continue;
-        }
-        const float v = (a.sigmoid ? sigmoid(l[i]) : expf(l[i] - top) * largest) + b;
-        far = fmaxf(far, fabsf(v));
-        key[i] = key_of(v);
+        const float b = bias[i], l = c[i];
+        const bool usable = fabsf(b) < INFINITY;
+        odd |= !usable && b != -INFINITY && l != -INFINITY;
+        const float v = (a.sigmoid ? sigmoid_quick(l) : expf(l - top) * largest) + b;
+        c[i] = usable && l != -INFINITY ? v : -INFINITY;
+        far = fmaxf(far, c[i] == -INFINITY ? 0.f : fabsf(v));
       }
-      // |error of s| <= 4 eps for the sigmoid (exp 2 eps of it, the sum, the quotient, each s <= 1); for the
-      // softmax (VPL + 18) eps s, from the exponent (|l - top| eps, at most ln E in the mean of the sum), exp
-      // (2 eps), a lane's sum, the joins (5) and the two products.  The bias adds eps |c|.  Two values differ
-      // for sure beyond the sum of their bounds; half is added.
-      bound = 1.5f * kEps * (2.f * (a.sigmoid ? 4.f : (VPL + 18.f) * largest) + 2.f * warp_max_f32(far));
+      // |error of s| <= 5 eps for the sigmoid: exp's 4 eps and its argument's 2 |l| eps count by s (1 - s), 1.5 in
+      // all, then the sum's and the reciprocal's.  For the softmax (VPL + 18) eps of the largest s, from the
+      // exponents (|l - top| eps, at most ln E in the mean of the sum), exp (2 eps), a lane's sum, the joins (5) and
+      // the two products.  The bias adds eps |c|.  Two values differ for sure beyond the sum of their bounds; half
+      // is added.
+      bound = 1.5f * kEps * (2.f * (a.sigmoid ? 5.f : (VPL + 18.f) * largest) + 2.f * warp_max_redux(far));
     }
     if (odd) set_status(a.status, kStatusRange);
     bool again = false;
@@ -218,35 +242,71 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_topk(const __grid_constan
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (lane + 32 * i < a.E) c[lane + 32 * i] = key[i] ? value_of(key[i]) : -INFINITY;
+        if (lane + 32 * i < a.E) shared_f[lane + 32 * i] = c[i];
       __syncwarp();
       float gap;
-      const uint32_t groups = choose_groups(a, c, lane, gap);
+      const uint32_t groups = choose_groups(a, shared_f, lane, gap);
       again = !a.by_logit && gap <= 3.f * bound;  // of sums of two values, which are rounded too
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (!in_groups(a, groups, lane + 32 * i)) key[i] = 0u;
+        if (!in_groups(a, groups, lane + 32 * i)) c[i] = -INFINITY;
     }
-    // slot j's expert stays with lane j
-    int mine = -1;
-    uint32_t last = 0u;
-    const int rounds = again ? 0 : a.top_k + !a.by_logit;
-    for (int j = 0; j < rounds; ++j) {
-      uint32_t best = 0u;
-      int at = 0;
+    float most = c[0];
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (key[i] > best) best = key[i], at = i;
-      const uint32_t high = __reduce_max_sync(0xffffffffu, best);
-      if (!high) break;
-      if (!a.by_logit && last) again |= value_of(last) - value_of(high) <= bound;
-      last = high;
-      const int e = __reduce_min_sync(0xffffffffu, best == high ? lane + 32 * at : 1 << 20);
-      if (lane == j) mine = e;
-      if ((e & 31) == lane) {
+    for (int i = 1; i < VPL; ++i) most = fmaxf(most, c[i]);
+    const float from = a.top_k < 32 ? __shfl_sync(0xffffffffu, sort_lanes(most, lane), a.top_k & 31) : -INFINITY;
+    int found = 0;  // candidates, in the order of the experts
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const bool in = c[i] >= from && c[i] != -INFINITY;
+      const uint32_t mask = __ballot_sync(0xffffffffu, in);
+      const int at = found + __popc(mask & ((1u << lane) - 1));
+      if (in && at < 32) {
+        ch.value[at] = c[i];
+        ch.expert[at] = lane + 32 * i;
+      }
+      found += __popc(mask);
+    }
+    __syncwarp();
+    int mine = -1;  // slot j's expert stays with lane j
+    if (found <= 32) {
+      const float v = lane < found ? ch.value[lane] : -INFINITY;
+      int before = 0;
+      for (int o = 0; o < found; ++o) {
+        const float x = __shfl_sync(0xffffffffu, v, o);
+        before += x > v || (x == v && o < lane);
+      }
+      if (lane < found && before <= a.top_k) {
+        ch.slot_value[before] = v;
+        ch.slot_expert[before] = ch.expert[lane];
+      }
+      __syncwarp();
+      if (lane < min(found, a.top_k)) mine = ch.slot_expert[lane];
+      // neighbours up to the first one left out
+      if (!a.by_logit)
+        again |= __any_sync(0xffffffffu, lane < a.top_k && lane + 1 < found &&
+                                             ch.slot_value[lane] - ch.slot_value[lane + 1] <= bound);
+    } else {
+      // many equal values, or many of the largest in few lanes: the largest again and again
+      float last = 0.f;
+      for (int j = 0; j < a.top_k + !a.by_logit; ++j) {
+        float best = -INFINITY;
+        int at = 0;
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-          if (i == e / 32) key[i] = 0u;
+          if (c[i] > best) best = c[i], at = i;
+        const float high = warp_max_redux(best);
+        if (high == -INFINITY) break;
+        if (!a.by_logit && j > 0) again |= last - high <= bound;
+        last = high;
+        const int e = __reduce_min_sync(0xffffffffu, best == high ? lane + 32 * at : 1 << 20);
+        if (lane == j) mine = e;
+        if ((e & 31) == lane) {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i)
+            if (i == e / 32) c[i] = -INFINITY;
+        }
       }
     }
     if (again) mine = route_again(a, row, exact_c, lane);
@@ -255,8 +315,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_topk(const __grid_constan
     float s = 0.f;
     const float z = mine >= 0 ? usable_logit(row, mine) : -INFINITY;
     if (a.norm) {
-      const float n = a.sigmoid ? fminf(z, 0.f) : z, most = warp_max_f32(n);
-      if (mine >= 0) s = expf(n - most) / (a.sigmoid ? 1.f + expf(-fabsf(z)) : 1.f);
+      const float n = a.sigmoid ? fminf(z, 0.f) : z, high = warp_max_redux(n);
+      if (mine >= 0) s = expf(n - high) / (a.sigmoid ? 1.f + expf(-fabsf(z)) : 1.f);
       const float sum = warp_sum_f32(s);
       s = sum > 0.f ? s * a.scale / sum : 0.f;
     } else if (mine >= 0) {
@@ -355,6 +415,8 @@ RouteKernelArgs kernel_args(const TrainDevice& d, const ftmoe_route_args& r) {
   a.group_best = r.group_best;
   a.group_size = r.E / r.n_groups;
   a.group_magic = (uint32_t)(((1 << 20) + a.group_size - 1) / a.group_size);
+  a.group_lanes = 32;
+  while (a.group_lanes * a.n_groups > 32) a.group_lanes >>= 1;
   a.by_logit = !r.bias && (r.n_groups == 1 || r.group_best == 1);
   a.idx = r.topk_idx;
   a.w = r.topk_w;
