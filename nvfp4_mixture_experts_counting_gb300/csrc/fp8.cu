@@ -27,9 +27,10 @@ __device__ __forceinline__ void load16(const T* p, float (&v)[kPer]) {
 
 // The scale of the block that this lane's group of eight holds, and this lane's codes.
 __device__ __forceinline__ uint4 quantize16(const float (&v)[kPer], float& scale) {
-  uint32_t top = 0;
+  float most = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) top = max(top, magnitude(v[i]));
+  for (int i = 0; i < kPer; ++i) most = max_magnitude(most, v[i]);
+  uint32_t top = magnitude(most);
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
   const BlockScale b = block_scale(top);
@@ -42,8 +43,10 @@ __device__ __forceinline__ uint4 quantize16(const float (&v)[kPer], float& scale
   return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
-// A warp takes four neighbouring blocks of a row.  With `inv`, token t's codes
-// go to the rows inv[t * top_k + j].
+// A warp takes eight neighbouring blocks of a row, two at each lane's place
+// whose loads go out together.  With `inv`, token t's codes go to the rows
+// inv[t * top_k + j].
+constexpr int kTwice = 2;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_fp8_quantize(const T* x, int T_, int K, const int32_t* inv, int top_k,
                                                            const int32_t* used, uint8_t* codes, float* scales,
@@ -51,39 +54,42 @@ __global__ void __launch_bounds__(kThreads) k_fp8_quantize(const T* x, int T_, i
   pdl_wait();
   const int rows = used_rows(used, T_, status);
   const int64_t places = inv ? (int64_t)T_ * top_k : T_;
-  const int blocks = (K + kFp8Block - 1) / kFp8Block, quads = (blocks + 3) / 4;
+  const int blocks = (K + kFp8Block - 1) / kFp8Block, parts = (blocks + 4 * kTwice - 1) / (4 * kTwice);
   const int lane = threadIdx.x & 31, sub = lane & (kLanes - 1);
-  const int64_t units = (int64_t)rows * quads, step = (int64_t)gridDim.x * (kThreads / 32);
+  const int64_t units = (int64_t)rows * parts, step = (int64_t)gridDim.x * (kThreads / 32);
   for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; u < units; u += step) {
-    const int64_t t = quotient(u, quads);
-    const int b = (int)(u - t * quads) * 4 + lane / kLanes, k0 = b * kFp8Block + sub * kPer;
-    const bool on = k0 < K;  // K is a multiple of 16: a lane's values are all there or none is
-    float v[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = 0.f;
-    if (on) load16(x + t * K + k0, v);
-    float scale;
-    const uint4 c = quantize16(v, scale);
-    if (!inv) {
-      if (on) {
-        *reinterpret_cast<uint4*>(codes + t * K + k0) = c;
-        if (sub == 0) scales[(int64_t)b * places + t] = scale;
-      }
-      continue;
-    }
+    const int64_t t = quotient(u, parts);
+    const int b0 = (int)(u - t * parts) * (4 * kTwice) + lane / kLanes;
     int mine = -1;
-    if (lane < top_k) {
+    if (inv && lane < top_k) {
       mine = inv[t * top_k + lane];
       if (mine < -1 || mine >= places) {
         set_status(status, kStatusRange);
         mine = -1;
       }
     }
+    float v[kTwice][kPer];
+#pragma unroll
+    for (int h = 0; h < kTwice; ++h) {
+      const int k0 = (b0 + 4 * h) * kFp8Block + sub * kPer;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[h][i] = 0.f;
+      if (k0 < K) load16(x + t * K + k0, v[h]);  // K is a multiple of 16: a lane's values are all there or none is
+    }
+    uint4 c[kTwice];
+    float scale[kTwice];
+#pragma unroll
+    for (int h = 0; h < kTwice; ++h) c[h] = quantize16(v[h], scale[h]);
     for (int j = 0; j < top_k; ++j) {
-      const int at = __shfl_sync(0xffffffffu, mine, j);
-      if (at < 0 || !on) continue;
-      *reinterpret_cast<uint4*>(codes + (int64_t)at * K + k0) = c;
-      if (sub == 0) scales[(int64_t)b * places + at] = scale;
+      const int64_t at = inv ? __shfl_sync(0xffffffffu, mine, j) : t;
+      if (at < 0) continue;
+#pragma unroll
+      for (int h = 0; h < kTwice; ++h) {
+        const int b = b0 + 4 * h, k0 = b * kFp8Block + sub * kPer;
+        if (k0 >= K) continue;
+        *reinterpret_cast<uint4*>(codes + at * K + k0) = c[h];
+        if (sub == 0) scales[(int64_t)b * places + at] = scale[h];
+      }
     }
   }
 }
@@ -242,7 +248,7 @@ cudaError_t launch_fp8_quantize(const TrainDevice& d, const void* x, int dtype, 
                                 int top_k, const int32_t* used, uint8_t* codes, float* scales, cudaStream_t s) {
   return with_dtype(dtype, [&](auto zero) {
     using V = decltype(zero);
-    const int64_t units = (int64_t)T * ((fp8_blocks(K) + 3) / 4);
+    const int64_t units = (int64_t)T * ((fp8_blocks(K) + 4 * kTwice - 1) / (4 * kTwice));
     return launch_after(k_fp8_quantize<V>, grid_of(d, units, kThreads / 32, 16), kThreads, s,
                         static_cast<const V*>(x), T, K, inv, top_k, used, codes, scales, d.status);
   });

@@ -27,6 +27,13 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
   return {__fdiv_rn(a, kFp8Max), __fdiv_rn(kFp8Max, a)};
 }
 
+// The larger magnitude; NaN if one is.
+__device__ __forceinline__ float max_magnitude(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // Rows that a call handles: `used` (a count on the device) where it is given.

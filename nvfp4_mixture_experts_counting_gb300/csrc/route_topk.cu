@@ -37,6 +37,7 @@ struct RouteKernelArgs {
   int n_groups, top_groups, group_best, group_size;
   uint32_t group_magic;  // ceil(2^20 / group_size): e / group_size = e * magic >> 20 for e < 2^10
   int group_lanes;       // lanes that look at a group
+  int group_quads;       // each at whole quads of experts
   int by_logit;          // c's order is the logits'
   int32_t* idx;
   float* w;
@@ -54,29 +55,51 @@ __device__ __forceinline__ double warp_max_d(double v) {
   return v;
 }
 
+__device__ __forceinline__ float warp_max_redux(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
+__device__ __forceinline__ double smaller(double a, double b) { return a < b ? a : b; }
+
 // The chosen groups as a mask (group g at bit g L), from the experts' values
 // c[E] (-inf: not available).  L lanes take a group.  `gap`: the least chosen
 // group's value less the best other one's (infinite where there is no such pair).
+// `least_in`: the smallest value that counts in this lane's group.
 template <typename V>
-__device__ __forceinline__ uint32_t choose_groups(const RouteKernelArgs& a, const V* c, int lane, V& gap) {
+__device__ __forceinline__ uint32_t choose_groups(const RouteKernelArgs& a, const V* c, int lane, V& gap, V& least_in) {
   const int L = a.group_lanes, g = lane / L;
   const V none = -(V)INFINITY;
-  V m0 = none, m1 = none;
-  if (g < a.n_groups)
-    for (int i = lane % L; i < a.group_size; i += L) {
-      const V v = c[g * a.group_size + i];
-      m1 = v > m0 ? m0 : v > m1 ? v : m1;
-      m0 = v > m0 ? v : m0;
+  V m0 = none, m1 = none;  // the two largest
+  const auto take = [&](V v) {
+    m1 = larger(m1, smaller(m0, v));
+    m0 = larger(m0, v);
+  };
+  if (g < a.n_groups) {
+    const int per = (a.group_size + L - 1) / L, first = lane % L * per, n = min(per, a.group_size - first);
+    const V* from = c + g * a.group_size + first;
+    if (sizeof(V) == 4 && a.group_quads) {
+      for (int i = 0; i < n; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(from + i);
+        take(v.x), take(v.y), take(v.z), take(v.w);
+      }
+    } else {
+      for (int i = 0; i < n; ++i) take(from[i]);
     }
+  }
   for (int o = L / 2; o > 0; o >>= 1) {
     const V p0 = __shfl_xor_sync(0xffffffffu, m0, o), p1 = __shfl_xor_sync(0xffffffffu, m1, o);
-    const V low = p0 < m0 ? p0 : m0, high = p0 < m0 ? m0 : p0;
-    const V next = m1 > p1 ? m1 : p1;
-    m0 = high;
-    m1 = low > next ? low : next;
+    m1 = larger(larger(m1, p1), smaller(m0, p0));
+    m0 = larger(m0, p0);
   }
   // one available expert counts alone
-  const V mine = a.group_best == 2 && m1 != none ? m0 + m1 : m0;
+  const bool two = a.group_best == 2 && m1 != none;
+  const V mine = two ? m0 + m1 : m0;
+  least_in = two ? m1 : m0;
   int before = 0;
   for (int o = 0; o < a.n_groups; ++o) {
     const V other = __shfl_sync(0xffffffffu, mine, o * L);
@@ -84,14 +107,10 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteKernelArgs& a, cons
   }
   const bool head = lane % L == 0 && g < a.n_groups, in = head && before < a.top_groups;
   const uint32_t mask = __ballot_sync(0xffffffffu, in);
-  V least = in ? mine : (V)INFINITY, best = head && !in ? mine : none;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const V x = __shfl_xor_sync(0xffffffffu, least, o), y = __shfl_xor_sync(0xffffffffu, best, o);
-    least = x < least ? x : least;
-    best = y > best ? y : best;
+  if (sizeof(V) == 4) {
+    const V least = -(V)warp_max_redux((float)(in ? -mine : none)), best = (V)warp_max_redux((float)(head && !in ? mine : none));
+    gap = best == none ? (V)INFINITY : least - best;
   }
-  gap = best == none ? (V)INFINITY : least - best;
   return mask;
 }
 
@@ -101,11 +120,12 @@ __device__ __forceinline__ float usable_logit(const T* row, int e) {
   return l < INFINITY ? l : -INFINITY;  // NaN too
 }
 
-// The choice in fp64; returns the expert of slot `lane`, or -1.
-template <typename T>
-__device__ __noinline__ int route_again(const RouteKernelArgs& a, const T* row, double* c, int lane) {
-  double m = 0, total = 1;
-  if (!a.sigmoid) {
+// What an expert is ranked by, in fp64.
+struct Exact {
+  double m = 0, total = 1;  // the softmax's largest logit and sum
+  template <typename T>
+  __device__ Exact(const RouteKernelArgs& a, const T* row, int lane) {
+    if (a.sigmoid) return;
     float top = -INFINITY;
     for (int e = lane; e < a.E; e += 32) top = fmaxf(top, usable_logit(row, e));
     m = warp_max_f32(top);
@@ -113,17 +133,77 @@ __device__ __noinline__ int route_again(const RouteKernelArgs& a, const T* row, 
     for (int e = lane; e < a.E; e += 32) sum += exp((double)usable_logit(row, e) - m);
     total = warp_sum_d(sum);
   }
-  __syncwarp();
-  for (int e = lane; e < a.E; e += 32) {
+  template <typename T>
+  __device__ double operator()(const RouteKernelArgs& a, const T* row, int e) const {
     const float l = usable_logit(row, e), b = a.bias ? a.bias[e] : 0.f;
     const double s = a.sigmoid ? 1 / (1 + exp(-(double)l)) : exp((double)l - m) / total;
-    c[e] = l == -INFINITY || !(fabsf(b) < INFINITY) ? -INFINITY : s + b;
+    return l == -INFINITY || !(fabsf(b) < INFINITY) ? -INFINITY : s + b;
   }
+};
+
+// The candidates of a token and its slots.
+struct Chosen {
+  float value[32], slot_value[33];
+  int expert[32], slot_expert[33];
+};
+
+// The candidates ranked in fp64, a lane each (an SM does two fp64 operations a
+// cycle: all experts would take a warp some 5 us); returns the expert of slot
+// `lane`, or -1.
+template <typename T>
+__device__ __noinline__ int rank_again(const RouteKernelArgs& a, const T* row, Chosen& ch, int found, int lane) {
+  const Exact exact(a, row, lane);
+  const int e = lane < found ? ch.expert[lane] : 0;
+  const double v = lane < found ? exact(a, row, e) : -INFINITY;
+  int before = 0;
+  for (int o = 0; o < found; ++o) {
+    const double x = __shfl_sync(0xffffffffu, v, o);
+    before += x > v || (x == v && o < lane);
+  }
+  __syncwarp();
+  if (lane < found && before < a.top_k) ch.slot_expert[before] = e;
+  __syncwarp();
+  return lane < min(found, a.top_k) ? ch.slot_expert[lane] : -1;
+}
+
+// The groups chosen in fp64, from the experts that may be among those that
+// count in their group, a lane each.
+template <typename T>
+__device__ __noinline__ uint32_t groups_again(const RouteKernelArgs& a, const T* row, const Chosen& ch, int found,
+                                              int lane) {
+  const Exact exact(a, row, lane);
+  const int e = lane < found ? ch.expert[lane] : 0, mine = lane < found ? e * a.group_magic >> 20 : -1;
+  const double v = lane < found ? exact(a, row, e) : -INFINITY;
+  double m0 = -INFINITY, m1 = -INFINITY;  // of group `lane`
+  for (int o = 0; o < found; ++o) {
+    const double x = __shfl_sync(0xffffffffu, v, o);
+    if (__shfl_sync(0xffffffffu, mine, o) == lane) {
+      m1 = larger(m1, smaller(m0, x));
+      m0 = larger(m0, x);
+    }
+  }
+  const double score = a.group_best == 2 && m1 != -INFINITY ? m0 + m1 : m0;
+  int before = 0;
+  for (int o = 0; o < a.n_groups; ++o) {
+    const double x = __shfl_sync(0xffffffffu, score, o);
+    before += x > score || (x == score && o < lane);
+  }
+  const bool in = lane < a.n_groups && before < a.top_groups;
+  const bool here = __shfl_sync(0xffffffffu, in, lane / a.group_lanes);
+  return __ballot_sync(0xffffffffu, here && lane % a.group_lanes == 0);
+}
+
+// The whole choice in fp64, groups too.
+template <typename T>
+__device__ __noinline__ int route_again(const RouteKernelArgs& a, const T* row, double* c, int lane) {
+  const Exact exact(a, row, lane);
+  __syncwarp();
+  for (int e = lane; e < a.E; e += 32) c[e] = exact(a, row, e);
   __syncwarp();
   uint32_t groups = 0xffffffffu;
   if (a.n_groups > 1) {
-    double gap;
-    groups = choose_groups(a, c, lane, gap);
+    double gap, least;
+    groups = choose_groups(a, c, lane, gap, least);
   }
   int mine = -1;
   for (int j = 0; j < a.top_k; ++j) {
@@ -143,18 +223,19 @@ __device__ __noinline__ int route_again(const RouteKernelArgs& a, const T* row, 
   return mine;
 }
 
+// The larger value; NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // 1 / (1 + exp(-l)) by the approximate power of two (4 eps) and reciprocal (2 eps).
 __device__ __forceinline__ float sigmoid_quick(float l) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
-}
-
-__device__ __forceinline__ float warp_max_redux(float v) {
-  float m;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
-  return m;
 }
 
 // The warp's values, largest in lane 0 (a bitonic sort).
@@ -169,44 +250,53 @@ __device__ __forceinline__ float sort_lanes(float v, int lane) {
   return v;
 }
 
-// The candidates and slots of a token.
-struct Chosen {
-  float value[32], slot_value[33];
-  int expert[32], slot_expert[33];
-};
-
 // VPL: experts a lane holds.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(kWarps * 32) k_route_topk(const __grid_constant__ RouteKernelArgs a) {
-  extern __shared__ double shared_c[];
+  extern __shared__ __align__(16) double shared_c[];
   __shared__ Chosen shared_chosen[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  double* exact_c = shared_c + warp * a.E;
+  double* exact_c = shared_c + warp * ((a.E + 1) & ~1);
   float* shared_f = reinterpret_cast<float*>(exact_c);
   Chosen& ch = shared_chosen[warp];
   pdl_wait();
-  float bias[VPL];
+  // Of this lane's experts: the bias (-inf: not available), and the bit of the group in the mask of the chosen.
+  float bias[VPL], widest = 0.f;
+  uint8_t group_bit[VPL];
+  bool bad_bias = false;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = lane + 32 * i;
     bias[i] = a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
+    if (fabsf(bias[i]) < INFINITY) {
+      widest = fmaxf(widest, fabsf(bias[i]));
+    } else {
+      bad_bias |= bias[i] != -INFINITY;
+      bias[i] = -INFINITY;
+    }
+    group_bit[i] = (uint8_t)(min(e, a.E - 1) * a.group_magic >> 20) * a.group_lanes;
   }
+  widest = warp_max_redux(widest);
+  if (bad_bias) set_status(a.status, kStatusRange);
   for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
     float c[VPL];  // the logits, then what is ranked; -inf: not available
-    bool odd = false;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = lane + 32 * i;
       c[i] = e < a.E ? to_f32(row[e]) : -INFINITY;
     }
-    float top = -INFINITY;
+    float top = c[0];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const bool usable = c[i] < INFINITY;
-      odd |= !usable;
-      c[i] = usable ? c[i] : -INFINITY;
-      top = fmaxf(top, c[i]);
+    for (int i = 1; i < VPL; ++i) top = max_nan(top, c[i]);
+    if (__any_sync(0xffffffffu, !(top < INFINITY))) {
+      if (!(top < INFINITY)) set_status(a.status, kStatusRange);
+      top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        c[i] = c[i] < INFINITY ? c[i] : -INFINITY;
+        top = fmaxf(top, c[i]);
+      }
     }
     float total = 1.f, largest = 1.f;  // the softmax's sum; the largest score
     if (!a.sigmoid && (!a.by_logit || !a.norm)) {
@@ -219,60 +309,69 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_topk(const __grid_constan
     }
     float bound = 0.f;
     if (!a.by_logit) {
-      float far = 0.f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        const float b = bias[i], l = c[i];
-        const bool usable = fabsf(b) < INFINITY;
-        odd |= !usable && b != -INFINITY && l != -INFINITY;
-        const float v = (a.sigmoid ? sigmoid_quick(l) : expf(l - top) * largest) + b;
-        c[i] = usable && l != -INFINITY ? v : -INFINITY;
-        far = fmaxf(far, c[i] == -INFINITY ? 0.f : fabsf(v));
+        const float v = (a.sigmoid ? sigmoid_quick(c[i]) : expf(c[i] - top) * largest) + bias[i];
+        c[i] = c[i] == -INFINITY ? -INFINITY : v;
       }
       // |error of s| <= 5 eps for the sigmoid: exp's 4 eps and its argument's 2 |l| eps count by s (1 - s), 1.5 in
       // all, then the sum's and the reciprocal's.  For the softmax (VPL + 18) eps of the largest s, from the
       // exponents (|l - top| eps, at most ln E in the mean of the sum), exp (2 eps), a lane's sum, the joins (5) and
-      // the two products.  The bias adds eps |c|.  Two values differ for sure beyond the sum of their bounds; half
-      // is added.
-      bound = 1.5f * kEps * (2.f * (a.sigmoid ? 5.f : (VPL + 18.f) * largest) + 2.f * warp_max_redux(far));
+      // the two products.  The bias adds eps |c|, |c| <= the largest s and bias.  Two values differ for sure beyond
+      // the sum of their bounds; half is added.
+      bound = 1.5f * kEps * (2.f * (a.sigmoid ? 5.f : (VPL + 18.f) * largest) + 2.f * (largest + widest));
     }
-    if (odd) set_status(a.status, kStatusRange);
-    bool again = false;
+    // experts that `in` takes, in order, into ch; their number (32 are kept)
+    const auto gather = [&](auto in) {
+      int found = 0;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const bool yes = in(i) && c[i] != -INFINITY;
+        const uint32_t mask = __ballot_sync(0xffffffffu, yes);
+        const int at = found + __popc(mask & ((1u << lane) - 1));
+        if (yes && at < 32) {
+          ch.value[at] = c[i];
+          ch.expert[at] = lane + 32 * i;
+        }
+        found += __popc(mask);
+      }
+      __syncwarp();
+      return found;
+    };
+    bool again = false, all_again = false;  // is the order in doubt; can only all experts in fp64 settle it
     if (a.n_groups > 1) {
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
         if (lane + 32 * i < a.E) shared_f[lane + 32 * i] = c[i];
       __syncwarp();
-      float gap;
-      const uint32_t groups = choose_groups(a, shared_f, lane, gap);
-      again = !a.by_logit && gap <= 3.f * bound;  // of sums of two values, which are rounded too
+      float gap, least;
+      uint32_t groups = choose_groups(a, shared_f, lane, gap, least);
+      if (!a.by_logit && gap <= 3.f * bound) {  // of sums of two values, which are rounded too
+        const int found =
+            gather([&](int i) { return c[i] >= __shfl_sync(0xffffffffu, least, group_bit[i]) - bound; });
+        if (found <= 32)
+          groups = groups_again(a, row, ch, found, lane);
+        else
+          all_again = true;
+      }
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (!in_groups(a, groups, lane + 32 * i)) c[i] = -INFINITY;
+        c[i] = groups >> group_bit[i] & 1 ? c[i] : -INFINITY;
     }
     float most = c[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i) most = fmaxf(most, c[i]);
-    const float from = a.top_k < 32 ? __shfl_sync(0xffffffffu, sort_lanes(most, lane), a.top_k & 31) : -INFINITY;
-    int found = 0;  // candidates, in the order of the experts
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const bool in = c[i] >= from && c[i] != -INFINITY;
-      const uint32_t mask = __ballot_sync(0xffffffffu, in);
-      const int at = found + __popc(mask & ((1u << lane) - 1));
-      if (in && at < 32) {
-        ch.value[at] = c[i];
-        ch.expert[at] = lane + 32 * i;
-      }
-      found += __popc(mask);
-    }
-    __syncwarp();
+    // from the (k+1)-th on, and those that may be its equals (bound is 0 where logits are ranked)
+    const float from =
+        a.top_k < 32 ? __shfl_sync(0xffffffffu, sort_lanes(most, lane), a.top_k & 31) - bound : -INFINITY;
+    const int found = gather([&](int i) { return c[i] >= from; });
     int mine = -1;  // slot j's expert stays with lane j
     if (found <= 32) {
       const float v = lane < found ? ch.value[lane] : -INFINITY;
       int before = 0;
+#pragma unroll 4
       for (int o = 0; o < found; ++o) {
         const float x = __shfl_sync(0xffffffffu, v, o);
         before += x > v || (x == v && o < lane);
@@ -309,16 +408,19 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_topk(const __grid_constan
         }
       }
     }
-    if (again) mine = route_again(a, row, exact_c, lane);
+    if (all_again || (again && found > 32))
+      mine = route_again(a, row, exact_c, lane);
+    else if (again)
+      mine = rank_again(a, row, ch, found, lane);
     if (lane >= a.top_k) mine = -1;
     // weights relative to the largest chosen score, so that scores below fp32's range keep their ratios
     float s = 0.f;
     const float z = mine >= 0 ? usable_logit(row, mine) : -INFINITY;
     if (a.norm) {
       const float n = a.sigmoid ? fminf(z, 0.f) : z, high = warp_max_redux(n);
-      if (mine >= 0) s = expf(n - high) / (a.sigmoid ? 1.f + expf(-fabsf(z)) : 1.f);
+      if (mine >= 0) s = a.sigmoid ? __fdividef(expf(n - high), 1.f + expf(-fabsf(z))) : expf(n - high);
       const float sum = warp_sum_f32(s);
-      s = sum > 0.f ? s * a.scale / sum : 0.f;
+      s = sum > 0.f ? __fdividef(s * a.scale, sum) : 0.f;
     } else if (mine >= 0) {
       s = a.scale * (a.sigmoid ? sigmoid(z) : expf(z - top) * largest);
     }
@@ -417,6 +519,7 @@ RouteKernelArgs kernel_args(const TrainDevice& d, const ftmoe_route_args& r) {
   a.group_magic = (uint32_t)(((1 << 20) + a.group_size - 1) / a.group_size);
   a.group_lanes = 32;
   while (a.group_lanes * a.n_groups > 32) a.group_lanes >>= 1;
+  a.group_quads = a.group_size % (4 * a.group_lanes) == 0;
   a.by_logit = !r.bias && (r.n_groups == 1 || r.group_best == 1);
   a.idx = r.topk_idx;
   a.w = r.topk_w;
@@ -439,7 +542,7 @@ cudaError_t launch_route_topk(const TrainDevice& d, const ftmoe_route_args& r, c
     auto* k = per <= 1 ? k_route_topk<T, 1> : per <= 2 ? k_route_topk<T, 2> : per <= 4 ? k_route_topk<T, 4>
               : per <= 8 ? k_route_topk<T, 8> : per <= 16 ? k_route_topk<T, 16> : k_route_topk<T, 32>;
     // 32 KB at E = 1024: within what a kernel has without asking
-    return launch_after_smem(k, route_grid(d, r.T), kWarps * 32, kWarps * r.E * sizeof(double), s, a);
+    return launch_after_smem(k, route_grid(d, r.T), kWarps * 32, kWarps * ((r.E + 1) & ~1) * sizeof(double), s, a);
   });
 }
 

@@ -524,6 +524,31 @@ def test_route_values_closer_than_fp32(score):
     check_route(logits, 4, score, bias=bias, groups=(8, 4, 2))
 
 
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_groups_closer_than_fp32(score, best):
+    """Groups whose worth differs by one fp32 step of one logit, or not at all, and tokens of which all values do."""
+    g = gen(66)
+    T, E, G = 200, 96, 8
+    logits = randn(g, T, E)
+    z = logits.view(T, G, E // G)
+    for t in range(T):
+        z[t, (3 * t + 1) % G] = z[t, t % G]  # the same values, in another order
+        z[t, (3 * t + 1) % G] = z[t, (3 * t + 1) % G].flip(0)
+        if t % 3:
+            at = int(z[t, t % G].argmax())
+            z[t, t % G, at] = torch.nextafter(z[t, t % G, at].cpu(), torch.tensor(9.0 if t % 2 else -9.0)).to(DEV)
+    bias = torch.full((E,), 0.375, device=DEV)
+    check_route(logits, 5, score, bias=bias, groups=(G, 4, best))
+    check_route(logits, 5, score, bias=bias, groups=(G, 1, best))
+    steps = torch.randint(0, 4, (40, E), generator=g, device=DEV).int()
+    near = (torch.full((40, E), 1.25, device=DEV).view(torch.int32) + steps).view(FP32)  # up to three steps apart
+    check_route(near, 5, score, bias=bias, groups=(G, 4, best))
+    check_route(near, 5, score, bias=bias)
+    check_route(near, 32, score, bias=bias)
+    check_route(near, 5, score)
+
+
 def test_route_masked_and_bad_logits():
     inf, nan = math.inf, math.nan
     z = torch.full((6, 8), -inf, device=DEV)
