@@ -636,18 +636,29 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
 
 // The pair's forms: loads that complete on the first CTA's barrier, MMAs over
 // both CTAs' operands and tensor memories, commits that arrive in both.
+//
+// A whole warp runs each with the same operands, and one lane, always the
+// same, is elected inside.  The operands so stay in uniform registers: four
+// MMAs take 67 cycles to issue; from a branch of one lane, which the compiler
+// cannot know to be uniform, they took 208.
+#define FTMOE_ELECTED(instruction) "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n" instruction "}\n"
+__device__ __forceinline__ void many_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile(FTMOE_ELECTED("@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n") ::"r"(smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
 template <int CTAS>
 __device__ __forceinline__ void many_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   if (CTAS == 1)
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(smem_u32(dst)),
+        FTMOE_ELECTED("@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                      "[%1, {%2, %3}], [%4];\n") ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
   else
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        FTMOE_ELECTED("@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                      "[%0], [%1, {%2, %3}], [%4];\n") ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
@@ -655,14 +666,14 @@ template <int CTAS>
 __device__ __forceinline__ void many_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   if (CTAS == 1)
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(smem_u32(dst)),
+        FTMOE_ELECTED("@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                      "[%1, {%2, %3, %4}], [%5];\n") ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
   else
     asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        FTMOE_ELECTED("@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                      "[%0], [%1, {%2, %3, %4}], [%5];\n") ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
@@ -670,23 +681,28 @@ template <int CTAS>
 __device__ __forceinline__ void many_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accumulate) {
   if (CTAS == 1)
-    tc_mma_e4m3(d, adesc, bdesc, idesc, accumulate);
+    asm volatile(FTMOE_ELECTED("setp.ne.b32 p, %4, 0;\n"
+                               " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n") ::"r"(d),
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
   else
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
+    asm volatile(FTMOE_ELECTED("setp.ne.b32 p, %4, 0;\n"
+                               " @q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n") ::"r"(d),
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
 }
+// `both`: in both CTAs of a pair.
 template <int CTAS>
-__device__ __forceinline__ void many_commit(uint64_t* bar) {
+__device__ __forceinline__ void many_commit(uint64_t* bar, bool both = true) {
   if (CTAS == 1)
-    tc_commit(bar);
+    asm volatile(FTMOE_ELECTED(
+                     "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n") ::"r"(smem_u32(bar))
+                 : "memory");
   else
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"((uint16_t)3)
+        FTMOE_ELECTED("@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+                      "[%0], %1;\n") ::"r"(smem_u32(bar)),
+        "h"((uint16_t)(both ? 3 : 1))
         : "memory");
 }
 template <int CTAS>
@@ -842,21 +858,21 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 
   if (warp < kEpiWarp0) {
     regs_down<kLowRegs>();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ---------------- copies
       int s = 0, k = 0;
       uint32_t phase = 1;
       for (int u = worker; u < n_units && !*abort_flag; u += workers) {
         const Unit x = unit(u);
         for (int kb = 0; kb < nkb; ++kb, ++k) {
-          if (!wait(&empty[s], phase, a.status)) {
+          if (!warp_wait(&empty[s], phase, a.status)) {
             *abort_flag = 1;
             break;
           }
           unsigned char* sa = sm + s * F::kStageBytes;
           unsigned char* sb = sa + F::kABytes;
           const uint32_t bar = CTAS == 2 ? at_rank(&full[s], 0) : smem_u32(&full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], CTAS * F::kStageBytes);
+          if (rank == 0) many_expect(&full[s], CTAS * F::kStageBytes);
           many_load_2d<CTAS>(sa, &map_x, kb * 128, x.row0, bar);
 #pragma unroll
           for (int h = 0; h < 2 / CTAS; ++h) {
@@ -876,7 +892,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       // nothing this warp issued may still be landing when the CTA exits (the pair's second CTA waits for the first)
       if (rank == 0)
         for (int q = k > kStages ? k - kStages : 0; q < k; ++q) mbar_wait(&full[q % kStages], (q / kStages) & 1, a.status);
-    } else if ((warp == 1 || warp == 3) && lane == 0 && rank == 0) {
+    } else if ((warp == 1 || warp == 3) && rank == 0) {
       // ---------------- products: warp 1 has the even blocks, warp 3 the odd ones.  Issuing waits while the tensor
       // cores are behind, and what comes between two blocks (the commits, the waits for the next one's buffers) is
       // longer than what they then still have to do; so one warp issues while the other one waits.
@@ -894,7 +910,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       for (int u = worker; ok && u < n_units && !*abort_flag; u += workers) {
         int kb = first;
         for (; kb < nkb; kb += 2) {
-          if (!wait(&acc_empty[b], acc_phase, a.status) || !wait(&full[s], full_phase, a.status)) {
+          if (!warp_wait(&acc_empty[b], acc_phase, a.status) || !warp_wait(&full[s], full_phase, a.status)) {
             *abort_flag = 1;
             ok = false;
             break;
@@ -920,11 +936,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
         first = kb - nkb;  // 0 or 1: the blocks of all units are counted on
       }
-      if (CTAS == 1)
-        tc_commit(drain);
-      else
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
-                     : "memory");
+      many_commit<CTAS>(drain, false);
       mbar_wait(drain, 0, a.status);
     }
   } else {
