@@ -80,13 +80,42 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_by_column
          | ((b_by_columns ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void tc_mma_e4m3(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// What the copying and the issuing warps do.  The whole warp runs each with
+// the same operands, and one lane, always the same, is elected inside: the
+// operands so stay in uniform registers.  Four MMAs take 67 cycles to issue;
+// from a branch of one lane, which the compiler cannot know to be uniform,
+// they took 208.
+#define FTMOE_ELECTED(instruction) "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n" instruction "}\n"
+__device__ __forceinline__ void elected_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile(FTMOE_ELECTED("@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n") ::"r"(smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void elected_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      FTMOE_ELECTED("@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                    "[%1, {%2, %3}], [%4];\n") ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
+}
+__device__ __forceinline__ void elected_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      FTMOE_ELECTED("@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                    "[%1, {%2, %3, %4}], [%5];\n") ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void elected_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(FTMOE_ELECTED("setp.ne.b32 p, %4, 0;\n"
+                             " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n") ::"r"(d),
+               "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+               : "memory");
+}
+__device__ __forceinline__ void elected_commit(uint64_t* bar) {
+  asm volatile(FTMOE_ELECTED("@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n") ::"r"(
+                   smem_u32(bar))
+               : "memory");
 }
 
 template <int N>
@@ -298,7 +327,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int n_units = t_first[a.E];
 
   if (warp < kEpiWarp0) {
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ---------------- copies
       int k = 0;
       for (int u = blockIdx.x; u < n_units && !*abort_flag; u += gridDim.x) {
@@ -306,26 +335,26 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const int boxes = (x.N + F::kBox - 1) / F::kBox;
         for (int kb = 0; kb < nkb; ++kb, ++k) {
           const int s = k % kStages;
-          if (k >= kStages && !wait(&empty[s], (k / kStages - 1) & 1, a.status)) {
+          if (k >= kStages && !warp_wait(&empty[s], (k / kStages - 1) & 1, a.status)) {
             *abort_flag = 1;
             break;
           }
           unsigned char* sa = sm + s * F::kStageBytes;
           unsigned char* sb = sa + F::kABytes;
-          mbar_arrive_expect_tx(&full[s], F::kABytes + boxes * F::kBox * 128);
+          elected_expect(&full[s], F::kABytes + boxes * F::kBox * 128);
           if (TRANS) {
-            tma_load_3d(sa, &map_w, x.jt * 128, kb * 128, x.e, &full[s]);
+            elected_load_3d(sa, &map_w, x.jt * 128, kb * 128, x.e, &full[s]);
           } else {
-            tma_load_3d(sa, &map_w, kb * 128, x.jt * 128, x.e, &full[s]);
-            if (SWIGLU) tma_load_3d(sa + kTile, &map_w, kb * 128, a.O + x.jt * 128, x.e, &full[s]);
+            elected_load_3d(sa, &map_w, kb * 128, x.jt * 128, x.e, &full[s]);
+            if (SWIGLU) elected_load_3d(sa + kTile, &map_w, kb * 128, a.O + x.jt * 128, x.e, &full[s]);
           }
           for (int b = 0; b < boxes; ++b)
-            tma_load_2d(sb + b * F::kBox * 128, &map_x, kb * 128, x.row0 + b * F::kBox, &full[s]);
+            elected_load_2d(sb + b * F::kBox * 128, &map_x, kb * 128, x.row0 + b * F::kBox, &full[s]);
         }
       }
       // nothing this warp issued may still be landing when the CTA exits
       for (int q = k > kStages ? k - kStages : 0; q < k; ++q) mbar_wait(&full[q % kStages], (q / kStages) & 1, a.status);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ---------------- products
       int k = 0;
       bool ok = true;
@@ -334,8 +363,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const uint32_t idesc = idesc_e4m3(128, x.N, TRANS, false);
         for (int kb = 0; kb < nkb; ++kb, ++k) {
           const int s = k % kStages, b = k % kBufs;
-          if ((k >= kBufs && !wait(&acc_empty[b], (k / kBufs - 1) & 1, a.status)) ||
-              !wait(&full[s], (k / kStages) & 1, a.status)) {
+          if ((k >= kBufs && !warp_wait(&acc_empty[b], (k / kBufs - 1) & 1, a.status)) ||
+              !warp_wait(&full[s], (k / kStages) & 1, a.status)) {
             *abort_flag = 1;
             ok = false;
             break;
@@ -345,17 +374,19 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           const uint64_t adesc = sdesc_k_sw128(sa), bdesc = sdesc_k_sw128(sa + F::kABytes);
           const int steps = (min(128, a.C - kb * 128) + 31) / 32;
           const uint32_t d = tmem + b * F::kCols;
-          for (int i = 0; i < steps; ++i) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i >= steps) break;
             // 32 contracted values: 32 bytes on within the swizzled rows, or 32 rows on
             const uint64_t on = TRANS ? i * (32 * 128 >> 4) : i * (32 >> 4);
-            tc_mma_e4m3(d, adesc + on, bdesc + i * (32 >> 4), idesc, i != 0);
-            if (SWIGLU) tc_mma_e4m3(d + NMAX, adesc + on + (kTile >> 4), bdesc + i * (32 >> 4), idesc, i != 0);
+            elected_mma(d, adesc + on, bdesc + i * (32 >> 4), idesc, i != 0);
+            if (SWIGLU) elected_mma(d + NMAX, adesc + on + (kTile >> 4), bdesc + i * (32 >> 4), idesc, i != 0);
           }
-          tc_commit(&empty[s]);
-          tc_commit(&acc_full[b]);
+          elected_commit(&empty[s]);
+          elected_commit(&acc_full[b]);
         }
       }
-      tc_commit(drain);
+      elected_commit(drain);
       mbar_wait(drain, 0, a.status);
     } else if (warp == 2) {
       // ---------------- scales: the block's sx sw of each token
@@ -593,135 +624,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
 // ---------------------------------------------------------------- many tokens
 
-// Tiles of 128 tokens a CTA (the MMA's rows) and 256 weight rows (gate's 128
-// and the matching up's 128 with SwiGLU).  A lane of tensor memory is a token,
-// so a thread's scale of a block is one number for all its columns, and no
-// scales pass through shared memory.
-//
-// CTAS = 2: a pair of CTAs makes one MMA of 256 tokens, each CTA with its own
-// 128 and half of the weight rows, which the tensor cores of both read.  A
-// CTA's shared memory so takes in and gives out 32 KB a block instead of 48
-// for the same products.
-template <int CTAS>
+// Tiles of 128 tokens (the MMA's rows) and 256 weight rows (gate's 128 and the
+// matching up's 128 with SwiGLU).  A lane of tensor memory is a token, so a
+// thread's scale of a block is one number for all its columns, and no scales
+// pass through shared memory.
 struct Many {
-  static constexpr int kTokens = 128 * CTAS;
-  static constexpr int kABytes = kTile, kBBytes = 2 * kTile / CTAS;
-  static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kBufs = 2, kCols = 256;  // a warp that issues MMAs has a buffer
+  static constexpr int kTokens = 128;
+  static constexpr int kABytes = kTile, kBBytes = 2 * kTile, kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = 4, kBufs = 2, kCols = 256;  // a warp that issues MMAs has a buffer
+  static constexpr int kWarpOut = 2048, kOut = kManyWarps * kWarpOut;  // staging: 32 tokens' 64 bytes
   static constexpr int kTops = 128 * 2 * 4;  // a token's largest magnitude in each warpgroup
-  static constexpr int kStages = CTAS == 2 ? 6 : 4;
-  static constexpr int smem(int E) { return 1024 + kStages * kStageBytes + kTops + 512 + 3 * 4 * (E + 1); }
-  static_assert(1024 + kStages * kStageBytes + kTops + 512 + 3 * 4 * (kMaxBins + 1) <= kSmemMax, "");
+  static constexpr int kFixed = kOut + kTops;
+  static constexpr int smem(int E) { return 1024 + kStages * kStageBytes + kFixed + 512 + 3 * 4 * (E + 1); }
+  static_assert(1024 + kStages * kStageBytes + kFixed + 512 + 3 * 4 * (kMaxBins + 1) <= kSmemMax, "");
 };
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-}
-// The address of `p`'s counterpart in the cluster's CTA `rank`.
-__device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
-  // the default scope: at .cluster the arrival took some 1000 cycles, and only reads of tensor memory, which are
-  // over, go before it
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// The pair's forms: loads that complete on the first CTA's barrier, MMAs over
-// both CTAs' operands and tensor memories, commits that arrive in both.
-//
-// A whole warp runs each with the same operands, and one lane, always the
-// same, is elected inside.  The operands so stay in uniform registers: four
-// MMAs take 67 cycles to issue; from a branch of one lane, which the compiler
-// cannot know to be uniform, they took 208.
-#define FTMOE_ELECTED(instruction) "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n" instruction "}\n"
-__device__ __forceinline__ void many_expect(uint64_t* bar, uint32_t bytes) {
-  asm volatile(FTMOE_ELECTED("@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n") ::"r"(smem_u32(bar)),
-               "r"(bytes)
-               : "memory");
-}
-template <int CTAS>
-__device__ __forceinline__ void many_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  if (CTAS == 1)
-    asm volatile(
-        FTMOE_ELECTED("@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-                      "[%1, {%2, %3}], [%4];\n") ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        FTMOE_ELECTED("@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                      "[%0], [%1, {%2, %3}], [%4];\n") ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-template <int CTAS>
-__device__ __forceinline__ void many_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-  if (CTAS == 1)
-    asm volatile(
-        FTMOE_ELECTED("@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-                      "[%1, {%2, %3, %4}], [%5];\n") ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        FTMOE_ELECTED("@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                      "[%0], [%1, {%2, %3, %4}], [%5];\n") ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-template <int CTAS>
-__device__ __forceinline__ void many_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t accumulate) {
-  if (CTAS == 1)
-    asm volatile(FTMOE_ELECTED("setp.ne.b32 p, %4, 0;\n"
-                               " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n") ::"r"(d),
-                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-                 : "memory");
-  else
-    asm volatile(FTMOE_ELECTED("setp.ne.b32 p, %4, 0;\n"
-                               " @q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n") ::"r"(d),
-                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-                 : "memory");
-}
-// `both`: in both CTAs of a pair.
-template <int CTAS>
-__device__ __forceinline__ void many_commit(uint64_t* bar, bool both = true) {
-  if (CTAS == 1)
-    asm volatile(FTMOE_ELECTED(
-                     "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n") ::"r"(smem_u32(bar))
-                 : "memory");
-  else
-    asm volatile(
-        FTMOE_ELECTED("@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-                      "[%0], %1;\n") ::"r"(smem_u32(bar)),
-        "h"((uint16_t)(both ? 3 : 1))
-        : "memory");
-}
-template <int CTAS>
-__device__ __forceinline__ void many_alloc(uint32_t* dst, uint32_t cols) {
-  if (CTAS == 1) {
-    tmem_alloc(dst, cols);
-    return;
-  }
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-template <int CTAS>
-__device__ __forceinline__ void many_dealloc(uint32_t taddr, uint32_t cols) {
-  if (CTAS == 1)
-    tmem_dealloc(taddr, cols);
-  else
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
-}
 
 // g / (1 + exp(-g)) by the approximate power of two and reciprocal: within (|g| + 8) 2^-24 of it, while the code that h
 // gets is rounded by up to 2^-4.  (The precise forms made a tile's end 9700 cycles long instead of some 3000.)
@@ -749,62 +665,84 @@ __device__ __forceinline__ void store_32(void* p, const uint32_t (&v)[8]) {
                : "memory");
 }
 
-// Columns [c0, c0 + N) of a token's row.
-template <int N>
-__device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int c0, const float* v) {
-  const int64_t at = row * a.O + c0;
-  if (a.dtype != FTMOE_FP32) {
-    uint16_t* out = static_cast<uint16_t*>(a.out) + at;
-    if (c0 + N <= a.O && a.O % 16 == 0 && ((uintptr_t)out & 31) == 0) {
+// A warp's sums, lane l those of token l in the columns c0 .. c0 + 127, to the
+// rows from `row` on, `rows` of them.  Whole pieces of 32 bytes go straight
+// from a lane to its token's row.  Otherwise 64 bytes of every token at a time
+// pass through shared memory (`st`), so that a store covers up to eight rows'
+// 64 bytes and not 32 rows' few (a product of 666 fp32 columns 60 -> 36 us).
+template <bool WIDE>
+__device__ __forceinline__ void store_tile(const MatmulArgs& a, unsigned char* st, int64_t row, int rows, int c0,
+                                           const float (&acc)[128], int lane) {
+  const int bytes = WIDE ? 4 : 2;
+  constexpr int kCols = WIDE ? 16 : 32;
+  unsigned char* out = static_cast<unsigned char*>(a.out) + (row * a.O + c0) * bytes;
+  const int64_t pitch = (int64_t)a.O * bytes;
+  if (!WIDE && pitch % 32 == 0 && ((uintptr_t)a.out & 31) == 0 && c0 + 128 <= a.O) {
+    if (lane < rows) {
 #pragma unroll
-      for (int i = 0; i < N; i += 16) {
+      for (int i = 0; i < 128; i += 16) {
         uint32_t p[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = halves(v[i + 2 * j], v[i + 2 * j + 1], a.dtype);
-        store_32(out + i, p);
-      }
-      return;
-    }
-    const bool wide = a.O % 8 == 0;
-#pragma unroll
-    for (int i = 0; i < N; i += 8) {
-      uint32_t p[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = halves(v[i + 2 * j], v[i + 2 * j + 1], a.dtype);
-      if (wide) {
-        if (c0 + i < a.O) *reinterpret_cast<uint4*>(out + i) = make_uint4(p[0], p[1], p[2], p[3]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c0 + i + j < a.O) out[i + j] = (uint16_t)(p[j / 2] >> (j % 2 * 16));
+        for (int j = 0; j < 8; ++j) p[j] = halves(acc[i + 2 * j], acc[i + 2 * j + 1], a.dtype);
+        store_32(out + lane * pitch + i * bytes, p);
       }
     }
     return;
   }
-  float* out = static_cast<float*>(a.out) + at;
-  const bool wide = a.O % 4 == 0;
+  const bool aligned = pitch % 16 == 0;
 #pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    if (wide) {
-      if (c0 + i < a.O) *reinterpret_cast<float4*>(out + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  for (int p = 0; p < 128 / kCols; ++p) {
+    const int left = (a.O - c0 - p * kCols) * bytes;  // bytes of the row from this piece on
+    if (left <= 0) continue;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float* v = acc + p * kCols + i * (kCols / 4);
+      uint4 w;
+      if constexpr (WIDE)
+        w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+      else
+        w = make_uint4(halves(v[0], v[1], a.dtype), halves(v[2], v[3], a.dtype), halves(v[4], v[5], a.dtype),
+                       halves(v[6], v[7], a.dtype));
+      // the 16-byte pieces of a row turned by the token, against bank conflicts
+      *reinterpret_cast<uint4*>(st + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) = w;
+    }
+    __syncwarp();
+    if (aligned) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int token = 8 * i + lane / 4, piece = lane & 3;
+        if (token < rows && piece * 16 < left)
+          *reinterpret_cast<uint4*>(out + token * pitch + p * 64 + piece * 16) =
+              *reinterpret_cast<const uint4*>(st + token * 64 + ((piece ^ (token >> 1 & 3)) << 4));
+      }
     } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (c0 + i + j < a.O) out[i + j] = v[i + j];
+      const int at = lane % kCols * bytes;
+      if (at < left) {
+        for (int token = lane / kCols; token < rows; token += 32 / kCols) {
+          const unsigned char* from = st + token * 64 + (((at >> 4) ^ (token >> 1 & 3)) << 4) + (at & 15);
+          unsigned char* to = out + token * pitch + p * 64 + at;
+          if constexpr (WIDE)
+            *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from);
+          else
+            *reinterpret_cast<uint16_t*>(to) = *reinterpret_cast<const uint16_t*>(from);
+        }
+      }
     }
   }
 }
 
-template <int CTAS, bool SWIGLU, bool TRANS>
+template <bool SWIGLU, bool TRANS>
 __global__ void __launch_bounds__(kManyThreads, 1)
     k_fp8_matmul_many(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_w,
                       const __grid_constant__ CUtensorMap map_x) {
-  using F = Many<CTAS>;
+  using F = Many;
   constexpr int kStages = F::kStages, kBufs = F::kBufs;
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
-  uint32_t* tops = reinterpret_cast<uint32_t*>(sm + kStages * F::kStageBytes);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kStages * F::kStageBytes + F::kTops);
+  unsigned char* staged = sm + kStages * F::kStageBytes;
+  uint32_t* tops = reinterpret_cast<uint32_t*>(staged + F::kOut);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staged + F::kFixed);
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + kBufs;
@@ -812,12 +750,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   uint64_t* row_bar = drain + 1;  // [4], the warps that hold the same tokens
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(row_bar + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* t_start = reinterpret_cast<int*>(sm + kStages * F::kStageBytes + F::kTops + 512);
+  int* t_start = reinterpret_cast<int*>(staged + F::kFixed + 512);
   int *t_count = t_start + a.E, *t_first = t_count + a.E;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nkb = (a.C + 127) / 128;
-  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
-  const int worker = blockIdx.x / CTAS, workers = gridDim.x / CTAS;
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -826,7 +762,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     }
     for (int b = 0; b < kBufs; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], CTAS * kManyWarps);
+      mbar_init(&acc_empty[b], kManyWarps);
     }
     mbar_init(drain, 2);
     for (int w = 0; w < 4; ++w) mbar_init(&row_bar[w], kManyWarps / 4);
@@ -835,11 +771,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     tma_prefetch_desc(&map_w);
     tma_prefetch_desc(&map_x);
   }
-  if (warp == 1) many_alloc<CTAS>(tmem_slot, kBufs * F::kCols);
+  if (warp == 1) tmem_alloc(tmem_slot, kBufs * F::kCols);
   pdl_wait();
   make_tables<F::kTokens>(a, t_start, t_count, t_first);
   tc_fence_before();
-  if (CTAS == 2) cluster_sync(); else __syncthreads();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Tables tables{t_start, t_count, t_first, a.E};
@@ -849,10 +785,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     Unit x;
     x.e = e;
     x.jt = r / tiles;
-    const int at = (r - x.jt * tiles) * F::kTokens + (int)rank * 128;  // this CTA's tokens
+    const int at = (r - x.jt * tiles) * F::kTokens;
     x.row0 = t_start[e] + at;
-    x.rows = min(128, n - at);  // none (or fewer than none) in a pair's second CTA, maybe
-    x.N = 256;
+    x.rows = min(F::kTokens, n - at);
+    x.N = F::kCols;
     return x;
   };
 
@@ -862,7 +798,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       // ---------------- copies
       int s = 0, k = 0;
       uint32_t phase = 1;
-      for (int u = worker; u < n_units && !*abort_flag; u += workers) {
+      for (int u = blockIdx.x; u < n_units && !*abort_flag; u += gridDim.x) {
         const Unit x = unit(u);
         for (int kb = 0; kb < nkb; ++kb, ++k) {
           if (!warp_wait(&empty[s], phase, a.status)) {
@@ -871,17 +807,15 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           }
           unsigned char* sa = sm + s * F::kStageBytes;
           unsigned char* sb = sa + F::kABytes;
-          const uint32_t bar = CTAS == 2 ? at_rank(&full[s], 0) : smem_u32(&full[s]);
-          if (rank == 0) many_expect(&full[s], CTAS * F::kStageBytes);
-          many_load_2d<CTAS>(sa, &map_x, kb * 128, x.row0, bar);
+          elected_expect(&full[s], F::kStageBytes);
+          elected_load_2d(sa, &map_x, kb * 128, x.row0, &full[s]);
 #pragma unroll
-          for (int h = 0; h < 2 / CTAS; ++h) {
-            const int half = CTAS == 2 ? (int)rank : h;  // of the weight rows
-            const int n0 = SWIGLU ? half * a.O + x.jt * 128 : x.jt * 256 + half * 128;
+          for (int h = 0; h < 2; ++h) {
+            const int n0 = SWIGLU ? h * a.O + x.jt * 128 : x.jt * 256 + h * 128;
             if (TRANS)
-              many_load_3d<CTAS>(sb + h * kTile, &map_w, n0, kb * 128, x.e, bar);
+              elected_load_3d(sb + h * kTile, &map_w, n0, kb * 128, x.e, &full[s]);
             else
-              many_load_3d<CTAS>(sb + h * kTile, &map_w, kb * 128, n0, x.e, bar);
+              elected_load_3d(sb + h * kTile, &map_w, kb * 128, n0, x.e, &full[s]);
           }
           if (++s == kStages) {
             s = 0;
@@ -889,15 +823,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           }
         }
       }
-      // nothing this warp issued may still be landing when the CTA exits (the pair's second CTA waits for the first)
-      if (rank == 0)
-        for (int q = k > kStages ? k - kStages : 0; q < k; ++q) mbar_wait(&full[q % kStages], (q / kStages) & 1, a.status);
-    } else if ((warp == 1 || warp == 3) && rank == 0) {
+      // nothing this warp issued may still be landing when the CTA exits
+      for (int q = k > kStages ? k - kStages : 0; q < k; ++q) mbar_wait(&full[q % kStages], (q / kStages) & 1, a.status);
+    } else if (warp == 1 || warp == 3) {
       // ---------------- products: warp 1 has the even blocks, warp 3 the odd ones.  Issuing waits while the tensor
       // cores are behind, and what comes between two blocks (the commits, the waits for the next one's buffers) is
       // longer than what they then still have to do; so one warp issues while the other one waits.
       // Few instructions matter here: the summing warps leave few issue slots.
-      constexpr uint32_t idesc = idesc_e4m3(F::kTokens, TRANS && CTAS == 1 ? 128 : 256, false, TRANS);
+      constexpr uint32_t idesc = idesc_e4m3(F::kTokens, TRANS ? 128 : 256, false, TRANS);
       static_assert(kStages % 2 == 0, "a warp has every other stage");
       // 32 contracted values: 32 bytes on within the swizzled rows, or 32 rows on
       constexpr uint64_t kStepA = 32 >> 4, kStepB = TRANS ? 32 * 128 >> 4 : 32 >> 4;
@@ -907,7 +840,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       int s = b, first = b;  // the stage; this warp's first block of the unit
       uint32_t full_phase = 0, acc_phase = 1;  // a new barrier's phase 1 counts as over
       bool ok = true;
-      for (int u = worker; ok && u < n_units && !*abort_flag; u += workers) {
+      for (int u = blockIdx.x; ok && u < n_units && !*abort_flag; u += gridDim.x) {
         int kb = first;
         for (; kb < nkb; kb += 2) {
           if (!warp_wait(&acc_empty[b], acc_phase, a.status) || !warp_wait(&full[s], full_phase, a.status)) {
@@ -921,12 +854,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (i >= steps) break;
-            many_mma<CTAS>(d, adesc + i * kStepA, bdesc + i * kStepB, idesc, i != 0);
-            if (TRANS && CTAS == 1)
-              many_mma<CTAS>(d + 128, adesc + i * kStepA, bdesc + i * kStepB + (kTile >> 4), idesc, i != 0);
+            elected_mma(d, adesc + i * kStepA, bdesc + i * kStepB, idesc, i != 0);
+            if (TRANS)  // rows of 128 bytes hold 128 columns
+              elected_mma(d + 128, adesc + i * kStepA, bdesc + i * kStepB + (kTile >> 4), idesc, i != 0);
           }
-          many_commit<CTAS>(&acc_full[b]);
-          many_commit<CTAS>(&empty[s]);
+          elected_commit(&acc_full[b]);
+          elected_commit(&empty[s]);
           acc_phase ^= 1;
           s += 2;
           if (s >= kStages) {
@@ -936,7 +869,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
         first = kb - nkb;  // 0 or 1: the blocks of all units are counted on
       }
-      many_commit<CTAS>(drain, false);
+      elected_commit(drain);
       mbar_wait(drain, 0, a.status);
     }
   } else {
@@ -948,7 +881,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     int k = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int u = worker; ok && u < n_units && !*abort_flag; u += workers) {
+    for (int u = blockIdx.x; ok && u < n_units && !*abort_flag; u += gridDim.x) {
       const Unit x = unit(u);
       const int token = 32 * q + lane;
       const bool on = token < x.rows;
@@ -995,9 +928,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           if (h == 7) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-              if (CTAS == 2) mbar_arrive_at(at_rank(&acc_empty[b], 0)); else mbar_arrive(&acc_empty[b]);
-            }
+            if (lane == 0) mbar_arrive(&acc_empty[b]);
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -1011,7 +942,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       for (int i = 0; i < 64; ++i) unpack2(acc2[i], acc[2 * i], acc[2 * i + 1]);
       if constexpr (!SWIGLU) {
         const int c0 = x.jt * 256 + 128 * wg;
-        if (on && c0 < a.O) store_row<128>(a, x.row0 + token, c0, acc);
+        const int rows = min(32, x.rows - 32 * q);
+        unsigned char* st = staged + (warp - kEpiWarp0) * F::kWarpOut;
+        if (a.dtype == FTMOE_FP32)
+          store_tile<true>(a, st, x.row0 + 32 * q, rows, c0, acc, lane);
+        else
+          store_tile<false>(a, st, x.row0 + 32 * q, rows, c0, acc, lane);
       } else {
         // a token's 128 values of h lie in the two warps of its rows
         uint32_t best = 0;
@@ -1057,12 +993,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     }
   }
   tc_fence_before();
-  // the pair leaves together: neither may signal into a CTA that is gone
   __syncthreads();
-  if (CTAS == 2) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    many_dealloc<CTAS>(tmem, kBufs * F::kCols);
+    tmem_dealloc(tmem, kBufs * F::kCols);
   }
 }
 
@@ -1103,26 +1037,13 @@ cudaError_t make_maps(const ftmoe_fp8_matmul_args& m, int C, int box, CUtensorMa
   return encode_map(map_x, m.a, 2, xd, xs, xb);
 }
 
-// `most`: units there may be; a cluster of `ctas` works on one at a time.
+// `most`: units there may be.
 template <typename K>
-cudaError_t launch_units(K* k, int threads, const TrainDevice& d, int64_t most, int ctas, int smem, int smem_max,
+cudaError_t launch_units(K* k, int threads, const TrainDevice& d, int64_t most, int smem, int smem_max,
                          const MatmulArgs& a, const CUtensorMap& map_w, const CUtensorMap& map_x, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max);
   if (e != cudaSuccess) return e;
-  const int64_t workers = d.num_sms / ctas;
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)((most < workers ? most : workers) * ctas));
-  c.blockDim = dim3(threads);
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim = {(unsigned)ctas, 1, 1};
-  c.attrs = at;
-  c.numAttrs = 2;
-  return cudaLaunchKernelEx(&c, k, a, map_w, map_x);
+  return launch_after_smem(k, (unsigned)(most < d.num_sms ? most : d.num_sms), threads, smem, s, a, map_w, map_x);
 }
 
 template <int NMAX, bool SWIGLU, bool TRANS>
@@ -1133,18 +1054,18 @@ cudaError_t launch_few(const TrainDevice& d, const ftmoe_fp8_matmul_args& m, Mat
   if (e != cudaSuccess) return e;
   a.JT = fp8_blocks(a.O);
   return launch_units(k_fp8_matmul_few<NMAX, SWIGLU, TRANS>, kFewThreads, d,
-                      (m.M / NMAX + (m.M < m.E ? m.M : m.E)) * a.JT, 1, F::smem(m.E), F::smem(kMaxBins), a, map_w, map_x, s);
+                      (m.M / NMAX + (m.M < m.E ? m.M : m.E)) * a.JT, F::smem(m.E), F::smem(kMaxBins), a, map_w, map_x, s);
 }
 
-template <int CTAS, bool SWIGLU, bool TRANS>
+template <bool SWIGLU, bool TRANS>
 cudaError_t launch_many(const TrainDevice& d, const ftmoe_fp8_matmul_args& m, MatmulArgs a, cudaStream_t s) {
-  using F = Many<CTAS>;
+  using F = Many;
   CUtensorMap map_w, map_x;
   const cudaError_t e = make_maps(m, a.C, 128, &map_w, &map_x);
   if (e != cudaSuccess) return e;
   a.JT = SWIGLU ? a.O / 128 : (a.O + 255) / 256;
-  return launch_units(k_fp8_matmul_many<CTAS, SWIGLU, TRANS>, kManyThreads, d,
-                      (m.M / F::kTokens + (m.M < m.E ? m.M : m.E)) * a.JT, CTAS, F::smem(m.E), F::smem(kMaxBins), a, map_w, map_x, s);
+  return launch_units(k_fp8_matmul_many<SWIGLU, TRANS>, kManyThreads, d,
+                      (m.M / F::kTokens + (m.M < m.E ? m.M : m.E)) * a.JT, F::smem(m.E), F::smem(kMaxBins), a, map_w, map_x, s);
 }
 
 }  // namespace
@@ -1169,9 +1090,8 @@ cudaError_t launch_fp8_matmul(const TrainDevice& d, const ftmoe_fp8_matmul_args&
     if (m.swiglu) return launch_few<32, true, false>(d, m, a, s);
     return m.transpose ? launch_few<32, false, true>(d, m, a, s) : launch_few<32, false, false>(d, m, a, s);
   }
-  constexpr int kCtas = 1;
-  if (m.swiglu) return launch_many<kCtas, true, false>(d, m, a, s);
-  return m.transpose ? launch_many<kCtas, false, true>(d, m, a, s) : launch_many<kCtas, false, false>(d, m, a, s);
+  if (m.swiglu) return launch_many<true, false>(d, m, a, s);
+  return m.transpose ? launch_many<false, true>(d, m, a, s) : launch_many<false, false>(d, m, a, s);
 }
 
 }  // namespace ftmoe
