@@ -30,6 +30,7 @@ cudaError_t launch_swiglu(const TrainDevice& d, const void* gu, const void* dh, 
                           const int32_t* used, void* out, float* scales, cudaStream_t s);
 
 // Grouped product (fp8_matmul.cu).
+cudaError_t fp8_matmul_set_limits();
 cudaError_t launch_fp8_matmul(const TrainDevice& d, const ftmoe_fp8_matmul_args& a, cudaStream_t s);
 
 }  // namespace ftmoe

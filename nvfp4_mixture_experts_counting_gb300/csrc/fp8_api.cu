@@ -94,8 +94,8 @@ int ftmoe_fp8_matmul(const ftmoe_fp8_matmul_args* a, ftmoe_stream_t stream) {
     return FTMOE_ERR_INVALID_ARG;
   if ((!a->offsets && a->E != 1) || (a->transpose && a->swiglu)) return FTMOE_ERR_INVALID_ARG;
   if (!a->swiglu && !known(a->out_dtype)) return FTMOE_ERR_INVALID_ARG;
-  // tiles of at least 32 rows and 128 columns are counted in 32 bits
-  if ((a->M / 32 + a->E) * (((int64_t)(a->transpose ? a->K : a->N) + 127) / 128) > INT32_MAX) return FTMOE_ERR_INVALID_ARG;
+  // tiles of 128 rows and at least 128 columns are counted in 32 bits
+  if ((a->M / 128 + a->E) * (((int64_t)(a->transpose ? a->K : a->N) + 127) / 128) > INT32_MAX) return FTMOE_ERR_INVALID_ARG;
   if (a->K % 16 || (a->transpose && a->N % 16) || (a->swiglu && a->N % (2 * kFp8Block))) return FTMOE_ERR_ALIGNMENT;
   if (a->M == 0) return FTMOE_OK;
   if (!a->a || !a->a_scale || !a->w || !a->w_scale || !a->out || a->out == a->a || (a->swiglu && !a->out_scale))

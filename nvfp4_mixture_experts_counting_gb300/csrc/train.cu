@@ -52,6 +52,7 @@ int current_device(TrainDevice* out) {
     if (e == cudaSuccess) e = dispatch_set_limits(&sort_ctas);
     if (e == cudaSuccess) e = embed_set_limits(&sort_ctas);
     if (e == cudaSuccess) e = policy_set_limits();
+    if (e == cudaSuccess) e = fp8_matmul_set_limits();
     if (e != cudaSuccess) {
       cudaGetLastError();
       return cuda_fail(e, "training operators' set-up");

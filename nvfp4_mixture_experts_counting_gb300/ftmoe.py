@@ -335,9 +335,12 @@ _INT32, _INT64 = 3, 4
 class _Codes(dict):
     """torch.dtype -> code, filled once torch is there; -1 for other types."""
 
+    fp32 = int32 = codes = None
+
     def __missing__(self, dtype):
         import torch
         self.fp32 = torch.float32
+        self.int32 = torch.int32
         self.codes = (torch.uint8, torch.float8_e4m3fn)
         self.update({torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16, torch.int32: _INT32,
                      torch.int64: _INT64})
@@ -531,12 +534,17 @@ def ftmoe_adamw(tensors: AdamwList, lr: float, beta1: float = 0.9, beta2: float 
 SCORES = {"softmax": 0, "sigmoid": 1}
 
 
+def _fill():
+    """The types of codes, once torch is there."""
+    _CODES[None]
+    return _CODES.codes
+
+
 def _codes8(t, n: int):
     """Address of a contiguous tensor of n E4M3 codes or more (float8_e4m3fn, or their bytes)."""
     if t is None:
         return None
-    _CODES[t.dtype]  # fills the table
-    if t.dtype not in _CODES.codes:
+    if t.dtype not in (_CODES.codes or _fill()):
         raise TypeError(f"float8_e4m3fn or uint8 expected, got {t.dtype}")
     if t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{n} or more contiguous codes expected, got {t.numel()} with strides {t.stride()}")
@@ -545,8 +553,6 @@ def _codes8(t, n: int):
 
 def _rows(t):
     """(rows, columns, values between rows) of a matrix whose rows are dense."""
-    if t.dim() != 2:
-        raise ValueError(f"a matrix expected, got {t.dim()} dimensions")
     n, width = t.shape
     ld, step = t.stride()
     if width > 1 and step != 1:
@@ -554,17 +560,25 @@ def _rows(t):
     return n, width, width if n <= 1 else ld  # a single row's stride says nothing
 
 
+# The calls below take some 4 us on the host, as long as their smallest kernels: their tensors are looked at together,
+# and one by one (_array and the like, which say what is wrong) only where something is absent or wrong.
+
 def route_args(logits, topk_idx, topk_w, score: str = "softmax", norm_topk_prob: bool = True, scale: float = 1.0,
                bias=None, n_groups: int = 1, top_groups: int = 1, group_best: int = 1) -> RouteArgs:
     """Arguments of ftmoe_route_topk and its gradient, kept with references to the tensors; logits [T, E] may have
     any row stride, top_k is the width of topk_idx [T, top_k]."""
     T, E, ld = _rows(logits)
-    if topk_idx.dim() != 2 or topk_idx.shape[0] != T or topk_w.shape != topk_idx.shape:
+    shape = topk_idx.shape
+    if len(shape) != 2 or shape[0] != T or topk_w.shape != shape:
         raise ValueError("topk_idx and topk_w have a row for each of the logits' and one shape")
-    k = topk_idx.shape[1]
-    args = RouteArgs(logits.data_ptr(), _dtype(logits), T, E, ld, SCORES[score], k, int(norm_topk_prob), scale,
-                     _array(bias, FP32, E), n_groups, top_groups, group_best, _array(topk_idx, _INT32, T * k),
-                     _array(topk_w, FP32, T * k))
+    k, dtype = shape[1], _dtype(logits)
+    if (topk_idx.dtype is _CODES.int32 and topk_w.dtype is _CODES.fp32 and topk_idx.is_contiguous()
+            and topk_w.is_contiguous()):
+        idx, w = topk_idx.data_ptr(), topk_w.data_ptr()
+    else:
+        idx, w = _array(topk_idx, _INT32, T * k), _array(topk_w, FP32, T * k)
+    args = RouteArgs(logits.data_ptr(), dtype, T, E, ld, SCORES[score], k, norm_topk_prob, scale,
+                     _array(bias, FP32, E), n_groups, top_groups, group_best, idx, w)
     args.tensors = (logits, topk_idx, topk_w, bias)
     return args
 
@@ -575,7 +589,7 @@ def ftmoe_route_topk(args: RouteArgs, stream=None):
 
 def ftmoe_route_topk_backward(args: RouteArgs, dw, dlogits, stream=None):
     T, E, ld = _rows(dlogits)
-    if (T, E) != (args.T, args.E) or _dtype(dlogits) != args.dtype:
+    if T != args.T or E != args.E or _dtype(dlogits) != args.dtype:
         raise TypeError("dlogits has the shape and type of logits")
     _check(lib().ftmoe_route_topk_backward(C.byref(args), _array(dw, FP32, T * args.top_k), dlogits.data_ptr(), ld,
                                            _stream(stream)), "ftmoe_route_topk_backward")
@@ -584,9 +598,17 @@ def ftmoe_route_topk_backward(args: RouteArgs, dw, dlogits, stream=None):
 def ftmoe_fp8_quantize(x, T: int, K: int, inv, top_k: int, codes, scales, used=None, stream=None):
     """E4M3 codes of x's rows with a scale for 128 values; with inv, in the rows that ftmoe_dispatch's table names."""
     dtype, rows, blocks = _dtype(x), T * top_k, (K + 127) // 128
-    _check(lib().ftmoe_fp8_quantize(_array(x, dtype, T * K), dtype, T, K, _array(inv, _INT32, rows), top_k,
-                                    _array(used, _INT32, 1), _codes8(codes, rows * K),
-                                    _array(scales, FP32, blocks * rows), _stream(stream)), "ftmoe_fp8_quantize")
+    if (inv is not None and used is None and inv.dtype is _CODES.int32 and codes.dtype in _CODES.codes
+            and scales.dtype is _CODES.fp32 and x.numel() >= T * K and inv.numel() >= rows
+            and codes.numel() >= rows * K and scales.numel() >= blocks * rows and x.is_contiguous()
+            and inv.is_contiguous() and codes.is_contiguous() and scales.is_contiguous()):
+        rc = lib().ftmoe_fp8_quantize(x.data_ptr(), dtype, T, K, inv.data_ptr(), top_k, None, codes.data_ptr(),
+                                      scales.data_ptr(), _stream(stream))
+    else:
+        rc = lib().ftmoe_fp8_quantize(_array(x, dtype, T * K), dtype, T, K, _array(inv, _INT32, rows), top_k,
+                                      _array(used, _INT32, 1), _codes8(codes, rows * K),
+                                      _array(scales, FP32, blocks * rows), _stream(stream))
+    _check(rc, "ftmoe_fp8_quantize")
 
 
 def ftmoe_fp8_quantize_weights(w, E: int, N: int, K: int, codes, scales, stream=None):
@@ -601,12 +623,22 @@ def ftmoe_fp8_matmul(a, a_scale, w, w_scale, offsets, M: int, E: int, N: int, K:
     """Each expert's rows of codes times its matrix [N, K] (transpose: times its columns; swiglu: h as codes)."""
     width, out_width = (N, K) if transpose else (K, N // 2 if swiglu else N)
     nb, kb = (N + 127) // 128, (K + 127) // 128
+    n_scales, n_out = (nb if transpose else kb) * M, M * out_width
+    codes, fp32 = _CODES.codes or _fill(), _CODES.fp32
     dtype = 0 if swiglu else _dtype(out)
-    args = Fp8MatmulArgs(_codes8(a, M * width), _array(a_scale, FP32, (nb if transpose else kb) * M),
-                         _codes8(w, E * N * K), _array(w_scale, FP32, E * nb * kb), _array(offsets, _INT32, E + 1), M,
-                         E, N, K, int(transpose), int(swiglu), dtype,
-                         _codes8(out, M * out_width) if swiglu else _array(out, dtype, M * out_width),
-                         _array(out_scale, FP32, out_width // 128 * M) if swiglu else None)
+    if (offsets is not None and a.dtype in codes and w.dtype in codes and a_scale.dtype is fp32
+            and w_scale.dtype is fp32 and offsets.dtype is _CODES.int32 and a.numel() >= M * width
+            and a_scale.numel() >= n_scales and w.numel() >= E * N * K and w_scale.numel() >= E * nb * kb
+            and offsets.numel() > E and out.numel() >= n_out and a.is_contiguous() and a_scale.is_contiguous()
+            and w.is_contiguous() and w_scale.is_contiguous() and offsets.is_contiguous() and out.is_contiguous()
+            and not swiglu):
+        args = Fp8MatmulArgs(a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), offsets.data_ptr(), M,
+                             E, N, K, transpose, 0, dtype, out.data_ptr(), None)
+    else:
+        args = Fp8MatmulArgs(_codes8(a, M * width), _array(a_scale, FP32, n_scales), _codes8(w, E * N * K),
+                             _array(w_scale, FP32, E * nb * kb), _array(offsets, _INT32, E + 1), M, E, N, K, transpose,
+                             swiglu, dtype, _codes8(out, n_out) if swiglu else _array(out, dtype, n_out),
+                             _array(out_scale, FP32, out_width // 128 * M) if swiglu else None)
     _check(lib().ftmoe_fp8_matmul(C.byref(args), _stream(stream)), "ftmoe_fp8_matmul")
 
 

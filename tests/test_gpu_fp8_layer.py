@@ -285,6 +285,7 @@ COUNTS = [
     # M, counts of each expert
     (1, [1]), (1, [0, 1, 0]), (5, [2, 0, 3]), (40, [17, 0, 1, 22]), (64, [0, 0, 64]), (300, [129, 1, 127, 43]),
     (1000, [700, 0, 300]), (37, [10, 7, 3]),  # the last leaves rows of no expert
+    (63, [0] * 20 + [37, 0, 0, 23] + [0] * 9), (90, [1, 0, 2] * 30), (700, [0] * 300 + [1] * 500 + [200]),
 ]
 SHAPES = [(16, 16), (128, 128), (144, 272), (256, 640), (333, 400), (640, 2000), (1280, 2560), (96, 4112)]
 
