@@ -180,12 +180,12 @@ __device__ __forceinline__ void make_tables(const MatmulArgs& a, int* start, int
   __syncthreads();
 }
 
-__device__ __forceinline__ Unit unit_of(const Tables& t, int u) {
-  int e = 0, hi = t.E;  // the last expert whose first unit is not after u: those without units share their successor's
-  while (hi - e > 1) {
-    const int mid = (e + hi) >> 1;
-    if (t.first[mid] <= u) e = mid; else hi = mid;
-  }
+// Unit u, whose expert is not before e.  An expert's units go by weight tile,
+// and token tile by token tile within one: CTAs side by side read the same 32
+// KB of weights and their own 16 KB of tokens of each block.  (The other way
+// round a product of 4096^3 took 84 us instead of 76.)
+__device__ __forceinline__ Unit unit_of(const Tables& t, int u, int e) {
+  while (t.first[e + 1] <= u) ++e;
   const int n = t.start[e + 1] - t.start[e], tiles = (n + kTokens - 1) / kTokens, r = u - t.first[e];
   const int jt = r / tiles, at = (r - jt * tiles) * kTokens;
   return {e, jt, t.start[e] + at, min(kTokens, n - at)};
@@ -363,10 +363,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_down<kLowRegs>();
     if (warp == 0) {
       // ---------------- copies
-      int s = 0, k = 0;
+      int s = 0, k = 0, e = 0;
       uint32_t phase = 1;  // a new barrier's phase 1 counts as over
       for (int u = blockIdx.x; u < n_units && !*abort_flag; u += gridDim.x) {
-        const Unit x = unit_of(tables, u);
+        const Unit x = unit_of(tables, u, e);
+        e = x.e;
         const int boxes = (x.rows + kBox - 1) / kBox;  // the rows behind them in shared memory are nobody's
         for (int kb = 0; kb < nkb; ++kb, ++k) {
           if (!warp_wait(&empty[s], phase, a.status)) {
@@ -447,11 +448,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // [64 wg, 64 wg + 64) of gate and up.  Packed FMAs: no faster than plain ones here, but half the instructions.
     const int q = warp & 3, wg = (warp - kSumWarp0) >> 2, token = 32 * q + lane;
     const uint32_t from = tmem + ((uint32_t)(32 * q) << 16) + (SWIGLU ? 64 : 128) * wg;
-    int k = 0;
+    int k = 0, e = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < n_units && !*abort_flag; u += gridDim.x) {
-      const Unit x = unit_of(tables, u);
+      const Unit x = unit_of(tables, u, e);
+      e = x.e;
       const bool on = token < x.rows;
       const float* sx = a.a_scale + x.row0 + token;
       // weights' scales: [e][block of rows][block of columns]; TRANS contracts the rows
