@@ -85,11 +85,19 @@ __global__ void __launch_bounds__(kThreads) k_fp8_quantize(const T* x, int T_, i
       if (at < 0) continue;
 #pragma unroll
       for (int h = 0; h < kTwice; ++h) {
-        const int b = b0 + 4 * h, k0 = b * kFp8Block + sub * kPer;
-        if (k0 >= K) continue;
-        *reinterpret_cast<uint4*>(codes + at * K + k0) = c[h];
-        if (sub == 0) scales[(int64_t)b * places + at] = scale[h];
+        const int k0 = (b0 + 4 * h) * kFp8Block + sub * kPer;
+        if (k0 < K) *reinterpret_cast<uint4*>(codes + at * K + k0) = c[h];
       }
+    }
+    // The scales, each to a line of its own: lane l those of block l % 8, of every fourth place.
+    static_assert(kTwice == 2 && kLanes == 8, "eight blocks a warp");
+    const float s0 = __shfl_sync(0xffffffffu, scale[0], (lane & 3) * kLanes);
+    const float s1 = __shfl_sync(0xffffffffu, scale[1], (lane & 3) * kLanes);
+    const int b = (int)(u - t * parts) * 8 + (lane & 7);
+    for (int j = lane >> 3; j < (top_k + 3 & ~3); j += 4) {
+      const int to = __shfl_sync(0xffffffffu, mine, j & 31);
+      const int64_t at = inv ? (int64_t)to : t;
+      if (j < top_k && at >= 0 && b < blocks) scales[(int64_t)b * places + at] = lane & 4 ? s1 : s0;
     }
   }
 }
@@ -189,16 +197,19 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_fp8(const T* gu, const T* d
   }
 }
 
-// Output in the input's type.  A warp takes 128 V columns of a row: four
-// pieces a lane, 32 pieces apart, of V = 16 bytes' values, or of one value
-// where rows are not a multiple of 16 bytes (whose loads are so issued
-// together and stay whole lines).
-constexpr int kPieces = 4;
+// Output in the input's type.  A warp takes neighbouring pieces of a row, a
+// lane one (or four, 32 pieces apart) of V = 16 bytes' values, or of one value
+// where rows are not a multiple of 16 bytes.  Four where a lane has little on
+// its way otherwise (the gradient of 8191 x 1001 fp16 values 18 us, 28 with
+// one); with two 16-byte loads a lane more warps at a time are better (131072 x
+// 640 bf16 values 79 us, 96 with four).
+template <int V, bool GRAD>
+constexpr int kPieces = V > 1 && !GRAD ? 1 : 4;
 template <typename T, int V, bool GRAD>
 __global__ void __launch_bounds__(kThreads) k_swiglu(const T* gu, const T* dh, int rows_, int I, const int32_t* used,
                                                      T* out, uint32_t* status) {
   pdl_wait();
-  constexpr int kWide = 32 * V * kPieces;
+  constexpr int kN = kPieces<V, GRAD>, kWide = 32 * V * kN;
   const int rows = used_rows(used, rows_, status), chunks = (I + kWide - 1) / kWide;
   const int64_t units = (int64_t)rows * chunks, step = (int64_t)gridDim.x * (kThreads / 32);
   for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; i < units; i += step) {
@@ -206,9 +217,9 @@ __global__ void __launch_bounds__(kThreads) k_swiglu(const T* gu, const T* dh, i
     const int k0 = (int)(i - r * chunks) * kWide + (threadIdx.x & 31) * V;
     const T *g = gu + r * 2 * I, *u = g + I, *d = GRAD ? dh + r * I : nullptr;
     T* o = out + r * (GRAD ? 2 : 1) * I;
-    Pack<T, V> pg[kPieces], pu[kPieces], pd[kPieces];
+    Pack<T, V> pg[kN], pu[kN], pd[kN];
 #pragma unroll
-    for (int p = 0; p < kPieces; ++p) {
+    for (int p = 0; p < kN; ++p) {
       const int k = k0 + 32 * V * p;
       if (k >= I) continue;
       pg[p] = load_pack<T, V>(g + k);
@@ -216,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) k_swiglu(const T* gu, const T* dh, i
       if (GRAD) pd[p] = load_pack<T, V>(d + k);
     }
 #pragma unroll
-    for (int p = 0; p < kPieces; ++p) {
+    for (int p = 0; p < kN; ++p) {
       const int k = k0 + 32 * V * p;
       if (k >= I) continue;
       Pack<T, V> a, b;
@@ -249,7 +260,7 @@ cudaError_t launch_fp8_quantize(const TrainDevice& d, const void* x, int dtype, 
   return with_dtype(dtype, [&](auto zero) {
     using V = decltype(zero);
     const int64_t units = (int64_t)T * ((fp8_blocks(K) + 4 * kTwice - 1) / (4 * kTwice));
-    return launch_after(k_fp8_quantize<V>, grid_of(d, units, kThreads / 32, 16), kThreads, s,
+    return launch_after(k_fp8_quantize<V>, grid_of(d, units, kThreads / 32, 64), kThreads, s,
                         static_cast<const V*>(x), T, K, inv, top_k, used, codes, scales, d.status);
   });
 }
@@ -276,7 +287,7 @@ cudaError_t launch_swiglu(const TrainDevice& d, const void* gu, const void* dh, 
     }
     constexpr int W = 16 / sizeof(V);
     const bool wide = I % W == 0;
-    const int per_warp = 32 * kPieces * (wide ? W : 1);
+    const int per_warp = 32 * (wide ? W * (dh ? kPieces<W, true> : kPieces<W, false>) : kPieces<1, true>);
     const unsigned grid = grid_of(d, (int64_t)rows * ((I + per_warp - 1) / per_warp), kThreads / 32, 16);
     auto* k = wide ? (dh ? k_swiglu<V, W, true> : k_swiglu<V, W, false>)
                    : (dh ? k_swiglu<V, 1, true> : k_swiglu<V, 1, false>);
