@@ -250,9 +250,12 @@ __device__ __forceinline__ float sort_lanes(float v, int lane) {
   return v;
 }
 
-// VPL: experts a lane holds.
+// VPL: experts a lane holds.  Up to 256 experts are held to 64 registers, so
+// that eight CTAs fit an SM, and the grid is no larger: what a warp works out
+// of the biases serves several tokens (16384 tokens in groups 25 -> 23 us).
+constexpr int kCtasPerSm = 8;
 template <typename T, int VPL>
-__global__ void __launch_bounds__(kWarps * 32) k_route_topk(const __grid_constant__ RouteKernelArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, VPL <= 8 ? kCtasPerSm : VPL == 16 ? 4 : 2) k_route_topk(const __grid_constant__ RouteKernelArgs a) {
   extern __shared__ __align__(16) double shared_c[];
   __shared__ Chosen shared_chosen[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -527,8 +530,8 @@ RouteKernelArgs kernel_args(const TrainDevice& d, const ftmoe_route_args& r) {
   return a;
 }
 
-unsigned route_grid(const TrainDevice& d, int T) {
-  const int need = (T - 1) / kWarps + 1, most = d.num_sms * 16;
+unsigned route_grid(const TrainDevice& d, int T, int ctas_per_sm) {
+  const int need = (T - 1) / kWarps + 1, most = d.num_sms * ctas_per_sm;
   return (unsigned)(need < most ? need : most);
 }
 
@@ -542,7 +545,7 @@ cudaError_t launch_route_topk(const TrainDevice& d, const ftmoe_route_args& r, c
     auto* k = per <= 1 ? k_route_topk<T, 1> : per <= 2 ? k_route_topk<T, 2> : per <= 4 ? k_route_topk<T, 4>
               : per <= 8 ? k_route_topk<T, 8> : per <= 16 ? k_route_topk<T, 16> : k_route_topk<T, 32>;
     // 32 KB at E = 1024: within what a kernel has without asking
-    return launch_after_smem(k, route_grid(d, r.T), kWarps * 32, kWarps * ((r.E + 1) & ~1) * sizeof(double), s, a);
+    return launch_after_smem(k, route_grid(d, r.T, kCtasPerSm), kWarps * 32, kWarps * ((r.E + 1) & ~1) * sizeof(double), s, a);
   });
 }
 
@@ -553,7 +556,7 @@ cudaError_t launch_route_topk_backward(const TrainDevice& d, const ftmoe_route_a
     using T = decltype(zero);
     constexpr int V = 16 / sizeof(T);
     const bool wide = r.E % V == 0 && ld_d % V == 0 && ((uintptr_t)dlogits & 15) == 0;
-    return launch_after(wide ? k_route_topk_backward<T, V> : k_route_topk_backward<T, 1>, route_grid(d, r.T),
+    return launch_after(wide ? k_route_topk_backward<T, V> : k_route_topk_backward<T, 1>, route_grid(d, r.T, 16),
                         kWarps * 32, s, a, dw, static_cast<T*>(dlogits), ld_d);
   });
 }

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -532,6 +533,8 @@ def ftmoe_adamw(tensors: AdamwList, lr: float, beta1: float = 0.9, beta2: float 
 # ----------------------------------------------------------------- the layer on 8-bit codes
 
 SCORES = {"softmax": 0, "sigmoid": 1}
+# The fields of RouteArgs and Fp8MatmulArgs, to be filled at once (a third of the time that their constructors take).
+_ROUTE, _MATMUL = struct.Struct("@PiiiqiiifPiiiPP"), struct.Struct("@PPPPPqiiiiiiPP")
 
 
 def _fill():
@@ -577,8 +580,9 @@ def route_args(logits, topk_idx, topk_w, score: str = "softmax", norm_topk_prob:
         idx, w = topk_idx.data_ptr(), topk_w.data_ptr()
     else:
         idx, w = _array(topk_idx, _INT32, T * k), _array(topk_w, FP32, T * k)
-    args = RouteArgs(logits.data_ptr(), dtype, T, E, ld, SCORES[score], k, norm_topk_prob, scale,
-                     _array(bias, FP32, E), n_groups, top_groups, group_best, idx, w)
+    args = RouteArgs()
+    _ROUTE.pack_into(args, 0, logits.data_ptr(), dtype, T, E, ld, SCORES[score], k, norm_topk_prob, scale,
+                     _array(bias, FP32, E) or 0, n_groups, top_groups, group_best, idx, w)
     args.tensors = (logits, topk_idx, topk_w, bias)
     return args
 
@@ -632,8 +636,9 @@ def ftmoe_fp8_matmul(a, a_scale, w, w_scale, offsets, M: int, E: int, N: int, K:
             and offsets.numel() > E and out.numel() >= n_out and a.is_contiguous() and a_scale.is_contiguous()
             and w.is_contiguous() and w_scale.is_contiguous() and offsets.is_contiguous() and out.is_contiguous()
             and not swiglu):
-        args = Fp8MatmulArgs(a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), offsets.data_ptr(), M,
-                             E, N, K, transpose, 0, dtype, out.data_ptr(), None)
+        args = Fp8MatmulArgs()
+        _MATMUL.pack_into(args, 0, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+                          offsets.data_ptr(), M, E, N, K, transpose, False, dtype, out.data_ptr(), 0)
     else:
         args = Fp8MatmulArgs(_codes8(a, M * width), _array(a_scale, FP32, n_scales), _codes8(w, E * N * K),
                              _array(w_scale, FP32, E * nb * kb), _array(offsets, _INT32, E + 1), M, E, N, K, transpose,

@@ -102,6 +102,17 @@ def test_swiglu(lib):  # noqa: F811
         ({7: None, 6: B}, DEVICE), ({7: None, 4: 3}, DEVICE)])
 
 
+def test_packed_arguments():
+    """The packed fields are the structures'."""
+    for packed, struct in ((ftmoe._ROUTE, ftmoe.RouteArgs), (ftmoe._MATMUL, ftmoe.Fp8MatmulArgs)):
+        fields = struct._fields_
+        values = [0.5 if t is C.c_float else 3 + i for i, (_, t) in enumerate(fields)]
+        args = struct()
+        packed.pack_into(args, 0, *values)
+        assert [getattr(args, n) for n, _ in fields] == values
+        assert packed.size <= C.sizeof(struct) < packed.size + 8
+
+
 def test_binding_refuses():
     """Tensors of a wrong type, shape or size never reach the library."""
     z = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype)
