@@ -60,6 +60,7 @@ struct MatmulArgs {
   int NB, KB;  // blocks of the weights' rows and columns
   int JT;      // weight tiles of an expert
   int dtype;
+  int map_out;  // rows are whole 16 bytes: tiles may go out by TMA
   void* out;
   float* out_scale;
   uint32_t* status;
@@ -185,7 +186,17 @@ __device__ __forceinline__ void make_tables(const MatmulArgs& a, int* start, int
 // KB of weights and their own 16 KB of tokens of each block.  (The other way
 // round a product of 4096^3 took 84 us instead of 76.)
 __device__ __forceinline__ Unit unit_of(const Tables& t, int u, int e) {
-  while (t.first[e + 1] <= u) ++e;
+  // the last expert whose first unit is not after u (those without units share their successor's), in growing steps
+  // from e, then by halves
+  int step = 1;
+  while (e + step < t.E && t.first[e + step] <= u) {
+    e += step;
+    step *= 2;
+  }
+  for (int hi = min(e + step, t.E); hi - e > 1;) {
+    const int mid = (e + hi) >> 1;
+    if (t.first[mid] <= u) e = mid; else hi = mid;
+  }
   const int n = t.start[e + 1] - t.start[e], tiles = (n + kTokens - 1) / kTokens, r = u - t.first[e];
   const int jt = r / tiles, at = (r - jt * tiles) * kTokens;
   return {e, jt, t.start[e] + at, min(kTokens, n - at)};
@@ -247,17 +258,53 @@ __device__ __forceinline__ void store_32(void* p, const uint32_t (&v)[8]) {
 }
 
 // A warp's sums, lane l those of token l in the columns c0 .. c0 + 127, to the
-// rows from `row` on, `rows` of them.  Whole pieces of 32 bytes go straight
-// from a lane to its token's row.  Otherwise 64 bytes of every token at a time
-// pass through shared memory (`st`), so that a store covers up to eight rows'
-// 64 bytes and not 32 rows' few (a product of 666 fp32 columns 60 -> 36 us).
+// rows from `row` on, `rows` of them, through shared memory (`st`).  A whole 32
+// of aligned rows (`map`) go out by TMA behind the warp's back: stores of its
+// own pass a 32-byte sector a cycle, 2200 cycles for a tile's 64 KB, in which
+// the tensor cores come to a stop (16384 tokens through down 361 us, so 342).
+// Others go as stores that cover up to eight rows' 64 bytes each, and not 32
+// rows' few (a product of 666 fp32 columns 60 -> 34 us).
 template <bool WIDE>
 __device__ __forceinline__ void store_tile(const MatmulArgs& a, unsigned char* st, int64_t row, int rows, int c0,
-                                           const float (&acc)[128], int lane) {
+                                           const float (&acc)[128], int lane, const CUtensorMap* map) {
   const int bytes = WIDE ? 4 : 2;
   constexpr int kCols = WIDE ? 16 : 32;
   unsigned char* out = static_cast<unsigned char*>(a.out) + (row * a.O + c0) * bytes;
   const int64_t pitch = (int64_t)a.O * bytes;
+  if (map && rows == 32) {
+    // 32 bytes of every token at a time, two pieces in turn, copied out behind the warp's back
+    constexpr int kPiece = WIDE ? 8 : 16;
+#pragma unroll
+    for (int p = 0; p < 128 / kPiece; ++p) {
+      if (c0 + p * kPiece >= a.O) continue;
+      unsigned char* to = st + (p & 1) * 1024;
+      if (lane == 0) bulk_wait_read<1>();
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float* v = acc + p * kPiece + i * (kPiece / 2);
+        uint4 w;
+        if constexpr (WIDE)
+          w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        else
+          w = make_uint4(halves(v[0], v[1], a.dtype), halves(v[2], v[3], a.dtype), halves(v[4], v[5], a.dtype),
+                         halves(v[6], v[7], a.dtype));
+        *reinterpret_cast<uint4*>(to + lane * 32 + ((i ^ (lane >> 2 & 1)) << 4)) = w;
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"(c0 + p * kPiece), "r"((int)row), "r"(smem_u32(to))
+                     : "memory");
+        bulk_commit();
+      }
+    }
+    return;
+  }
+  if (lane == 0) bulk_wait_read<0>();
+  __syncwarp();
   if (!WIDE && pitch % 32 == 0 && ((uintptr_t)a.out & 31) == 0 && c0 + 128 <= a.O) {
     if (lane < rows) {
 #pragma unroll
@@ -316,7 +363,7 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, unsigned char* s
 template <bool SWIGLU, bool TRANS>
 __global__ void __launch_bounds__(kThreads, 1)
     k_fp8_matmul(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_w,
-                 const __grid_constant__ CUtensorMap map_x) {
+                 const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_out) {
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
   unsigned char* staged = sm + kStages * kStageBytes;
@@ -515,9 +562,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c0 = x.jt * 256 + 128 * wg, rows = min(32, x.rows - 32 * q);
         unsigned char* st = staged + (warp - kSumWarp0) * kStaged;
         if (a.dtype == FTMOE_FP32)
-          store_tile<true>(a, st, x.row0 + 32 * q, rows, c0, acc, lane);
+          store_tile<true>(a, st, x.row0 + 32 * q, rows, c0, acc, lane, a.map_out ? &map_out : nullptr);
         else
-          store_tile<false>(a, st, x.row0 + 32 * q, rows, c0, acc, lane);
+          store_tile<false>(a, st, x.row0 + 32 * q, rows, c0, acc, lane, a.map_out ? &map_out : nullptr);
       } else {
         // a token's 128 values of h lie in the two warps of its rows
         uint32_t best = 0;
@@ -561,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) *abort_flag = 1;
     }
+    if (!SWIGLU && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -573,7 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- host
 
 cudaError_t encode_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-                       const uint32_t* box) {
+                       const uint32_t* box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                       CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -590,8 +639,8 @@ cudaError_t encode_map(CUtensorMap* m, const void* base, int rank, const uint64_
     b[i] = box[i];
   }
   for (int i = 0; i < rank - 1; ++i) st[i] = strides[i];
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), d, st, b, es,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const CUresult r = fn(m, type, rank, const_cast<void*>(base), d, st, b, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -630,11 +679,24 @@ cudaError_t launch_fp8_matmul(const TrainDevice& d, const ftmoe_fp8_matmul_args&
   const uint64_t xd[2] = {(uint64_t)a.C, (uint64_t)m.M}, xs[1] = {(uint64_t)a.C};
   const uint32_t xb[2] = {128, kBox};
   if ((e = encode_map(&map_x, m.a, 2, xd, xs, xb)) != cudaSuccess) return e;
+  CUtensorMap map_out = map_x;
+  if (!m.swiglu) {
+    const int size = m.out_dtype == FTMOE_FP32 ? 4 : 2;
+    a.map_out = (int64_t)a.O * size % 16 == 0;
+    if (a.map_out) {
+      const uint64_t od[2] = {(uint64_t)a.O, (uint64_t)m.M}, os[1] = {(uint64_t)a.O * size};
+      const uint32_t ob[2] = {(uint32_t)(32 / size), 32};
+      e = encode_map(&map_out, m.out, 2, od, os, ob,
+                     size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                     CU_TENSOR_MAP_SWIZZLE_32B);
+      if (e != cudaSuccess) return e;
+    }
+  }
   const int64_t units = (m.M / kTokens + (m.M < m.E ? m.M : m.E)) * a.JT;  // at most
   return launch_after_smem(m.swiglu ? k_fp8_matmul<true, false> : m.transpose ? k_fp8_matmul<false, true>
                                                                               : k_fp8_matmul<false, false>,
                            (unsigned)(units < d.num_sms ? units : d.num_sms), kThreads, smem_bytes(m.E), s, a, map_w,
-                           map_x);
+                           map_x, map_out);
 }
 
 }  // namespace ftmoe
