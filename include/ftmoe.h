@@ -606,7 +606,8 @@ int ftmoe_adamw(const ftmoe_adamw_tensor* tensors, int n_tensors, const ftmoe_ad
  * Like the training operators they need no handle, run on the current device,
  * are asynchronous on `stream`, allocate nothing, may be captured once one of
  * them has run on the device, give the same bits run to run, and mark the word
- * that ftmoe_ops_status reads.  One forward pass of a layer:
+ * that ftmoe_ops_status reads.  Matrices are dense and their pointers 16-byte
+ * aligned, but for the router's logits.  One forward pass of a layer:
  *
  *   ftmoe_route_topk       logits -> experts and weights of each token
  *   ftmoe_dispatch         (x NULL) tables of the pairs sorted by expert
@@ -726,11 +727,11 @@ int ftmoe_swiglu_backward(const void* dh, const void* gu, int dtype, int rows, i
                           float* scales, ftmoe_stream_t stream);
 
 /* Synchronise `stream`, read and clear the current device's status word of
- * the training operators since the last call: FTMOE_OK,
+ * the training operators and the 8-bit layer since the last call: FTMOE_OK,
  * FTMOE_ERR_DEVICE_CHECK if a kernel met an index out of range, or
- * FTMOE_ERR_TIMEOUT if a bounded wait of the policy loss ran out: that call's
- * outputs are not valid (its loss is NaN as a rule), and the next call starts
- * clean.  One word serves all streams. */
+ * FTMOE_ERR_TIMEOUT if a bounded wait of the policy loss or of
+ * ftmoe_fp8_matmul ran out: that call's outputs are not valid (a loss is NaN as
+ * a rule), and the next call starts clean.  One word serves all streams. */
 int ftmoe_ops_status(ftmoe_stream_t stream);
 
 #ifdef __cplusplus

@@ -562,9 +562,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c0 = x.jt * 256 + 128 * wg, rows = min(32, x.rows - 32 * q);
         unsigned char* st = staged + (warp - kSumWarp0) * kStaged;
         if (a.dtype == FTMOE_FP32)
-          store_tile<true>(a, st, x.row0 + 32 * q, rows, c0, acc, lane, a.map_out ? &map_out : nullptr);
+          store_tile<true>(a, st, (int64_t)x.row0 + 32 * q, rows, c0, acc, lane, a.map_out ? &map_out : nullptr);
         else
-          store_tile<false>(a, st, x.row0 + 32 * q, rows, c0, acc, lane, a.map_out ? &map_out : nullptr);
+          store_tile<false>(a, st, (int64_t)x.row0 + 32 * q, rows, c0, acc, lane, a.map_out ? &map_out : nullptr);
       } else {
         // a token's 128 values of h lie in the two warps of its rows
         uint32_t best = 0;

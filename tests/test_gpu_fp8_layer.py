@@ -666,6 +666,73 @@ def test_route_backward_equal_and_bad_indices():
     assert d.tolist() == [[0.0, 0.0, 0.5, 0.0]]
 
 
+def test_route_backward_into_strided_rows():
+    """Only the rows' own values are written, wherever they start."""
+    g = gen(67)
+    logits, dw = randn(g, 9, 24, dtype=BF16), randn(g, 9, 3)
+    idx, w = route(logits, 3, "sigmoid")
+    want, wide = torch.empty_like(logits), torch.full((9, 33), 5.0, dtype=BF16, device=DEV)
+    args = ftmoe.route_args(logits, idx, w, score="sigmoid")
+    ftmoe.ftmoe_route_topk_backward(args, dw, want)
+    ftmoe.ftmoe_route_topk_backward(args, dw, wide[:, 5:29])
+    assert torch.equal(wide[:, 5:29], want)
+    wide[:, 5:29] = 5.0
+    assert bool((wide == 5.0).all())
+
+
+# ----------------------------------------------------------------- sizes whose offsets pass 32 bits
+
+def big_codes(g, *shape):
+    """Random codes, NaN left out."""
+    c = torch.randint(0, 127, shape, generator=g, device=DEV, dtype=torch.uint8)
+    return torch.where(torch.rand(shape[-1], generator=g, device=DEV) < 0.5, c | 128, c).view(E4M3)
+
+
+def test_product_of_many_rows():
+    """Rows times width beyond 2^31 values: the last rows are as a short call gives them."""
+    g = gen(100)
+    M, N, K = 600_000, 4096, 128
+    a, a_scale = big_codes(g, M, K), torch.rand(1, M, generator=g, device=DEV)
+    w, w_scale = bank(g, 1, N, K)
+    out = torch.empty(M, N, dtype=BF16, device=DEV)
+    ftmoe.ftmoe_fp8_matmul(a, a_scale, w, w_scale, None, M, 1, N, K, out)
+    few = torch.empty(100, N, dtype=BF16, device=DEV)
+    for at in (0, 524_200, M - 100):
+        ftmoe.ftmoe_fp8_matmul(a[at:at + 100].contiguous(), a_scale[:, at:at + 100].contiguous(), w, w_scale, None, 100, 1,
+                               N, K, few)
+        assert torch.equal(out[at:at + 100], few)
+
+
+def test_product_with_a_large_bank():
+    """Experts whose codes lie beyond 2^32 bytes."""
+    g = gen(101)
+    E, N, K = 72, 8192, 8192
+    w, w_scale = big_codes(g, E, N, K), torch.rand(E, 64, 64, generator=g, device=DEV)
+    a, a_scale = rows_of(g, 40, K)
+    out, one = torch.empty(40, N, device=DEV), torch.empty(40, N, device=DEV)
+    for e in (0, 63, 71):
+        ftmoe.ftmoe_fp8_matmul(a, a_scale, w, w_scale, offsets_of([0] * e + [40] + [0] * (E - 1 - e)), 40, E, N, K, out)
+        ftmoe.ftmoe_fp8_matmul(a, a_scale, w[e], w_scale[e], None, 40, 1, N, K, one)
+        assert torch.equal(out, one) and bool(out.isfinite().all())
+
+
+def test_elementwise_calls_past_32_bits():
+    g = gen(102)
+    T, K = 290_000, 8192
+    x = torch.randn(1000, K, generator=g, device=DEV).to(BF16).repeat(290, 1)
+    codes, scales = torch.empty(T, K, dtype=E4M3, device=DEV), torch.empty(64, T, device=DEV)
+    ftmoe.ftmoe_fp8_quantize(x, T, K, None, 1, codes, scales)
+    want, scale = quantized(x[:1000])
+    for at in (0, 262_000, T - 1000):
+        same_codes(codes[at:at + 1000], want)
+        assert torch.equal(scales[:, at:at + 1000], scale)
+    h = torch.empty(T, K // 2, dtype=BF16, device=DEV)
+    ftmoe.ftmoe_swiglu(x, T, K // 2, h)
+    exact = silu_up(x[:1000])
+    for at in (0, 262_000, T - 1000):
+        within(h[at:at + 1000], exact, UNIT[BF16] * exact.abs() + TINY[BF16] + 8 * EPS * exact.abs())
+
+
 # ----------------------------------------------------------------- together
 
 def layer(g, T, H, I, E, k):
