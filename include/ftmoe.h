@@ -639,8 +639,9 @@ typedef enum { FTMOE_SCORE_SOFTMAX = 0, FTMOE_SCORE_SIGMOID = 1 } ftmoe_score;
  *   slots 0..top_k-1: the largest c among them, largest first
  *   w_j = scale s_j / (sum of s over the chosen), or scale s_j without
  *   norm_topk_prob
- * Ties go to the lower group and the lower expert; experts are ranked as by
- * exact arithmetic on the given logits and biases.  An expert whose logit or
+ * Ties go to the lower group and the lower expert.  Experts are ranked by their
+ * logits where these decide (no bias, and one group or group_best 1), else as by
+ * fp64 arithmetic on the given logits and biases.  An expert whose logit or
  * bias is -inf is not available, nor is one whose logit is NaN or +inf or whose
  * bias is not finite, which also marks the status word.  Slots that no expert
  * is left for get index -1 and weight 0 (ftmoe_dispatch drops them). */
@@ -705,11 +706,11 @@ typedef struct {
   const float* w_scale;    /* [E][ceil(N/128)][ceil(K/128)] */
   const int32_t* offsets;  /* device [E + 1], or NULL with E == 1: all M rows */
   int64_t M;
-  int32_t E, N, K;         /* K a multiple of 16; transpose: N too; swiglu: N a multiple of 256 */
+  int32_t E, N, K;         /* N K < 2^40; K a multiple of 16; transpose: N too; swiglu: N a multiple of 256 */
   int32_t transpose, swiglu;
   int32_t out_dtype;       /* ftmoe_dtype (not with swiglu) */
   void* out;               /* not a */
-  float* out_scale;        /* swiglu only */
+  float* out_scale;        /* swiglu only; not a_scale */
 } ftmoe_fp8_matmul_args;
 
 int ftmoe_fp8_matmul(const ftmoe_fp8_matmul_args* args, ftmoe_stream_t stream);

@@ -96,9 +96,12 @@ int ftmoe_fp8_matmul(const ftmoe_fp8_matmul_args* a, ftmoe_stream_t stream) {
   if (!a->swiglu && !known(a->out_dtype)) return FTMOE_ERR_INVALID_ARG;
   // tiles of 128 rows and at least 128 columns are counted in 32 bits
   if ((a->M / 128 + a->E) * (((int64_t)(a->transpose ? a->K : a->N) + 127) / 128) > INT32_MAX) return FTMOE_ERR_INVALID_ARG;
+  // a tensor map's strides are below 2^40 bytes
+  if ((int64_t)a->N * a->K >= (int64_t)1 << 40) return FTMOE_ERR_INVALID_ARG;
   if (a->K % 16 || (a->transpose && a->N % 16) || (a->swiglu && a->N % (2 * kFp8Block))) return FTMOE_ERR_ALIGNMENT;
   if (a->M == 0) return FTMOE_OK;
-  if (!a->a || !a->a_scale || !a->w || !a->w_scale || !a->out || a->out == a->a || (a->swiglu && !a->out_scale))
+  if (!a->a || !a->a_scale || !a->w || !a->w_scale || !a->out || a->out == a->a ||
+      (a->swiglu && (!a->out_scale || a->out_scale == a->a_scale)))
     return FTMOE_ERR_INVALID_ARG;
   if (!on(a->a, 16) || !on(a->w, 16) || !on(a->out, 16) || !on(a->a_scale, 4) || !on(a->w_scale, 4) ||
       !on(a->offsets, 4) || !on(a->out_scale, 4))

@@ -138,6 +138,9 @@ struct Tables {
   int E;
 };
 
+// Token tiles of n rows, n up to the largest int.
+__device__ __forceinline__ int tiles_of(int n) { return n > 0 ? (n - 1) / kTokens + 1 : 0; }
+
 // Tables of the experts' rows and units, by the whole CTA.  An expert whose
 // rows begin before an earlier one's first row, fall or leave [0, M] has no
 // units and marks the status word.
@@ -165,7 +168,7 @@ __device__ __forceinline__ void make_tables(const MatmulArgs& a, int* start, int
       high = max(high, floor);
       const bool good = on && lo >= high && hi >= lo && hi <= a.M;
       if (on && !good) set_status(a.status, kStatusRange);
-      const int units = good ? (hi - lo + kTokens - 1) / kTokens * a.JT : 0;
+      const int units = good ? tiles_of(hi - lo) * a.JT : 0;
       int upto = units;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -197,7 +200,7 @@ __device__ __forceinline__ Unit unit_of(const Tables& t, int u, int e) {
     const int mid = (e + hi) >> 1;
     if (t.first[mid] <= u) e = mid; else hi = mid;
   }
-  const int n = t.start[e + 1] - t.start[e], tiles = (n + kTokens - 1) / kTokens, r = u - t.first[e];
+  const int n = t.start[e + 1] - t.start[e], tiles = tiles_of(n), r = u - t.first[e];
   const int jt = r / tiles, at = (r - jt * tiles) * kTokens;
   return {e, jt, t.start[e] + at, min(kTokens, n - at)};
 }

@@ -5,9 +5,9 @@
 //   the top_k largest c in them, ties to the lower index
 //   w_j = scale s_j / sum_i s_i, or scale s_j
 //
-// Experts are ranked as by exact arithmetic.  Where c is a monotone function
-// of the logit (no bias, and groups by their largest value) the logits
-// themselves are ranked, which is exact.  Otherwise c is computed in fp32 with
+// Experts are ranked as by fp64 arithmetic.  Where c is a monotone function of
+// the logit (no bias, and groups by their largest value) the logits themselves
+// are ranked, which is exact even where fp64 scores are equal (a sigmoid of 40).  Otherwise c is computed in fp32 with
 // an error bound, and a token where two values that decide are closer than
 // their bounds is ranked again in fp64.  Of N(0, 1) logits with E = 256 that is
 // one token in some hundreds.

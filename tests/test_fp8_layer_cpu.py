@@ -89,6 +89,13 @@ def test_matmul(lib):  # noqa: F811
     assert lib.ftmoe_fp8_matmul(None, None) == ARG
 
 
+def test_matmul_strides_and_aliases(lib):  # noqa: F811
+    good = dict(a=A, a_scale=A, w=A, w_scale=A, offsets=A, M=8, E=4, N=256, K=128, transpose=0, swiglu=1, out_dtype=0,
+                out=B, out_scale=D)
+    check_struct(lambda v: lib.ftmoe_fp8_matmul(C.byref(ftmoe.Fp8MatmulArgs(**v)), None), good, [
+        (dict(N=1 << 20, K=1 << 20), ARG), (dict(N=1 << 20, K=(1 << 20) - 16), DEVICE), (dict(out_scale=A), ARG)])
+
+
 def test_swiglu(lib):  # noqa: F811
     # gu dtype rows I used out scales stream
     check(lib, "ftmoe_swiglu", [A, 0, 4, 128, None, B, D, None], [

@@ -703,6 +703,22 @@ def test_product_of_many_rows():
         assert torch.equal(out[at:at + 100], few)
 
 
+def test_product_of_the_most_rows():
+    """M = 2^31 - 1, the largest count of rows."""
+    g = gen(103)
+    M, N, K = 2**31 - 1, 16, 16
+    a, a_scale = torch.zeros(M, K, dtype=torch.uint8, device=DEV), torch.ones(1, M, device=DEV)
+    w, w_scale = bank(g, 1, N, K)
+    out, few = torch.full((M, N), 7.0, dtype=BF16, device=DEV), torch.empty(100, N, dtype=BF16, device=DEV)
+    for at in (0, M - 100):
+        a[at:at + 100] = big_codes(g, 100, K).view(torch.uint8)
+    ftmoe.ftmoe_fp8_matmul(a, a_scale, w, w_scale, None, M, 1, N, K, out)
+    for at in (0, M - 100):
+        ftmoe.ftmoe_fp8_matmul(a[at:at + 100], a_scale[:, at:at + 100].contiguous(), w, w_scale, None, 100, 1, N, K, few)
+        assert torch.equal(out[at:at + 100], few)
+    assert not bool(out[M // 2:M // 2 + 1000].any())
+
+
 def test_product_with_a_large_bank():
     """Experts whose codes lie beyond 2^32 bytes."""
     g = gen(101)
