@@ -20,8 +20,10 @@
 // memory are 96 KB a block at 128 bytes a cycle), the commit's arrival 155,
 // reading and summing 450, two hand-offs by mbarrier some 150; half of the sum
 // is the time of a block.  16384 tokens of 8 of 256 experts, gate_up [1280,
-// 2560] with SwiGLU: 485 us, 1.75 PFLOP/s.  With few tokens the weights' bytes:
-// 256 tokens of the same 154 us, 5.3 TB/s.
+// 2560] with SwiGLU: 490 us, 1.75 PFLOP/s; its input's gradient 547 us; down
+// 346 us; one matrix of 4096 x 4096 with 4096 rows 74 us, 1.86 PFLOP/s.  With
+// few tokens the weights' bytes: 256 tokens of the same layer 154 us, 5.3 TB/s;
+// 16 tokens 50 us, 4.9 TB/s (units of uneven experts over 152 SMs).
 //
 // Measured and not kept: tokens as the MMA's columns (scales then differ by
 // column: 955 us); CTA pairs on one 256-token tile (the MMAs run at 530 cycles,

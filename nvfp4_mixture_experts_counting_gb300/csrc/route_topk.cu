@@ -17,6 +17,11 @@
 // of all values, so the few values from it on hold the choice: they are
 // gathered, a lane each, and each counts those before it.  (k rounds of finding
 // the largest value by two reductions took twice the instructions.)
+//
+// The forward call is bound by issue slots, not by its bytes (2.6 us of DRAM):
+// 16384 tokens of 256 experts in eight groups with biases 22 us, two thirds of
+// the slots busy; 16 tokens 5.4 us with the call, some 2.5 on the device.  The
+// gradient is a launch and one pass: 16384 tokens 6 us in a graph.
 #include <cfloat>
 
 #include "fp8_common.cuh"
