@@ -283,7 +283,8 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, unsigned char* s
     for (int p = 0; p < 128 / kPiece; ++p) {
       if (c0 + p * kPiece >= a.O) continue;
       unsigned char* to = st + (p & 1) * 1024;
-      if (lane == 0) bulk_wait_read<1>();
+      // the tile before may have ended with either piece
+      if (lane == 0) p == 0 ? bulk_wait_read<0>() : bulk_wait_read<1>();
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 2; ++i) {

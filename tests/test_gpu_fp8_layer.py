@@ -314,6 +314,21 @@ def test_product_rounds_once(M, counts, dtype):
     within(out, y, UNIT[dtype] * y.abs() + TINY[dtype] + bound * (1 + UNIT[dtype]))
 
 
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+@pytest.mark.parametrize("N", [8, 16, 24, 48, 80])
+def test_product_of_many_narrow_tiles(N, dtype):
+    """Hundreds of short tiles a CTA: none goes out from shared memory that the next one writes."""
+    g = gen(25 + N)
+    M, K = 2_000_000, 16
+    a, a_scale = rows_of(g, M, K)
+    w, w_scale = bank(g, 1, N, K)
+    y, bound = product(a, a_scale, w, w_scale, [M], False)
+    for _ in range(3):
+        out = run_product(a, a_scale, w, w_scale, [M], dtype)
+        unit = UNIT.get(dtype, 0.0)
+        within(out, y, unit * y.abs() + TINY[dtype] + bound * (1 + unit))
+
+
 @pytest.mark.parametrize("M,counts", COUNTS, ids=lambda v: str(v) if isinstance(v, int) else "")
 @pytest.mark.parametrize("N,K", [(16, 16), (128, 128), (144, 272), (640, 400), (1280, 2560)])
 def test_product_with_columns(N, K, M, counts):
