@@ -20,7 +20,7 @@
 // memory are 96 KB a block at 128 bytes a cycle), the commit's arrival 155,
 // reading and summing 450, two hand-offs by mbarrier some 150; half of the sum
 // is the time of a block.  16384 tokens of 8 of 256 experts, gate_up [1280,
-// 2560] with SwiGLU: 490 us, 1.75 PFLOP/s; its input's gradient 547 us; down
+// 2560] with SwiGLU: 467 us, 1.84 PFLOP/s; its input's gradient 547 us; down
 // 346 us; one matrix of 4096 x 4096 with 4096 rows 74 us, 1.86 PFLOP/s.  With
 // few tokens the weights' bytes: 256 tokens of the same layer 154 us, 5.3 TB/s;
 // 16 tokens 50 us, 4.9 TB/s (units of uneven experts over 152 SMs).
@@ -28,8 +28,9 @@
 // Measured and not kept: tokens as the MMA's columns (scales then differ by
 // column: 955 us); CTA pairs on one 256-token tile (the MMAs run at 530 cycles,
 // but the hand-offs cross CTAs and a quarter of the rows are empty: 512 us);
-// 16 summing warps (spills: 893 us); scales by a warp of their own through
-// shared memory (479 us, but 590 instead of 557 us for the input's gradient).
+// 16 summing warps of 64 columns (543 us: warp 0's copies slow those beside it);
+// wider or double-buffered reads of tensor memory (537 us, spills); blocks by
+// twos with registers of their own for the scales (524 us).
 // For few tokens: narrow tiles of the tokens as columns (64 tokens through down
 // 80 us, here 68), pairs of CTAs that share a unit's blocks (16 tokens through
 // gate_up 76 us, here 58; the exchange of sums costs more than idle SMs).
@@ -73,7 +74,11 @@ constexpr int kStageBytes = 3 * kTile, kStages = 4;  // a block's tokens and 256
 constexpr int kBox = 32;                             // tokens of one copy
 constexpr int kStaged = 2048, kOut = 8 * kStaged;    // of a summing warp: 64 bytes of 32 tokens
 constexpr int kTops = kTokens * 2 * 4;               // a token's largest magnitude in each warpgroup
-constexpr int kFixed = kOut + kTops;
+// Scales of a block on their way through shared memory (with SwiGLU): its tokens', gate's and up's.  A slot is written
+// once the MMAs of the block four before are done, hence the sums of the block six before.
+constexpr int kScaleSlots = 8, kScaleBytes = (kTokens + 4) * 4;
+static_assert(kScaleSlots >= kStages + kBufs, "");
+constexpr int kFixed = kOut + kTops + kScaleSlots * kScaleBytes;
 constexpr int smem_bytes(int E) { return 1024 + kStages * kStageBytes + kFixed + 512 + 2 * 4 * (E + 1); }
 static_assert(smem_bytes(kMaxBins) <= kSmemMax, "");
 
@@ -119,6 +124,14 @@ __device__ __forceinline__ void elected_commit(uint64_t* bar) {
   asm volatile(FTMOE_ELECTED("@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n") ::"r"(
                    smem_u32(bar))
                : "memory");
+}
+
+// 4 bytes to shared memory behind the warp's back; the barrier gets an arrival from each lane when its copies are there.
+__device__ __forceinline__ void copy_4(void* to, const float* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void arrive_copied(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 template <int N>
@@ -374,13 +387,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
   unsigned char* staged = sm + kStages * kStageBytes;
   uint32_t* tops = reinterpret_cast<uint32_t*>(staged + kOut);
+  float* scales = reinterpret_cast<float*>(staged + kOut + kTops);
   uint64_t* full = reinterpret_cast<uint64_t*>(staged + kFixed);
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + kBufs;
   uint64_t* drain = acc_empty + kBufs;
   uint64_t* row_bar = drain + 1;  // [4], the warps that hold the same tokens
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(row_bar + 4);
+  uint64_t* scaled = row_bar + 4;  // [kScaleSlots]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scaled + kScaleSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int *t_start = reinterpret_cast<int*>(staged + kFixed + 512), *t_first = t_start + a.E + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -397,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(drain, 2);
     for (int w = 0; w < 4; ++w) mbar_init(&row_bar[w], 2);
+    for (int i = 0; i < kScaleSlots; ++i) mbar_init(&scaled[i], 32);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&map_w);
@@ -422,6 +438,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Unit x = unit_of(tables, u, e);
         e = x.e;
         const int boxes = (x.rows + kBox - 1) / kBox;  // the rows behind them in shared memory are nobody's
+        // with SwiGLU: this lane's tokens' scales, and lane 0 gate's, lane 1 up's
+        const float* from_x = a.a_scale + x.row0 + lane;
+        const float* from_w = a.w_scale + ((int64_t)x.e * a.NB + x.jt + lane * (a.O / 128)) * a.KB;
         for (int kb = 0; kb < nkb; ++kb, ++k) {
           if (!warp_wait(&empty[s], phase, a.status)) {
             *abort_flag = 1;
@@ -440,6 +459,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           for (int i = 0; i < boxes; ++i)
             elected_load_2d(sx + i * kBox * 128, &map_x, kb * 128, x.row0 + i * kBox, &full[s]);
+          if constexpr (SWIGLU) {
+            float* sc = scales + k % kScaleSlots * (kScaleBytes / 4);
+#pragma unroll
+            for (int i = 0; i < kTokens; i += 32)
+              if (lane + i < x.rows) copy_4(sc + lane + i, from_x + i);
+            if (lane < 2) copy_4(sc + kTokens + lane, from_w + kb);
+            arrive_copied(&scaled[k % kScaleSlots]);
+            from_x += a.M;
+          }
           if (++s == kStages) {
             s = 0;
             phase ^= 1;
@@ -447,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // nothing this warp issued may still be landing when the CTA exits
+      if (SWIGLU) asm volatile("cp.async.wait_all;" ::: "memory");
       for (int q = k > kStages ? k - kStages : 0; q < k; ++q) mbar_wait(&full[q % kStages], (q / kStages) & 1, a.status);
     } else if (warp == 1 || warp == 3) {
       // ---------------- products: warp 1 has the even blocks, warp 3 the odd ones.  Issuing waits while the tensor
@@ -510,35 +539,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool on = token < x.rows;
       const float* sx = a.a_scale + x.row0 + token;
       // weights' scales: [e][block of rows][block of columns]; TRANS contracts the rows
-      const int nb = SWIGLU ? x.jt : 2 * x.jt + wg;
+      const int nb = 2 * x.jt + wg;
       const bool there = nb * 128 < a.O;  // a last tile may have only its first half
-      const int64_t sw_step = TRANS ? a.KB : 1, up = (int64_t)(a.O / 128) * a.KB;
+      const int64_t sw_step = TRANS ? a.KB : 1;
       const float* sw = a.w_scale + ((int64_t)x.e * a.NB + (TRANS ? 0 : nb)) * a.KB + (TRANS ? nb : 0);
       uint64_t acc2[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc2[i] = 0ull;
-      // scales of three blocks on their way: each comes from another line, maybe from DRAM
+      // Scales: each comes from another line, maybe from DRAM.  With SwiGLU, three a block, warp 0 copies them to shared
+      // memory beside the tiles (16384 tokens 490 -> 467 us, 4096 tokens 200 -> 182).  Otherwise, two a block, this warp
+      // loads them three blocks ahead (by warp 0: one matrix of 4096 x 4096 with 4096 rows 84 instead of 75 us, 16384
+      // tokens through gate_up 487 instead of 478, its input's gradient 567 instead of 547).
       constexpr int kAhead = 3;
-      float v[kAhead], w0[kAhead], w1[kAhead];
+      float v[kAhead], w0[kAhead];
       const auto fetch = [&](int kb, int to) {
-        if (kb >= nkb) return;
+        if (SWIGLU || kb >= nkb) return;
         v[to] = on ? sx[(int64_t)kb * a.M] : 0.f;
         w0[to] = there ? sw[kb * sw_step] : 0.f;
-        if (SWIGLU) w1[to] = sw[up + kb];
       };
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) fetch(i, i);
       for (int kb = 0; kb < nkb; ++kb, ++k) {
         const int b = k & 1;
-        const float s0 = v[0] * w0[0], s1 = SWIGLU ? v[0] * w1[0] : s0;
-        const uint64_t s2[2] = {pack2(s0, s0), pack2(s1, s1)};
+        float s0, s1;
+        if constexpr (SWIGLU) {
+          if (!warp_wait(&scaled[k % kScaleSlots], k / kScaleSlots & 1, a.status)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          const float* sc = scales + k % kScaleSlots * (kScaleBytes / 4);
+          s0 = sc[token] * sc[kTokens];
+          s1 = sc[token] * sc[kTokens + 1];
+        } else {
+          s0 = s1 = v[0] * w0[0];
 #pragma unroll
-        for (int i = 0; i + 1 < kAhead; ++i) {
-          v[i] = v[i + 1];
-          w0[i] = w0[i + 1];
-          if (SWIGLU) w1[i] = w1[i + 1];
+          for (int i = 0; i + 1 < kAhead; ++i) {
+            v[i] = v[i + 1];
+            w0[i] = w0[i + 1];
+          }
+          fetch(kb + kAhead, kAhead - 1);
         }
-        fetch(kb + kAhead, kAhead - 1);
+        const uint64_t s2[2] = {pack2(s0, s0), pack2(s1, s1)};
         if (!warp_wait(&acc_full[b], (k >> 1) & 1, a.status)) {
           *abort_flag = 1;
           ok = false;
