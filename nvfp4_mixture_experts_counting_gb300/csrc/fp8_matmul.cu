@@ -15,21 +15,23 @@
 // columns.  tcgen05 sums a block of 128 products in fp32, so an output rounds
 // once per block and once at the end.
 //
-// What bounds it: with many tokens the ring over the two buffers.  A block's
-// MMAs take 512 cycles (700 beside the copies: operands in and out of shared
-// memory are 96 KB a block at 128 bytes a cycle), the commit's arrival 155,
-// reading and summing 450, two hand-offs by mbarrier some 150; half of the sum
-// is the time of a block.  16384 tokens of 8 of 256 experts, gate_up [1280,
-// 2560] with SwiGLU: 467 us, 1.84 PFLOP/s; its input's gradient 547 us; down
-// 346 us; one matrix of 4096 x 4096 with 4096 rows 74 us, 1.86 PFLOP/s.  With
-// few tokens the weights' bytes: 256 tokens of the same layer 154 us, 5.3 TB/s;
-// 16 tokens 50 us, 4.9 TB/s (units of uneven experts over 152 SMs).
+// What bounds it: with many tokens, tensor memory's two uses.  A block takes 1150
+// to 1300 cycles, of which its MMAs are busy 512 (585 from the first issue to
+// the last) and a warp's reads and sums 550.  Clocks taken in the kernel show
+// both waiting for little else, and the time stays the same with twice the
+// summing warps, with reads that overlap the sums, and with scales that are
+// there in time: reads and MMAs seem to share tensor memory's port and hardly
+// overlap.  16384 tokens of 8 of 256 experts, gate_up [1280, 2560] with SwiGLU:
+// 467 us, 1.84 PFLOP/s; its input's gradient 543 us; down 342 us; one matrix of
+// 4096 x 4096 with 4096 rows 75 us, 1.82 PFLOP/s.  With few tokens the weights'
+// bytes: 256 tokens of the same layer 152 us, 5.4 TB/s; 16 tokens 49 us, 5.0
+// TB/s (units of uneven experts over 152 SMs).
 //
 // Measured and not kept: tokens as the MMA's columns (scales then differ by
 // column: 955 us); CTA pairs on one 256-token tile (the MMAs run at 530 cycles,
 // but the hand-offs cross CTAs and a quarter of the rows are empty: 512 us);
 // 16 summing warps of 64 columns (543 us: warp 0's copies slow those beside it);
-// wider or double-buffered reads of tensor memory (537 us, spills); blocks by
+// reads of 32 columns of tensor memory (537 us, spills); blocks by
 // twos with registers of their own for the scales (524 us).
 // For few tokens: narrow tiles of the tokens as columns (64 tokens through down
 // 80 us, here 68), pairs of CTAs that share a unit's blocks (16 tokens through
@@ -258,14 +260,23 @@ __device__ __forceinline__ float silu_quick(float g) {
   return g * r;
 }
 
-// 32 lanes x 16 columns of tensor memory, a lane's columns in its registers (see tc_ld_16x32 on memory order).
+// 32 lanes x 16 columns of tensor memory, a lane's columns in its registers, which are there after tc_wait (see
+// tc_ld_16x32 on memory order).
 __device__ __forceinline__ void tc_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+// The registers pass through it, so that no use of them moves before it.
+__device__ __forceinline__ void tc_wait(uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+        "+r"(r[14]), "+r"(r[15]));
 }
 
 // 32 bytes to a 32-byte-aligned address.
@@ -587,10 +598,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
+        // 16 columns are on their way while 16 are added (the input's gradient 547 -> 543 us, down 346 -> 342)
+        uint32_t r[2][16];
+        const auto column = [&](int h) { return from + b * kCols + (SWIGLU && h >= 4 ? 128 - 64 : 0) + 16 * h; };
+        tc_ld_32x16(column(0), r[0]);
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
-          uint32_t r[16];
-          tc_ld_32x16(from + b * kCols + (SWIGLU && h >= 4 ? 128 - 64 : 0) + 16 * h, r);
+          tc_wait(r[h & 1]);
+          if (h < 7) tc_ld_32x16(column(h + 1), r[h + 1 & 1]);
           if (h == 7) {
             tc_fence_before();
             __syncwarp();
@@ -598,8 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            acc2[8 * h + i] =
-                fma2(pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), s2[h / 4], acc2[8 * h + i]);
+            acc2[8 * h + i] = fma2(pack2(__uint_as_float(r[h & 1][2 * i]), __uint_as_float(r[h & 1][2 * i + 1])), s2[h / 4],
+                                   acc2[8 * h + i]);
         }
       }
       if (!ok) break;
