@@ -159,9 +159,9 @@ __device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float& d
 
 // Quantised output: eight lanes take 128 columns of a row.  GRAD writes a row
 // of 2 I codes, gate's first.  131072 x 640 from bf16: 74 us, 5.7 TB/s, the issue
-// slots three quarters busy with the exponentials' instructions (the
-// approximate reciprocal is within the stated error; with the division that
-// the compiler makes it was bound by them altogether).
+// slots three quarters busy with the exponentials' instructions (104 us with a
+// division in the sigmoid instead of the approximate reciprocal; its gradient to
+// codes 151 instead of 112 us, 6.0 TB/s).
 template <typename T, bool GRAD>
 __global__ void __launch_bounds__(kThreads) k_swiglu_fp8(const T* gu, const T* dh, int rows_, int I,
                                                          const int32_t* used, uint8_t* codes, float* scales,

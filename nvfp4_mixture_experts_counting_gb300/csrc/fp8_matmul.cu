@@ -37,7 +37,8 @@
 // 80 us, here 68), pairs of CTAs that share a unit's blocks (16 tokens through
 // gate_up 76 us, here 58; the exchange of sums costs more than idle SMs).
 //
-// Warps: 0 copies tiles by TMA, 1 and 3 issue the MMAs, 4-11 add up.
+// Warps: 0 copies tiles by TMA (and with SwiGLU the scales), 1 and 3 issue the
+// MMAs, 4-11 add up.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
