@@ -66,6 +66,7 @@ struct MatmulArgs {
   int NB, KB;  // blocks of the weights' rows and columns
   int JT;      // weight tiles of an expert
   int dtype;
+  int box;      // tokens of one copy: 32, or 128
   int map_out;  // rows are whole 16 bytes: tiles may go out by TMA
   void* out;
   float* out_scale;
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = blockIdx.x; u < n_units && !*abort_flag; u += gridDim.x) {
         const Unit x = unit_of(tables, u, e);
         e = x.e;
-        const int boxes = (x.rows + kBox - 1) / kBox;  // the rows behind them in shared memory are nobody's
+        const int boxes = (x.rows + a.box - 1) / a.box;  // the rows behind them in shared memory are nobody's
         // with SwiGLU: this lane's tokens' scales, and lane 0 gate's, lane 1 up's
         const float* from_x = a.a_scale + x.row0 + lane;
         const float* from_w = a.w_scale + ((int64_t)x.e * a.NB + x.jt + lane * (a.O / 128)) * a.KB;
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           unsigned char* sx = sm + s * kStageBytes;
           unsigned char* sw = sx + kTile;
-          elected_expect(&full[s], 2 * kTile + boxes * kBox * 128);
+          elected_expect(&full[s], 2 * kTile + boxes * a.box * 128);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int n0 = SWIGLU ? h * a.O + x.jt * 128 : x.jt * 256 + h * 128;
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               elected_load_3d(sw + h * kTile, &map_w, kb * 128, n0, x.e, &full[s]);
           }
           for (int i = 0; i < boxes; ++i)
-            elected_load_2d(sx + i * kBox * 128, &map_x, kb * 128, x.row0 + i * kBox, &full[s]);
+            elected_load_2d(sx + i * a.box * 128, &map_x, kb * 128, x.row0 + i * a.box, &full[s]);
           if constexpr (SWIGLU) {
             float* sc = scales + k % kScaleSlots * (kScaleBytes / 4);
 #pragma unroll
@@ -741,7 +742,8 @@ cudaError_t launch_fp8_matmul(const TrainDevice& d, const ftmoe_fp8_matmul_args&
   cudaError_t e = encode_map(&map_w, m.w, 3, wd, ws, wb);
   if (e != cudaSuccess) return e;
   const uint64_t xd[2] = {(uint64_t)a.C, (uint64_t)m.M}, xs[1] = {(uint64_t)a.C};
-  const uint32_t xb[2] = {128, kBox};
+  a.box = m.M / m.E >= kTokens ? kTokens : kBox;
+  const uint32_t xb[2] = {128, (uint32_t)a.box};
   if ((e = encode_map(&map_x, m.a, 2, xd, xs, xb)) != cudaSuccess) return e;
   CUtensorMap map_out = map_x;
   if (!m.swiglu) {
