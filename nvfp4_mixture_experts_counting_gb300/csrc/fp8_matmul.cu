@@ -15,30 +15,34 @@
 // columns.  tcgen05 sums a block of 128 products in fp32, so an output rounds
 // once per block and once at the end.
 //
-// What bounds it: with many tokens, tensor memory's two uses.  A block takes 1150
-// to 1300 cycles, of which its MMAs are busy 512 (585 from the first issue to
-// the last) and a warp's reads and sums 550.  Clocks taken in the kernel show
-// both waiting for little else, and the time stays the same with twice the
-// summing warps, with reads that overlap the sums, and with scales that are
-// there in time: reads and MMAs seem to share tensor memory's port and hardly
-// overlap.  16384 tokens of 8 of 256 experts, gate_up [1280, 2560] with SwiGLU:
-// 467 us, 1.84 PFLOP/s; its input's gradient 543 us; down 342 us; one matrix of
-// 4096 x 4096 with 4096 rows 75 us, 1.82 PFLOP/s.  With few tokens the weights'
-// bytes: 256 tokens of the same layer 152 us, 5.4 TB/s; 16 tokens 49 us, 5.0
-// TB/s (units of uneven experts over 152 SMs).
+// What bounds it: with many tokens the summing warps.  A block takes some 1050
+// cycles, of which its MMAs are busy 512 (585 from the first issue to the last)
+// and a warp's reads and sums 550; the waits for the block and for its scales are
+// 120 to 150 each even where nothing is to be waited for, and what other warps
+// issue slows those beside them.  16384 tokens of 8 of 256 experts, gate_up [1280,
+// 2560] with SwiGLU: 442 us, 1.94 PFLOP/s; its input's gradient 516 us; down 330
+// us; one matrix of 4096 x 4096 with 4096 rows 74 us, 1.86 PFLOP/s.  With few
+// tokens the weights' bytes: 256 tokens of the same layer 152 us, 5.4 TB/s; 16
+// tokens 49 us, 5.0 TB/s (units of uneven experts over 152 SMs).
+//
+// So the copies are spread: one of 128 tokens where experts have that many (32
+// otherwise: the smaller copies read less of the next expert's rows; 16384 tokens
+// with SwiGLU 436 instead of 465 us), weights by one warp and tokens by another,
+// on different schedulers, and the scales through shared memory by the second
+// (loaded by the summing warps three blocks ahead: the input's gradient 539, down
+// 344, gate_up without SwiGLU 473 instead of 446 us).
 //
 // Measured and not kept: tokens as the MMA's columns (scales then differ by
 // column: 955 us); CTA pairs on one 256-token tile (the MMAs run at 530 cycles,
 // but the hand-offs cross CTAs and a quarter of the rows are empty: 512 us);
-// 16 summing warps of 64 columns (543 us: warp 0's copies slow those beside it);
-// reads of 32 columns of tensor memory (537 us, spills); blocks by
-// twos with registers of their own for the scales (524 us).
+// 16 summing warps of 64 columns (543 us when one warp made all copies); reads of
+// 32 columns of tensor memory (537 us).
 // For few tokens: narrow tiles of the tokens as columns (64 tokens through down
 // 80 us, here 68), pairs of CTAs that share a unit's blocks (16 tokens through
 // gate_up 76 us, here 58; the exchange of sums costs more than idle SMs).
 //
-// Warps: 0 copies tiles by TMA (and with SwiGLU the scales), 1 and 3 issue the
-// MMAs, 4-11 add up.
+// Warps: 0 copies the weights' tiles by TMA, 2 the tokens' and the scales, 1 and 3
+// issue the MMAs, 4-11 add up.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -78,7 +82,7 @@ constexpr int kStageBytes = 3 * kTile, kStages = 4;  // a block's tokens and 256
 constexpr int kBox = 32;                             // tokens of one copy
 constexpr int kStaged = 2048, kOut = 8 * kStaged;    // of a summing warp: 64 bytes of 32 tokens
 constexpr int kTops = kTokens * 2 * 4;               // a token's largest magnitude in each warpgroup
-// Scales of a block on their way through shared memory (with SwiGLU): its tokens', gate's and up's.  A slot is written
+// Scales of a block on their way through shared memory: its tokens' and two of the weights'.  A slot is written
 // once the MMAs of the block four before are done, hence the sums of the block six before.
 constexpr int kScaleSlots = 8, kScaleBytes = (kTokens + 4) * 4;
 static_assert(kScaleSlots >= kStages + kBufs, "");
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < kBufs; ++b) {
@@ -443,17 +447,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kSumWarp0) {
     regs_down<kLowRegs>();
-    if (warp == 0) {
-      // ---------------- copies
+    if (warp == 0 || warp == 2) {
+      // ---------------- copies: warp 0 has the weights, warp 2 the tokens and the scales
       int s = 0, k = 0, e = 0;
       uint32_t phase = 1;  // a new barrier's phase 1 counts as over
       for (int u = blockIdx.x; u < n_units && !*abort_flag; u += gridDim.x) {
         const Unit x = unit_of(tables, u, e);
         e = x.e;
         const int boxes = (x.rows + a.box - 1) / a.box;  // the rows behind them in shared memory are nobody's
-        // with SwiGLU: this lane's tokens' scales, and lane 0 gate's, lane 1 up's
+        // this lane's tokens' scales, and of lanes 0 and 1 the weights' ([e][block of rows][block of columns]; TRANS
+        // contracts the rows)
+        const int nb = SWIGLU ? x.jt + lane * (a.O / 128) : 2 * x.jt + lane;
+        const bool mine = lane < 2 && (SWIGLU || nb * 128 < a.O);  // a last tile may have only its first half
+        const int w_step = TRANS ? a.KB : 1;
         const float* from_x = a.a_scale + x.row0 + lane;
-        const float* from_w = a.w_scale + ((int64_t)x.e * a.NB + x.jt + lane * (a.O / 128)) * a.KB;
+        const float* from_w = a.w_scale + ((int64_t)x.e * a.NB + (TRANS ? 0 : nb)) * a.KB + (TRANS ? nb : 0);
         for (int kb = 0; kb < nkb; ++kb, ++k) {
           if (!warp_wait(&empty[s], phase, a.status)) {
             *abort_flag = 1;
@@ -461,25 +469,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           unsigned char* sx = sm + s * kStageBytes;
           unsigned char* sw = sx + kTile;
-          elected_expect(&full[s], 2 * kTile + boxes * a.box * 128);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int n0 = SWIGLU ? h * a.O + x.jt * 128 : x.jt * 256 + h * 128;
-            if (TRANS)
-              elected_load_3d(sw + h * kTile, &map_w, n0, kb * 128, x.e, &full[s]);
-            else
-              elected_load_3d(sw + h * kTile, &map_w, kb * 128, n0, x.e, &full[s]);
-          }
-          for (int i = 0; i < boxes; ++i)
-            elected_load_2d(sx + i * a.box * 128, &map_x, kb * 128, x.row0 + i * a.box, &full[s]);
-          if constexpr (SWIGLU) {
+          if (warp == 0) {
+            elected_expect(&full[s], 2 * kTile);
+            if constexpr (SWIGLU) {
+              elected_load_3d(sw, &map_w, kb * 128, x.jt * 128, x.e, &full[s]);
+              elected_load_3d(sw + kTile, &map_w, kb * 128, a.O + x.jt * 128, x.e, &full[s]);
+            } else if constexpr (TRANS) {
+              elected_load_3d(sw, &map_w, x.jt * 256, kb * 128, x.e, &full[s]);
+              elected_load_3d(sw + kTile, &map_w, x.jt * 256 + 128, kb * 128, x.e, &full[s]);
+            } else {
+              elected_load_3d(sw, &map_w, kb * 128, x.jt * 256, x.e, &full[s]);
+            }
+          } else {
+            elected_expect(&full[s], boxes * a.box * 128);
+            for (int i = 0; i < boxes; ++i)
+              elected_load_2d(sx + i * a.box * 128, &map_x, kb * 128, x.row0 + i * a.box, &full[s]);
             float* sc = scales + k % kScaleSlots * (kScaleBytes / 4);
 #pragma unroll
             for (int i = 0; i < kTokens; i += 32)
               if (lane + i < x.rows) copy_4(sc + lane + i, from_x + i);
-            if (lane < 2) copy_4(sc + kTokens + lane, from_w + kb);
+            if (mine) copy_4(sc + kTokens + lane, from_w);
             arrive_copied(&scaled[k % kScaleSlots]);
             from_x += a.M;
+            from_w += w_step;
           }
           if (++s == kStages) {
             s = 0;
@@ -488,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // nothing this warp issued may still be landing when the CTA exits
-      if (SWIGLU) asm volatile("cp.async.wait_all;" ::: "memory");
+      asm volatile("cp.async.wait_all;" ::: "memory");
       for (int q = k > kStages ? k - kStages : 0; q < k; ++q) mbar_wait(&full[q % kStages], (q / kStages) & 1, a.status);
     } else if (warp == 1 || warp == 3) {
       // ---------------- products: warp 1 has the even blocks, warp 3 the odd ones.  Issuing waits while the tensor
@@ -550,49 +562,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Unit x = unit_of(tables, u, e);
       e = x.e;
       const bool on = token < x.rows;
-      const float* sx = a.a_scale + x.row0 + token;
-      // weights' scales: [e][block of rows][block of columns]; TRANS contracts the rows
-      const int nb = 2 * x.jt + wg;
-      const bool there = nb * 128 < a.O;  // a last tile may have only its first half
-      const int64_t sw_step = TRANS ? a.KB : 1;
-      const float* sw = a.w_scale + ((int64_t)x.e * a.NB + (TRANS ? 0 : nb)) * a.KB + (TRANS ? nb : 0);
       uint64_t acc2[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc2[i] = 0ull;
-      // Scales: each comes from another line, maybe from DRAM.  With SwiGLU, three a block, warp 0 copies them to shared
-      // memory beside the tiles (16384 tokens 490 -> 467 us, 4096 tokens 200 -> 182).  Otherwise, two a block, this warp
-      // loads them three blocks ahead (by warp 0: one matrix of 4096 x 4096 with 4096 rows 84 instead of 75 us, 16384
-      // tokens through gate_up 487 instead of 478, its input's gradient 567 instead of 547).
-      constexpr int kAhead = 3;
-      float v[kAhead], w0[kAhead];
-      const auto fetch = [&](int kb, int to) {
-        if (SWIGLU || kb >= nkb) return;
-        v[to] = on ? sx[(int64_t)kb * a.M] : 0.f;
-        w0[to] = there ? sw[kb * sw_step] : 0.f;
-      };
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) fetch(i, i);
       for (int kb = 0; kb < nkb; ++kb, ++k) {
         const int b = k & 1;
-        float s0, s1;
-        if constexpr (SWIGLU) {
-          if (!warp_wait(&scaled[k % kScaleSlots], k / kScaleSlots & 1, a.status)) {
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-          const float* sc = scales + k % kScaleSlots * (kScaleBytes / 4);
-          s0 = sc[token] * sc[kTokens];
-          s1 = sc[token] * sc[kTokens + 1];
-        } else {
-          s0 = s1 = v[0] * w0[0];
-#pragma unroll
-          for (int i = 0; i + 1 < kAhead; ++i) {
-            v[i] = v[i + 1];
-            w0[i] = w0[i + 1];
-          }
-          fetch(kb + kAhead, kAhead - 1);
+        if (!warp_wait(&scaled[k % kScaleSlots], k / kScaleSlots & 1, a.status)) {
+          *abort_flag = 1;
+          ok = false;
+          break;
         }
+        const float* sc = scales + k % kScaleSlots * (kScaleBytes / 4);
+        const float v = sc[token], s0 = v * sc[kTokens + (SWIGLU ? 0 : wg)], s1 = SWIGLU ? v * sc[kTokens + 1] : s0;
         const uint64_t s2[2] = {pack2(s0, s0), pack2(s1, s1)};
         if (!warp_wait(&acc_full[b], (k >> 1) & 1, a.status)) {
           *abort_flag = 1;
@@ -738,7 +719,7 @@ cudaError_t launch_fp8_matmul(const TrainDevice& d, const ftmoe_fp8_matmul_args&
   a.status = d.status;
   CUtensorMap map_w, map_x;
   const uint64_t wd[3] = {(uint64_t)m.K, (uint64_t)m.N, (uint64_t)m.E}, ws[2] = {(uint64_t)m.K, (uint64_t)m.N * m.K};
-  const uint32_t wb[3] = {128, 128, 1};
+  const uint32_t wb[3] = {128, m.swiglu || m.transpose ? 128u : 256u, 1};
   cudaError_t e = encode_map(&map_w, m.w, 3, wd, ws, wb);
   if (e != cudaSuccess) return e;
   const uint64_t xd[2] = {(uint64_t)a.C, (uint64_t)m.M}, xs[1] = {(uint64_t)a.C};
