@@ -20,7 +20,7 @@
 // and a warp's reads and sums 550; the waits for the block and for its scales are
 // 120 to 150 each even where nothing is to be waited for, and what other warps
 // issue slows those beside them.  16384 tokens of 8 of 256 experts, gate_up [1280,
-// 2560] with SwiGLU: 442 us, 1.94 PFLOP/s; its input's gradient 516 us; down 330
+// 2560] with SwiGLU: 432 us, 1.99 PFLOP/s; its input's gradient 512 us; down 330
 // us; one matrix of 4096 x 4096 with 4096 rows 74 us, 1.86 PFLOP/s.  With few
 // tokens the weights' bytes: 256 tokens of the same layer 152 us, 5.4 TB/s; 16
 // tokens 49 us, 5.0 TB/s (units of uneven experts over 152 SMs).
