@@ -715,6 +715,13 @@ typedef struct {
 
 int ftmoe_fp8_matmul(const ftmoe_fp8_matmul_args* args, ftmoe_stream_t stream);
 
+/* Test hook of ftmoe_fp8_matmul's failure path, like ftmoe_test_withhold_policy.
+ * While enabled, a call's first CTA never asks for the tokens of its first
+ * block, and the call's waits give up after wait_limit_ns.  The kernel sets the
+ * status word's timeout bit and finishes; the tiles of that CTA stay as they
+ * were, others come out as usual. */
+int ftmoe_test_withhold_matmul(int enable, int64_t wait_limit_ns);
+
 /* h = SiLU(gu[:, :I]) * gu[:, I:] in fp32, for gu [rows, 2I] of `dtype`.
  * scales NULL: out [rows, I] of `dtype`.  Otherwise out is codes [rows, I] and
  * scales [I/128][rows], I a multiple of 128.  `used`: NULL, or the device count

@@ -75,6 +75,8 @@ struct MatmulArgs {
   void* out;
   float* out_scale;
   uint32_t* status;
+  uint32_t wait_ns;  // limit of a wait
+  int withhold;      // a test's: the first CTA never asks for its first block's tokens and scales
 };
 
 constexpr int kTokens = 128;
@@ -229,7 +231,7 @@ __device__ __forceinline__ Unit unit_of(const Tables& t, int u, int e) {
 }
 
 // mbar_wait for waits that are mostly over when they begin.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const MatmulArgs& a) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
   for (uint32_t i = 1;; ++i) {
@@ -238,15 +240,17 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* s
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done) : "r"(smem_u32(bar)), "r"(parity), "r"(20000u) : "memory");
     if (done) return true;
-    if (globaltimer() - t0 > kWaitLimitNs) {
-      set_status(status, kStatusTimeout);
+    if (globaltimer() - t0 > a.wait_ns) {
+      set_status(a.status, kStatusTimeout);
       return false;
     }
   }
 }
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
-  return __all_sync(0xffffffffu, wait(bar, parity, status));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const MatmulArgs& a) {
+  return __all_sync(0xffffffffu, wait(bar, parity, a));
 }
+// Has a wait of the CTA run out?  The lanes agree: one that left its loop alone would leave the others waiting for it.
+__device__ __forceinline__ bool given_up(const volatile int* flag) { return __any_sync(0xffffffffu, *flag); }
 
 __device__ __forceinline__ uint32_t halves(float lo, float hi, int dtype) {
   if (dtype == FTMOE_FP16) {
@@ -449,9 +453,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_down<kLowRegs>();
     if (warp == 0 || warp == 2) {
       // ---------------- copies: warp 0 has the weights, warp 2 the tokens and the scales
+      const bool withhold = a.withhold && blockIdx.x == 0;
       int s = 0, k = 0, e = 0;
       uint32_t phase = 1;  // a new barrier's phase 1 counts as over
-      for (int u = blockIdx.x; u < n_units && !*abort_flag; u += gridDim.x) {
+      for (int u = blockIdx.x; u < n_units && !given_up(abort_flag); u += gridDim.x) {
         const Unit x = unit_of(tables, u, e);
         e = x.e;
         const int boxes = (x.rows + a.box - 1) / a.box;  // the rows behind them in shared memory are nobody's
@@ -463,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* from_x = a.a_scale + x.row0 + lane;
         const float* from_w = a.w_scale + ((int64_t)x.e * a.NB + (TRANS ? 0 : nb)) * a.KB + (TRANS ? nb : 0);
         for (int kb = 0; kb < nkb; ++kb, ++k) {
-          if (!warp_wait(&empty[s], phase, a.status)) {
+          if (!warp_wait(&empty[s], phase, a)) {
             *abort_flag = 1;
             break;
           }
@@ -480,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               elected_load_3d(sw, &map_w, kb * 128, x.jt * 256, x.e, &full[s]);
             }
-          } else {
+          } else if (k > 0 || !withhold) {
             elected_expect(&full[s], boxes * a.box * 128);
             for (int i = 0; i < boxes; ++i)
               elected_load_2d(sx + i * a.box * 128, &map_x, kb * 128, x.row0 + i * a.box, &full[s]);
@@ -490,9 +495,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (lane + i < x.rows) copy_4(sc + lane + i, from_x + i);
             if (mine) copy_4(sc + kTokens + lane, from_w);
             arrive_copied(&scaled[k % kScaleSlots]);
-            from_x += a.M;
-            from_w += w_step;
           }
+          from_x += a.M;
+          from_w += w_step;
           if (++s == kStages) {
             s = 0;
             phase ^= 1;
@@ -501,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // nothing this warp issued may still be landing when the CTA exits
       asm volatile("cp.async.wait_all;" ::: "memory");
-      for (int q = k > kStages ? k - kStages : 0; q < k; ++q) mbar_wait(&full[q % kStages], (q / kStages) & 1, a.status);
+      for (int q = k > kStages ? k - kStages : 0; q < k; ++q) mbar_wait(&full[q % kStages], (q / kStages) & 1, a.status, a.wait_ns);
     } else if (warp == 1 || warp == 3) {
       // ---------------- products: warp 1 has the even blocks, warp 3 the odd ones.  Issuing waits while the tensor
       // cores are behind, and what comes between two blocks (the commits, the waits for the next one's buffers) is
@@ -517,10 +522,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = b, first = b;  // the stage; this warp's first block of the unit
       uint32_t full_phase = 0, acc_phase = 1;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < n_units && !*abort_flag; u += gridDim.x) {
+      for (int u = blockIdx.x; ok && u < n_units && !given_up(abort_flag); u += gridDim.x) {
         int kb = first;
         for (; kb < nkb; kb += 2) {
-          if (!warp_wait(&acc_empty[b], acc_phase, a.status) || !warp_wait(&full[s], full_phase, a.status)) {
+          if (!warp_wait(&acc_empty[b], acc_phase, a) || !warp_wait(&full[s], full_phase, a)) {
             *abort_flag = 1;
             ok = false;
             break;
@@ -547,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         first = kb - nkb;  // 0 or 1: the blocks of all units are counted on
       }
       elected_commit(drain);
-      mbar_wait(drain, 0, a.status);
+      mbar_wait(drain, 0, a.status, a.wait_ns);
     }
   } else {
     regs_up<kSumRegs>();
@@ -558,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k = 0, e = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < n_units && !*abort_flag; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < n_units && !given_up(abort_flag); u += gridDim.x) {
       const Unit x = unit_of(tables, u, e);
       e = x.e;
       const bool on = token < x.rows;
@@ -567,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 64; ++i) acc2[i] = 0ull;
       for (int kb = 0; kb < nkb; ++kb, ++k) {
         const int b = k & 1;
-        if (!warp_wait(&scaled[k % kScaleSlots], k / kScaleSlots & 1, a.status)) {
+        if (!warp_wait(&scaled[k % kScaleSlots], k / kScaleSlots & 1, a)) {
           *abort_flag = 1;
           ok = false;
           break;
@@ -575,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* sc = scales + k % kScaleSlots * (kScaleBytes / 4);
         const float v = sc[token], s0 = v * sc[kTokens + (SWIGLU ? 0 : wg)], s1 = SWIGLU ? v * sc[kTokens + 1] : s0;
         const uint64_t s2[2] = {pack2(s0, s0), pack2(s1, s1)};
-        if (!warp_wait(&acc_full[b], (k >> 1) & 1, a.status)) {
+        if (!warp_wait(&acc_full[b], (k >> 1) & 1, a)) {
           *abort_flag = 1;
           ok = false;
           break;
@@ -622,13 +627,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tops[token * 2 + wg] = best;
         __syncwarp();
         if (lane == 0) mbar_arrive(&row_bar[q]);
-        ok = warp_wait(&row_bar[q], phase, a.status);
+        ok = warp_wait(&row_bar[q], phase, a);
         phase ^= 1;
         const BlockScale s = block_scale(max(best, tops[token * 2 + (wg ^ 1)]));
         // met once more, so that none writes the next tile's `tops` before all have read this one's
         __syncwarp();
         if (lane == 0) mbar_arrive(&row_bar[q]);
-        ok = warp_wait(&row_bar[q], phase, a.status) && ok;
+        ok = warp_wait(&row_bar[q], phase, a) && ok;
         phase ^= 1;
         if (on) {
           const float mul = s.mul;
@@ -717,6 +722,8 @@ cudaError_t launch_fp8_matmul(const TrainDevice& d, const ftmoe_fp8_matmul_args&
   a.out = m.out;
   a.out_scale = m.out_scale;
   a.status = d.status;
+  a.wait_ns = d.test_matmul_ns ? d.test_matmul_ns : (uint32_t)kWaitLimitNs;
+  a.withhold = d.test_matmul_ns != 0;
   CUtensorMap map_w, map_x;
   const uint64_t wd[3] = {(uint64_t)m.K, (uint64_t)m.N, (uint64_t)m.E}, ws[2] = {(uint64_t)m.K, (uint64_t)m.N * m.K};
   const uint32_t wb[3] = {128, m.swiglu || m.transpose ? 128u : 256u, 1};

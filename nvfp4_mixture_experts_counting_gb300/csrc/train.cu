@@ -20,7 +20,8 @@ constexpr int kMaxH = 1 << 24;
 static __device__ uint32_t g_ops_status[2];  // what the checks mark; what the latest reader took
 
 std::mutex g_mu;
-std::atomic<uint32_t> g_test_wait_ns{0};  // ftmoe_test_withhold_policy
+std::atomic<uint32_t> g_test_wait_ns{0};    // ftmoe_test_withhold_policy
+std::atomic<uint32_t> g_test_matmul_ns{0};  // ftmoe_test_withhold_matmul
 std::mutex g_status_mu;  // one reader at a time: they share the second word
 TrainDevice g_devices[kMaxDevices] = {};
 
@@ -57,10 +58,11 @@ int current_device(TrainDevice* out) {
       cudaGetLastError();
       return cuda_fail(e, "training operators' set-up");
     }
-    g_devices[dev] = {static_cast<uint32_t*>(p), sms, sort_ctas, 0};
+    g_devices[dev] = {static_cast<uint32_t*>(p), sms, sort_ctas, 0, 0};
   }
   *out = g_devices[dev];
   out->test_wait_ns = g_test_wait_ns;
+  out->test_matmul_ns = g_test_matmul_ns;
   return FTMOE_OK;
 }
 
@@ -197,10 +199,18 @@ int ftmoe_policy_loss(const ftmoe_policy_args* a, ftmoe_stream_t stream) {
   return launched(launch_policy_loss(d, *a, (cudaStream_t)stream), "ftmoe_policy_loss");
 }
 
-int ftmoe_test_withhold_policy(int enable, int64_t wait_limit_ns) {
+static int withhold(std::atomic<uint32_t>& limit, int enable, int64_t wait_limit_ns) {
   if (wait_limit_ns < 0 || wait_limit_ns > (int64_t)kWaitLimitNs) return FTMOE_ERR_INVALID_ARG;
-  g_test_wait_ns = !enable ? 0 : wait_limit_ns ? (uint32_t)wait_limit_ns : (uint32_t)kWaitLimitNs;
+  limit = !enable ? 0 : wait_limit_ns ? (uint32_t)wait_limit_ns : (uint32_t)kWaitLimitNs;
   return FTMOE_OK;
+}
+
+int ftmoe_test_withhold_policy(int enable, int64_t wait_limit_ns) {
+  return withhold(g_test_wait_ns, enable, wait_limit_ns);
+}
+
+int ftmoe_test_withhold_matmul(int enable, int64_t wait_limit_ns) {
+  return withhold(g_test_matmul_ns, enable, wait_limit_ns);
 }
 
 int ftmoe_adamw(const ftmoe_adamw_tensor* tensors, int n, const ftmoe_adamw_params* hp, ftmoe_stream_t stream) {

@@ -14,7 +14,8 @@ struct TrainDevice {
   uint32_t* status;  // device word that the operators' range checks mark
   int num_sms;
   int sort_ctas;  // CTAs of the cluster that sorts
-  uint32_t test_wait_ns;  // ftmoe_test_withhold_policy's limit, or 0
+  uint32_t test_wait_ns;    // ftmoe_test_withhold_policy's limit, or 0
+  uint32_t test_matmul_ns;  // ftmoe_test_withhold_matmul's
 };
 
 constexpr int kMaxBins = 1024;  // experts, or values of one radix digit

@@ -153,6 +153,7 @@ SIGNATURES = {
     "ftmoe_fp8_quantize_weights": ([C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p,
                                     C.c_void_p], C.c_int),
     "ftmoe_fp8_matmul": ([C.POINTER(Fp8MatmulArgs), C.c_void_p], C.c_int),
+    "ftmoe_test_withhold_matmul": ([C.c_int, C.c_int64], C.c_int),
     "ftmoe_swiglu": ([C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p], C.c_int),
     "ftmoe_swiglu_backward": ([C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p,
                                C.c_void_p], C.c_int),
@@ -645,6 +646,10 @@ def ftmoe_fp8_matmul(a, a_scale, w, w_scale, offsets, M: int, E: int, N: int, K:
                              swiglu, dtype, _codes8(out, n_out) if swiglu else _array(out, dtype, n_out),
                              _array(out_scale, FP32, out_width // 128 * M) if swiglu else None)
     _check(lib().ftmoe_fp8_matmul(C.byref(args), _stream(stream)), "ftmoe_fp8_matmul")
+
+
+def ftmoe_test_withhold_matmul(enable: bool, wait_limit_ns: int = 0):
+    _check(lib().ftmoe_test_withhold_matmul(int(enable), wait_limit_ns), "ftmoe_test_withhold_matmul")
 
 
 def _swiglu_out(out, scales, dtype: int, rows: int, width: int):

@@ -167,3 +167,11 @@ def test_binding_refuses():
         ftmoe.ftmoe_swiglu(z(4, 256), 4, 128, codes)
     with pytest.raises(ValueError):
         ftmoe.ftmoe_swiglu_backward(z(4, 128), z(4, 256), 4, 128, z(4, 256, dtype=E4M3), z(1, 4))
+
+
+def test_withhold_matmul_limits(lib):  # noqa: F811
+    for limit in (-1, 1_000_000_001):
+        with pytest.raises(ftmoe.FtmoeError):
+            ftmoe.ftmoe_test_withhold_matmul(True, limit)
+    ftmoe.ftmoe_test_withhold_matmul(True, 1_000_000_000)
+    ftmoe.ftmoe_test_withhold_matmul(False)

@@ -1,0 +1,75 @@
+"""The layer on 8-bit codes where its calls give up, or where their arithmetic has least to spare.  Bounds are those
+of the layer's other tests: EPS is half a step of fp32, 2^-24."""
+
+import pytest
+import torch
+
+from nvfp4_mixture_experts_counting_gb300 import ftmoe
+
+from test_gpu_fp8_layer import E4M3, bank, offsets_of, rows_of
+from test_gpu_train_ops import BF16, DEV, FP32, Guarded, built, gen  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+FORMS = pytest.mark.parametrize("form", ["plain", "transpose", "swiglu"])
+
+
+# ----------------------------------------------------------------- a wait that runs out
+
+def call_product(a, a_scale, w, w_scale, counts, form, dtype=BF16):
+    """Outputs between guards, as bytes (codes and scales with SwiGLU) filled beforehand, and their rows' width."""
+    new, M, (E, N, K) = Guarded(), a.shape[0], w.shape
+    O = K if form == "transpose" else N // 2 if form == "swiglu" else N
+    out = new((M, O), E4M3 if form == "swiglu" else dtype)
+    out.view(torch.uint8).fill_(9)
+    scales = new((O // 128, M), FP32, 5.0) if form == "swiglu" else None
+    ftmoe.ftmoe_fp8_matmul(a, a_scale, w, w_scale, offsets_of(counts), M, E, N, K, out, scales,
+                           transpose=form == "transpose", swiglu=form == "swiglu")
+    new.check()
+    return out, scales
+
+
+def first_ctas_tiles(M, O, counts, form):
+    """(rows, columns) of the tiles that the first CTA has: an expert's tiles in order, 128 rows by 256 columns (128 of
+    h), rows fastest; a CTA takes every one of as many as there are SMs, or could be tiles."""
+    width = 128 if form == "swiglu" else 256
+    columns = -(-O // width)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    grid = min((M // 128 + min(M, len(counts))) * columns, sms)
+    units, at = [], 0
+    for n in counts:
+        units += [(slice(at + r, at + min(n, r + 128)), slice(j * width, min(O, (j + 1) * width)))
+                  for j in range(columns) for r in range(0, n, 128)]
+        at += n
+    return units[::grid]
+
+
+@FORMS
+@pytest.mark.parametrize("counts,N,K", [
+    ([2, 0, 3], 256, 144), ([1], 256, 16),           # a tile or two of one block or two
+    ([700, 0, 300], 1280, 640), ([129, 1, 0, 127, 43], 256, 2000),
+    ([2500, 0, 4000, 1500, 333], 1280, 1040)])       # the first CTA has several tiles
+def test_product_wait_that_runs_out(counts, N, K, form):
+    """The first CTA's first tokens are never asked for: its waits end after 2 ms each, the call reports it and leaves
+    that CTA's tiles, the others are as they should be, and the next call is as good as new."""
+    g, M, E = gen(110 + N + K + len(counts)), sum(counts), len(counts)
+    a, a_scale = rows_of(g, M, N if form == "transpose" else K)
+    w, w_scale = bank(g, E, N, K)
+    want, want_scale = call_product(a, a_scale, w, w_scale, counts, form)
+    assert ftmoe.ftmoe_ops_status() == 0
+    ftmoe.ftmoe_test_withhold_matmul(True, 2_000_000)
+    try:
+        got, got_scale = call_product(a, a_scale, w, w_scale, counts, form)
+    finally:
+        ftmoe.ftmoe_test_withhold_matmul(False)
+    assert ftmoe.ftmoe_ops_status() == -7 and ftmoe.ftmoe_ops_status() == 0
+    again, again_scale = call_product(a, a_scale, w, w_scale, counts, form)
+    assert ftmoe.ftmoe_ops_status() == 0
+    assert torch.equal(again.view(torch.uint8), want.view(torch.uint8))
+    for rows, cols in first_ctas_tiles(M, want.shape[1], counts, form):
+        size = want.element_size()
+        want.view(torch.uint8).view(M, -1)[rows, cols.start * size:cols.stop * size] = 9
+        if form == "swiglu":
+            want_scale[cols.start // 128, rows] = 5.0
+    assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+    if form == "swiglu":
+        assert torch.equal(got_scale, want_scale)
