@@ -158,10 +158,10 @@ __device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float& d
 }
 
 // Quantised output: eight lanes take 128 columns of a row.  GRAD writes a row
-// of 2 I codes, gate's first.  131072 x 640 from bf16: 74 us, 5.7 TB/s, the issue
-// slots three quarters busy with the exponentials' instructions (104 us with a
-// division in the sigmoid instead of the approximate reciprocal; its gradient to
-// codes 151 instead of 112 us, 6.0 TB/s).
+// of 2 I codes, gate's first.  131072 x 640 from bf16: 79 us, 5.3 TB/s, the issue
+// slots busiest with the exponentials' instructions (104 us with a division in
+// the sigmoid instead of the approximate reciprocal; its gradient to codes 151
+// instead of 116 us, 5.8 TB/s).
 template <typename T, bool GRAD>
 __global__ void __launch_bounds__(kThreads) k_swiglu_fp8(const T* gu, const T* dh, int rows_, int I,
                                                          const int32_t* used, uint8_t* codes, float* scales,
@@ -210,9 +210,9 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_fp8(const T* gu, const T* d
 // Output in the input's type.  A warp takes neighbouring pieces of a row, a
 // lane one (or four, 32 pieces apart) of V = 16 bytes' values, or of one value
 // where rows are not a multiple of 16 bytes.  Four where a lane has little on
-// its way otherwise (the gradient of 8191 x 1001 fp16 values 18 us, 28 with
+// its way otherwise (the gradient of 8191 x 1001 fp16 values 19 us, 28 with
 // one); with two 16-byte loads a lane more warps at a time are better (131072 x
-// 640 bf16 values 79 us, 96 with four).
+// 640 bf16 values 84 us, 96 with four).
 template <int V, bool GRAD>
 constexpr int kPieces = V > 1 && !GRAD ? 1 : 4;
 template <typename T, int V, bool GRAD>

@@ -7,7 +7,7 @@ import torch
 from nvfp4_mixture_experts_counting_gb300 import ftmoe
 
 from test_gpu_fp8_layer import E4M3, bank, offsets_of, rows_of
-from test_gpu_train_ops import BF16, DEV, FP32, Guarded, built, gen  # noqa: F401
+from test_gpu_train_ops import BF16, DEV, EPS, FP32, UNIT, Guarded, built, gen, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 FORMS = pytest.mark.parametrize("form", ["plain", "transpose", "swiglu"])
@@ -73,3 +73,35 @@ def test_product_wait_that_runs_out(counts, N, K, form):
     assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
     if form == "swiglu":
         assert torch.equal(got_scale, want_scale)
+
+
+# ----------------------------------------------------------------- SwiGLU of far negative gates
+
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+def test_swiglu_of_far_negative_gates(dtype):
+    """Sigmoids next to fp32's smallest numbers times large factors.  exp is within two of fp32's last places, which
+    are 2^-149 there, and its product with the reciprocal adds half of one: sigmoid is within 2.5 2^-149, SiLU's
+    rounding adds 2^-150; all else is relative as for other gates."""
+    I, big = 128, 2.0 ** 50
+    g = torch.linspace(-104.0, -80.0, 64 * I, device=DEV).view(64, I).to(dtype)
+    gu = torch.cat([g, torch.full_like(g, big)], 1)
+    dh = torch.full_like(g, big)
+    z, s = g.double(), torch.sigmoid(g.double())
+    exact, unit, last = z * s * big, UNIT[dtype], 2.5 * 2.0 ** -149
+    bound = (last * z.abs() + 2.0 ** -150) * big + 8 * EPS * exact.abs()
+    new = Guarded()
+    h, dgu = new((64, I), dtype), new((64, 2 * I), dtype)
+    ftmoe.ftmoe_swiglu(gu, 64, I, h)
+    within(h, exact, bound * (1 + unit) + unit * exact.abs())
+    codes, scales = new((64, I), E4M3), new((1, 64), FP32)
+    ftmoe.ftmoe_swiglu(gu, 64, I, codes, scales)
+    top = exact.abs().amax(1)
+    within(scales[0], top / 448, (bound.amax(1) + 2 * EPS * top) / 448)
+    ftmoe.ftmoe_swiglu_backward(dh, gu, 64, I, dgu)
+    dg, du = big * big * s * (1 + z * (1 - s)), big * z * s
+    rel = 2.0 ** -20
+    dg_bound = big * big * (1 + z.abs()) * (last + rel * s)
+    du_bound = big * z.abs() * (last + rel * s)
+    within(dgu[:, :I], dg, dg_bound * (1 + unit) + unit * dg.abs())
+    within(dgu[:, I:], du, du_bound * (1 + unit) + unit * du.abs())
+    new.check()
