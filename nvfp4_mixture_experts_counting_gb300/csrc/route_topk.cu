@@ -426,9 +426,9 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 8 ? kCtasPerSm : VPL == 16
     const float z = mine >= 0 ? usable_logit(row, mine) : -INFINITY;
     if (a.norm) {
       const float n = a.sigmoid ? fminf(z, 0.f) : z, high = warp_max_redux(n);
-      if (mine >= 0) s = a.sigmoid ? __fdividef(expf(n - high), 1.f + expf(-fabsf(z))) : expf(n - high);
+      if (mine >= 0) s = a.sigmoid ? expf(n - high) / (1.f + expf(-fabsf(z))) : expf(n - high);
       const float sum = warp_sum_f32(s);
-      s = sum > 0.f ? __fdividef(s * a.scale, sum) : 0.f;
+      s = sum > 0.f ? s * a.scale / sum : 0.f;
     } else if (mine >= 0) {
       s = a.scale * (a.sigmoid ? sigmoid(z) : expf(z - top) * largest);
     }

@@ -105,3 +105,24 @@ def test_swiglu_of_far_negative_gates(dtype):
     within(dgu[:, :I], dg, dg_bound * (1 + unit) + unit * dg.abs())
     within(dgu[:, I:], du, du_bound * (1 + unit) + unit * du.abs())
     new.check()
+
+
+# ----------------------------------------------------------------- routing
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("scale", [1.0, 2.5, 0.1, 1.7, 3.3])
+def test_route_equal_weights_round_once(scale, score):
+    """n equal logits: scores are 1 (or 1/2), their sum n (or n/2), all exact, so that a weight is scale / n rounded."""
+    k, E = 32, 64
+    logits = torch.full((k, E), -float("inf"), device=DEV)
+    for n in range(1, k + 1):
+        logits[n - 1, :n] = 0.0
+    new = Guarded()
+    idx, w = new((k, k), torch.int32), new((k, k), FP32)
+    ftmoe.ftmoe_route_topk(ftmoe.route_args(logits, idx, w, score=score, scale=scale))
+    new.check()
+    at = torch.arange(k, device=DEV)
+    on = at[None] <= at[:, None]
+    want = torch.full((k, k), scale, device=DEV) / (at + 1.0)[:, None]
+    assert torch.equal(w, torch.where(on, want, 0.0))
+    assert torch.equal(idx, torch.where(on, at[None], -1).int())
