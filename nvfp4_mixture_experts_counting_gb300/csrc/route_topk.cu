@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 8 ? kCtasPerSm : VPL == 16
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = lane + 32 * i;
-    bias[i] = a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
+    // no read-only load: the stream's previous kernel may write the biases while this one starts
+    bias[i] = a.bias && e < a.E ? a.bias[e] : 0.f;
     if (fabsf(bias[i]) < INFINITY) {
       widest = fmaxf(widest, fabsf(bias[i]));
     } else {

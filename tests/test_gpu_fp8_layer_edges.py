@@ -126,3 +126,42 @@ def test_route_equal_weights_round_once(scale, score):
     want = torch.full((k, k), scale, device=DEV) / (at + 1.0)[:, None]
     assert torch.equal(w, torch.where(on, want, 0.0))
     assert torch.equal(idx, torch.where(on, at[None], -1).int())
+
+
+def test_route_reads_the_biases_that_the_previous_kernel_wrote():
+    """Biases change between calls in a row, in the stream and in a graph (the call starts while the copy ends)."""
+    g = gen(120)
+    T, E, k, n = 64, 256, 8, 6
+    logits, biases = torch.randn(T, E, generator=g, device=DEV), torch.randn(n, E, generator=g, device=DEV)
+    bias, idx = torch.zeros(E, device=DEV), torch.empty(n, T, k, dtype=torch.int32, device=DEV)
+    w = torch.empty(n, T, k, device=DEV)
+    args = [ftmoe.route_args(logits, idx[i], w[i], score="sigmoid", bias=bias) for i in range(n)]
+    for i in range(n):
+        bias.copy_(biases[i])
+        torch.cuda.synchronize()
+        ftmoe.ftmoe_route_topk(args[i])
+        torch.cuda.synchronize()
+    want, want_w = idx.clone(), w.clone()
+
+    def pass_():
+        for i in range(n):
+            bias.copy_(biases[i])
+            ftmoe.ftmoe_route_topk(args[i])
+
+    def same():
+        torch.cuda.synchronize()
+        ok = torch.equal(idx, want) and torch.equal(w, want_w)
+        idx.fill_(-9)
+        return ok
+
+    assert not torch.equal(want[0], want[1])
+    idx.fill_(-9)
+    for _ in range(50):
+        pass_()
+        assert same()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pass_()
+    for _ in range(50):
+        graph.replay()
+        assert same()
