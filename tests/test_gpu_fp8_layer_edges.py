@@ -165,3 +165,24 @@ def test_route_reads_the_biases_that_the_previous_kernel_wrote():
     for _ in range(50):
         graph.replay()
         assert same()
+
+
+# ----------------------------------------------------------------- the product's scales and its SwiGLU
+
+def test_product_swiglu_of_all_gates():
+    """Rows whose gate is one number and whose up is its magnitude times 2^60, so that their scale is |h| / 448 and
+    shows h's error: (1.25 |g| + 8) of SiLU, the product with up and the scale's rounding; 0 below -87.3."""
+    n, I, K = 1 << 14, 128, 16
+    size = torch.linspace(0.005, 87.3, n, device=DEV)
+    a, a_scale = torch.zeros(2 * n + 64, K, device=DEV), torch.empty(1, 2 * n + 64, device=DEV)
+    a[:, 0], a[:, 1] = -1.0, 1.0
+    a[:n, 0] = 1.0
+    a_scale[0] = torch.cat([size, size, torch.linspace(87.4, 300.0, 64, device=DEV)])
+    w, w_scale = torch.zeros(1, 2 * I, K, device=DEV), torch.tensor([[[1.0], [2.0 ** 60]]], device=DEV)
+    w[0, :I, 0] = 1.0
+    w[0, I:, 1] = 1.0
+    _, scales = call_product(a.to(E4M3), a_scale, w.to(E4M3), w_scale, [2 * n + 64], "swiglu")
+    g = torch.cat([size, -size]).double()
+    h = g * torch.sigmoid(g) * g.abs() * 2.0 ** 60
+    within(scales[0, :2 * n], h.abs() / 448, (1.25 * g.abs() + 10) * EPS * h.abs() / 448 * (1 + 2.0 ** -16))
+    assert bool((scales[0, 2 * n:] == 0).all())
