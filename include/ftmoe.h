@@ -695,7 +695,10 @@ int ftmoe_fp8_quantize_weights(const void* w, int dtype, int E, int N, int K, ui
  *               quantised: out codes [M, N/2], out_scale [N/256][M]
  * x and w are the values that codes and scales stand for.  Products are exact,
  * summed on the tensor cores over a block of 128 and in fp32 over the blocks.
- * y is not rounded before SwiGLU; there SiLU of y is within (1.25 |y| + 8) 2^-24 of itself, and 0 below
+ * The scales of a block, the rows' and the weights', are multiplied in fp32
+ * first: where that product is below 2^-126 the block loses bits or vanishes,
+ * and from 2^128 on it comes out infinite or NaN.  y is not rounded before
+ * SwiGLU; there SiLU of y is within (1.25 |y| + 8) 2^-24 of itself, and 0 below
  * -87.3, before h's rounding to a code.  Rows of no expert (from offsets[E] on) stay
  * as they were and may hold anything.  An expert whose rows begin before an
  * earlier one's first row, fall or leave [0, M] is left out and marks the

@@ -186,3 +186,19 @@ def test_product_swiglu_of_all_gates():
     h = g * torch.sigmoid(g) * g.abs() * 2.0 ** 60
     within(scales[0, :2 * n], h.abs() / 448, (1.25 * g.abs() + 10) * EPS * h.abs() / 448 * (1 + 2.0 ** -16))
     assert bool((scales[0, 2 * n:] == 0).all())
+
+
+@pytest.mark.parametrize("form", ["plain", "transpose"])
+@pytest.mark.parametrize("of_rows,of_weights", [(-120, -6), (-6, -120), (120, -120), (-120, 120), (100, 20), (20, 100)])
+def test_product_of_far_scales(of_rows, of_weights, form):
+    """Scales are powers of two whose product fp32 holds; small whole codes, so that every sum is exact."""
+    g = gen(130)
+    M, N, K = 150, 272, 400
+    C = N if form == "transpose" else K
+    q = lambda *s: torch.randint(-2, 3, s, generator=g, device=DEV).float()
+    x, m = q(M, C), q(1, N, K)
+    a_scale = torch.full((-(-C // 128), M), 2.0 ** of_rows, device=DEV)
+    w_scale = torch.full((1, -(-N // 128), -(-K // 128)), 2.0 ** of_weights, device=DEV)
+    out, _ = call_product(x.to(E4M3), a_scale, m.to(E4M3), w_scale, [M], form, FP32)
+    y = x.double() @ (m[0] if form == "transpose" else m[0].t()).double()
+    assert torch.equal(out.double(), y * 2.0 ** (of_rows + of_weights))
