@@ -6,8 +6,8 @@ import torch
 
 from nvfp4_mixture_experts_counting_gb300 import ftmoe
 
-from test_gpu_fp8_layer import E4M3, bank, offsets_of, rows_of
-from test_gpu_train_ops import BF16, DEV, EPS, FP32, UNIT, Guarded, built, gen, within  # noqa: F401
+from test_gpu_fp8_layer import CODE, CODE_TINY, E4M3, bank, offsets_of, product, rows_of, value
+from test_gpu_train_ops import BF16, DEV, EPS, FP32, TINY, UNIT, Guarded, built, gen, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 FORMS = pytest.mark.parametrize("form", ["plain", "transpose", "swiglu"])
@@ -16,13 +16,15 @@ FORMS = pytest.mark.parametrize("form", ["plain", "transpose", "swiglu"])
 # ----------------------------------------------------------------- a wait that runs out
 
 def call_product(a, a_scale, w, w_scale, counts, form, dtype=BF16):
-    """Outputs between guards, as bytes (codes and scales with SwiGLU) filled beforehand, and their rows' width."""
+    """Outputs between guards (codes and scales with SwiGLU), their bytes 9 and scales 5.0 beforehand; `counts` of each
+    expert, or the offsets."""
     new, M, (E, N, K) = Guarded(), a.shape[0], w.shape
     O = K if form == "transpose" else N // 2 if form == "swiglu" else N
     out = new((M, O), E4M3 if form == "swiglu" else dtype)
     out.view(torch.uint8).fill_(9)
     scales = new((O // 128, M), FP32, 5.0) if form == "swiglu" else None
-    ftmoe.ftmoe_fp8_matmul(a, a_scale, w, w_scale, offsets_of(counts), M, E, N, K, out, scales,
+    offsets = counts if torch.is_tensor(counts) else offsets_of(counts)
+    ftmoe.ftmoe_fp8_matmul(a, a_scale, w, w_scale, offsets, M, E, N, K, out, scales,
                            transpose=form == "transpose", swiglu=form == "swiglu")
     new.check()
     return out, scales
@@ -202,3 +204,79 @@ def test_product_of_far_scales(of_rows, of_weights, form):
     out, _ = call_product(x.to(E4M3), a_scale, m.to(E4M3), w_scale, [M], form, FP32)
     y = x.double() @ (m[0] if form == "transpose" else m[0].t()).double()
     assert torch.equal(out.double(), y * 2.0 ** (of_rows + of_weights))
+
+
+# ----------------------------------------------------------------- the product's units and offsets
+
+MANY = [2555, 0, 4011, 1533, 3901]  # copies of 128 tokens, several units a CTA, ragged last tiles
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+@pytest.mark.parametrize("C", [272, 512, 1040])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_product_of_many_tokens_an_expert(transpose, C, dtype):
+    g, M, O = gen(140 + C), sum(MANY), 1280
+    N, K = (C, O) if transpose else (O, C)
+    a, a_scale = rows_of(g, M, C)
+    w, w_scale = bank(g, len(MANY), N, K)
+    y, bound = product(a, a_scale, w, w_scale, MANY, transpose)
+    form, unit = "transpose" if transpose else "plain", 0.0 if dtype is FP32 else UNIT[dtype]
+    first, _ = call_product(a, a_scale, w, w_scale, MANY, form, dtype)
+    within(first, y, bound * (1 + unit) + unit * y.abs() + TINY[dtype])
+    for _ in range(3):
+        assert torch.equal(call_product(a, a_scale, w, w_scale, MANY, form, dtype)[0], first)
+
+
+@pytest.mark.parametrize("K", [272, 512, 1040])
+def test_product_with_swiglu_of_many_tokens_an_expert(K):
+    g, M, I = gen(150 + K), sum(MANY), 640
+    a, a_scale = rows_of(g, M, K)
+    w, w_scale = bank(g, len(MANY), 2 * I, K, std=0.1)
+    y, bound = product(a, a_scale, w, w_scale, MANY, False)
+    gate, up = y.chunk(2, 1)
+    dg, du = bound.chunk(2, 1)
+    h = gate * torch.sigmoid(gate) * up
+    # |d SiLU| <= 1.1; SiLU's own error, and the product's
+    err = 1.1 * dg * (up.abs() + du) + (gate * torch.sigmoid(gate)).abs() * du + (1.25 * gate.abs() + 9) * EPS * h.abs()
+    worst, top = (v.view(M, -1, 128).amax(2) for v in (err, h.abs()))
+    first, scales = call_product(a, a_scale, w, w_scale, MANY, "swiglu")
+    within(scales.t(), top / 448, (worst + 2 * EPS * top) / 448 + 1e-30)
+    wide, spread = (v.repeat_interleave(128, 1) for v in (top / 448, worst))
+    within(value(first, scales), h,
+           (CODE * h.abs() + CODE_TINY * wide) * (1 + 2.0 ** -16) + 2 * err + 2 * spread + 1e-30)
+    for _ in range(3):
+        again, again_scales = call_product(a, a_scale, w, w_scale, MANY, "swiglu")
+        assert torch.equal(again.view(torch.uint8), first.view(torch.uint8)) and torch.equal(again_scales, scales)
+
+
+BIG = 2 ** 31 - 1
+TABLES = [
+    [0, 5, 10, 9, 20], [0, 5, 10, 21, 20], [0, 5, 10, -4, 20], [0, 5, 10, 1 << 30, -(1 << 30)], [0, 5, 4, 10, 20],
+    [3, 5, 10, 15, 21], [-1, 5, 10, 15, 20], [BIG, 5, 10, 15, 20], [0, BIG, 10, 15, 20], [0, 0, 20, 0, 20],
+    [5, 4, 3, 2, 1], [-BIG - 1, BIG, -BIG - 1, BIG, 20]]
+
+
+@FORMS
+@pytest.mark.parametrize("table", TABLES, ids=str)
+def test_product_leaves_out_bad_experts_alone(table, form):
+    """Only the rows of experts that the header calls good are written, and each as it would be by itself."""
+    g, M, E, N, K = gen(160), 20, 4, 256, 128
+    a, a_scale = rows_of(g, M, N if form == "transpose" else K)
+    w, w_scale = bank(g, E, N, K)
+    alone = [call_product(a, a_scale, w[e:e + 1], w_scale[e:e + 1], [M], form) for e in range(E)]
+    offsets = torch.tensor(table, dtype=torch.int32, device=DEV)
+    got, scales = call_product(a, a_scale, w, w_scale, offsets, form)
+    want = torch.full_like(got.view(torch.uint8), 9)
+    want_scales = None if scales is None else torch.full_like(scales, 5.0)
+    bad = False
+    for e in range(E):
+        lo, hi = table[e], table[e + 1]
+        if not max([0] + table[:e + 1]) <= lo <= hi <= M:
+            bad = True
+            continue
+        want[lo:hi] = alone[e][0].view(torch.uint8)[lo:hi]
+        if scales is not None:
+            want_scales[:, lo:hi] = alone[e][1][:, lo:hi]
+    assert bad and ftmoe.ftmoe_ops_status() == -10
+    assert torch.equal(got.view(torch.uint8), want)
+    assert scales is None or torch.equal(scales, want_scales)
