@@ -474,7 +474,9 @@ int ftmoe_combine_backward(const void* dout, const void* ys, int dtype, int T, i
  *                   p = softmax(logits), logits fp32 [T, E] with the bias
  * topk_idx is the router's own choice, before any slot is dropped; an index
  * outside [0, E) is left out and marks the status word.  dlogits: fp32
- * [T, E], written whole; may be `logits` itself. */
+ * [T, E], written whole; may be `logits` itself.  For ftmoe_route_static's
+ * router; that of ftmoe_route_topk has ftmoe_route_topk_backward, which also
+ * takes 16-bit logits, sigmoid scores, a scale, masked logits and slots of -1. */
 int ftmoe_route_backward(const float* logits, const int32_t* topk_idx, const float* topk_w, const float* dw, int T,
                          int E, int top_k, int norm_topk_prob, float* dlogits, ftmoe_stream_t stream);
 
@@ -668,7 +670,9 @@ int ftmoe_route_topk(const ftmoe_route_args* args, ftmoe_stream_t stream);
  * the gradient of topk_w; topk_idx and topk_w are the forward call's.  The
  * choice itself and the bias have none.  Written whole; slots of -1 have no
  * part, an index outside [-1, E) is left out and marks the status word, equal
- * indices add up.  dlogits may be logits itself (ld_d == ld). */
+ * indices add up.  dlogits may be logits itself (ld_d == ld).
+ * (ftmoe_route_backward is ftmoe_route_static's: there -1 marks the status word
+ * too, and every logit counts.) */
 int ftmoe_route_topk_backward(const ftmoe_route_args* args, const float* dw, void* dlogits, int64_t ld_d,
                               ftmoe_stream_t stream);
 

@@ -20,10 +20,11 @@
 // and a warp's reads and sums 550; the waits for the block and for its scales are
 // 120 to 150 each even where nothing is to be waited for, and what other warps
 // issue slows those beside them.  16384 tokens of 8 of 256 experts, gate_up [1280,
-// 2560] with SwiGLU: 432 us, 1.99 PFLOP/s; its input's gradient 512 us; down 330
-// us; one matrix of 4096 x 4096 with 4096 rows 74 us, 1.86 PFLOP/s.  With few
-// tokens the weights' bytes: 256 tokens of the same layer 152 us, 5.4 TB/s; 16
-// tokens 49 us, 5.0 TB/s (units of uneven experts over 152 SMs).
+// 2560] with SwiGLU: 435 us, 1.97 PFLOP/s, in short runs of passes, and 481 in long
+// ones, which meet the power limit; its input's gradient 516 and 548; down 328; one
+// matrix of 4096 x 4096 with 4096 rows 70 us, 1.96 PFLOP/s.  With few tokens the
+// weights' bytes: 256 tokens of the same layer 137 us, 6.0 TB/s; 16 tokens 50 us,
+// 5.0 TB/s (units of uneven experts over 152 SMs).
 //
 // So the copies are spread: one of 128 tokens where experts have that many (32
 // otherwise: the smaller copies read less of the next expert's rows; 16384 tokens
@@ -32,14 +33,15 @@
 // (loaded by the summing warps three blocks ahead: the input's gradient 539, down
 // 344, gate_up without SwiGLU 473 instead of 446 us).
 //
-// Measured and not kept: tokens as the MMA's columns (scales then differ by
+// Measured and not kept, each against the kernel of its time in short runs, in
+// which some 9 us are the events': tokens as the MMA's columns (scales then differ by
 // column: 955 us); CTA pairs on one 256-token tile (the MMAs run at 530 cycles,
 // but the hand-offs cross CTAs and a quarter of the rows are empty: 512 us);
 // 16 summing warps of 64 columns (543 us when one warp made all copies); reads of
 // 32 columns of tensor memory (537 us).
 // For few tokens: narrow tiles of the tokens as columns (64 tokens through down
-// 80 us, here 68), pairs of CTAs that share a unit's blocks (16 tokens through
-// gate_up 76 us, here 58; the exchange of sums costs more than idle SMs).
+// 80 us, 68 without), pairs of CTAs that share a unit's blocks (16 tokens through
+// gate_up 76 us, 58 without; the exchange of sums costs more than idle SMs).
 //
 // Warps: 0 copies the weights' tiles by TMA, 2 the tokens' and the scales, 1 and 3
 // issue the MMAs, 4-11 add up.
@@ -302,9 +304,9 @@ __device__ __forceinline__ void store_32(void* p, const uint32_t (&v)[8]) {
 // rows from `row` on, `rows` of them, through shared memory (`st`).  A whole 32
 // of aligned rows (`map`) go out by TMA behind the warp's back: stores of its
 // own pass a 32-byte sector a cycle, 2200 cycles for a tile's 64 KB, in which
-// the tensor cores come to a stop (16384 tokens through down 361 us, so 342).
-// Others go as stores that cover up to eight rows' 64 bytes each, and not 32
-// rows' few (a product of 666 fp32 columns 60 -> 34 us).
+// the tensor cores come to a stop (16384 tokens through down 361 us, and 342 with
+// the copies).  Others go as stores that cover up to eight rows' 64 bytes each,
+// and not 32 rows' few (a product of 666 fp32 columns 60 -> 34 us).
 template <bool WIDE>
 __device__ __forceinline__ void store_tile(const MatmulArgs& a, unsigned char* st, int64_t row, int rows, int c0,
                                            const float (&acc)[128], int lane, const CUtensorMap* map) {

@@ -9,8 +9,12 @@
 // the logit (no bias, and groups by their largest value) the logits themselves
 // are ranked, which is exact even where fp64 scores are equal (a sigmoid of 40).  Otherwise c is computed in fp32 with
 // an error bound, and a token where two values that decide are closer than
-// their bounds is ranked again in fp64.  Of N(0, 1) logits with E = 256 that is
-// one token in some hundreds.
+// their bounds is ranked again in fp64.  How many those are is the data's: of
+// fp32 N(0, 1) logits with E = 256 and biases one token in some hundreds; many of
+// logits that are equal where their biases are (16-bit ones with zero biases: the
+// doubt is settled by the index, but only in fp64), of softmax scores whose
+// logits spread far (the bound is in proportion to the largest score), and of
+// saturated sigmoids.  The times below show what that costs.
 //
 // A warp takes a token; lane i holds the experts i, i + 32, ...  With the
 // lanes' largest values sorted, the (k+1)-th of them is below or at the (k+1)-th
@@ -20,8 +24,15 @@
 //
 // The forward call is bound by issue slots, not by its bytes (2.6 us of DRAM):
 // 16384 tokens of 256 experts in eight groups with biases 22 us, two thirds of
-// the slots busy; 16 tokens 5.4 us with the call, some 2.5 on the device.  The
-// gradient is a launch and one pass: 16384 tokens 6 us in a graph.
+// the slots busy, some 1060 instructions a token; without biases or groups 13; 16
+// tokens 5.3 us with the call, some 2.5 on the device.  With more tokens ranked in
+// fp64 (top 8 of 256, no groups): bf16 N(0, 1) logits and zero biases, sigmoid 32
+// us, softmax 107; fp32 logits of deviation 6 and zero biases, sigmoid 54; softmax
+// with biases in steps of 0.001, deviation 4 102, 6 180; all logits and biases
+// equal, sigmoid 347 (without a bias 25, as logits alone are ranked exactly),
+// softmax in groups 533.  The gradient is a launch and one pass, 16384 tokens 6 us
+// in a graph: each row is written after a chain of loads (index, logit) and
+// shuffles, and the grid's 16 CTAs an SM are more than are resident at once.
 #include <cfloat>
 
 #include "fp8_common.cuh"
@@ -257,7 +268,8 @@ __device__ __forceinline__ float sort_lanes(float v, int lane) {
 
 // VPL: experts a lane holds.  Up to 256 experts are held to 64 registers, so
 // that eight CTAs fit an SM, and the grid is no larger: what a warp works out
-// of the biases serves several tokens (16384 tokens in groups 25 -> 23 us).
+// of the biases serves several tokens (16384 tokens in groups 25 -> 23 us).  At
+// 256 that spills some (72 bytes stored, 124 loaded).
 constexpr int kCtasPerSm = 8;
 template <typename T, int VPL>
 __global__ void __launch_bounds__(kWarps * 32, VPL <= 8 ? kCtasPerSm : VPL == 16 ? 4 : 2) k_route_topk(const __grid_constant__ RouteKernelArgs a) {
